@@ -90,6 +90,45 @@ rlq_status check_scales(const char *name, const void *p, int64_t ld, int64_t ext
 
 cudaStream_t cs(rlq_stream_t s) { return reinterpret_cast<cudaStream_t>(s); }
 
+// Shapes of the residual norm and its backward pass.
+rlq_status check_norm_shape(int64_t M, int64_t K)
+{
+    RLQ_REQUIRE(M >= 0 && K >= 0, RLQ_ERR_INVALID_ARG, "negative size (M=%lld, K=%lld)", (long long)M, (long long)K);
+    RLQ_REQUIRE(K % G == 0, RLQ_ERR_UNSUPPORTED, "K=%lld is not a multiple of 128", (long long)K);
+    RLQ_REQUIRE(K <= 16384, RLQ_ERR_UNSUPPORTED, "K=%lld is beyond 16384", (long long)K);
+    RLQ_REQUIRE(M < MAX_DIM, RLQ_ERR_UNSUPPORTED, "dimension beyond 2^31");
+    return RLQ_OK;
+}
+
+// Logits and targets of the token log probabilities and the policy loss.
+rlq_status check_logits(PolicyLossArgs *a, const void *logits, rlq_dtype dtype, int64_t ld, int64_t rows, int64_t V,
+                        const int64_t *targets, float temperature)
+{
+    RLQ_REQUIRE(dtype == RLQ_DTYPE_BF16 || dtype == RLQ_DTYPE_F32, RLQ_ERR_INVALID_ARG, "unknown dtype %d", (int)dtype);
+    RLQ_REQUIRE(rows >= 0, RLQ_ERR_INVALID_ARG, "negative size (rows=%lld)", (long long)rows);
+    RLQ_REQUIRE(V >= 1, RLQ_ERR_INVALID_ARG, "V=%lld: a row has at least one logit", (long long)V);
+    RLQ_REQUIRE(V <= policy_max_vocab(dtype), RLQ_ERR_UNSUPPORTED, "V=%lld is beyond %lld", (long long)V,
+                (long long)policy_max_vocab(dtype));
+    RLQ_REQUIRE(rows < MAX_DIM / 8, RLQ_ERR_UNSUPPORTED, "rows beyond 2^28");
+    RLQ_REQUIRE(std::isfinite(temperature) && temperature > 0.0f, RLQ_ERR_INVALID_ARG,
+                "temperature must be finite and > 0");
+    if (rows == 0)
+        return RLQ_OK;
+    RLQ_REQUIRE(logits, RLQ_ERR_INVALID_ARG, "logits is NULL");
+    RLQ_REQUIRE(ld >= V, RLQ_ERR_INVALID_ARG, "logits: pitch %lld < row length %lld", (long long)ld, (long long)V);
+    RLQ_REQUIRE(al(logits, dtype == RLQ_DTYPE_F32 ? 4 : 2), RLQ_ERR_MISALIGNED, "logits is not aligned to its element");
+    RLQ_REQUIRE(targets, RLQ_ERR_INVALID_ARG, "targets is NULL");
+    RLQ_REQUIRE(al(targets, 8), RLQ_ERR_MISALIGNED, "targets is not 8-byte aligned");
+    a->logits = logits;
+    a->dtype = dtype;
+    a->ld = ld;
+    a->rows = rows;
+    a->V = V;
+    a->targets = targets;
+    a->temperature = temperature;
+    return RLQ_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -517,6 +556,212 @@ rlq_status rlq_gemm_wgrad_splitk(const uint8_t *dyqT, int64_t lddyqT, const floa
     RLQ_TRY(check_workspace(workspace, workspace_bytes));
     return gemm_wgrad(dyqT, lddyqT, dysc, lddysc, xqT, ldxqT, xsc, ldxsc, dw, lddw, M, N, K, workspace,
                       workspace_bytes, stream);
+}
+
+rlq_status rlq_add_rmsnorm_quant_act_1x128(const uint16_t *res, int64_t ldr, const uint16_t *delta, int64_t ldd,
+                                           int64_t M, int64_t K, const uint16_t *gamma, float eps, uint16_t *h,
+                                           int64_t ldh, float *rstd, uint8_t *q, int64_t ldq, float *s, int64_t lds,
+                                           uint8_t *qT, int64_t ldqT, float *sc, int64_t ldsc, rlq_stream_t stream)
+{
+    RLQ_TRY(check_norm_shape(M, K));
+    RLQ_REQUIRE((qT == nullptr) == (sc == nullptr), RLQ_ERR_INVALID_ARG,
+                "qT and sc must be both NULL (row-wise only) or both set (fused 128x1)");
+    RLQ_REQUIRE(std::isfinite(eps) && eps >= 0.0f, RLQ_ERR_INVALID_ARG, "eps must be finite and >= 0");
+    if (M == 0 || K == 0)
+        return RLQ_OK;
+    RLQ_TRY(check_bf16("res", res, ldr, K));
+    if (delta)
+        RLQ_TRY(check_bf16("delta", delta, ldd, K));
+    RLQ_REQUIRE(h || !delta, RLQ_ERR_INVALID_ARG, "h is NULL: the sum of res and delta has to be written");
+    if (h)
+        RLQ_TRY(check_bf16("h", h, ldh, K));
+    RLQ_REQUIRE(h != res || ldh == ldr, RLQ_ERR_INVALID_ARG, "h is res in place, with another pitch");
+    RLQ_REQUIRE(!h || h != delta || ldh == ldd, RLQ_ERR_INVALID_ARG, "h is delta in place, with another pitch");
+    RLQ_REQUIRE(gamma, RLQ_ERR_INVALID_ARG, "gamma is NULL");
+    RLQ_REQUIRE(al(gamma, 16), RLQ_ERR_MISALIGNED, "gamma is not 16-byte aligned");
+    RLQ_TRY(check_scales("rstd", rstd, M, M));
+    RLQ_TRY(check_codes("q", q, ldq, K));
+    RLQ_TRY(check_scales("s", s, lds, M));
+    if (qT) {
+        RLQ_TRY(check_codes("qT", qT, ldqT, M));
+        RLQ_TRY(check_scales("sc", sc, ldsc, K));
+    }
+    return cuda_status(launch_add_rmsnorm_quant(res, ldr, delta, ldd, M, K, gamma, eps, h, ldh, rstd, q, ldq, s, lds, qT,
+                                                ldqT, sc, ldsc, cs(stream)),
+                       "residual + RMSNorm + quantizer launch");
+}
+
+rlq_status rlq_rmsnorm_backward_workspace_bytes(int64_t M, int64_t K, int64_t *bytes)
+{
+    RLQ_REQUIRE(bytes, RLQ_ERR_INVALID_ARG, "bytes is NULL");
+    RLQ_TRY(check_norm_shape(M, K));
+    *bytes = (M == 0 || K == 0) ? 0 : rmsnorm_backward_ws_bytes(M, K);
+    return RLQ_OK;
+}
+
+rlq_status rlq_rmsnorm_backward(const uint16_t *dx, int64_t lddx, const uint16_t *h, int64_t ldh, const float *rstd,
+                                const uint16_t *gamma, const uint16_t *dres, int64_t lddres, uint16_t *dh, int64_t lddh,
+                                float *dgamma, int64_t M, int64_t K, void *workspace, int64_t workspace_bytes,
+                                rlq_stream_t stream)
+{
+    RLQ_TRY(check_norm_shape(M, K));
+    if (K == 0)
+        return RLQ_OK;
+    RLQ_REQUIRE(dgamma, RLQ_ERR_INVALID_ARG, "dgamma is NULL");
+    RLQ_REQUIRE(al(dgamma, 16), RLQ_ERR_MISALIGNED, "dgamma is not 16-byte aligned");
+    if (M == 0)  // no rows: the sum is zero
+        return cuda_status(cudaMemsetAsync(dgamma, 0, (size_t)K * 4, cs(stream)), "cudaMemsetAsync (no rows)");
+    RLQ_TRY(check_workspace(workspace, workspace_bytes));
+    RLQ_TRY(check_bf16("dx", dx, lddx, K));
+    RLQ_TRY(check_bf16("h", h, ldh, K));
+    RLQ_TRY(check_scales("rstd", rstd, M, M));
+    RLQ_REQUIRE(gamma, RLQ_ERR_INVALID_ARG, "gamma is NULL");
+    RLQ_REQUIRE(al(gamma, 16), RLQ_ERR_MISALIGNED, "gamma is not 16-byte aligned");
+    if (dres)
+        RLQ_TRY(check_bf16("dres", dres, lddres, K));
+    RLQ_TRY(check_bf16("dh", dh, lddh, K));
+    RLQ_REQUIRE(dh != dres || lddh == lddres, RLQ_ERR_INVALID_ARG, "dh is dres in place, with another pitch");
+    const int64_t need = rmsnorm_backward_ws_bytes(M, K);
+    RLQ_REQUIRE(need == 0 || (workspace && workspace_bytes >= need), RLQ_ERR_INVALID_ARG,
+                "workspace of %lld bytes, %lld needed", (long long)(workspace ? workspace_bytes : 0), (long long)need);
+    return cuda_status(launch_rmsnorm_backward(dx, lddx, h, ldh, rstd, gamma, dres, lddres, dh, lddh, dgamma, M, K,
+                                               static_cast<float *>(workspace), cs(stream)),
+                       "RMSNorm backward launch");
+}
+
+rlq_status rlq_gemm_gated_fprop(const uint8_t *xq, int64_t ldxq, const float *xs, int64_t ldxs, const uint8_t *wq,
+                                int64_t ldwq, const float *ws, int64_t ldws, uint8_t *aq, int64_t ldaq, float *as,
+                                int64_t ldas, uint8_t *guq, int64_t ldguq, float *gus, int64_t ldgus, int64_t M,
+                                int64_t F, int64_t K, rlq_stream_t stream)
+{
+    RLQ_REQUIRE(M >= 0 && F >= 0 && K >= 0, RLQ_ERR_INVALID_ARG, "negative size");
+    RLQ_REQUIRE(F % G == 0 && K % G == 0, RLQ_ERR_UNSUPPORTED, "F=%lld and K=%lld must be multiples of 128",
+                (long long)F, (long long)K);
+    RLQ_REQUIRE(M < MAX_DIM && 2 * F < MAX_DIM && K < MAX_DIM, RLQ_ERR_UNSUPPORTED, "dimension beyond 2^31");
+    RLQ_REQUIRE((guq == nullptr) == (gus == nullptr), RLQ_ERR_INVALID_ARG,
+                "guq and gus must be both NULL (no checkpoint) or both set");
+    if (M == 0 || F == 0)
+        return RLQ_OK;
+    RLQ_REQUIRE(K > 0, RLQ_ERR_UNSUPPORTED, "K is 0: the block has no input");
+    RLQ_TRY(check_codes("xq", xq, ldxq, K));
+    RLQ_TRY(check_scales("xs", xs, ldxs, M));
+    RLQ_TRY(check_codes("wq", wq, ldwq, K));
+    RLQ_TRY(check_scales("ws", ws, ldws, K / G));
+    RLQ_TRY(check_codes("aq", aq, ldaq, F));
+    RLQ_TRY(check_scales("as", as, ldas, M));
+    if (guq) {
+        RLQ_TRY(check_codes("guq", guq, ldguq, 2 * F));
+        RLQ_TRY(check_scales("gus", gus, ldgus, M));
+    }
+    GemmArgs a{};
+    a.A = xq;
+    a.lda = ldxq;
+    a.B = wq;
+    a.ldb = ldwq;
+    a.sa = xs;
+    a.ld_sa = ldxs;
+    a.sb = ws;
+    a.sb_bstride = 1;
+    a.sb_cstride = ldws;
+    a.R = M;
+    a.C = F;
+    a.L = K;
+    a.aq = aq;
+    a.ldaq = ldaq;
+    a.as = as;
+    a.ld_as = ldas;
+    a.guq = guq;
+    a.ldguq = ldguq;
+    a.gus = gus;
+    a.ld_gus = ldgus;
+    return launch_gemm(a, cs(stream));
+}
+
+rlq_status rlq_gated_backward(const uint16_t *da, int64_t ldda, const uint8_t *guq, int64_t ldguq, const float *gus,
+                              int64_t ldgus, uint8_t *q, int64_t ldq, float *s, int64_t lds, uint8_t *qT, int64_t ldqT,
+                              float *sc, int64_t ldsc, uint8_t *aT, int64_t ldaT, float *ac, int64_t ldac, int64_t M,
+                              int64_t F, rlq_stream_t stream)
+{
+    RLQ_REQUIRE(M >= 0 && F >= 0, RLQ_ERR_INVALID_ARG, "negative size (M=%lld, F=%lld)", (long long)M, (long long)F);
+    RLQ_REQUIRE(F % G == 0, RLQ_ERR_UNSUPPORTED, "F=%lld is not a multiple of 128", (long long)F);
+    // (F / 128 is the launch grid's second extent)
+    RLQ_REQUIRE(M < MAX_DIM && F / G <= 65535, RLQ_ERR_UNSUPPORTED, "M beyond 2^31 or F beyond 8388480");
+    if (M == 0 || F == 0)
+        return RLQ_OK;
+    RLQ_TRY(check_bf16("da", da, ldda, F));
+    RLQ_TRY(check_codes("guq", guq, ldguq, 2 * F));
+    RLQ_TRY(check_scales("gus", gus, ldgus, M));
+    RLQ_TRY(check_codes("q", q, ldq, 2 * F));
+    RLQ_TRY(check_scales("s", s, lds, M));
+    RLQ_TRY(check_codes("qT", qT, ldqT, M));
+    RLQ_TRY(check_scales("sc", sc, ldsc, 2 * F));
+    RLQ_TRY(check_codes("aT", aT, ldaT, M));
+    RLQ_TRY(check_scales("ac", ac, ldac, F));
+    return cuda_status(launch_gated_backward(da, ldda, guq, ldguq, gus, ldgus, q, ldq, s, lds, qT, ldqT, sc, ldsc, aT,
+                                             ldaT, ac, ldac, M, F, cs(stream)),
+                       "gated backward launch");
+}
+
+rlq_status rlq_token_logprobs(const void *logits, rlq_dtype dtype, int64_t ld, int64_t rows, int64_t V,
+                              const int64_t *targets, float temperature, float *lp, float *lse, rlq_stream_t stream)
+{
+    PolicyLossArgs a{};
+    RLQ_TRY(check_logits(&a, logits, dtype, ld, rows, V, targets, temperature));
+    if (rows == 0)
+        return RLQ_OK;
+    RLQ_TRY(check_scales("lp", lp, rows, rows));
+    if (lse)
+        RLQ_TRY(check_scales("lse", lse, rows, rows));
+    a.lp = lp;
+    a.lse = lse;
+    return cuda_status(launch_policy_rows(a, cs(stream)), "token log probability launch");
+}
+
+rlq_status rlq_policy_loss(const void *logits, rlq_dtype dtype, int64_t ld, int64_t rows, int64_t V,
+                           const int64_t *targets, float temperature, const float *lp_old, const float *adv,
+                           const float *weight, const float *lp_behav, const float *lp_ref, const float *clip_hi,
+                           float eps_lo, float eps_hi, float tis_cap, float kl_beta, float *loss, float *lp,
+                           void *dlogits, int64_t ldd, rlq_stream_t stream)
+{
+    PolicyLossArgs a{};
+    RLQ_TRY(check_logits(&a, logits, dtype, ld, rows, V, targets, temperature));
+    RLQ_REQUIRE(eps_lo >= 0.0f && eps_lo <= 1.0f, RLQ_ERR_INVALID_ARG, "eps_lo must be in [0, 1]");
+    RLQ_REQUIRE(std::isfinite(eps_hi) && eps_hi >= 0.0f, RLQ_ERR_INVALID_ARG, "eps_hi must be finite and >= 0");
+    RLQ_REQUIRE(std::isfinite(tis_cap) && tis_cap > 0.0f, RLQ_ERR_INVALID_ARG, "tis_cap must be finite and > 0");
+    RLQ_REQUIRE(std::isfinite(kl_beta) && kl_beta >= 0.0f, RLQ_ERR_INVALID_ARG, "kl_beta must be finite and >= 0");
+    if (rows == 0)
+        return RLQ_OK;
+    const struct {
+        const char *name;
+        const float *p;
+        bool optional;
+    } vec[] = {{"lp_old", lp_old, false},     {"adv", adv, false},       {"weight", weight, false}, {"loss", loss, false},
+               {"lp", lp, false},             {"lp_behav", lp_behav, true}, {"lp_ref", lp_ref, true},
+               {"clip_hi", clip_hi, true}};
+    for (const auto &v : vec)
+        if (v.p || !v.optional)
+            RLQ_TRY(check_scales(v.name, v.p, rows, rows));
+    if (dlogits) {
+        RLQ_REQUIRE(ldd >= V, RLQ_ERR_INVALID_ARG, "dlogits: pitch %lld < row length %lld", (long long)ldd, (long long)V);
+        RLQ_REQUIRE(al(dlogits, dtype == RLQ_DTYPE_F32 ? 4 : 2), RLQ_ERR_MISALIGNED,
+                    "dlogits is not aligned to its element");
+        RLQ_REQUIRE(dlogits != logits || ldd == ld, RLQ_ERR_INVALID_ARG, "dlogits is logits in place, with another pitch");
+    }
+    a.lp_old = lp_old;
+    a.adv = adv;
+    a.weight = weight;
+    a.lp_behav = lp_behav;
+    a.lp_ref = lp_ref;
+    a.clip_hi = clip_hi;
+    a.eps_lo = eps_lo;
+    a.eps_hi = eps_hi;
+    a.tis_cap = tis_cap;
+    a.kl_beta = kl_beta;
+    a.loss = loss;
+    a.lp = lp;
+    a.dlogits = dlogits;
+    a.ldd = ldd;
+    return cuda_status(launch_policy_rows(a, cs(stream)), "policy loss launch");
 }
 
 rlq_status rlq_uaq_fold(uint16_t *w, int64_t N, int64_t K, int64_t ldw, const float *s, uint16_t *prev, int64_t R,

@@ -47,6 +47,7 @@
 #include <cstdlib>
 #include <mutex>
 
+#include "rlq_elem.cuh"
 #include "rlq_internal.h"
 #include "rlq_tc.cuh"
 
@@ -213,6 +214,16 @@ struct Params {
     // epilogue writes fp32 partials (OUT_F32_PARTIAL) to the workspace ws [splits][R][C]
     int splits, kbps, num_units;
     float *ws;
+    // MODE_GATED: FP8 codes and 1x128 scales of the product [R][C], and (guq set) of
+    // the gate and up projections [R][2 C]
+    uint8_t *aq;
+    int64_t ldaq;
+    float *as;
+    int64_t ld_as;
+    uint8_t *guq;
+    int64_t ldguq;
+    float *gus;
+    int64_t ld_gus;
     uint64_t timeout_ns;
     // diagnostic (single CTA only): the producer withholds the loads of the CTA's
     // first stage, so the MMA warp's bounded wait on it runs out
@@ -254,10 +265,80 @@ __device__ __forceinline__ Unit unit_of(const Params &p, int u)
 //   MODE_ONCE:   sa and sb are constant along the contraction (per-token x
 //                per-channel FProp): the MMAs accumulate the whole contraction
 //                range in TMEM and the epilogue scales once, out = P * (sa * sb[c]).
-enum : int { MODE_BLOCK = 0, MODE_COLS = 1, MODE_ONCE = 2 };
+//   MODE_GATED:  the gated feed-forward block.  B is [2F][L], gate rows first; a tile is
+//                128 output columns: MMA columns 0-127 are the gate projection's, 128-255
+//                the up projection's of the same columns.  An epilogue thread promotes 64
+//                of each, as MODE_BLOCK does, forms a = silu(g) * u and leaves a's (and
+//                optionally g's and u's) FP8 codes: a tile's columns are one 1x128 group,
+//                whose maximum its two threads exchange through shared memory.
+enum : int { MODE_BLOCK = 0, MODE_COLS = 1, MODE_ONCE = 2, MODE_GATED = 3 };
 
 // Epilogue outputs.
 enum : int { OUT_BF16 = 0, OUT_F32_PARTIAL = 1, OUT_F32_ACC = 2 };
+
+// silu(g) * u for two columns: g * u / (1 + 2^(-g log2 e)), the exponential and the
+// reciprocal on the special-function units (about 2 and 1 ulp).
+__device__ __forceinline__ float2 silu_mul2(float2 g, float2 u)
+{
+    float2 d, r;
+    const float2 e = __fmul2_rn(g, make_float2(-1.4426950408889634f, -1.4426950408889634f));
+    asm("ex2.approx.f32 %0, %1;" : "=f"(d.x) : "f"(e.x));
+    asm("ex2.approx.f32 %0, %1;" : "=f"(d.y) : "f"(e.y));
+    d = __fadd2_rn(d, make_float2(1.0f, 1.0f));
+    asm("rcp.approx.f32 %0, %1;" : "=f"(r.x) : "f"(d.x));
+    asm("rcp.approx.f32 %0, %1;" : "=f"(r.y) : "f"(d.y));
+    // (g * r first: r is 0 where g is far below zero, and u may be large)
+    return __fmul2_rn(__fmul2_rn(g, r), u);
+}
+
+// max |.| over 32 pairs.
+__device__ __forceinline__ float amax32(const float2 *v)
+{
+    float a = 0.0f, b = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+        a = fmaxf(a, fabsf(v[j].x));
+        b = fmaxf(b, fabsf(v[j].y));
+    }
+    return fmaxf(a, b);
+}
+
+// 64 FP8 codes of 32 pairs with scale s, written to 64 consecutive bytes.
+__device__ __forceinline__ void store_codes64(uint8_t *__restrict__ dst, const float2 *v, float s)
+{
+    const float r = scale_rcp(s);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float2 a = v[8 * j + 2 * i], b = v[8 * j + 2 * i + 1];
+            if (r != 0.0f) {
+                const float2 r2 = make_float2(r, r);
+                a = __fmul2_rn(a, r2);
+                b = __fmul2_rn(b, r2);
+            } else {
+                a = make_float2(__fdiv_rn(a.x, s), __fdiv_rn(a.y, s));
+                b = make_float2(__fdiv_rn(b.x, s), __fdiv_rn(b.y, s));
+            }
+            w[i] = e4m3x2(a.x, a.y) | (e4m3x2(b.x, b.y) << 16);
+        }
+        *reinterpret_cast<uint4 *>(dst + 16 * j) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
+
+// Exchange buffer of MODE_GATED: per unit parity, column half and row, the thread's
+// maxima of g, u and a and whether its warp is still running.
+constexpr int XCH_BYTES = 2 * 2 * BM * 16;
+
+template <int kMode, bool kPair>
+constexpr int smem_bytes()
+{
+    // a pair's output staging buffer holds the exchange (the codes are stored directly)
+    return Cfg<kPair>::SMEM_BYTES + (kMode == MODE_GATED && !kPair ? XCH_BYTES + 16 : 0);
+}
+static_assert(smem_bytes<MODE_GATED, false>() <= 232448, "shared memory budget");
+static_assert(Cfg<true>::STAGING >= XCH_BYTES, "the exchange fits the staging buffer");
 
 template <int kMode, bool kBMajorMN, bool kPair>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
@@ -270,6 +351,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     constexpr int STAGE_BYTES = Cf::STAGE_BYTES;
     constexpr int NUM_BARS = Cf::NUM_BARS;
     constexpr bool kOnce = kMode == MODE_ONCE;
+    constexpr bool kGated = kMode == MODE_GATED;
+    constexpr bool kOneScale = kMode == MODE_BLOCK || kGated;  // one B scale per 128 MMA columns and block
+    static_assert(!kGated || !kBMajorMN, "the gated block reads K-major weights");
     // A CTA pair (cluster of 2) shares one 256-row tile: CTA `rank` owns rows
     // rank * 128 .. rank * 128 + 127 of it; the even CTA issues the pair's MMAs.
     // (The rank is re-read where it is used rather than kept in a register.)
@@ -282,6 +366,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + STAGES * STAGE_BYTES + Cf::STAGING + RING_BYTES);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + NUM_BARS);
     volatile uint32_t *abort_flag = tmem_slot + 1;
+    // (single CTA: behind the abort flag, on the next 16-byte boundary)
+    const uint32_t xch = kPair ? smem_u32(staging) : ((smem_u32(tmem_slot) + 8 + 15) & ~15u);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t smem0 = smem_u32(smem);
@@ -333,7 +419,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     if (warp == 0 && lane == 0) {
         prefetch_tmap(&tmA);
         prefetch_tmap(&tmB);
-        if (kPair && p.out_mode != OUT_F32_PARTIAL)
+        if (kPair && !kGated && p.out_mode != OUT_F32_PARTIAL)
             prefetch_tmap(&tmOut);
     }
     tc_fence_before();
@@ -372,6 +458,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                                               pol_a);
                         if (kBMajorMN)  // this CTA's 128 output columns: one 128 x 128 box
                             tma_load_2d_pair_hint(b_stage(s), &tmB, fb, nt * BN + row_offset<kPair>(), kb * BK, pol_b);
+                        else if (kGated)  // the even CTA stages the gate's rows, the odd one the up projection's
+                            tma_load_2d_pair_hint(b_stage(s), &tmB, fb, kb * BK, nt * 128 + (int)cta_rank() * p.C, pol_b);
                         else
                             tma_load_2d_pair_hint(b_stage(s), &tmB, fb, kb * BK, nt * BN + row_offset<kPair>(), pol_b);
                     } else {
@@ -383,6 +471,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                             // B stored [contraction][output]: two 128-column boxes of 128 rows
                             tma_load_2d(b_stage(s), &tmB, full_bar(s), nt * BN, kb * BK);
                             tma_load_2d(b_stage(s) + Cf::B_BYTES / 2, &tmB, full_bar(s), nt * BN + 128, kb * BK);
+                        } else if (kGated) {
+                            tma_load_2d(b_stage(s), &tmB, full_bar(s), kb * BK, nt * 128);
+                            tma_load_2d(b_stage(s) + Cf::B_BYTES / 2, &tmB, full_bar(s), kb * BK, p.C + nt * 128);
                         } else {
                             tma_load_2d(b_stage(s), &tmB, full_bar(s), kb * BK, nt * BN);
                         }
@@ -503,7 +594,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                     const int r = mt * Cf::TILE_M + row_offset<kPair>() + lane + 32 * j;
                     cp_async4(slot + 4u * (lane + 32 * j), r < p.R ? sa_row + r : sa_row, r < p.R ? 4u : 0u);
                 }
-                if (kMode != MODE_BLOCK) {
+                if (!kOneScale) {
                     const float *sb_row = p.sb + (int64_t)kb * p.sb_bstride;
                     // 256 column scales as 64 aligned 16-byte pieces (rows of sb are 16-byte
                     // aligned, C % 128 == 0: a piece is wholly inside or outside the tensor)
@@ -514,9 +605,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                                    c < p.C ? 16u : 0u);
                     }
                 } else if (lane < BN / 128) {
-                    const int c = nt * BN + lane * 128;
+                    // (gated: lane 1's scale is the up projection's, always inside)
+                    const int c = kGated ? nt * 128 + lane * p.C : nt * BN + lane * 128;
                     const float *src = p.sb + (int64_t)kb * p.sb_bstride + (int64_t)(c >> 7) * p.sb_cstride;
-                    cp_async4(slot + 4u * (BM + lane), c < p.C ? src : p.sb, c < p.C ? 4u : 0u);
+                    const bool in = kGated || c < p.C;
+                    cp_async4(slot + 4u * (BM + lane), in ? src : p.sb, in ? 4u : 0u);
                 }
                 cp_async_arrive(sfull_bar(k));
             }
@@ -534,7 +627,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         for (int u = unit0; ok && u < p.num_units; u += unit_step, ++uc) {
             const Unit wu = unit_of(p, u);
             const int mt = wu.mt, nt = wu.nt;
-            const int col0 = nt * BN + h * 128;
+            const int col0 = kGated ? nt * 128 + h * 64 : nt * BN + h * 128;
             const bool half_ok = col0 < p.C;
             float2 acc[64];
 #pragma unroll
@@ -551,7 +644,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                 // independent shared-memory operations in flight; measured 2% on
                 // WGrad); the block-scaled epilogue has no registers to spare for it.
                 bool w;
-                if (kMode != MODE_BLOCK && mbar_try_wait(sfull_bar(k), sph) & mbar_try_wait(tfull_bar(buf), bph))
+                if (!kOneScale && mbar_try_wait(sfull_bar(k), sph) & mbar_try_wait(tfull_bar(buf), bph))
                     w = true;
                 else
                     w = mbar_wait(sfull_bar(k), sph, abort_flag, p.timeout_ns, SITE_EPI_SCALE_FULL) &&
@@ -565,7 +658,25 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                 const float sa = lds_f32(slot + 4u * row);
                 const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * BN + h * 128);
                 uint32_t ra[32], rb[32];
-                if (kMode == MODE_BLOCK) {
+                if (kGated) {
+                    // acc[0..31]: 64 gate columns, acc[32..63]: the same columns of up
+                    const uint32_t tg = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * BN + h * 64);
+                    const float sg = sa * lds_f32(slot + 4u * BM), su = sa * lds_f32(slot + 4u * (BM + 1));
+                    const float2 sg2 = make_float2(sg, sg), su2 = make_float2(su, su);
+                    tmem_ld32_async(tg, ra);
+                    tmem_wait32(ra);
+                    tmem_ld32_async(tg + 32, rb);
+                    promote_chunk(&acc[0], ra, sg2);
+                    tmem_wait32(rb);
+                    tmem_ld32_async(tg + 128, ra);
+                    promote_chunk(&acc[16], rb, sg2);
+                    tmem_wait32(ra);
+                    tmem_ld32_async(tg + 160, rb);
+                    promote_chunk(&acc[32], ra, su2);
+                    tmem_wait32(rb);
+                    promote_chunk(&acc[48], rb, su2);
+                    release_tmem<kPair>(tempty_bar(buf), lane);
+                } else if (kMode == MODE_BLOCK) {
                     const float scl = sa * lds_f32(slot + 4u * (BM + h));
                     const float2 scl2 = make_float2(scl, scl);
                     tmem_ld32_async(taddr, ra);
@@ -606,6 +717,43 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                 __syncwarp();
                 if (lane == 0)
                     mbar_arrive(sempty_bar(k));  // the scales are read
+            }
+            if constexpr (kGated) {
+                // The two threads of a row (column halves h) exchange their maxima, and
+                // whether their warps still run, so that both leave after the same unit
+                // (the barrier below counts on it).  Alternating buffers: a half's
+                // values are overwritten only after the partner has passed the next barrier.
+                float2 av[32];
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                    av[j] = silu_mul2(acc[j], acc[32 + j]);
+                float mg = p.guq ? amax32(&acc[0]) : 0.0f, mu = p.guq ? amax32(&acc[32]) : 0.0f, ma = amax32(av);
+                const uint32_t mine = xch + (uint32_t)((((uc & 1) * 2 + h) * BM + row) * 16);
+                const uint32_t other = xch + (uint32_t)((((uc & 1) * 2 + (h ^ 1)) * BM + row) * 16);
+                asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(mine), "f"(mg), "f"(mu), "f"(ma),
+                             "f"(ok ? 1.0f : 0.0f)
+                             : "memory");
+                asm volatile("bar.sync %0, 64;" ::"r"(1 + q) : "memory");
+                const float4 o = lds_v4(other);
+                ok = ok && o.w != 0.0f;
+                const int grow = mt * Cf::TILE_M + row_offset<kPair>() + row;
+                if (ok && grow < p.R) {
+                    const float sca = group_scale(fmaxf(ma, o.z));
+                    store_codes64(p.aq + (int64_t)grow * p.ldaq + col0, av, sca);
+                    if (h == 0)
+                        p.as[(int64_t)nt * p.ld_as + grow] = sca;
+                    if (p.guq) {
+                        const float scg = group_scale(fmaxf(mg, o.x)), scu = group_scale(fmaxf(mu, o.y));
+                        uint8_t *dst = p.guq + (int64_t)grow * p.ldguq + col0;
+                        store_codes64(dst, &acc[0], scg);
+                        store_codes64(dst + p.C, &acc[32], scu);
+                        if (h == 0) {
+                            p.gus[(int64_t)nt * p.ld_gus + grow] = scg;
+                            p.gus[(int64_t)(p.n_tiles + nt) * p.ld_gus + grow] = scu;
+                        }
+                    }
+                }
+                continue;
             }
             if (kPair && p.out_mode == OUT_F32_ACC) {
                 // this warp's 32 rows x 128 fp32 columns added into the caller's gradient
@@ -971,7 +1119,9 @@ rlq_status launch_impl(const GemmArgs &a, int splits, cudaStream_t st, bool with
         return rs;
     // B is [C][L] (K-major; boxes of the B rows one CTA stages) or [L][C] (MN-major,
     // boxes of 128 columns x 128 rows)
-    rs = kBMN ? encode_map(&tmB, a.B, a.C, a.L, a.ldb, BK) : encode_map(&tmB, a.B, a.L, a.C, a.ldb, Cf::B_ROWS);
+    constexpr bool kGated = kMode == MODE_GATED;  // boxes of 128 gate or up rows
+    rs = kBMN ? encode_map(&tmB, a.B, a.C, a.L, a.ldb, BK)
+              : encode_map(&tmB, a.B, a.L, kGated ? 2 * a.C : a.C, a.ldb, kGated ? 128 : Cf::B_ROWS);
     if (rs != RLQ_OK)
         return rs;
     int dev = 0;
@@ -982,7 +1132,7 @@ rlq_status launch_impl(const GemmArgs &a, int splits, cudaStream_t st, bool with
     const int variant = kMode * 4 + (kBMN ? 2 : 0) + (kPair ? 1 : 0);
     auto kernel = k_gemm_block_scaled<kMode, kBMN, kPair>;
     if (!di.attr_set[variant]) {
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cf::SMEM_BYTES);
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<kMode, kPair>());
         if (e != cudaSuccess)
             return cuda_status(e, "cudaFuncSetAttribute(max dynamic shared memory)");
         di.attr_set[variant] = true;
@@ -998,7 +1148,7 @@ rlq_status launch_impl(const GemmArgs &a, int splits, cudaStream_t st, bool with
     attrs[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(NUM_THREADS, 1, 1);
-    cfg.dynamicSmemBytes = Cf::SMEM_BYTES;
+    cfg.dynamicSmemBytes = smem_bytes<kMode, kPair>();
     cfg.stream = st;
     cfg.attrs = attrs;
     cfg.numAttrs = kPair ? 2 : 1;
@@ -1031,10 +1181,18 @@ rlq_status launch_impl(const GemmArgs &a, int splits, cudaStream_t st, bool with
     p.C = (int)a.C;
     p.kblocks = (int)((a.L + BK - 1) / BK);
     p.m_tiles = (int)((a.R + Cf::TILE_M - 1) / Cf::TILE_M);
-    p.n_tiles = (int)((a.C + BN - 1) / BN);
+    p.n_tiles = (int)(kGated ? a.C / 128 : (a.C + BN - 1) / BN);
     p.num_tiles = p.m_tiles * p.n_tiles;
     // keep the smaller operand resident in L2: sweep the tiles along it
-    p.m_fastest = (a.R * a.L <= a.C * a.L) ? 1 : 0;
+    p.m_fastest = (a.R * a.L <= (kGated ? 2 : 1) * a.C * a.L) ? 1 : 0;
+    p.aq = a.aq;
+    p.ldaq = a.ldaq;
+    p.as = a.as;
+    p.ld_as = a.ld_as;
+    p.guq = a.guq;
+    p.ldguq = a.ldguq;
+    p.gus = a.gus;
+    p.ld_gus = a.ld_gus;
     p.timeout_ns = wait_limit_ns();
     p.withhold_first_load = (!kPair && withhold_first_load) ? 1 : 0;
     p.kbps = (p.kblocks + splits - 1) / splits;
@@ -1046,7 +1204,7 @@ rlq_status launch_impl(const GemmArgs &a, int splits, cudaStream_t st, bool with
         rs = encode_acc_map(&tmO, a.acc, a.C, a.R, a.ld_acc);
         if (rs != RLQ_OK)
             return rs;
-    } else if (kPair && p.out_mode == OUT_BF16) {
+    } else if (kPair && !kGated && p.out_mode == OUT_BF16) {
         rs = encode_out_map(&tmO, a.out, a.C, a.R, a.ldo);
         if (rs != RLQ_OK)
             return rs;
@@ -1120,6 +1278,8 @@ rlq_status launch_gemm(const GemmArgs &a, cudaStream_t st)
     // CTA pairs for tiles of 256 output rows; one CTA per 128 rows when the output
     // has fewer rows or the contraction is split
     const bool pair = splits == 1 && a.R >= 2 * BM && pair_mode_enabled() && !stall;
+    if (a.aq)
+        return launch_mode<MODE_GATED, false>(a, 1, st, pair, stall);
     if (a.scale_once)
         return launch_mode<MODE_ONCE, false>(a, splits, st, pair, stall);
     if (a.per_col_sb)

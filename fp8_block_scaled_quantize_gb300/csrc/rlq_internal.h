@@ -4,6 +4,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../../include/rlq.h"
 
 namespace rlq {
@@ -41,6 +43,23 @@ inline cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, s
     return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
 }
 
+// SMs of the current device, looked up once per device (1 if it cannot be told).
+inline int device_sms()
+{
+    static std::atomic<int> known[64];
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess)
+        return 1;
+    std::atomic<int> &k = known[dev & 63];
+    n = k.load(std::memory_order_relaxed);
+    if (n == 0) {
+        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1)
+            n = 1;
+        k.store(n, std::memory_order_relaxed);
+    }
+    return n;
+}
+
 // Records a failure description for rlq_last_error() and returns `st`.
 rlq_status fail(rlq_status st, const char *fmt, ...);
 
@@ -73,6 +92,42 @@ cudaError_t launch_quant_nvfp4(const uint16_t *w, int64_t N, int64_t K, int64_t 
 cudaError_t launch_aqn_perturb(uint16_t *gamma, int64_t K, const float *z, float sigma, cudaStream_t st);
 cudaError_t launch_uaq_fold(uint16_t *w, int64_t N, int64_t K, int64_t ldw, const float *s,
                             uint16_t *prev, int64_t R, int64_t ldp, cudaStream_t st);
+
+// ---- residual + RMSNorm + quantizer and its backward (rlq_norm.cu) ----
+// delta, h and (qT, sc) may be NULL; without h the norm is of res as it is.  K <= 16384.
+cudaError_t launch_add_rmsnorm_quant(const uint16_t *res, int64_t ldr, const uint16_t *delta, int64_t ldd, int64_t M,
+                                     int64_t K, const uint16_t *gamma, float eps, uint16_t *h, int64_t ldh, float *rstd,
+                                     uint8_t *q, int64_t ldq, float *s, int64_t lds, uint8_t *qT, int64_t ldqT,
+                                     float *sc, int64_t ldsc, cudaStream_t st);
+// Workspace of the backward pass (0: none): the partial sums of dgamma.
+int64_t rmsnorm_backward_ws_bytes(int64_t M, int64_t K);
+cudaError_t launch_rmsnorm_backward(const uint16_t *dx, int64_t lddx, const uint16_t *h, int64_t ldh, const float *rstd,
+                                    const uint16_t *gamma, const uint16_t *dres, int64_t lddres, uint16_t *dh,
+                                    int64_t lddh, float *dgamma, int64_t M, int64_t K, float *ws, cudaStream_t st);
+
+// ---- backward of the gated block's activation (rlq_gate_bwd.cu) ----
+cudaError_t launch_gated_backward(const uint16_t *da, int64_t ldda, const uint8_t *guq, int64_t ldguq, const float *gus,
+                                  int64_t ld_gus, uint8_t *q, int64_t ldq, float *s, int64_t lds, uint8_t *qT,
+                                  int64_t ldqT, float *sc, int64_t ldsc, uint8_t *aT, int64_t ldaT, float *ac,
+                                  int64_t ldac, int64_t M, int64_t F, cudaStream_t st);
+
+// ---- token log probabilities and policy loss (rlq_loss.cu) ----
+struct PolicyLossArgs {
+    const void *logits;  // [rows][V], pitch ld elements
+    int dtype;           // RLQ_DTYPE_BF16 or RLQ_DTYPE_F32, of logits and dlogits
+    int64_t ld, rows, V;
+    const int64_t *targets;
+    float temperature;
+    // the loss (adv set), each [rows]; lp_behav, lp_ref and clip_hi may be NULL
+    const float *lp_old, *adv, *weight, *lp_behav, *lp_ref, *clip_hi;
+    float eps_lo, eps_hi, tis_cap, kl_beta;
+    float *lp, *lse, *loss;  // [rows]; lse and loss may be NULL
+    void *dlogits;           // NULL: no gradient
+    int64_t ldd;
+};
+// Longest row the kernel holds.
+int64_t policy_max_vocab(int dtype);
+cudaError_t launch_policy_rows(const PolicyLossArgs &p, cudaStream_t st);
 
 // ---- block-scaled GEMM (rlq_gemm.cu) ----
 //
@@ -109,6 +164,17 @@ struct GemmArgs {
     // from the GEMM's epilogue, or from the split-K partials where the plan splits
     float *acc;
     int64_t ld_acc;
+    // gated block (aq set): B is [2 C][L], gate rows first; a = silu(A Bg^T) * (A Bu^T)
+    // leaves as codes aq [R][C] with scales as[c / 128][r], and with guq set the two
+    // projections as codes [R][2 C] with scales gus[c / 128][r].  L > 0, no workspace.
+    uint8_t *aq;
+    int64_t ldaq;
+    float *as;
+    int64_t ld_as;
+    uint8_t *guq;
+    int64_t ldguq;
+    float *gus;
+    int64_t ld_gus;
 };
 rlq_status launch_gemm(const GemmArgs &a, cudaStream_t st);
 

@@ -1,0 +1,404 @@
+// Residual addition + RMSNorm + FP8 quantizer, and the norm's backward pass (sm_103a).
+//
+// Forward, per row m of the residual stream:
+//   h = bf16_RN(res + delta)                     written back, the stream is held in bf16
+//   rstd = 1 / sqrt(mean(h^2) + eps)             fp32, the sum taken over h as stored
+//   x = (h * rstd) * gamma                       fp32, not rounded before it is quantized
+//   1x128 codes and scales of x (and 128x1, transposed, for WGrad)
+// Backward, with xh = h * rstd and dn = dx * gamma:
+//   dh = dres + rstd * (dn - xh * mean(dn * xh)),   dgamma = sum_m dx * xh
+//
+// Both are bound by memory: 7.03 bytes per element forward (2 + 2 read, 2 + 1 and a
+// scale per 128 written), 8 backward.
+#include <cuda_runtime.h>
+
+#include "rlq_elem.cuh"
+#include "rlq_internal.h"
+
+namespace rlq {
+namespace {
+
+constexpr int GRP = 128;
+
+// A load that may alias an output of the same kernel (read by the thread that
+// later overwrites it), so not through the read-only path.
+__device__ __forceinline__ uint4 ld_once(const uint16_t *p)
+{
+    uint4 v;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p)
+                 : "memory");
+    return v;
+}
+
+__device__ __forceinline__ uint32_t add_bf16x2(uint32_t a, uint32_t b)
+{
+    return pack_bf16x2(make_float2(bf_lo(a) + bf_lo(b), bf_hi(a) + bf_hi(b)));
+}
+
+// Sum over the threads of one team: warps `w0 ..` of `nw` warps, partials in `sh`
+// (nw floats), named barrier `bar` of 32 * nw threads.  Every thread gets the sum,
+// added in the same order in each.  `sh` may be reused after the next barrier.
+__device__ __forceinline__ float team_sum(float v, float *sh, int wi, int nw, int bar)
+{
+#pragma unroll
+    for (int o = 16; o; o >>= 1)
+        v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    if (nw == 1)
+        return v;
+    const int lane = threadIdx.x & 31;
+    if (lane == 0)
+        sh[wi] = v;
+    asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(32 * nw) : "memory");
+    v = lane < nw ? sh[lane] : 0.0f;
+#pragma unroll
+    for (int o = 16; o; o >>= 1)
+        v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    return v;
+}
+
+// One CTA per row; thread t holds the 16-byte vectors t + i * blockDim.x, i < NV,
+// all loads in flight before the sum.  A 1x128 group is 16 consecutive lanes of one
+// vector index.
+template <int NV, bool kAdd>
+__global__ void __launch_bounds__(1024) k_add_rmsnorm_rows(const uint16_t *res, int64_t ldr, const uint16_t *delta, int64_t ldd,
+                                   const uint16_t *__restrict__ gamma, float eps, int K, uint16_t *h, int64_t ldh,
+                                   float *__restrict__ rstd, uint8_t *__restrict__ q, int64_t ldq,
+                                   float *__restrict__ s, int64_t lds)
+{
+    pdl_begin();
+    __shared__ float sh[32];
+    const int64_t m = blockIdx.x;
+    const int t = threadIdx.x, T = blockDim.x, nvec = K / 8;
+    uint4 v[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = t + i * T;
+        v[i] = c < nvec ? ld_once(res + m * ldr + 8 * c) : make_uint4(0, 0, 0, 0);
+    }
+    if (kAdd) {
+        uint4 d[NV];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = t + i * T;
+            d[i] = c < nvec ? ld_once(delta + m * ldd + 8 * c) : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            v[i] = make_uint4(add_bf16x2(v[i].x, d[i].x), add_bf16x2(v[i].y, d[i].y), add_bf16x2(v[i].z, d[i].z),
+                              add_bf16x2(v[i].w, d[i].w));
+    }
+    float ss = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = t + i * T;
+        if (h && c < nvec)
+            *reinterpret_cast<uint4 *>(h + m * ldh + 8 * c) = v[i];
+        float f[8];
+        unpack8(v[i], f);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            ss = fmaf(f[j], f[j], ss);
+    }
+    ss = team_sum(ss, sh, t >> 5, T >> 5, 0);
+    const float r = __frcp_rn(__fsqrt_rn(ss / (float)K + eps));
+    if (t == 0)
+        rstd[m] = r;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = t + i * T;
+        const bool in = c < nvec;
+        float f[8], g[8];
+        unpack8(v[i], f);
+        unpack8(in ? *reinterpret_cast<const uint4 *>(gamma + 8 * c) : make_uint4(0, 0, 0, 0), g);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            f[j] = (f[j] * r) * g[j];
+        const float sc = group_scale(half_warp_max(max_abs8(f)));
+        if (in) {
+            if ((t & 15) == 0)
+                s[(int64_t)(c >> 4) * lds + m] = sc;
+            *reinterpret_cast<uint2 *>(q + m * ldq + 8 * c) = encode8f(f, sc, scale_rcp(sc));
+        }
+    }
+}
+
+// The 128x1 groups of the same x, read back from h and rstd: a CTA takes a 128 x 128
+// tile, thread t rows 8 (t / 16) .. + 7 and columns 8 (t % 16) .. + 7.  The codes
+// are turned in shared memory ([column][16 chunks of 8 rows], chunks XOR-swizzled by
+// column / 8: conflict-free both ways) and leave as whole 128-byte lines of qT.
+__global__ void __launch_bounds__(256) k_norm_cols(const uint16_t *__restrict__ h, int64_t ldh,
+                                                   const float *__restrict__ rstd,
+                                                   const uint16_t *__restrict__ gamma, int64_t M, int64_t K,
+                                                   uint8_t *__restrict__ qT, int64_t ldqT, float *__restrict__ sc,
+                                                   int64_t ldsc)
+{
+    pdl_begin();
+    __shared__ __align__(16) uint8_t tile[128 * 128];
+    __shared__ float part[8][128];
+    const int t = threadIdx.x, cg = t & 15, rg = t >> 4, warp = t >> 5;
+    const int64_t m0 = (int64_t)blockIdx.x * GRP, k0 = (int64_t)blockIdx.y * GRP;
+    const int rows = (int)(M - m0 < GRP ? M - m0 : GRP);
+    uint4 v[8];
+    float r[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int m = 8 * rg + i;
+        v[i] = m < rows ? ld_stream(h + (m0 + m) * ldh + k0 + 8 * cg) : make_uint4(0, 0, 0, 0);
+        r[i] = m < rows ? rstd[m0 + m] : 0.0f;
+    }
+    float g[8], x[8][8], cmax[8];
+    unpack8(*reinterpret_cast<const uint4 *>(gamma + k0 + 8 * cg), g);
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        cmax[j] = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        unpack8(v[i], x[i]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            x[i][j] = (x[i][j] * r[i]) * g[j];
+            cmax[j] = fmaxf(cmax[j], fabsf(x[i][j]));
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const float c = fmaxf(cmax[j], __shfl_xor_sync(0xFFFFFFFFu, cmax[j], 16));
+        if ((t & 16) == 0)
+            part[warp][8 * cg + j] = c;
+    }
+    __syncthreads();
+    if (t < 128) {
+        float a = part[0][t];
+#pragma unroll
+        for (int w = 1; w < 8; ++w)
+            a = fmaxf(a, part[w][t]);
+        a = group_scale(a);
+        part[0][t] = a;
+        part[1][t] = scale_rcp(a);
+        sc[(int64_t)blockIdx.x * ldsc + k0 + t] = a;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const int c = 8 * cg + j;
+        float col[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            col[i] = x[i][j];
+        *reinterpret_cast<uint2 *>(tile + c * 128 + 8 * (rg ^ cg)) = encode8f(col, part[0][c], part[1][c]);
+    }
+    __syncthreads();
+    store_tile_T(tile, t, 256, rows, qT + k0 * ldqT + m0, ldqT);
+}
+
+// Backward.  A CTA holds `teams` teams of T threads; a team takes rows
+// blockIdx.x * teams + team, + gridDim.x * teams, ..., each thread the same columns of
+// every row, so the norm weight's gradient adds up in registers.  The next row's loads
+// are in flight while this row is reduced and written (NV == 2; four vectors a thread
+// leave no registers for it).  The teams' sums are added in
+// team order in shared memory and leave as one partial row per CTA (or as dgamma
+// itself from a single CTA); k_dgamma_sum adds the partial rows in order.
+template <int NV>
+__global__ void __launch_bounds__(512)
+    k_rmsnorm_bwd(const uint16_t *__restrict__ dx, int64_t lddx, const uint16_t *__restrict__ h, int64_t ldh,
+                  const float *__restrict__ rstd, const uint16_t *__restrict__ gamma, const uint16_t *dres,
+                  int64_t lddres, uint16_t *dh, int64_t lddh, float *__restrict__ dgamma_part, int M, int K, int T,
+                  int teams)
+{
+    pdl_begin();
+    extern __shared__ float dyn[];  // K sums
+    __shared__ float sh[2][32];
+    const int team = threadIdx.x / T, t = threadIdx.x - team * T;
+    const int nvec = K / 8, nw = T >> 5, wi = t >> 5;
+    const int step = gridDim.x * teams;
+    float acc[NV][8];
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            acc[i][j] = 0.0f;
+    uint4 a[NV], b[NV], d[NV];
+    float r = 0.0f;
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    auto load = [&](int m) {
+        const bool row = m < M;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = t + i * T;
+            const bool in = row && c < nvec;
+            a[i] = in ? ld_stream(dx + (int64_t)m * lddx + 8 * c) : zero;
+            b[i] = in ? ld_stream(h + (int64_t)m * ldh + 8 * c) : zero;
+            d[i] = in && dres ? ld_once(dres + (int64_t)m * lddres + 8 * c) : zero;
+        }
+        r = row ? rstd[m] : 0.0f;
+    };
+    int m = blockIdx.x * teams + team;
+    if (NV == 2)
+        load(m);
+    for (int par = 0; m < M; m += step, par ^= 1) {
+        if (NV != 2)
+            load(m);
+        uint4 ca[NV], cb[NV], cd[NV];
+        const float cr = r;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            ca[i] = a[i];
+            cb[i] = b[i];
+            cd[i] = d[i];
+        }
+        if (NV == 2)
+            load(m + step < M ? m + step : M);
+        float dot = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = t + i * T;
+            float x[8], y[8], g[8];
+            unpack8(ca[i], x);
+            unpack8(cb[i], y);
+            unpack8(c < nvec ? __ldg(reinterpret_cast<const uint4 *>(gamma + 8 * c)) : zero, g);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float xh = y[j] * cr;
+                acc[i][j] = fmaf(x[j], xh, acc[i][j]);
+                dot = fmaf(x[j] * g[j], xh, dot);
+            }
+        }
+        // (the parity keeps a fast warp's next partials apart from the ones being read)
+        dot = team_sum(dot, sh[par] + team * nw, wi, nw, 1 + team) / (float)K;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = t + i * T;
+            if (c >= nvec)
+                continue;
+            float x[8], y[8], g[8], e[8];
+            unpack8(ca[i], x);
+            unpack8(cb[i], y);
+            unpack8(__ldg(reinterpret_cast<const uint4 *>(gamma + 8 * c)), g);
+            unpack8(cd[i], e);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                e[j] = fmaf(cr, x[j] * g[j] - (y[j] * cr) * dot, e[j]);
+            *reinterpret_cast<uint4 *>(dh + (int64_t)m * lddh + 8 * c) =
+                make_uint4(pack_bf16x2(make_float2(e[0], e[1])), pack_bf16x2(make_float2(e[2], e[3])),
+                           pack_bf16x2(make_float2(e[4], e[5])), pack_bf16x2(make_float2(e[6], e[7])));
+        }
+    }
+    for (int k = 0; k < teams; ++k) {
+        if (team == k) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int c = t + i * T;
+                if (c >= nvec)
+                    continue;
+                float4 *p = reinterpret_cast<float4 *>(dyn + 8 * c);
+                float4 lo = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+                float4 hi = make_float4(acc[i][4], acc[i][5], acc[i][6], acc[i][7]);
+                if (k > 0) {
+                    const float4 x = p[0], y = p[1];
+                    lo = make_float4(lo.x + x.x, lo.y + x.y, lo.z + x.z, lo.w + x.w);
+                    hi = make_float4(hi.x + y.x, hi.y + y.y, hi.z + y.z, hi.w + y.w);
+                }
+                p[0] = lo;
+                p[1] = hi;
+            }
+        }
+        __syncthreads();
+    }
+    float *out = dgamma_part + (int64_t)blockIdx.x * K;
+    for (int c = threadIdx.x; c < K; c += blockDim.x)
+        out[c] = dyn[c];
+}
+
+// dgamma[c] = sum over p < parts, in a fixed order, of part[p][c]: a CTA takes 32
+// columns, warp w the partial rows w, w + 8, ...; the eight warp sums are added in order.
+__global__ void __launch_bounds__(256) k_dgamma_sum(const float *__restrict__ part, int parts, int K,
+                                                    float *__restrict__ dgamma)
+{
+    pdl_begin();
+    __shared__ float sh[8][32];
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    const int c = blockIdx.x * 32 + lane;  // K % 128 == 0: always in range
+    float v = 0.0f;
+    for (int p = w; p < parts; p += 8)
+        v += part[(int64_t)p * K + c];
+    sh[w][lane] = v;
+    __syncthreads();
+    if (w == 0) {
+#pragma unroll
+        for (int i = 1; i < 8; ++i)
+            v += sh[i][lane];
+        dgamma[c] = v;
+    }
+}
+
+// Launch shape of the backward kernel.
+struct BwdPlan {
+    int nv, T, teams, grid;
+};
+
+BwdPlan bwd_plan(int64_t M, int64_t K)
+{
+    BwdPlan p;
+    const int nvec = (int)(K / 8);
+    p.nv = K <= 8192 ? 2 : 4;
+    p.T = ((nvec + p.nv - 1) / p.nv + 31) / 32 * 32;
+    p.teams = p.T >= 512 ? 1 : (512 / p.T > 8 ? 8 : 512 / p.T);  // named barriers 1..8
+    if (p.teams > M)
+        p.teams = (int)M;
+    const int64_t want = (M + p.teams - 1) / p.teams;
+    const int sms = device_sms();
+    p.grid = (int)(want < sms ? want : sms);
+    return p;
+}
+
+}  // namespace
+
+cudaError_t launch_add_rmsnorm_quant(const uint16_t *res, int64_t ldr, const uint16_t *delta, int64_t ldd, int64_t M,
+                                     int64_t K, const uint16_t *gamma, float eps, uint16_t *h, int64_t ldh, float *rstd,
+                                     uint8_t *q, int64_t ldq, float *s, int64_t lds, uint8_t *qT, int64_t ldqT,
+                                     float *sc, int64_t ldsc, cudaStream_t st)
+{
+    // Few rows: one vector per thread, the shortest path through a row.  More rows
+    // than SMs: four per thread, more bytes in flight per thread and fewer warps per sum.
+    const int nvec = (int)(K / 8);
+    const int nv = (M <= device_sms() && nvec <= 1024) ? 1 : 4;
+    const int T = ((nvec + nv - 1) / nv + 31) / 32 * 32;
+    auto kernel = nv == 1 ? (delta ? k_add_rmsnorm_rows<1, true> : k_add_rmsnorm_rows<1, false>)
+                          : (delta ? k_add_rmsnorm_rows<4, true> : k_add_rmsnorm_rows<4, false>);
+    cudaError_t e = launch_pdl(kernel, dim3((unsigned)M), dim3(T), 0, st, res, ldr, delta, ldd, gamma, eps, (int)K, h,
+                               ldh, rstd, q, ldq, s, lds);
+    if (e != cudaSuccess || !qT)
+        return e;
+    const uint16_t *x = h ? h : res;
+    return launch_pdl(k_norm_cols, dim3((unsigned)((M + GRP - 1) / GRP), (unsigned)(K / GRP)), dim3(256), 0, st, x,
+                      h ? ldh : ldr, rstd, gamma, M, K, qT, ldqT, sc, ldsc);
+}
+
+int64_t rmsnorm_backward_ws_bytes(int64_t M, int64_t K)
+{
+    const BwdPlan p = bwd_plan(M, K);
+    return p.grid > 1 ? (int64_t)p.grid * K * 4 : 0;
+}
+
+cudaError_t launch_rmsnorm_backward(const uint16_t *dx, int64_t lddx, const uint16_t *h, int64_t ldh, const float *rstd,
+                                    const uint16_t *gamma, const uint16_t *dres, int64_t lddres, uint16_t *dh,
+                                    int64_t lddh, float *dgamma, int64_t M, int64_t K, float *ws, cudaStream_t st)
+{
+    const BwdPlan p = bwd_plan(M, K);
+    auto kernel = p.nv == 2 ? k_rmsnorm_bwd<2> : k_rmsnorm_bwd<4>;
+    const size_t smem = (size_t)K * 4;
+    cudaError_t e = cudaSuccess;
+    if (smem > 48 * 1024)  // K > 12288
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess)
+        return e;
+    e = launch_pdl(kernel, dim3(p.grid), dim3(p.T * p.teams), smem, st, dx, lddx, h, ldh, rstd, gamma, dres, lddres, dh,
+                   lddh, p.grid > 1 ? ws : dgamma, (int)M, (int)K, p.T, p.teams);
+    if (e != cudaSuccess || p.grid == 1)
+        return e;
+    return launch_pdl(k_dgamma_sum, dim3((unsigned)(K / 32)), dim3(256), 0, st, ws, p.grid, (int)K, dgamma);
+}
+
+}  // namespace rlq

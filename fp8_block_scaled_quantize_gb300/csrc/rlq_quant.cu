@@ -20,44 +20,13 @@
 // Build without fast-math: subnormal inputs and scales are honoured.
 #include <cuda_runtime.h>
 
+#include "rlq_elem.cuh"
 #include "rlq_internal.h"
 
 namespace rlq {
 namespace {
 
 constexpr int GRP = 128;
-
-// Loads of a kernel's input, which no thread of the kernel writes: the read-only
-// path without L1 allocation (measured 2% faster for the dual quantizer than an
-// evict-first streaming load, the same elsewhere).
-__device__ __forceinline__ uint4 ld_stream(const uint16_t *p)
-{
-    uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p));
-    return v;
-}
-
-__device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
-
-__device__ __forceinline__ void unpack8(const uint4 &v, float (&f)[8])
-{
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        f[2 * i] = bf_lo(w[i]);
-        f[2 * i + 1] = bf_hi(w[i]);
-    }
-}
-
-__device__ __forceinline__ uint32_t pack_bf16x2(float2 v)
-{
-    uint32_t d;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(v.y), "f"(v.x));
-    return d;
-}
 
 // RMSNorm of 8 consecutive bf16 elements of one row with that row's r and the
 // matching 8 norm weights: x = bf16_RN(fl32(fl32(h * r) * gamma)), each product
@@ -75,14 +44,6 @@ __device__ __forceinline__ uint4 norm8(const uint4 &v, float r, const uint4 &g)
     return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-// Two E4M3 codes, RN-even with saturation to +-448: `lo` in bits 0..7.
-__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi)
-{
-    uint16_t d;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(d) : "f"(hi), "f"(lo));
-    return d;
-}
-
 // Division context of one group (or of a pair of groups, one per lane of a
 // packed fp32x2 operation).
 struct Quot {
@@ -90,11 +51,6 @@ struct Quot {
     float sd;  // s * f (exact)
     float r;   // RN(1 / sd)
 };
-
-__device__ __forceinline__ float group_scale(float amax)
-{
-    return amax == 0.0f ? 1.0f : __fdiv_rn(amax, 448.0f);
-}
 
 __device__ __forceinline__ Quot make_quot(float s)
 {

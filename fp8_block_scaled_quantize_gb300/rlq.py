@@ -22,6 +22,7 @@ GRP = 128
 
 _P = ctypes.c_void_p
 _I = ctypes.c_int64
+_F = ctypes.c_float
 
 _SIGS = {
     "rlq_quant_act_1x128": [_P, _I, _I, _I, _P, _I, _P, _I, _P, _I, _P, _I, _P],
@@ -45,6 +46,14 @@ _SIGS = {
     "rlq_gemm_nvfp4_weight_only_splitk": [_P, _I, _P, _I, _P, _I, _P, _P, _I, _I, _I, _I, _P, _I, _P],
     "rlq_aqn_sigma": [ctypes.c_float, ctypes.c_float, _I, _I, ctypes.POINTER(ctypes.c_float)],
     "rlq_aqn_perturb": [_P, _I, _P, ctypes.c_float, _P],
+    "rlq_add_rmsnorm_quant_act_1x128": [_P, _I, _P, _I, _I, _I, _P, _F, _P, _I, _P, _P, _I, _P, _I, _P, _I, _P, _I, _P],
+    "rlq_rmsnorm_backward_workspace_bytes": [_I, _I, ctypes.POINTER(_I)],
+    "rlq_rmsnorm_backward": [_P, _I, _P, _I, _P, _P, _P, _I, _P, _I, _P, _I, _I, _P, _I, _P],
+    "rlq_gemm_gated_fprop": [_P, _I, _P, _I, _P, _I, _P, _I, _P, _I, _P, _I, _P, _I, _P, _I, _I, _I, _I, _P],
+    "rlq_gated_backward": [_P, _I, _P, _I, _P, _I, _P, _I, _P, _I, _P, _I, _P, _I, _P, _I, _P, _I, _I, _I, _P],
+    "rlq_token_logprobs": [_P, ctypes.c_int, _I, _I, _I, _P, _F, _P, _P, _P],
+    "rlq_policy_loss": [_P, ctypes.c_int, _I, _I, _I, _P, _F, _P, _P, _P, _P, _P, _P, _F, _F, _F, _F, _P, _P, _P, _I,
+                        _P],
     "rlq_check": [_P],
     "rlq_diag_bounded_wait": [_I, _P],
     "rlq_diag_arm_gemm_stall": [],
@@ -91,11 +100,16 @@ def lib() -> ctypes.CDLL:
     return _lib
 
 
+_fns: dict = {}  # entry points looked up so far
+
+
 def _call(name: str, *args) -> int:
-    L = lib()
-    st = getattr(L, name)(*args)
+    fn = _fns.get(name)
+    if fn is None:
+        fn = _fns[name] = getattr(lib(), name)
+    st = fn(*args)
     if st != 0:
-        raise RlqError(st, L.rlq_last_error().decode(errors="replace"))
+        raise RlqError(st, lib().rlq_last_error().decode(errors="replace"))
     return st
 
 
@@ -213,6 +227,49 @@ def rlq_uaq_fold(w, N, K, ldw, s, prev, R, ldp, stream):
     return _call("rlq_uaq_fold", w, N, K, ldw, s, prev, R, ldp, stream)
 
 
+def rlq_add_rmsnorm_quant_act_1x128(res, ldr, delta, ldd, M, K, gamma, eps, h, ldh, rstd, q, ldq, s, lds, qT, ldqT, sc,
+                                    ldsc, stream):
+    return _call("rlq_add_rmsnorm_quant_act_1x128", res, ldr, delta, ldd, M, K, gamma, eps, h, ldh, rstd, q, ldq, s, lds,
+                 qT, ldqT, sc, ldsc, stream)
+
+
+def rlq_rmsnorm_backward_workspace_bytes(M, K) -> int:
+    out = _I(0)
+    _call("rlq_rmsnorm_backward_workspace_bytes", M, K, ctypes.byref(out))
+    return out.value
+
+
+def rlq_rmsnorm_backward(dx, lddx, h, ldh, rstd, gamma, dres, lddres, dh, lddh, dgamma, M, K, workspace,
+                         workspace_bytes, stream):
+    return _call("rlq_rmsnorm_backward", dx, lddx, h, ldh, rstd, gamma, dres, lddres, dh, lddh, dgamma, M, K, workspace,
+                 workspace_bytes, stream)
+
+
+def rlq_gemm_gated_fprop(xq, ldxq, xs, ldxs, wq, ldwq, ws, ldws, aq, ldaq, as_, ldas, guq, ldguq, gus, ldgus, M, F, K,
+                         stream):
+    return _call("rlq_gemm_gated_fprop", xq, ldxq, xs, ldxs, wq, ldwq, ws, ldws, aq, ldaq, as_, ldas, guq, ldguq, gus,
+                 ldgus, M, F, K, stream)
+
+
+def rlq_gated_backward(da, ldda, guq, ldguq, gus, ldgus, q, ldq, s, lds, qT, ldqT, sc, ldsc, aT, ldaT, ac, ldac, M, F,
+                       stream):
+    return _call("rlq_gated_backward", da, ldda, guq, ldguq, gus, ldgus, q, ldq, s, lds, qT, ldqT, sc, ldsc, aT, ldaT,
+                 ac, ldac, M, F, stream)
+
+
+DTYPE_BF16, DTYPE_F32 = 0, 1
+
+
+def rlq_token_logprobs(logits, dtype, ld, rows, V, targets, temperature, lp, lse, stream):
+    return _call("rlq_token_logprobs", logits, dtype, ld, rows, V, targets, temperature, lp, lse, stream)
+
+
+def rlq_policy_loss(logits, dtype, ld, rows, V, targets, temperature, lp_old, adv, weight, lp_behav, lp_ref, clip_hi,
+                    eps_lo, eps_hi, tis_cap, kl_beta, loss, lp, dlogits, ldd, stream):
+    return _call("rlq_policy_loss", logits, dtype, ld, rows, V, targets, temperature, lp_old, adv, weight, lp_behav,
+                 lp_ref, clip_hi, eps_lo, eps_hi, tis_cap, kl_beta, loss, lp, dlogits, ldd, stream)
+
+
 def rlq_check(stream):
     return _call("rlq_check", stream)
 
@@ -241,7 +298,8 @@ def rlq_version() -> str:
 
 def _stream(stream) -> int:
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        # the current stream's handle without building a Stream object around it
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -252,10 +310,11 @@ def _ptr(t) -> int | None:
 
 
 def _ld(t) -> int:
-    """Row pitch in elements of a 2-D tensor whose rows are contiguous."""
-    if t.dim() != 2 or t.stride(1) != 1:
+    """Row pitch in elements of a 2-D tensor whose rows are contiguous.  The stride of a
+    dimension of size 1 is arbitrary (torch counts any as contiguous) and not looked at."""
+    if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1):
         raise ValueError("expected a 2-D tensor with contiguous rows")
-    return t.stride(0)
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
 
 
 def _round_up(v: int, m: int) -> int:
@@ -500,6 +559,183 @@ def aqn_perturb_(gamma: torch.Tensor, z: torch.Tensor, sigma: float, stream=None
         raise ValueError("gamma and z must be contiguous")
     rlq_aqn_perturb(gamma.data_ptr(), gamma.numel(), z.data_ptr(), sigma, _stream(stream))
     return gamma
+
+
+def _rows_of(name, t, M, K, dtype=torch.bfloat16):
+    """Row pitch of ``t``, a [M, K] CUDA tensor of ``dtype`` with contiguous rows; an error
+    that names it otherwise."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {str(dtype).replace('torch.', '')}")
+    if t.shape != (M, K):
+        raise ValueError(f"{name} must be a [{M}, {K}] tensor")
+    ld, inner = t.stride()
+    if inner != 1 and K > 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return ld if M > 1 else max(ld, K)
+
+
+def _vector(name, t, n, dtype=torch.float32):
+    """Address of ``t``, a contiguous [n] CUDA tensor of ``dtype``."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {str(dtype).replace('torch.', '')}")
+    if t.shape != (n,) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous [{n}] tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return t.data_ptr()
+
+
+def add_rmsnorm_quant_act_1x128(res: torch.Tensor, delta: torch.Tensor | None, gamma: torch.Tensor, eps: float,
+                                colwise: bool = False, inplace: bool = False, stream=None):
+    """h = bf16(res + delta), then RMSNorm with the bf16 weight gamma [K], quantized
+    1x128 (and with ``colwise`` 128x1) from fp32.  ``inplace`` writes h over res;
+    without ``delta``, h is res itself.
+
+    Returns (h [M, K] bf16, q, s, qT, sc) with q .. sc as ``quant_act_1x128``, and rstd [M] f32."""
+    if res.dim() != 2:
+        raise ValueError("res must be a [M, K] tensor")
+    M, K = res.shape
+    ldr = _rows_of("res", res, M, K)
+    ldd = _rows_of("delta", delta, M, K) if delta is not None else 0
+    g = _vector("gamma", gamma, K, torch.bfloat16)
+    dev = res.device
+    h = res if delta is None or inplace else torch.empty((M, K), dtype=torch.bfloat16, device=dev)
+    q = torch.empty((M, K), dtype=torch.uint8, device=dev)
+    s = torch.empty((K // GRP, M), dtype=torch.float32, device=dev)
+    rstd = torch.empty((M,), dtype=torch.float32, device=dev)
+    qT = sc = None
+    if colwise:
+        qT = empty_codes_T(K, M, dev)
+        sc = torch.empty(((M + GRP - 1) // GRP, K), dtype=torch.float32, device=dev)
+    rlq_add_rmsnorm_quant_act_1x128(res.data_ptr(), ldr, _ptr(delta), ldd, M, K, g, eps,
+                                    h.data_ptr() if delta is not None else None, _ld(h), rstd.data_ptr(),
+                                    q.data_ptr(), K, s.data_ptr(), max(M, 1), _ptr(qT),
+                                    _ld(qT) if colwise else 0, _ptr(sc), K if colwise else 0, _stream(stream))
+    return h, q, s, qT, sc, rstd
+
+
+def rmsnorm_backward(dx: torch.Tensor, h: torch.Tensor, rstd: torch.Tensor, gamma: torch.Tensor,
+                     dres: torch.Tensor | None = None, inplace: bool = False, workspace=None, stream=None):
+    """Gradient of the residual norm: dh = dres + d rmsnorm(h) * gamma / dh . dx (bf16) and
+    the norm weight's gradient (fp32 [K]).  ``inplace`` writes dh over dres.
+
+    Returns (dh [M, K] bf16, dgamma [K] f32)."""
+    if dx.dim() != 2:
+        raise ValueError("dx must be a [M, K] tensor")
+    M, K = dx.shape
+    lddx, ldh = _rows_of("dx", dx, M, K), _rows_of("h", h, M, K)
+    ldres = _rows_of("dres", dres, M, K) if dres is not None else 0
+    g, r = _vector("gamma", gamma, K, torch.bfloat16), _vector("rstd", rstd, M)
+    dh = dres if inplace and dres is not None else torch.empty((M, K), dtype=torch.bfloat16, device=dx.device)
+    dgamma = torch.empty((K,), dtype=torch.float32, device=dx.device)
+    nbytes = rlq_rmsnorm_backward_workspace_bytes(M, K)
+    if workspace is None and nbytes:
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=dx.device)
+    rlq_rmsnorm_backward(dx.data_ptr(), lddx, h.data_ptr(), ldh, r, g, _ptr(dres), ldres, dh.data_ptr(), _ld(dh),
+                         dgamma.data_ptr(), M, K, _ptr(workspace),
+                         workspace.numel() * workspace.element_size() if workspace is not None else 0, _stream(stream))
+    return dh, dgamma
+
+
+def gemm_gated_fprop(xq, xs, wq, ws, checkpoint: bool = False, stream=None):
+    """Gated feed-forward block: a = silu(X Wg^T) * (X Wu^T) from 1x128 X codes and the
+    stacked 128x128 codes [2F, K] of the gate and the up projection, gate first.
+
+    Returns (aq [M, F] u8, as [F/128, M] f32, guq, gus): a's 1x128 codes and scales and,
+    with ``checkpoint``, those of the two projections [M, 2F] (else None)."""
+    if xq.dim() != 2:
+        raise ValueError("xq must be a [M, K] tensor")
+    M, K = xq.shape
+    F = wq.shape[0] // 2
+    ldx, ldw = _rows_of("xq", xq, M, K, torch.uint8), _rows_of("wq", wq, 2 * F, K, torch.uint8)
+    ldxs = _rows_of("xs", xs, K // GRP, M, torch.float32)
+    ldws = _rows_of("ws", ws, 2 * F // GRP, K // GRP, torch.float32)
+    dev = xq.device
+    aq = torch.empty((M, F), dtype=torch.uint8, device=dev)
+    a_s = torch.empty((F // GRP, M), dtype=torch.float32, device=dev)
+    guq = gus = None
+    if checkpoint:
+        guq = torch.empty((M, 2 * F), dtype=torch.uint8, device=dev)
+        gus = torch.empty((2 * F // GRP, M), dtype=torch.float32, device=dev)
+    rlq_gemm_gated_fprop(xq.data_ptr(), ldx, xs.data_ptr(), max(ldxs, 1), wq.data_ptr(), ldw, ws.data_ptr(), ldws,
+                         aq.data_ptr(), F, a_s.data_ptr(), max(M, 1), _ptr(guq), 2 * F, _ptr(gus), max(M, 1), M, F, K,
+                         _stream(stream))
+    return aq, a_s, guq, gus
+
+
+def gated_backward(da: torch.Tensor, guq, gus, stream=None):
+    """Gradient of the gated block's activation from its 8-bit checkpoint.
+
+    Returns (q [M, 2F], s, qT [2F, M], sc) of [dg | du], as ``quant_act_1x128`` with
+    ``colwise``, and (aT [F, M], ac) the 128x1 codes and scales of a."""
+    if da.dim() != 2:
+        raise ValueError("da must be a [M, F] tensor")
+    M, F = da.shape
+    ldda, ldgu = _rows_of("da", da, M, F), _rows_of("guq", guq, M, 2 * F, torch.uint8)
+    ldgs = _rows_of("gus", gus, 2 * F // GRP, M, torch.float32)
+    dev = da.device
+    nb = (M + GRP - 1) // GRP
+    q = torch.empty((M, 2 * F), dtype=torch.uint8, device=dev)
+    s = torch.empty((2 * F // GRP, M), dtype=torch.float32, device=dev)
+    qT, aT = empty_codes_T(2 * F, M, dev), empty_codes_T(F, M, dev)
+    sc = torch.empty((nb, 2 * F), dtype=torch.float32, device=dev)
+    ac = torch.empty((nb, F), dtype=torch.float32, device=dev)
+    rlq_gated_backward(da.data_ptr(), ldda, guq.data_ptr(), ldgu, gus.data_ptr(), ldgs, q.data_ptr(), 2 * F,
+                       s.data_ptr(), max(M, 1), qT.data_ptr(), _ld(qT), sc.data_ptr(), 2 * F, aT.data_ptr(), _ld(aT),
+                       ac.data_ptr(), F, M, F, _stream(stream))
+    return q, s, qT, sc, aT, ac
+
+
+def _logits(logits, targets):
+    """(rows, V, dtype code, pitch, targets' address) of the logits."""
+    if logits.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError("logits must be bfloat16 or float32")
+    if logits.dim() != 2:
+        raise ValueError("logits must be a [rows, V] tensor")
+    T, V = logits.shape
+    ld = _rows_of("logits", logits, T, V, logits.dtype)
+    return T, V, (DTYPE_BF16 if logits.dtype is torch.bfloat16 else DTYPE_F32), ld, _vector("targets", targets, T,
+                                                                                         torch.int64)
+
+
+def token_logprobs(logits: torch.Tensor, targets: torch.Tensor, temperature: float = 1.0, stream=None):
+    """Log probabilities (fp32 [rows]) of the int64 ``targets`` under bf16 or fp32
+    ``logits`` [rows, V] divided by ``temperature``, and each row's log-sum-exp."""
+    T, V, dt, ld, tg = _logits(logits, targets)
+    lp = torch.empty((T,), dtype=torch.float32, device=logits.device)
+    lse = torch.empty((T,), dtype=torch.float32, device=logits.device)
+    rlq_token_logprobs(logits.data_ptr(), dt, ld, T, V, tg, temperature, lp.data_ptr(), lse.data_ptr(),
+                       _stream(stream))
+    return lp, lse
+
+
+def policy_loss(logits: torch.Tensor, targets: torch.Tensor, logp_old: torch.Tensor, adv: torch.Tensor,
+                weight: torch.Tensor, logp_behav=None, logp_ref=None, clip_hi=None, eps_lo: float = 0.2,
+                eps_hi: float = 0.2, tis_cap: float = 2.0, kl_beta: float = 0.0, temperature: float = 1.0,
+                grad: bool = True, inplace: bool = False, stream=None):
+    """Clipped policy loss with a truncated importance weight and a KL term (see
+    rlq_policy_loss in include/rlq.h): per-row losses whose sum is the batch's loss,
+    and the gradient of that sum with respect to the logits.  ``inplace`` writes the
+    gradient over the logits.
+
+    Returns (loss [rows] f32, logp [rows] f32, dlogits like logits or None)."""
+    T, V, dt, ld, tg = _logits(logits, targets)
+    opt = lambda name, t: None if t is None else _vector(name, t, T)  # noqa: E731
+    loss = torch.empty((T,), dtype=torch.float32, device=logits.device)
+    lp = torch.empty((T,), dtype=torch.float32, device=logits.device)
+    d = None
+    if grad and inplace:
+        d = logits
+    elif grad:
+        # the logits' own pitch, so that their rows share 16-byte phases
+        d = torch.empty_strided((T, V), (ld, 1), dtype=logits.dtype, device=logits.device)
+    rlq_policy_loss(logits.data_ptr(), dt, ld, T, V, tg, temperature, _vector("logp_old", logp_old, T),
+                    _vector("adv", adv, T), _vector("weight", weight, T), opt("logp_behav", logp_behav),
+                    opt("logp_ref", logp_ref), opt("clip_hi", clip_hi), eps_lo, eps_hi, tis_cap, kl_beta,
+                    loss.data_ptr(), lp.data_ptr(), _ptr(d), ld if grad else 0, _stream(stream))
+    return loss, lp, d
 
 
 def check(stream=None):

@@ -463,6 +463,176 @@ rlq_status rlq_gemm_fprop_splitk_static(const uint8_t *xq, int64_t ldxq, const f
                                         rlq_stream_t stream);
 
 /*
+ * ---- The actor's feed-forward sublayer and its loss around the quantized GEMMs ----
+ */
+
+/*
+ * Residual addition, RMSNorm and activation quantization in one pass over the
+ * residual stream (the norm in front of a quantized linear layer, where the
+ * previous sublayer's output is added first):
+ *
+ *   h[m, k]  = bf16_RN(res[m, k] + delta[m, k])
+ *   rstd[m]  = 1 / sqrt(mean_k h[m, k]^2 + eps)
+ *   x[m, k]  = (h[m, k] * rstd[m]) * gamma[k]
+ *
+ * with x in fp32, quantized as it is: 1x128 groups, and with qT / sc set 128x1
+ * groups too, in the layouts of rlq_quant_act_1x128 and with its scale rule.  It
+ * differs from rlq_rmsnorm_quant_act_1x128 in two ways besides the addition: x
+ * is not rounded to bf16 before it is quantized, and the sum of squares is taken
+ * in parallel (fp32, in an order fixed by K and by whether M exceeds the number
+ * of SMs), so codes may differ in the last place from that call's.  A code is the
+ * encoding of x * RN(1 / s), within 1.5 ulp of the quotient x / s.
+ *
+ *   res    bf16 [M, K], pitch ldr                        (input)
+ *   delta  bf16 [M, K], pitch ldd, or NULL (no addition) (input)
+ *   gamma  bf16 [K], 16-byte aligned; eps finite, >= 0
+ *   h      bf16 [M, K], pitch ldh (output); may be res or delta itself (in place, same
+ *          pitch); may be NULL only where delta is NULL
+ *   rstd   f32 [M]                                       (output)
+ *   q, s, qT, ldqT, sc, ldsc: as in rlq_quant_act_1x128  (outputs)
+ * K % 128 == 0, K <= 16384.  One launch, two with qT (the second reads h back).
+ */
+rlq_status rlq_add_rmsnorm_quant_act_1x128(const uint16_t *res, int64_t ldr, const uint16_t *delta, int64_t ldd,
+                                           int64_t M, int64_t K, const uint16_t *gamma, float eps,
+                                           uint16_t *h, int64_t ldh, float *rstd,
+                                           uint8_t *q, int64_t ldq, float *s, int64_t lds,
+                                           uint8_t *qT, int64_t ldqT, float *sc, int64_t ldsc,
+                                           rlq_stream_t stream);
+
+/*
+ * Backward pass of x = rmsnorm(h) * gamma with the residual's gradient added,
+ * xh = h * rstd:
+ *
+ *   dh[m, k]  = bf16_RN(dres[m, k] + rstd[m] * (dx[m, k] gamma[k] - xh[m, k] * c[m])),
+ *   c[m]      = mean_k dx[m, k] gamma[k] xh[m, k]
+ *   dgamma[k] = sum_m dx[m, k] xh[m, k]
+ *
+ * in fp32.  dh is the gradient of both the residual and the added delta.
+ *
+ *   dx     bf16 [M, K], pitch lddx (the linear layer's input gradient)
+ *   h      bf16 [M, K], pitch ldh and rstd f32 [M], of the forward call
+ *   gamma  bf16 [K], 16-byte aligned
+ *   dres   bf16 [M, K], pitch lddres, or NULL (no residual)
+ *   dh     bf16 [M, K], pitch lddh (output); may be dres itself (in place, same pitch)
+ *   dgamma f32 [K], 16-byte aligned (output, overwritten; zeros for M == 0)
+ *   workspace  device scratch of rlq_rmsnorm_backward_workspace_bytes(M, K), 16-byte
+ *          aligned (NULL where that is 0); contents on entry do not matter
+ * K % 128 == 0, K <= 16384.  Repeats bit for bit on one device (no atomics).
+ */
+rlq_status rlq_rmsnorm_backward_workspace_bytes(int64_t M, int64_t K, int64_t *bytes);
+
+rlq_status rlq_rmsnorm_backward(const uint16_t *dx, int64_t lddx, const uint16_t *h, int64_t ldh, const float *rstd,
+                                const uint16_t *gamma, const uint16_t *dres, int64_t lddres,
+                                uint16_t *dh, int64_t lddh, float *dgamma, int64_t M, int64_t K,
+                                void *workspace, int64_t workspace_bytes, rlq_stream_t stream);
+
+/*
+ * Gated feed-forward block, FP8 in and out: both projections, the activation and
+ * the product in one kernel.
+ *
+ *   g = X Wg^T, u = X Wu^T      (as rlq_gemm_fprop forms them, kept in fp32)
+ *   a = g * sigmoid(g) * u
+ *
+ * a leaves as 1x128 codes and scales, the down projection's operand.  With guq
+ * set, g and u leave as 1x128 codes too: the checkpoint that rlq_gated_backward
+ * reads, two bytes per column.  Neither is rounded to bf16 on the way.
+ *
+ *   xq   E4M3 [M, K], pitch ldxq; xs f32, xs[kb * ldxs + m]      (1x128)
+ *   wq   E4M3 [2F, K], pitch ldwq: the F rows of the gate projection, then the F
+ *        rows of the up projection; ws f32, ws[nb * ldws + kb], nb < 2F/128 (128x128)
+ *   aq   E4M3 [M, F], pitch ldaq; as f32, as[fb * ldas + m], fb < F/128 (outputs)
+ *   guq  E4M3 [M, 2F], pitch ldguq: g's codes, then u's; gus f32,
+ *        gus[fb * ldgus + m], fb < 2F/128                  (outputs; both or neither)
+ * F % 128 == 0, K % 128 == 0, K > 0.  Errors as for the other GEMMs (bounded
+ * device waits report at rlq_check).
+ */
+rlq_status rlq_gemm_gated_fprop(const uint8_t *xq, int64_t ldxq, const float *xs, int64_t ldxs,
+                                const uint8_t *wq, int64_t ldwq, const float *ws, int64_t ldws,
+                                uint8_t *aq, int64_t ldaq, float *as, int64_t ldas,
+                                uint8_t *guq, int64_t ldguq, float *gus, int64_t ldgus,
+                                int64_t M, int64_t F, int64_t K, rlq_stream_t stream);
+
+/*
+ * Backward pass of the gated block's activation from the 8-bit checkpoint.  With
+ * g and u the checkpoint's values (code * scale) and sg = sigmoid(g):
+ *
+ *   dg = da * u * sg * (1 + g * (1 - sg)),   du = da * g * sg,   a = g * sg * u
+ *
+ * in fp32.  [dg | du] [M, 2F] leaves quantized both ways, as rlq_quant_act_1x128
+ * lays it out: rlq_gemm_dgrad and rlq_gemm_wgrad with N = 2F over the stacked
+ * weight take it as it is.  a's 128x1 codes are the down projection's second
+ * WGrad operand.
+ *
+ *   da   bf16 [M, F], pitch ldda (the down projection's input gradient)
+ *   guq, gus: as rlq_gemm_gated_fprop writes them
+ *   q    E4M3 [M, 2F], pitch ldq; s f32, s[fb * lds + m], fb < 2F/128      (outputs)
+ *   qT   E4M3 [2F, M], pitch ldqT; sc f32, sc[mb * ldsc + n], ldsc >= 2F   (outputs)
+ *   aT   E4M3 [F, M], pitch ldaT;  ac f32, ac[mb * ldac + f], ldac >= F    (outputs)
+ * F % 128 == 0; M any value >= 0; the last token group may be partial.
+ */
+rlq_status rlq_gated_backward(const uint16_t *da, int64_t ldda, const uint8_t *guq, int64_t ldguq,
+                              const float *gus, int64_t ldgus, uint8_t *q, int64_t ldq, float *s, int64_t lds,
+                              uint8_t *qT, int64_t ldqT, float *sc, int64_t ldsc,
+                              uint8_t *aT, int64_t ldaT, float *ac, int64_t ldac,
+                              int64_t M, int64_t F, rlq_stream_t stream);
+
+/* Element type of logits. */
+typedef enum { RLQ_DTYPE_BF16 = 0, RLQ_DTYPE_F32 = 1 } rlq_dtype;
+
+/*
+ * Log probabilities of given tokens: z = logits / temperature,
+ *
+ *   lse[r] = log(sum_v exp(z[r, v])),   lp[r] = z[r, targets[r]] - lse[r]
+ *
+ * in fp32, one read of the logits.
+ *
+ *   logits  [rows, V] of `dtype`, pitch ld >= V, aligned to its element only (any
+ *           pitch; rows on 16-byte boundaries are read fastest)
+ *   targets int64 [rows], 8-byte aligned; a target outside [0, V) makes the row
+ *           empty: lp and lse are 0 and its logits are not read
+ *   lp      f32 [rows]; lse f32 [rows] or NULL           (outputs)
+ * Logits of -inf have probability 0; a row of nothing else has lp = lse = -inf.
+ * V >= 1, at most 524280 (bf16) or 262136 (fp32); temperature finite, > 0.
+ */
+rlq_status rlq_token_logprobs(const void *logits, rlq_dtype dtype, int64_t ld, int64_t rows, int64_t V,
+                              const int64_t *targets, float temperature, float *lp, float *lse,
+                              rlq_stream_t stream);
+
+/*
+ * Clipped policy loss with a KL term, and its gradient with respect to the logits.
+ * QuRL notes, 关键设计 (the decoupled objective: the clip ratio on full-precision
+ * log probabilities, a truncated importance weight for the quantized rollout, an
+ * adaptive upper clip).  Per row, with lp as above:
+ *
+ *   rho  = exp(lp - lp_old)
+ *   w    = min(exp(lp_old - lp_behav), tis_cap)          (1 where lp_behav is NULL)
+ *   pg   = -w * min(rho * adv, clip(rho, 1 - eps_lo, hi) * adv),
+ *          hi = clip_hi[r], or 1 + eps_hi where clip_hi is NULL
+ *   kl   = kl_beta * (exp(d) - 1 - d), d = lp_ref - lp   (0 where lp_ref is NULL)
+ *   loss = weight * (pg + kl)
+ *   dlogits[v] = dloss/dlp * (1[v = target] - softmax(z)[v]) / temperature
+ *
+ * w, adv and weight are constants of the gradient.  The batch's loss is the sum
+ * of loss[r]; weight carries the token mask and the normalisation (mask / tokens).
+ * A row of weight 0 or with a target outside [0, V) is empty: its logits are not
+ * read, loss and lp are 0 and its gradient is zeros.  A row of -inf logits only
+ * has lp = -inf, loss 0 and a zero gradient.
+ *
+ *   lp_old, adv, weight  f32 [rows]; lp_behav, lp_ref, clip_hi f32 [rows] or NULL
+ *   loss, lp  f32 [rows]                                  (outputs)
+ *   dlogits   [rows, V] of `dtype`, pitch ldd >= V, or NULL for the loss alone
+ *             (output); may be logits itself (in place, same pitch)
+ * eps_lo in [0, 1], eps_hi >= 0, tis_cap > 0, kl_beta >= 0, all finite.  Other
+ * arguments and limits as for rlq_token_logprobs.  One read and one write of the
+ * logits.
+ */
+rlq_status rlq_policy_loss(const void *logits, rlq_dtype dtype, int64_t ld, int64_t rows, int64_t V,
+                           const int64_t *targets, float temperature, const float *lp_old, const float *adv,
+                           const float *weight, const float *lp_behav, const float *lp_ref, const float *clip_hi,
+                           float eps_lo, float eps_hi, float tis_cap, float kl_beta,
+                           float *loss, float *lp, void *dlogits, int64_t ldd, rlq_stream_t stream);
+
+/*
  * UAQ invariant-scaling fold, in place.  QuRL notes, 关键设计 §1: WX = (W/s)(sX)
  * with s > 1 applied per column of W and per row of the previous activation
  * (foldable into a LayerNorm / RMSNorm scale); run once before RL.
