@@ -684,8 +684,8 @@ rlq_status rlq_gated_backward(const uint16_t *da, int64_t ldda, const uint8_t *g
 {
     RLQ_REQUIRE(M >= 0 && F >= 0, RLQ_ERR_INVALID_ARG, "negative size (M=%lld, F=%lld)", (long long)M, (long long)F);
     RLQ_REQUIRE(F % G == 0, RLQ_ERR_UNSUPPORTED, "F=%lld is not a multiple of 128", (long long)F);
-    // (F / 128 is the launch grid's second extent)
-    RLQ_REQUIRE(M < MAX_DIM && F / G <= 65535, RLQ_ERR_UNSUPPORTED, "M beyond 2^31 or F beyond 8388480");
+    RLQ_REQUIRE(M < MAX_DIM && 2 * F < MAX_DIM && ((M + G - 1) / G) * (F / G) < MAX_DIM / 2, RLQ_ERR_UNSUPPORTED,
+                "dimension beyond 2^31, or 2^30 tiles of 128 x 128");
     if (M == 0 || F == 0)
         return RLQ_OK;
     RLQ_TRY(check_bf16("da", da, ldda, F));

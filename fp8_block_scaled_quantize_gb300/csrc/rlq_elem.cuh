@@ -55,27 +55,45 @@ __device__ __forceinline__ float group_scale(float amax)
     return amax == 0.0f ? 1.0f : __fdiv_rn(amax, 448.0f);
 }
 
-// Multiplier that turns x into x / s before the encoding: RN(1 / s).  The
-// operators that quantize fp32 results use the product x * RN(1/s), at most
-// 1.5 ulp from the quotient, where the values themselves carry as much.  Scales
-// below 2^-100 (their reciprocal may overflow) return 0: encode8f divides then.
-__device__ __forceinline__ float scale_rcp(float s) { return s < 0x1p-100f ? 0.0f : __frcp_rn(s); }
+// A scale as the encoding applies it: codes are of (x * pre) * rcp, with pre = 1, or
+// 2^64 (exact) for scales below 2^-100, whose own reciprocal may overflow, and rcp =
+// RN(1 / (s * pre)).  The operators that quantize fp32 results use this product, at
+// most 1.5 ulp from the quotient x / s, where the values themselves carry as much.
+__device__ __forceinline__ float scale_pre(float s) { return s < 0x1p-100f ? 0x1p64f : 1.0f; }
+__device__ __forceinline__ float scale_rcp(float s) { return __frcp_rn(s * scale_pre(s)); }
 
-// E4M3 codes of 8 fp32 values of one group (scale s, rcp = scale_rcp(s)).
+// E4M3 codes of 8 fp32 values (adjacent pairs) of one group.
+__device__ __forceinline__ uint2 encode8f(const float2 (&v)[4], float pre, float rcp)
+{
+    const float2 r2 = make_float2(rcp, rcp);
+    float2 f[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        f[i] = v[i];
+    if (pre != 1.0f) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            f[i] = __fmul2_rn(f[i], make_float2(pre, pre));
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        f[i] = __fmul2_rn(f[i], r2);
+    return make_uint2(e4m3x2(f[0].x, f[0].y) | (e4m3x2(f[1].x, f[1].y) << 16),
+                      e4m3x2(f[2].x, f[2].y) | (e4m3x2(f[3].x, f[3].y) << 16));
+}
+
 __device__ __forceinline__ uint2 encode8f(const float (&v)[8], float s, float rcp)
 {
-    float f[8];
-    if (rcp != 0.0f) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            f[i] = v[i] * rcp;
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            f[i] = __fdiv_rn(v[i], s);
-    }
-    return make_uint2(e4m3x2(f[0], f[1]) | (e4m3x2(f[2], f[3]) << 16),
-                      e4m3x2(f[4], f[5]) | (e4m3x2(f[6], f[7]) << 16));
+    const float2 f[4] = {make_float2(v[0], v[1]), make_float2(v[2], v[3]), make_float2(v[4], v[5]),
+                         make_float2(v[6], v[7])};
+    return encode8f(f, scale_pre(s), rcp);
+}
+
+__device__ __forceinline__ float max_abs8(const float2 (&v)[4])
+{
+    const float a = fmaxf(fmaxf(fabsf(v[0].x), fabsf(v[0].y)), fmaxf(fabsf(v[1].x), fabsf(v[1].y)));
+    const float b = fmaxf(fmaxf(fabsf(v[2].x), fabsf(v[2].y)), fmaxf(fabsf(v[3].x), fabsf(v[3].y)));
+    return fmaxf(a, b);
 }
 
 __device__ __forceinline__ float max_abs8(const float (&v)[8])
@@ -85,13 +103,18 @@ __device__ __forceinline__ float max_abs8(const float (&v)[8])
     return fmaxf(a, b);
 }
 
-// 1 / (1 + exp(-g)) with the exponential and the reciprocal of the special-function
-// units (about 2 and 1 ulp); 0 where exp(-g) overflows.
-__device__ __forceinline__ float sigmoid_fast(float g)
+// 1 / (1 + exp(-g)) of two values, the exponential and the reciprocal on the
+// special-function units (about 2 and 1 ulp).  Their .ftz forms, a single instruction
+// each: exp(-g) below 2^-126 adds nothing to 1, and a sigmoid below 2^-126 is 0.
+__device__ __forceinline__ float2 sigmoid2(float2 g)
 {
-    float e, r;
-    asm("ex2.approx.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
-    asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(e + 1.0f));
+    float2 d, r;
+    const float2 e = __fmul2_rn(g, make_float2(-1.4426950408889634f, -1.4426950408889634f));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(d.x) : "f"(e.x));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(d.y) : "f"(e.y));
+    d = __fadd2_rn(d, make_float2(1.0f, 1.0f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(d.x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(d.y));
     return r;
 }
 

@@ -20,8 +20,15 @@ namespace {
 
 constexpr int GRP = 128;
 constexpr int THREADS = 512;
-constexpr int TILE_BYTES = GRP * GRP;                            // one operand's transposed codes
-constexpr int SMEM_BYTES = 3 * TILE_BYTES + 16 * 3 * GRP * 4;  // and 16 warps' column maxima
+// Shared memory: two prefetched tiles (per thread four rows of 16 + 8 + 8 bytes) and
+// their 2 x 128 scales, the three transposed code tiles, 16 warps' column maxima.
+constexpr int IN_BYTES = THREADS * 4 * 32;
+constexpr int TILE_BYTES = GRP * GRP;
+constexpr int OFF_SCALES = 2 * IN_BYTES;
+constexpr int OFF_TILES = OFF_SCALES + 2 * 2 * GRP * 4;
+constexpr int OFF_PART = OFF_TILES + 3 * TILE_BYTES;
+constexpr int SMEM_BYTES = OFF_PART + 16 * 3 * GRP * 4;
+static_assert(SMEM_BYTES <= 232448, "shared memory budget");
 
 struct GateBwd {
     const uint16_t *da;
@@ -43,11 +50,26 @@ struct GateBwd {
     float *ac;
     int64_t ldac;
     int64_t M, F;
+    int m_tiles, tiles;
 };
+
+// Global -> shared copies; bytes = 0 writes zeros without reading.
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, uint32_t bytes)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copy8(uint32_t dst, const void *src, uint32_t bytes)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t dst, const void *src, uint32_t bytes)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
 
 // 8 E4M3 codes -> fp32, times s (each code is exact in fp16, so the product is the
 // one rounding).
-__device__ __forceinline__ void decode8(uint2 c, float s, float (&f)[8])
+__device__ __forceinline__ void decode8(uint2 c, float s, float2 (&f)[4])
 {
     const uint32_t w[2] = {c.x, c.y};
 #pragma unroll
@@ -59,117 +81,197 @@ __device__ __forceinline__ void decode8(uint2 c, float s, float (&f)[8])
         asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
             : "=f"(lo), "=f"(hi)
             : "r"(h));
-        f[2 * i] = lo * s;
-        f[2 * i + 1] = hi * s;
+        f[i] = __fmul2_rn(make_float2(lo, hi), make_float2(s, s));
     }
 }
 
-// A CTA takes a 128 x 128 tile of [M, F]; thread t rows 4 (t / 16) .. + 3 and columns
-// 8 (t % 16) .. + 7, all in registers.  A row's 16 lanes are its 1x128 group; column
-// maxima go over the rows of a thread, the two halves of a warp and, in shared memory,
-// the 16 warps.
+// |running maximum| of two values.
+__device__ __forceinline__ void max2(float2 &m, float2 v)
+{
+    m.x = fmaxf(m.x, fabsf(v.x));
+    m.y = fmaxf(m.y, fabsf(v.y));
+}
+
+// Persistent, one CTA per SM, 128 x 128 tiles of [M, F], row block fastest.  Thread t
+// has rows 4 (t / 16) .. + 3 and columns 8 (t % 16) .. + 7 of a tile, all of it in
+// registers; it copies its own part of the next tile to shared memory meanwhile.  A
+// row's 16 lanes are its 1x128 group: the eight row maxima of a half-warp (four rows of
+// dg, four of du) are reduced in one transposed exchange (each step hands half of the
+// remaining ones to the partner lane), after which a lane pair holds one group's and
+// computes its scale once.  Column maxima go over the rows of a thread, the two halves
+// of a warp and, in shared memory, the 16 warps.
 __global__ void __launch_bounds__(THREADS, 1) k_gate_bwd(const GateBwd p)
 {
     pdl_begin();
     extern __shared__ __align__(16) uint8_t smem[];
-    float *part = reinterpret_cast<float *>(smem + 3 * TILE_BYTES);  // [warp][3][128]
+    float *part = reinterpret_cast<float *>(smem + OFF_PART);  // [warp][3][128]
+    uint8_t *tiles = smem + OFF_TILES;
+    const uint32_t smem0 = (uint32_t)__cvta_generic_to_shared(smem);
     const int t = threadIdx.x, cg = t & 15, rg = t >> 4, warp = t >> 5;
-    const int64_t m0 = (int64_t)blockIdx.x * GRP, f0 = (int64_t)blockIdx.y * GRP;
-    const int rows = (int)(p.M - m0 < GRP ? p.M - m0 : GRP);
-    const int64_t fb = p.F / GRP;  // scale rows of one projection
-    uint4 va[4];
-    uint2 vg[4], vu[4];
-    float sg_[4], su_[4];
+    const bool b3 = t & 8, b2 = t & 4, b1 = t & 2;
+    const int own = (t & 15) >> 1;  // the group maximum this lane ends up with: matrix own / 4, row own % 4
+    const int64_t fb = p.F / GRP;   // scale rows of one projection
+
+    auto prefetch = [&](int tile, int buf) {
+        const int mt = tile % p.m_tiles, ft = tile / p.m_tiles;
+        const int64_t m0 = (int64_t)mt * GRP, f = (int64_t)ft * GRP + 8 * cg;
+        const uint32_t in = smem0 + buf * IN_BYTES;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int r = 4 * rg + i;
-        const bool in = r < rows;
-        const int64_t m = m0 + r;
-        const uint8_t *gp = p.guq + m * p.ldguq + f0 + 8 * cg;
-        va[i] = in ? ld_stream(p.da + m * p.ldda + f0 + 8 * cg) : make_uint4(0, 0, 0, 0);
-        vg[i] = in ? *reinterpret_cast<const uint2 *>(gp) : make_uint2(0, 0);
-        vu[i] = in ? *reinterpret_cast<const uint2 *>(gp + p.F) : make_uint2(0, 0);
-        sg_[i] = in ? p.gus[(int64_t)blockIdx.y * p.ld_gus + m] : 0.0f;
-        su_[i] = in ? p.gus[(fb + blockIdx.y) * p.ld_gus + m] : 0.0f;
-    }
-    float dg[4][8], du[4][8], a[4][8], cmax[3][8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-        cmax[0][j] = cmax[1][j] = cmax[2][j] = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        float g[8], u[8], d[8];
-        decode8(vg[i], sg_[i], g);
-        decode8(vu[i], su_[i], u);
-        unpack8(va[i], d);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float sg = sigmoid_fast(g[j]);
-            const float gs = g[j] * sg;
-            du[i][j] = d[j] * gs;
-            a[i][j] = gs * u[j];
-            dg[i][j] = (d[j] * u[j]) * fmaf(gs, 1.0f - sg, sg);
-            cmax[0][j] = fmaxf(cmax[0][j], fabsf(dg[i][j]));
-            cmax[1][j] = fmaxf(cmax[1][j], fabsf(du[i][j]));
-            cmax[2][j] = fmaxf(cmax[2][j], fabsf(a[i][j]));
+        for (int i = 0; i < 4; ++i) {
+            const bool ok = m0 + 4 * rg + i < p.M;
+            const int64_t m = ok ? m0 + 4 * rg + i : 0;
+            const uint8_t *gp = p.guq + m * p.ldguq + f;
+            copy16(in + (i * THREADS + t) * 16, p.da + m * p.ldda + f, ok ? 16 : 0);
+            copy8(in + THREADS * 64 + (i * THREADS + t) * 8, gp, ok ? 8 : 0);
+            copy8(in + THREADS * 96 + (i * THREADS + t) * 8, gp + p.F, ok ? 8 : 0);
         }
-        const float s0 = group_scale(half_warp_max(max_abs8(dg[i])));
-        const float s1 = group_scale(half_warp_max(max_abs8(du[i])));
-        const int r = 4 * rg + i;
-        if (r < rows) {
-            const int64_t m = m0 + r;
-            uint8_t *qp = p.q + m * p.ldq + f0 + 8 * cg;
-            *reinterpret_cast<uint2 *>(qp) = encode8f(dg[i], s0, scale_rcp(s0));
-            *reinterpret_cast<uint2 *>(qp + p.F) = encode8f(du[i], s1, scale_rcp(s1));
-            if (cg == 0) {
-                p.s[(int64_t)blockIdx.y * p.lds + m] = s0;
-                p.s[(fb + blockIdx.y) * p.lds + m] = s1;
+        if (t < 2 * GRP) {
+            const bool ok = m0 + (t & 127) < p.M;
+            copy4(smem0 + OFF_SCALES + (buf * 2 * GRP + t) * 4,
+                  p.gus + ((t >> 7) * fb + ft) * p.ld_gus + (ok ? m0 + (t & 127) : 0), ok ? 4 : 0);
+        }
+    };
+
+    int tile = blockIdx.x;
+    if (tile < p.tiles)
+        prefetch(tile, 0);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    for (int buf = 0; tile < p.tiles; tile += gridDim.x, buf ^= 1) {
+        if (tile + (int)gridDim.x < p.tiles)
+            prefetch(tile + gridDim.x, buf ^ 1);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+        __syncthreads();  // this tile's scales are there; the last tile's codes have left shared memory
+        const int mt = tile % p.m_tiles, ft = tile / p.m_tiles;
+        const int64_t m0 = (int64_t)mt * GRP, f0 = (int64_t)ft * GRP;
+        const int rows = (int)(p.M - m0 < GRP ? p.M - m0 : GRP);
+        const uint8_t *in = smem + buf * IN_BYTES;
+        const float *scl = reinterpret_cast<const float *>(smem + OFF_SCALES) + buf * 2 * GRP + 4 * rg;
+        const float4 gs4 = *reinterpret_cast<const float4 *>(scl), us4 = *reinterpret_cast<const float4 *>(scl + GRP);
+        const float sg4[4] = {gs4.x, gs4.y, gs4.z, gs4.w}, su4[4] = {us4.x, us4.y, us4.z, us4.w};
+        float2 val[3][4][4], cmax[3][4];  // dg, du, a of [row][column pair]
+        float v[8];
+#pragma unroll
+        for (int k = 0; k < 3; ++k)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                cmax[k][j] = make_float2(0.0f, 0.0f);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float2 g[4], u[4];
+            decode8(*reinterpret_cast<const uint2 *>(in + THREADS * 64 + (i * THREADS + t) * 8), sg4[i], g);
+            decode8(*reinterpret_cast<const uint2 *>(in + THREADS * 96 + (i * THREADS + t) * 8), su4[i], u);
+            const uint4 dv = *reinterpret_cast<const uint4 *>(in + (i * THREADS + t) * 16);
+            const uint32_t dw[4] = {dv.x, dv.y, dv.z, dv.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float2 d = make_float2(bf_lo(dw[j]), bf_hi(dw[j]));
+                const float2 sg = sigmoid2(g[j]);
+                const float2 gs = __fmul2_rn(g[j], sg);
+                const float2 om = __ffma2_rn(sg, make_float2(-1.0f, -1.0f), make_float2(1.0f, 1.0f));
+                val[0][i][j] = __fmul2_rn(__fmul2_rn(d, u[j]), __ffma2_rn(gs, om, sg));
+                val[1][i][j] = __fmul2_rn(d, gs);
+                val[2][i][j] = __fmul2_rn(gs, u[j]);
+#pragma unroll
+                for (int k = 0; k < 3; ++k)
+                    max2(cmax[k][j], val[k][i][j]);
+            }
+            v[i] = max_abs8(val[0][i]);
+            v[4 + i] = max_abs8(val[1][i]);
+        }
+        // the halves of a warp exchange: the lower keeps columns 0-3 of its eight, the upper 4-7
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+            float4 c;
+            const bool up = t & 16;
+            float *cc = &c.x;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const float2 keep = up ? cmax[k][2 + j] : cmax[k][j], send = up ? cmax[k][j] : cmax[k][2 + j];
+                cc[2 * j] = fmaxf(keep.x, __shfl_xor_sync(0xFFFFFFFFu, send.x, 16));
+                cc[2 * j + 1] = fmaxf(keep.y, __shfl_xor_sync(0xFFFFFFFFu, send.y, 16));
+            }
+            *reinterpret_cast<float4 *>(part + (warp * 3 + k) * GRP + 8 * cg + (up ? 4 : 0)) = c;
+        }
+        __syncthreads();
+        float cs = 1.0f;
+        if (t < 3 * GRP) {
+            float c = part[t];
+#pragma unroll
+            for (int w = 1; w < 16; ++w)
+                c = fmaxf(c, part[w * 3 * GRP + t]);
+            cs = group_scale(c);
+            const int k = t >> 7, cc = t & 127;
+            if (k < 2)
+                p.sc[(int64_t)mt * p.ldsc + k * p.F + f0 + cc] = cs;
+            else
+                p.ac[(int64_t)mt * p.ldac + f0 + cc] = cs;
+            part[t] = scale_rcp(cs);  // (only this thread reads column t of the maxima)
+        }
+        // row groups
+        float x4[4], x2[2], x1;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            x4[k] = fmaxf(b3 ? v[k + 4] : v[k], __shfl_xor_sync(0xFFFFFFFFu, b3 ? v[k] : v[k + 4], 8));
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+            x2[k] = fmaxf(b2 ? x4[k + 2] : x4[k], __shfl_xor_sync(0xFFFFFFFFu, b2 ? x4[k] : x4[k + 2], 4));
+        x1 = fmaxf(b1 ? x2[1] : x2[0], __shfl_xor_sync(0xFFFFFFFFu, b1 ? x2[0] : x2[1], 2));
+        x1 = fmaxf(x1, __shfl_xor_sync(0xFFFFFFFFu, x1, 1));
+        const float rs = group_scale(x1), rr = scale_rcp(rs), rp = scale_pre(rs);
+        if ((t & 1) == 0 && 4 * rg + (own & 3) < rows)
+            p.s[((own >> 2) * fb + ft) * p.lds + m0 + 4 * rg + (own & 3)] = rs;
+        const bool pre_rows = __any_sync(0xFFFFFFFFu, rp != 1.0f);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int i = k & 3, r = 4 * rg + i, src = (t & 16) + 2 * k;
+            const float q = __shfl_sync(0xFFFFFFFFu, rr, src);
+            const float pre = pre_rows ? __shfl_sync(0xFFFFFFFFu, rp, src) : 1.0f;
+            if (r < rows)
+                *reinterpret_cast<uint2 *>(p.q + (m0 + r) * p.ldq + (k >> 2) * p.F + f0 + 8 * cg) =
+                    encode8f(val[k >> 2][i], pre, q);
+        }
+        // Column groups, with the reciprocals that now stand in the first warp's places.
+        // (Columns whose scale is below 2^-100 are scaled up first.)
+        if (__syncthreads_or(cs < 0x1p-100f)) {
+            if (t < 3 * GRP)
+                part[3 * GRP + t] = scale_pre(cs);
+            __syncthreads();
+#pragma unroll
+            for (int k = 0; k < 3; ++k)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float2 f = *reinterpret_cast<const float2 *>(part + (3 + k) * GRP + 8 * cg + 2 * j);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        val[k][i][j] = __fmul2_rn(val[k][i][j], f);
+                }
+        }
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+            const float4 r0 = *reinterpret_cast<const float4 *>(part + k * GRP + 8 * cg);
+            const float4 r1 = *reinterpret_cast<const float4 *>(part + k * GRP + 8 * cg + 4);
+            const float2 r[4] = {make_float2(r0.x, r0.y), make_float2(r0.z, r0.w), make_float2(r1.x, r1.y),
+                                 make_float2(r1.z, r1.w)};
+            uint8_t *out = tiles + k * TILE_BYTES + 8 * cg * GRP + 8 * ((rg >> 1) ^ cg) + 4 * (rg & 1);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                float2 y[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    y[i] = __fmul2_rn(val[k][i][j], r[j]);
+                *reinterpret_cast<uint32_t *>(out + 2 * j * GRP) =
+                    e4m3x2(y[0].x, y[1].x) | (e4m3x2(y[2].x, y[3].x) << 16);
+                *reinterpret_cast<uint32_t *>(out + (2 * j + 1) * GRP) =
+                    e4m3x2(y[0].y, y[1].y) | (e4m3x2(y[2].y, y[3].y) << 16);
             }
         }
+        __syncthreads();
+        store_tile_T(tiles, t, THREADS, rows, p.qT + f0 * p.ldqT + m0, p.ldqT);
+        store_tile_T(tiles + TILE_BYTES, t, THREADS, rows, p.qT + (p.F + f0) * p.ldqT + m0, p.ldqT);
+        store_tile_T(tiles + 2 * TILE_BYTES, t, THREADS, rows, p.aT + f0 * p.ldaT + m0, p.ldaT);
     }
-#pragma unroll
-    for (int k = 0; k < 3; ++k)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float c = fmaxf(cmax[k][j], __shfl_xor_sync(0xFFFFFFFFu, cmax[k][j], 16));
-            if ((t & 16) == 0)
-                part[(warp * 3 + k) * GRP + 8 * cg + j] = c;
-        }
-    __syncthreads();
-    if (t < 3 * GRP) {
-        float v = part[t];
-#pragma unroll
-        for (int w = 1; w < 16; ++w)
-            v = fmaxf(v, part[w * 3 * GRP + t]);
-        v = group_scale(v);
-        part[t] = v;
-        part[3 * GRP + t] = scale_rcp(v);
-        const int k = t >> 7, c = t & 127;
-        if (k < 2)
-            p.sc[(int64_t)blockIdx.x * p.ldsc + k * p.F + f0 + c] = v;
-        else
-            p.ac[(int64_t)blockIdx.x * p.ldac + f0 + c] = v;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < 3; ++k)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int c = 8 * cg + j;
-            const float s = part[k * GRP + c], r = part[(3 + k) * GRP + c];
-            float v[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float x = k == 0 ? dg[i][j] : k == 1 ? du[i][j] : a[i][j];
-                v[i] = r != 0.0f ? x * r : __fdiv_rn(x, s);
-            }
-            *reinterpret_cast<uint32_t *>(smem + k * TILE_BYTES + c * GRP + 8 * ((rg >> 1) ^ cg) + 4 * (rg & 1)) =
-                e4m3x2(v[0], v[1]) | (e4m3x2(v[2], v[3]) << 16);
-        }
-    __syncthreads();
-    store_tile_T(smem, t, THREADS, rows, p.qT + f0 * p.ldqT + m0, p.ldqT);
-    store_tile_T(smem + TILE_BYTES, t, THREADS, rows, p.qT + (p.F + f0) * p.ldqT + m0, p.ldqT);
-    store_tile_T(smem + 2 * TILE_BYTES, t, THREADS, rows, p.aT + f0 * p.ldaT + m0, p.ldaT);
+    asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
 }  // namespace
@@ -179,13 +281,16 @@ cudaError_t launch_gated_backward(const uint16_t *da, int64_t ldda, const uint8_
                                   int64_t ldqT, float *sc, int64_t ldsc, uint8_t *aT, int64_t ldaT, float *ac,
                                   int64_t ldac, int64_t M, int64_t F, cudaStream_t st)
 {
-    const GateBwd p = {da, ldda, guq, ldguq, gus, ld_gus, q,    ldq, s,    lds, qT,
-                       ldqT, sc, ldsc, aT, ldaT, ac, ldac, M,  F};
+    const int64_t m_tiles = (M + GRP - 1) / GRP, tiles = m_tiles * (F / GRP);
+    if (tiles > INT32_MAX / 2)
+        return cudaErrorInvalidValue;
+    const GateBwd p = {da, ldda, guq, ldguq, gus, ld_gus, q,  ldq, s, lds, qT,           ldqT,
+                       sc, ldsc, aT,  ldaT,  ac,  ldac,   M,  F,   (int)m_tiles, (int)tiles};
     const cudaError_t e = cudaFuncSetAttribute(k_gate_bwd, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
     if (e != cudaSuccess)
         return e;
-    return launch_pdl(k_gate_bwd, dim3((unsigned)((M + GRP - 1) / GRP), (unsigned)(F / GRP)), dim3(THREADS), SMEM_BYTES,
-                      st, p);
+    const int64_t sms = device_sms();
+    return launch_pdl(k_gate_bwd, dim3((unsigned)(tiles < sms ? tiles : sms)), dim3(THREADS), SMEM_BYTES, st, p);
 }
 
 }  // namespace rlq

@@ -276,20 +276,9 @@ enum : int { MODE_BLOCK = 0, MODE_COLS = 1, MODE_ONCE = 2, MODE_GATED = 3 };
 // Epilogue outputs.
 enum : int { OUT_BF16 = 0, OUT_F32_PARTIAL = 1, OUT_F32_ACC = 2 };
 
-// silu(g) * u for two columns: g * u / (1 + 2^(-g log2 e)), the exponential and the
-// reciprocal on the special-function units (about 2 and 1 ulp).
-__device__ __forceinline__ float2 silu_mul2(float2 g, float2 u)
-{
-    float2 d, r;
-    const float2 e = __fmul2_rn(g, make_float2(-1.4426950408889634f, -1.4426950408889634f));
-    asm("ex2.approx.f32 %0, %1;" : "=f"(d.x) : "f"(e.x));
-    asm("ex2.approx.f32 %0, %1;" : "=f"(d.y) : "f"(e.y));
-    d = __fadd2_rn(d, make_float2(1.0f, 1.0f));
-    asm("rcp.approx.f32 %0, %1;" : "=f"(r.x) : "f"(d.x));
-    asm("rcp.approx.f32 %0, %1;" : "=f"(r.y) : "f"(d.y));
-    // (g * r first: r is 0 where g is far below zero, and u may be large)
-    return __fmul2_rn(__fmul2_rn(g, r), u);
-}
+// silu(g) * u for two columns.  (g * sigmoid first: that is 0 where g is far below
+// zero, and u may be large.)
+__device__ __forceinline__ float2 silu_mul2(float2 g, float2 u) { return __fmul2_rn(__fmul2_rn(g, sigmoid2(g)), u); }
 
 // max |.| over 32 pairs.
 __device__ __forceinline__ float amax32(const float2 *v)
@@ -303,47 +292,58 @@ __device__ __forceinline__ float amax32(const float2 *v)
     return fmaxf(a, b);
 }
 
-// 64 FP8 codes of 32 pairs with scale s, written to 64 consecutive bytes.
-__device__ __forceinline__ void store_codes64(uint8_t *__restrict__ dst, const float2 *v, float s)
+// 64 FP8 codes of 32 pairs with scale s: to 64 consecutive bytes of global memory, or
+// (kStage) to row `row` of a staging buffer of 64-byte rows, 16-byte pieces XOR-swizzled
+// by (row / 2) % 4 (the tensor map's 64-byte swizzle).
+template <bool kStage>
+__device__ __forceinline__ void store_codes64(uint8_t *__restrict__ dst, uint32_t stg, int row, const float2 *v, float s)
 {
-    const float r = scale_rcp(s);
+    // (the exact pre-scale of scales below 2^-100 unconditionally: a branch here costs
+    // the epilogue's registers more than 32 products)
+    const float2 pre = make_float2(scale_pre(s), scale_pre(s));
+    const float2 r = make_float2(scale_rcp(s), scale_rcp(s));
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         uint32_t w[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            float2 a = v[8 * j + 2 * i], b = v[8 * j + 2 * i + 1];
-            if (r != 0.0f) {
-                const float2 r2 = make_float2(r, r);
-                a = __fmul2_rn(a, r2);
-                b = __fmul2_rn(b, r2);
-            } else {
-                a = make_float2(__fdiv_rn(a.x, s), __fdiv_rn(a.y, s));
-                b = make_float2(__fdiv_rn(b.x, s), __fdiv_rn(b.y, s));
-            }
+            const float2 a = __fmul2_rn(__fmul2_rn(v[8 * j + 2 * i], pre), r);
+            const float2 b = __fmul2_rn(__fmul2_rn(v[8 * j + 2 * i + 1], pre), r);
             w[i] = e4m3x2(a.x, a.y) | (e4m3x2(b.x, b.y) << 16);
         }
-        *reinterpret_cast<uint4 *>(dst + 16 * j) = make_uint4(w[0], w[1], w[2], w[3]);
+        if (kStage)
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                             stg + (uint32_t)(row * 64 + ((j ^ ((row >> 1) & 3)) << 4))),
+                         "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
+                         : "memory");
+        else
+            *reinterpret_cast<uint4 *>(dst + 16 * j) = make_uint4(w[0], w[1], w[2], w[3]);
     }
 }
 
 // Exchange buffer of MODE_GATED: per unit parity, column half and row, the thread's
-// maxima of g, u and a and whether its warp is still running.
+// maxima of g, u and a and whether its warp is still running.  A pair has in front of it
+// a staging buffer per epilogue warp for the codes of a, g and u (32 rows of 64 bytes
+// each), which leave by TMA stores.
 constexpr int XCH_BYTES = 2 * 2 * BM * 16;
+constexpr int CODE_STG_BYTES = 32 * 64;  // one warp's codes of one matrix
+
+// The gated mode's staging is beyond Cfg's (a pair: in place of it, and longer).
+template <int kMode, bool kPair>
+constexpr int EXTRA_BYTES = kMode != MODE_GATED ? 0
+                            : kPair ? NUM_EPI_WARPS * 3 * CODE_STG_BYTES + XCH_BYTES - Cfg<kPair>::STAGING
+                                    : XCH_BYTES + 16;
 
 template <int kMode, bool kPair>
-constexpr int smem_bytes()
-{
-    // a pair's output staging buffer holds the exchange (the codes are stored directly)
-    return Cfg<kPair>::SMEM_BYTES + (kMode == MODE_GATED && !kPair ? XCH_BYTES + 16 : 0);
-}
-static_assert(smem_bytes<MODE_GATED, false>() <= 232448, "shared memory budget");
-static_assert(Cfg<true>::STAGING >= XCH_BYTES, "the exchange fits the staging buffer");
+constexpr int SMEM_TOTAL = Cfg<kPair>::SMEM_BYTES + EXTRA_BYTES<kMode, kPair>;
+static_assert(SMEM_TOTAL<MODE_GATED, false> <= 232448 && SMEM_TOTAL<MODE_GATED, true> <= 232448,
+              "shared memory budget");
 
 template <int kMode, bool kBMajorMN, bool kPair>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
     k_gemm_block_scaled(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                        const __grid_constant__ CUtensorMap tmOut, const Params p)
+                        const __grid_constant__ CUtensorMap tmOut, const __grid_constant__ CUtensorMap tmOut2,
+                        const Params p)
 {
     pdl_begin();
     using Cf = Cfg<kPair>;
@@ -361,13 +361,15 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     const int unit_step = kPair ? (int)(gridDim.x >> 1) : (int)gridDim.x;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    constexpr int STAGING = Cf::STAGING + (kPair ? EXTRA_BYTES<kMode, kPair> : 0);
     uint8_t *staging = smem + STAGES * STAGE_BYTES;
-    float *ring = reinterpret_cast<float *>(smem + STAGES * STAGE_BYTES + Cf::STAGING);
-    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + STAGES * STAGE_BYTES + Cf::STAGING + RING_BYTES);
+    float *ring = reinterpret_cast<float *>(smem + STAGES * STAGE_BYTES + STAGING);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + STAGES * STAGE_BYTES + STAGING + RING_BYTES);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + NUM_BARS);
     volatile uint32_t *abort_flag = tmem_slot + 1;
     // (single CTA: behind the abort flag, on the next 16-byte boundary)
-    const uint32_t xch = kPair ? smem_u32(staging) : ((smem_u32(tmem_slot) + 8 + 15) & ~15u);
+    const uint32_t xch = kPair ? smem_u32(staging) + NUM_EPI_WARPS * 3 * CODE_STG_BYTES
+                               : ((smem_u32(tmem_slot) + 8 + 15) & ~15u);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t smem0 = smem_u32(smem);
@@ -419,8 +421,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     if (warp == 0 && lane == 0) {
         prefetch_tmap(&tmA);
         prefetch_tmap(&tmB);
-        if (kPair && !kGated && p.out_mode != OUT_F32_PARTIAL)
+        if (kPair && p.out_mode != OUT_F32_PARTIAL)
             prefetch_tmap(&tmOut);
+        if (kPair && kGated && p.guq)
+            prefetch_tmap(&tmOut2);
     }
     tc_fence_before();
     __syncthreads();
@@ -737,20 +741,46 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                 const float4 o = lds_v4(other);
                 ok = ok && o.w != 0.0f;
                 const int grow = mt * Cf::TILE_M + row_offset<kPair>() + row;
-                if (ok && grow < p.R) {
-                    const float sca = group_scale(fmaxf(ma, o.z));
-                    store_codes64(p.aq + (int64_t)grow * p.ldaq + col0, av, sca);
-                    if (h == 0)
-                        p.as[(int64_t)nt * p.ld_as + grow] = sca;
+                const bool row_ok = ok && grow < p.R;
+                const float sca = group_scale(fmaxf(ma, o.z));
+                const float scg = group_scale(fmaxf(mg, o.x)), scu = group_scale(fmaxf(mu, o.y));
+                if (row_ok && h == 0) {
+                    p.as[(int64_t)nt * p.ld_as + grow] = sca;
                     if (p.guq) {
-                        const float scg = group_scale(fmaxf(mg, o.x)), scu = group_scale(fmaxf(mu, o.y));
-                        uint8_t *dst = p.guq + (int64_t)grow * p.ldguq + col0;
-                        store_codes64(dst, &acc[0], scg);
-                        store_codes64(dst + p.C, &acc[32], scu);
-                        if (h == 0) {
-                            p.gus[(int64_t)nt * p.ld_gus + grow] = scg;
-                            p.gus[(int64_t)(p.n_tiles + nt) * p.ld_gus + grow] = scu;
+                        p.gus[(int64_t)nt * p.ld_gus + grow] = scg;
+                        p.gus[(int64_t)(p.n_tiles + nt) * p.ld_gus + grow] = scu;
+                    }
+                }
+                if constexpr (kPair) {
+                    // staged per warp (32 rows of 64 bytes a matrix), out by TMA: stores of
+                    // 16 bytes a thread straight to 32 rows left half of each sector unused
+                    // and held the warps; rows beyond R are clipped by the tensor maps
+                    const uint32_t stg = smem_u32(staging) + (uint32_t)((warp - FIRST_EPI_WARP) * 3 * CODE_STG_BYTES);
+                    const int y = mt * Cf::TILE_M + row_offset<kPair>() + q * 32;
+                    if (lane == 0)
+                        asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // buffer read out
+                    __syncwarp();
+                    store_codes64<true>(nullptr, stg, lane, av, sca);
+                    if (p.guq) {
+                        store_codes64<true>(nullptr, stg + CODE_STG_BYTES, lane, &acc[0], scg);
+                        store_codes64<true>(nullptr, stg + 2 * CODE_STG_BYTES, lane, &acc[32], scu);
+                    }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // generic writes -> TMA reads
+                    __syncwarp();
+                    if (lane == 0 && ok) {
+                        tma_store_2d(&tmOut, stg, col0, y);
+                        if (p.guq) {
+                            tma_store_2d(&tmOut2, stg + CODE_STG_BYTES, col0, y);
+                            tma_store_2d(&tmOut2, stg + 2 * CODE_STG_BYTES, p.C + col0, y);
                         }
+                        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+                    }
+                } else if (row_ok) {
+                    store_codes64<false>(p.aq + (int64_t)grow * p.ldaq + col0, 0, 0, av, sca);
+                    if (p.guq) {
+                        uint8_t *dst = p.guq + (int64_t)grow * p.ldguq + col0;
+                        store_codes64<false>(dst, 0, 0, &acc[0], scg);
+                        store_codes64<false>(dst + p.C, 0, 0, &acc[32], scu);
                     }
                 }
                 continue;
@@ -1035,6 +1065,26 @@ rlq_status encode_map(CUtensorMap *map, const uint8_t *base, int64_t inner, int6
     return RLQ_OK;
 }
 
+// E4M3 output [rows][cols], pitch ld bytes, for the gated mode's stores: box 64 columns
+// x 32 rows, 64-byte swizzle.
+rlq_status encode_codes_out_map(CUtensorMap *map, uint8_t *base, int64_t cols, int64_t rows, int64_t ld)
+{
+    auto enc = get_encode_fn();
+    if (!enc)
+        return fail(RLQ_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)ld};
+    const cuuint32_t box[2] = {64, 32};
+    const cuuint32_t estr[2] = {1, 1};
+    const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, base, dims, strides, box, estr,
+                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
+                           CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS)
+        return fail(RLQ_ERR_CUDA, "cuTensorMapEncodeTiled failed (CUresult %d) for the [%lld x %lld] code output",
+                    (int)r, (long long)rows, (long long)cols);
+    return RLQ_OK;
+}
+
 struct DevInfo {
     int sms = 0;
     bool attr_set[16] = {};
@@ -1113,7 +1163,7 @@ template <int kMode, bool kBMN, bool kPair>
 rlq_status launch_impl(const GemmArgs &a, int splits, cudaStream_t st, bool withhold_first_load = false)
 {
     using Cf = Cfg<kPair>;
-    CUtensorMap tmA, tmB, tmO;
+    CUtensorMap tmA, tmB, tmO, tmO2;
     rlq_status rs = encode_map(&tmA, a.A, a.L, a.R, a.lda, BM);
     if (rs != RLQ_OK)
         return rs;
@@ -1132,7 +1182,7 @@ rlq_status launch_impl(const GemmArgs &a, int splits, cudaStream_t st, bool with
     const int variant = kMode * 4 + (kBMN ? 2 : 0) + (kPair ? 1 : 0);
     auto kernel = k_gemm_block_scaled<kMode, kBMN, kPair>;
     if (!di.attr_set[variant]) {
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<kMode, kPair>());
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_TOTAL<kMode, kPair>);
         if (e != cudaSuccess)
             return cuda_status(e, "cudaFuncSetAttribute(max dynamic shared memory)");
         di.attr_set[variant] = true;
@@ -1148,7 +1198,7 @@ rlq_status launch_impl(const GemmArgs &a, int splits, cudaStream_t st, bool with
     attrs[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(NUM_THREADS, 1, 1);
-    cfg.dynamicSmemBytes = smem_bytes<kMode, kPair>();
+    cfg.dynamicSmemBytes = SMEM_TOTAL<kMode, kPair>;
     cfg.stream = st;
     cfg.attrs = attrs;
     cfg.numAttrs = kPair ? 2 : 1;
@@ -1200,11 +1250,18 @@ rlq_status launch_impl(const GemmArgs &a, int splits, cudaStream_t st, bool with
     p.num_units = p.num_tiles * p.splits;
     p.ws = p.splits > 1 ? a.ws : nullptr;
     p.out_mode = p.splits > 1 ? OUT_F32_PARTIAL : (a.acc ? OUT_F32_ACC : OUT_BF16);
-    if (kPair && p.out_mode == OUT_F32_ACC) {
+    tmO2 = tmA;  // read by the gated mode only
+    if (kPair && kGated) {
+        rs = encode_codes_out_map(&tmO, a.aq, a.C, a.R, a.ldaq);
+        if (rs == RLQ_OK && a.guq)
+            rs = encode_codes_out_map(&tmO2, a.guq, 2 * a.C, a.R, a.ldguq);
+        if (rs != RLQ_OK)
+            return rs;
+    } else if (kPair && p.out_mode == OUT_F32_ACC) {
         rs = encode_acc_map(&tmO, a.acc, a.C, a.R, a.ld_acc);
         if (rs != RLQ_OK)
             return rs;
-    } else if (kPair && !kGated && p.out_mode == OUT_BF16) {
+    } else if (kPair && p.out_mode == OUT_BF16) {
         rs = encode_out_map(&tmO, a.out, a.C, a.R, a.ldo);
         if (rs != RLQ_OK)
             return rs;
@@ -1217,7 +1274,7 @@ rlq_status launch_impl(const GemmArgs &a, int splits, cudaStream_t st, bool with
     } else {
         cfg.gridDim = dim3(p.num_units < di.sms ? p.num_units : di.sms, 1, 1);
     }
-    e = cudaLaunchKernelEx(&cfg, kernel, tmA, tmB, tmO, p);
+    e = cudaLaunchKernelEx(&cfg, kernel, tmA, tmB, tmO, tmO2, p);
     if (e == cudaSuccess)
         e = cudaGetLastError();
     if (e != cudaSuccess || p.splits == 1)

@@ -71,7 +71,7 @@ def test_gated_backward_refusals():
     #     da  ldda guq  ldguq gus ldgus q   ldq  s   lds qT  ldqT sc  ldsc aT  ldaT ac  ldac M  F  stream
     ok = (FAKE, 128, FAKE, 256, FAKE, 4, FAKE, 256, FAKE, 4, FAKE, 16, FAKE, 256, FAKE, 16, FAKE, 128, 4, 128, None)
     refusals(rlq.rlq_gated_backward, ok, [
-        ({18: -1}, INVALID), ({19: 64}, UNSUPPORTED), ({19: 128 * 65536}, UNSUPPORTED), ({0: None}, INVALID),
+        ({18: -1}, INVALID), ({19: 64}, UNSUPPORTED), ({19: 1 << 30}, UNSUPPORTED), ({0: None}, INVALID),
         ({1: 120}, INVALID), ({2: FAKE + 1}, MISALIGNED), ({3: 128}, INVALID), ({5: 3}, INVALID), ({6: None}, INVALID),
         ({7: 240}, INVALID), ({9: 3}, INVALID), ({10: None}, INVALID), ({11: 20}, MISALIGNED), ({13: 255}, INVALID),
         ({14: None}, INVALID), ({15: 2}, INVALID), ({16: None}, INVALID), ({17: 127}, INVALID)])

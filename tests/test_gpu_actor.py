@@ -530,3 +530,24 @@ def test_another_stream_and_a_graph():
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, want))
     rlq.check()
+
+
+@pytest.mark.parametrize("scale", [1e-30, 1e-38])
+def test_gated_backward_tiny_gradients(scale):
+    """Groups whose scales are subnormal (their reciprocals overflow) beside ordinary ones."""
+    g = gen(6)
+    M, F = 150, 256
+    guq, gus = R.quant_rows(normal(g, M, 2 * F))
+    da = normal(g, M, F).float()
+    da[:, 128:] *= scale
+    da[128:, :128] *= scale
+    da = da.to(torch.bfloat16)
+    q, s, qT, sc, aT, ac = rlq.gated_backward(da, guq, gus)
+    dg, du, a, edg, edu, ea = gate_reference(da, guq, gus)
+    # products and scales below the normal range round to a multiple of 2^-149, a scale
+    # counting 448 of them
+    tiny = 4 * 448 * 2.0 ** -149
+    d, e = torch.cat((dg, du), 1), torch.cat((edg, edu), 1) + tiny
+    R.check_rows(q, s, d, e, "rows")
+    R.check_cols(qT, sc, d, e, "columns")
+    R.check_cols(aT, ac, a, ea, "a's columns")
