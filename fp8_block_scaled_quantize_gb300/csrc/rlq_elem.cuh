@@ -89,18 +89,24 @@ __device__ __forceinline__ uint2 encode8f(const float (&v)[8], float s, float rc
     return encode8f(f, scale_pre(s), rcp);
 }
 
+// max(|a|, |b|, |c|) in one instruction.
+__device__ __forceinline__ float max3_abs(float a, float b, float c)
+{
+    float d;
+    asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
 __device__ __forceinline__ float max_abs8(const float2 (&v)[4])
 {
-    const float a = fmaxf(fmaxf(fabsf(v[0].x), fabsf(v[0].y)), fmaxf(fabsf(v[1].x), fabsf(v[1].y)));
-    const float b = fmaxf(fmaxf(fabsf(v[2].x), fabsf(v[2].y)), fmaxf(fabsf(v[3].x), fabsf(v[3].y)));
-    return fmaxf(a, b);
+    const float a = max3_abs(v[0].x, v[0].y, v[1].x), b = max3_abs(v[1].y, v[2].x, v[2].y);
+    return max3_abs(max3_abs(a, v[3].x, v[3].y), b, b);
 }
 
 __device__ __forceinline__ float max_abs8(const float (&v)[8])
 {
-    const float a = fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));
-    const float b = fmaxf(fmaxf(fabsf(v[4]), fabsf(v[5])), fmaxf(fabsf(v[6]), fabsf(v[7])));
-    return fmaxf(a, b);
+    const float a = max3_abs(v[0], v[1], v[2]), b = max3_abs(v[3], v[4], v[5]);
+    return max3_abs(max3_abs(a, v[6], v[7]), b, b);
 }
 
 // 1 / (1 + exp(-g)) of two values, the exponential and the reciprocal on the

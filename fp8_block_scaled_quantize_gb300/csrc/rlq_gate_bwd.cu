@@ -85,13 +85,6 @@ __device__ __forceinline__ void decode8(uint2 c, float s, float2 (&f)[4])
     }
 }
 
-// |running maximum| of two values.
-__device__ __forceinline__ void max2(float2 &m, float2 v)
-{
-    m.x = fmaxf(m.x, fabsf(v.x));
-    m.y = fmaxf(m.y, fabsf(v.y));
-}
-
 // Persistent, one CTA per SM, 128 x 128 tiles of [M, F], row block fastest.  Thread t
 // has rows 4 (t / 16) .. + 3 and columns 8 (t % 16) .. + 7 of a tile, all of it in
 // registers; it copies its own part of the next tile to shared memory meanwhile.  A
@@ -114,21 +107,24 @@ __global__ void __launch_bounds__(THREADS, 1) k_gate_bwd(const GateBwd p)
 
     auto prefetch = [&](int tile, int buf) {
         const int mt = tile % p.m_tiles, ft = tile / p.m_tiles;
-        const int64_t m0 = (int64_t)mt * GRP, f = (int64_t)ft * GRP + 8 * cg;
-        const uint32_t in = smem0 + buf * IN_BYTES;
+        const int64_t m = (int64_t)mt * GRP + 4 * rg, f = (int64_t)ft * GRP + 8 * cg;
+        const int left = (int)(p.M - m < 4 ? p.M - m : 4);  // rows of mine inside the matrix (may be <= 0)
+        const uint16_t *ap = p.da + m * p.ldda + f;
+        const uint8_t *gp = p.guq + m * p.ldguq + f;
+        const uint32_t in = smem0 + buf * IN_BYTES + t * 16, in8 = smem0 + buf * IN_BYTES + THREADS * 64 + t * 8;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const bool ok = m0 + 4 * rg + i < p.M;
-            const int64_t m = ok ? m0 + 4 * rg + i : 0;
-            const uint8_t *gp = p.guq + m * p.ldguq + f;
-            copy16(in + (i * THREADS + t) * 16, p.da + m * p.ldda + f, ok ? 16 : 0);
-            copy8(in + THREADS * 64 + (i * THREADS + t) * 8, gp, ok ? 8 : 0);
-            copy8(in + THREADS * 96 + (i * THREADS + t) * 8, gp + p.F, ok ? 8 : 0);
+            const bool ok = i < left;
+            copy16(in + i * THREADS * 16, ok ? ap : p.da, ok ? 16 : 0);
+            copy8(in8 + i * THREADS * 8, ok ? gp : p.guq, ok ? 8 : 0);
+            copy8(in8 + THREADS * 32 + i * THREADS * 8, ok ? gp + p.F : p.guq, ok ? 8 : 0);
+            ap += p.ldda;
+            gp += p.ldguq;
         }
-        if (t < 2 * GRP) {
-            const bool ok = m0 + (t & 127) < p.M;
-            copy4(smem0 + OFF_SCALES + (buf * 2 * GRP + t) * 4,
-                  p.gus + ((t >> 7) * fb + ft) * p.ld_gus + (ok ? m0 + (t & 127) : 0), ok ? 4 : 0);
+        if (cg < 8) {  // this half-warp's scales: four rows of g, four of u
+            const bool ok = (cg & 3) < left;
+            copy4(smem0 + OFF_SCALES + (buf * 2 * GRP + 8 * rg + cg) * 4,
+                  ok ? p.gus + ((cg >> 2) * fb + ft) * p.ld_gus + m + (cg & 3) : p.gus, ok ? 4 : 0);
         }
     };
 
@@ -141,21 +137,18 @@ __global__ void __launch_bounds__(THREADS, 1) k_gate_bwd(const GateBwd p)
             prefetch(tile + gridDim.x, buf ^ 1);
         asm volatile("cp.async.commit_group;" ::: "memory");
         asm volatile("cp.async.wait_group 1;" ::: "memory");
-        __syncthreads();  // this tile's scales are there; the last tile's codes have left shared memory
+        // A thread reads what its half-warp copied.  The last tile's codes may still be
+        // leaving: shared memory that they use is written after the next barrier only.
+        __syncwarp();
         const int mt = tile % p.m_tiles, ft = tile / p.m_tiles;
         const int64_t m0 = (int64_t)mt * GRP, f0 = (int64_t)ft * GRP;
         const int rows = (int)(p.M - m0 < GRP ? p.M - m0 : GRP);
         const uint8_t *in = smem + buf * IN_BYTES;
-        const float *scl = reinterpret_cast<const float *>(smem + OFF_SCALES) + buf * 2 * GRP + 4 * rg;
-        const float4 gs4 = *reinterpret_cast<const float4 *>(scl), us4 = *reinterpret_cast<const float4 *>(scl + GRP);
+        const float *scl = reinterpret_cast<const float *>(smem + OFF_SCALES) + buf * 2 * GRP + 8 * rg;
+        const float4 gs4 = *reinterpret_cast<const float4 *>(scl), us4 = *reinterpret_cast<const float4 *>(scl + 4);
         const float sg4[4] = {gs4.x, gs4.y, gs4.z, gs4.w}, su4[4] = {us4.x, us4.y, us4.z, us4.w};
         float2 val[3][4][4], cmax[3][4];  // dg, du, a of [row][column pair]
         float v[8];
-#pragma unroll
-        for (int k = 0; k < 3; ++k)
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                cmax[k][j] = make_float2(0.0f, 0.0f);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             float2 g[4], u[4];
@@ -172,13 +165,18 @@ __global__ void __launch_bounds__(THREADS, 1) k_gate_bwd(const GateBwd p)
                 val[0][i][j] = __fmul2_rn(__fmul2_rn(d, u[j]), __ffma2_rn(gs, om, sg));
                 val[1][i][j] = __fmul2_rn(d, gs);
                 val[2][i][j] = __fmul2_rn(gs, u[j]);
-#pragma unroll
-                for (int k = 0; k < 3; ++k)
-                    max2(cmax[k][j], val[k][i][j]);
             }
             v[i] = max_abs8(val[0][i]);
             v[4 + i] = max_abs8(val[1][i]);
         }
+#pragma unroll
+        for (int k = 0; k < 3; ++k)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float2 m = make_float2(max3_abs(val[k][0][j].x, val[k][1][j].x, val[k][2][j].x),
+                                             max3_abs(val[k][0][j].y, val[k][1][j].y, val[k][2][j].y));
+                cmax[k][j] = make_float2(fmaxf(m.x, fabsf(val[k][3][j].x)), fmaxf(m.y, fabsf(val[k][3][j].y)));
+            }
         // the halves of a warp exchange: the lower keeps columns 0-3 of its eight, the upper 4-7
 #pragma unroll
         for (int k = 0; k < 3; ++k) {

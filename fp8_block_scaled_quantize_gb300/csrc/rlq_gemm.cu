@@ -285,9 +285,9 @@ __device__ __forceinline__ float amax32(const float2 *v)
 {
     float a = 0.0f, b = 0.0f;
 #pragma unroll
-    for (int j = 0; j < 32; ++j) {
-        a = fmaxf(a, fabsf(v[j].x));
-        b = fmaxf(b, fabsf(v[j].y));
+    for (int j = 0; j < 32; j += 2) {
+        a = max3_abs(a, v[j].x, v[j].y);
+        b = max3_abs(b, v[j + 1].x, v[j + 1].y);
     }
     return fmaxf(a, b);
 }
