@@ -551,3 +551,22 @@ def test_gated_backward_tiny_gradients(scale):
     R.check_rows(q, s, d, e, "rows")
     R.check_cols(qT, sc, d, e, "columns")
     R.check_cols(aT, ac, a, ea, "a's columns")
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T,V,pitch,offset", [(6000, 515, 2, 1), (700, 33001, 1, 3), (300, 100001, 0, 0)])
+def test_policy_loss_many_rows(T, V, pitch, offset, dtype):
+    """More rows than are resident at once, cut units at different places from row to row,
+    runs of empty rows."""
+    st = loss_inputs(T, V, dtype, T + V, pitch, offset)
+    st["weight"][T // 3: T // 3 + 40] = 0
+    st["targets"][T // 2: T // 2 + 9] = -1
+    check_loss(st)
+    lp, lse = rlq.token_logprobs(st["logits"], st["targets"], temperature=0.9)
+    assert torch.equal(lp, rlq.token_logprobs(st["logits"], st["targets"], temperature=0.9)[0])
+    keep = st["targets"] >= 0
+    z = st["logits"].to(D) / 0.9
+    want = torch.log_softmax(z, 1).gather(1, st["targets"].clamp(min=0)[:, None])[:, 0]
+    drop = z.amax(1) - z.gather(1, st["targets"].clamp(min=0)[:, None])[:, 0]
+    assert bool(((lp.to(D) - want).abs() <= 156 * U + 6 * U * (drop + want.abs()))[keep].all())
+    assert bool((lp[~keep] == 0).all()) and bool((lse[~keep] == 0).all())
