@@ -10,14 +10,13 @@
 //   dlogits_v = dloss/dlp (1[v = t] - softmax(z)_v) / temperature
 //
 // Bound by memory: the logits are read once and the gradient written once.  A row is
-// held on chip by one CTA, or by a cluster of 2, 4 or 8 for long rows: a persistent
-// cluster copies its next rows to shared memory (bulk copies, up to three rows ahead)
-// while it works on one.  A thread takes its part of the row into registers, its
-// maximum and the sum of its exponentials; behind one cluster barrier per row the first
-// warp of each CTA joins all warps' (maximum, sum) pairs, read from the CTAs' shared
-// memory, and publishes the row's factors, and every warp writes its part of the
-// gradient.  The gradient may overwrite the logits: a row is read whole before any of
-// it is written.
+// held on chip by one CTA, or by a cluster of 2, 4 or 8 for long rows.  Persistent
+// CTAs: one warp copies the next rows to shared memory (bulk copies), another joins the
+// reducing warps' (maximum, sum) pairs of a row across the cluster and publishes the
+// row's factors, while those warps already reduce the next row; they write a row's
+// gradient after that.  So a row's chain of latencies (cluster barrier, remote reads, logarithm
+// and exponentials) lies beside the work on its neighbours.  The gradient may overwrite
+// the logits: a row is read whole before any of it is written.
 #include <cuda_runtime.h>
 
 #include <mutex>
@@ -182,7 +181,7 @@ __device__ __noinline__ void store_edge(T *dx, int e0, int V, uint4 v)
 
 constexpr int MAX_BUFS = 3;
 constexpr int MAX_CLUSTER = 8;
-constexpr int MAX_WARPS = 16;
+constexpr int MAX_WARPS = 16;  // that reduce, beside the joining and the copying warp
 
 struct RowsPlan {
     int csize;      // CTAs of a cluster (of a row)
@@ -194,12 +193,18 @@ struct RowsPlan {
 // A persistent cluster takes rows cluster, cluster + clusters, ...  Units are a row's
 // 16-byte pieces on 16-byte boundaries: unit u covers elements u N - off .. + N - 1, off
 // being the elements by which the row starts past a boundary.  The CTA of rank c takes
-// units c units_cta .. (c + 1) units_cta - 1, thread t of it units t + i * blockDim.x, i < NV.
-// Whole units come by bulk copy; a unit that the row's start or end cuts is put into
-// shared memory by a thread of the last warp, the missing elements as -inf.  Empty rows
-// are not copied, so buffers and their phases go by the count of live rows.
-template <typename T, int NV, int kThreads>
-__global__ void __launch_bounds__(kThreads, kThreads <= 256 ? 2 : 1)
+// units c units_cta .. (c + 1) units_cta - 1, thread t of its reducing warps units t,
+// t + threads, ... of those.  Whole units come by bulk copy; a unit that the row's start or
+// end cuts is put into shared memory by the copying warp, the missing elements as -inf.
+// Empty rows are not copied, so buffers and phases go by the count of live rows.
+//
+// Per live row L, the reducing warps reduce L, then write the gradient of L - 1 (with a
+// single buffer: of L); the joining warp joins L and publishes its factors; the copying
+// warp copies the row bufs - 1 (or 1) ahead, whose buffer's last row was at most L - 1
+// (or L) and is released by the reducing warps without its doing.  All warps of a
+// cluster meet in one hardware barrier per live row, behind which L's pairs are there.
+template <typename T, int kThreads>
+__global__ void __launch_bounds__(kThreads, kThreads <= 320 ? 2 : 1)
     k_policy_rows(const PolicyLossArgs p, const RowsPlan plan)
 {
     pdl_begin();
@@ -208,206 +213,156 @@ __global__ void __launch_bounds__(kThreads, kThreads <= 256 ? 2 : 1)
     extern __shared__ __align__(128) uint8_t data[];  // [bufs][units_cta] units
     // by the parity of the live row: this CTA's warps' pairs, the row's factors
     __shared__ __align__(16) float2 pairs[2][MAX_WARPS];
-    // Barriers: a buffer's row is there (one arrival by its copier, one by the warp that
-    // fills in cut units); the row's factors are there
-    __shared__ __align__(8) uint64_t bars[MAX_BUFS], coef_bars[2];
     __shared__ float4 coef[2];  // -dz / sum, the maximum, dz
+    // Barriers: a buffer's row is there (one arrival by the copy, one by the cut units),
+    // a buffer is free (each reducing warp), the pairs are there (a single CTA; a cluster
+    // has its hardware barrier), the factors are there
+    __shared__ __align__(8) uint64_t full_bars[MAX_BUFS], empty_bars[MAX_BUFS], pair_bars[2], coef_bars[2];
     __shared__ uint32_t abort_word;
     volatile uint32_t *abort_flag = &abort_word;
-    const int csize = plan.csize, cap = plan.units_cta, bufs = plan.bufs;
+    const int csize = plan.csize, cap = plan.units_cta, bufs = plan.bufs, lag = bufs > 1 ? 1 : 0;
     const int64_t clusters = gridDim.x / csize, first = blockIdx.x / csize;
     const int rank = (int)(blockIdx.x - first * csize);
-    const int t = threadIdx.x, lane = t & 31, warp = t >> 5, nw = blockDim.x >> 5;
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5, nw = (blockDim.x >> 5) - 2;
     const int V = (int)p.V, u0 = rank * cap;
-    const uint32_t data0 = smem_u32(data);
     const T *logits = reinterpret_cast<const T *>(p.logits);
     const float c = 1.4426950408889634f / p.temperature;
     const float2 c2 = make_float2(c, c);
 
     auto live_row = [&](int64_t target, float weight) { return target >= 0 && target < V && weight != 0.0f; };
     auto offset = [&](const T *x) { return (int)((reinterpret_cast<uintptr_t>(x) & 15) / sizeof(T)); };
-    // copies this CTA's whole units of a row (one thread)
-    auto issue = [&](int64_t row, int buf) {
-        const T *x = logits + row * p.ld;
-        const int off = offset(x);
-        const int a = max(u0, off ? 1 : 0), b = min(u0 + cap, (off + V) / N);
-        const uint32_t bytes = b > a ? (uint32_t)(b - a) * 16u : 0u;
-        mbar_arrive_expect_tx(smem_u32(&bars[buf]), bytes);
-        if (bytes)
-            bulk_load(data0 + (uint32_t)(buf * cap + a - u0) * 16u, x + ((int64_t)a * N - off), bytes,
-                      smem_u32(&bars[buf]));
-    };
-    // the unit that this lane of the last warp fills in: the row's first where it is cut
-    // (lane 0), its last where it is cut (lane 1; the same unit of a very short row is
-    // lane 0's); -1: none here
-    auto edge_unit = [&](const T *x) {
-        const int off = offset(x), last = (off + V) / N;  // the first unit not wholly before the row's end
-        const bool cut0 = off != 0, cut1 = (off + V) % N != 0;
-        int u = -1;
-        if (lane == 0 && cut0)
-            u = 0;
-        else if (lane == 1 && cut1 && !(cut0 && last == 0))
-            u = last;
-        return u >= u0 && u < u0 + cap ? u : -1;
+    // A wait that runs out is reported by rlq_check; its warp goes on, without waiting any
+    // more, so that the cluster's CTAs end together.
+    auto wait = [&](uint64_t *bar, int phase) {
+        if (!*abort_flag)
+            mbar_wait(smem_u32(bar), (uint32_t)phase & 1u, abort_flag, plan.timeout_ns, SITE_LOSS_ROW);
+        __syncwarp();
     };
 
     if (t == 0) {
-        for (int b = 0; b < bufs; ++b)
-            mbar_init(smem_u32(&bars[b]), 2);
-        for (int b = 0; b < 2; ++b)
+        for (int b = 0; b < bufs; ++b) {
+            mbar_init(smem_u32(&full_bars[b]), 2);
+            mbar_init(smem_u32(&empty_bars[b]), nw);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(smem_u32(&pair_bars[b]), nw);
             mbar_init(smem_u32(&coef_bars[b]), 1);
+        }
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
     __syncthreads();
-    // The rows ahead: row index, and the count of live rows in front of it.
-    int64_t ahead = first;
-    int ahead_live = 0;
-    for (int b = 0; b < bufs && ahead < p.rows; ++b, ahead += clusters) {
-        if (!live_row(p.targets[ahead], p.weight ? p.weight[ahead] : 1.0f))
-            continue;
-        if (t == 0)
-            issue(ahead, ahead_live % bufs);
-        if (warp == nw - 1) {
+
+    int64_t target = p.targets[first];
+    float weight = p.weight ? p.weight[first] : 1.0f;
+    int nlive = 0;  // live rows so far
+    if (warp == nw + 1) {
+        // -------------------------------------------------- copying warp ---
+        int64_t ahead = first;
+        int ahead_live = 0;
+        // copies this CTA's part of row `ahead` into its buffer, if it is live
+        auto refill = [&](int64_t tg, float w) {
+            if (ahead >= p.rows || !live_row(tg, w))
+                return;
+            const int buf = ahead_live % bufs, use = ahead_live / bufs;
+            if (use > 0)
+                wait(&empty_bars[buf], use - 1);
             const T *x = logits + ahead * p.ld;
-            const int u = edge_unit(x);
-            if (u >= 0) {
+            const int off = offset(x), last = (off + V) / N;  // the first unit not wholly before the row's end
+            uint4 *dst = reinterpret_cast<uint4 *>(data) + buf * cap;
+            if (lane == 0) {
+                const int a = max(u0, off ? 1 : 0), b = min(u0 + cap, last);
+                const uint32_t bytes = b > a ? (uint32_t)(b - a) * 16u : 0u;
+                mbar_arrive_expect_tx(smem_u32(&full_bars[buf]), bytes);
+                if (bytes)
+                    bulk_load(smem_u32(dst + a - u0), x + ((int64_t)a * N - off), bytes, smem_u32(&full_bars[buf]));
+            }
+            // cut units: the row's first (lane 0) and last (lane 1; lane 0's if it is the same)
+            int u = -1;
+            if (lane == 0 && off != 0)
+                u = 0;
+            else if (lane == 1 && (off + V) % N != 0 && !(off != 0 && last == 0))
+                u = last;
+            if (u >= u0 && u < u0 + cap) {
                 T raw[N];
-                load_edge(x, u * N - offset(x), V, raw);
-                reinterpret_cast<uint4 *>(data)[(ahead_live % bufs) * cap + u - u0] = join_edge<T>(raw);
+                load_edge(x, u * N - off, V, raw);
+                dst[u - u0] = join_edge<T>(raw);
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             }
             __syncwarp();
             if (lane == 0)
-                mbar_arrive(smem_u32(&bars[ahead_live % bufs]));
-        }
-        ++ahead_live;
-    }
-
-    int64_t target = 0;
-    float weight = 0.0f;
-    if (first < p.rows) {
-        target = p.targets[first];
-        weight = p.weight ? p.weight[first] : 1.0f;
-    }
-    int nlive = 0;  // live rows so far
-    for (int64_t row = first; row < p.rows; row += clusters, ahead += clusters) {
-        const T *x = logits + row * p.ld;
-        T *dx = p.dlogits ? reinterpret_cast<T *>(p.dlogits) + row * p.ldd : nullptr;
-        const int off = offset(x), u1 = min(u0 + cap, (off + V + N - 1) / N);
-        // the gradient's rows share the logits' 16-byte phase: whole units leave as one store
-        const bool vec_out = dx && ((reinterpret_cast<uintptr_t>(dx) ^ reinterpret_cast<uintptr_t>(x)) & 15) == 0;
-        auto store = [&](int u, const float2(&f)[N / 2]) {
-            const int e0 = u * N - off;
-            if (vec_out && e0 >= 0 && e0 + N <= V)
-                *reinterpret_cast<uint4 *>(dx + e0) = E::pack(f);
-            else
-                store_edge(dx, e0, V, E::pack(f));
+                mbar_arrive(smem_u32(&full_bars[buf]));
+            ++ahead_live;
         };
-        const int64_t tgt = target;
-        const bool live = live_row(target, weight);
-        // what the next iteration and the copies ahead need, loaded early
-        if (row + clusters < p.rows) {
-            target = p.targets[row + clusters];
-            weight = p.weight ? p.weight[row + clusters] : 1.0f;
-        }
-        int64_t ahead_target = -1;
-        float ahead_weight = 1.0f;
-        if (ahead < p.rows) {
-            ahead_target = p.targets[ahead];
-            ahead_weight = p.weight ? p.weight[ahead] : 1.0f;
-        }
-        if (!live) {
-            if (rank == 0 && t == 0) {
-                p.lp[row] = 0.0f;
-                if (p.lse)
-                    p.lse[row] = 0.0f;
-                if (p.loss)
-                    p.loss[row] = 0.0f;
+        for (int b = 0; b < bufs - lag && ahead < p.rows; ++b, ahead += clusters)
+            refill(p.targets[ahead], p.weight ? p.weight[ahead] : 1.0f);
+        for (int64_t row = first; row < p.rows; row += clusters, ahead += clusters) {
+            const bool live = live_row(target, weight);
+            // what the next iteration and the refill need, loaded early
+            if (row + clusters < p.rows) {
+                target = p.targets[row + clusters];
+                weight = p.weight ? p.weight[row + clusters] : 1.0f;
             }
-            if (dx) {
-                float2 z[N / 2];
-#pragma unroll
-                for (int j = 0; j < N / 2; ++j)
-                    z[j] = make_float2(0.0f, 0.0f);
-                for (int u = u0 + t; u < u1; u += blockDim.x)
-                    store(u, z);
+            int64_t ahead_target = -1;
+            float ahead_weight = 1.0f;
+            if (ahead < p.rows) {
+                ahead_target = p.targets[ahead];
+                ahead_weight = p.weight ? p.weight[ahead] : 1.0f;
             }
+            if (live && csize > 1) {
+                cluster_arrive();
+                cluster_wait();
+            }
+            refill(ahead_target, ahead_weight);
         }
-        const int par = nlive & 1;
-        const uint32_t pph = (uint32_t)(nlive >> 1) & 1u;
-        uint4 v[NV];
+    } else if (warp == nw) {
+        // -------------------------------------------------- joining warp ---
+        // A row's inputs are loaded while the row before is joined.
         float xt = 0.0f;
         RowInputs in = {};
-        if (live) {
-            if (warp == 0) {
-                xt = E::load(x + tgt);  // before any CTA of the cluster writes the row (below)
-                if (p.adv) {
-                    in.old = p.lp_old[row];
-                    in.adv = p.adv[row];
-                    in.weight = p.weight[row];
-                    in.behav = p.lp_behav ? p.lp_behav[row] : 0.0f;
-                    in.ref = p.lp_ref ? p.lp_ref[row] : 0.0f;
-                    in.hi = p.clip_hi ? p.clip_hi[row] : 1.0f + p.eps_hi;
-                }
+        auto load_inputs = [&](int64_t row) {
+            if (row >= p.rows || !live_row(target, weight))
+                return;
+            xt = E::load(logits + row * p.ld + target);
+            if (p.adv) {
+                in.old = p.lp_old[row];
+                in.adv = p.adv[row];
+                in.weight = weight;
+                in.behav = p.lp_behav ? p.lp_behav[row] : 0.0f;
+                in.ref = p.lp_ref ? p.lp_ref[row] : 0.0f;
+                in.hi = p.clip_hi ? p.clip_hi[row] : 1.0f + p.eps_hi;
             }
-            const int buf = nlive % bufs;
-            // (a wait that runs out is reported by rlq_check; the loop goes on, without
-            // waiting, so that the cluster's CTAs end together)
-            if (!*abort_flag)
-                mbar_wait(smem_u32(&bars[buf]), (uint32_t)(nlive / bufs) & 1u, abort_flag, plan.timeout_ns,
-                          SITE_LOSS_ROW);
-            const uint4 *src = reinterpret_cast<const uint4 *>(data) + buf * cap;
-            float m = -INFINITY;
-#pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const int u = t + i * (int)blockDim.x;
-                constexpr uint32_t ninf = sizeof(T) == 2 ? 0xFF80FF80u : 0xFF800000u;
-                v[i] = u0 + u < u1 ? src[u] : make_uint4(ninf, ninf, ninf, ninf);
-                m = E::max_of(m, v[i]);
+        };
+        load_inputs(first);
+        for (int64_t row = first; row < p.rows; row += clusters) {
+            const bool live = live_row(target, weight);
+            if (row + clusters < p.rows) {
+                target = p.targets[row + clusters];
+                weight = p.weight ? p.weight[row + clusters] : 1.0f;
             }
-            // a part that is all -inf sums zeros against any finite maximum
-            const float mm = m == -INFINITY ? 0.0f : m;
-            const float2 nm2 = make_float2(-mm, -mm);
-            float2 sum = make_float2(0.0f, 0.0f);
-#pragma unroll
-            for (int i = 0; i < NV; ++i)
-#pragma unroll
-                for (int j = 0; j < N / 2; ++j) {
-                    const float2 f = __fmul2_rn(__fadd2_rn(E::get2(v[i], j), nm2), c2);
-                    sum = __fadd2_rn(sum, make_float2(ex2(f.x), ex2(f.y)));
+            if (!live) {
+                if (rank == 0 && lane == 0) {
+                    p.lp[row] = 0.0f;
+                    if (p.lse)
+                        p.lse[row] = 0.0f;
+                    if (p.loss)
+                        p.loss[row] = 0.0f;
                 }
-            float S = sum.x + sum.y, wm = m;
-#pragma unroll
-            for (int o = 16; o; o >>= 1)
-                wm = fmaxf(wm, __shfl_xor_sync(0xFFFFFFFFu, wm, o));
-            S = S == 0.0f ? 0.0f : S * ex2((m - wm) * c);
-#pragma unroll
-            for (int o = 16; o; o >>= 1)
-                S += __shfl_xor_sync(0xFFFFFFFFu, S, o);
-            // A NaN target makes the sum NaN whichever warp holds it; this also has the
-            // first warp's arrival, and so any write to the row, wait for the load of xt.
-            if (warp == 0 && xt != xt)
-                S = xt;
-            if (lane == 0)
-                pairs[par][warp] = make_float2(wm, S);
-            __syncwarp();
-            // The pairs of this parity are written again two rows on, behind the next
-            // row's barrier, which the warps that read them reach afterwards.
-            if (csize > 1)
+                load_inputs(row + clusters);
+                continue;
+            }
+            const int par = nlive & 1;
+            // (the vote has the arrival, and so any write to the row, wait for the load of xt)
+            const float x_t = xt;
+            const RowInputs now = in;
+            const bool nan_target = __any_sync(0xFFFFFFFFu, x_t != x_t);
+            if (csize > 1) {
                 cluster_arrive();
-            else
-                __syncthreads();
-        }
-        const bool more = live_row(ahead_target, ahead_weight);
-        if (live && csize > 1)
-            cluster_wait();
-        // Behind the barrier every warp has its part of the row in registers: the row's
-        // buffer takes a later one.  (An empty row's: the last live row's is free since then.)
-        if (more && t == 0)
-            issue(ahead, ahead_live % bufs);
-        if (warp == 0 && live) {
+                cluster_wait();
+            } else {
+                wait(&pair_bars[par], nlive >> 1);
+            }
             float2 o[MAX_CLUSTER * MAX_WARPS / 32];
             float gm = -INFINITY, G = 0.0f;
 #pragma unroll
@@ -417,8 +372,11 @@ __global__ void __launch_bounds__(kThreads, kThreads <= 256 ? 2 : 1)
                 o[k] = make_float2(-INFINITY, 0.0f);
                 if (r < csize && w < nw)
                     o[k] = csize > 1 ? ld_cluster2(smem_u32(&pairs[par][w]), r) : pairs[par][w];
-                gm = fmaxf(gm, o[k].x);
             }
+            load_inputs(row + clusters);
+#pragma unroll
+            for (int k = 0; k < MAX_CLUSTER * MAX_WARPS / 32; ++k)
+                gm = fmaxf(gm, o[k].x);
 #pragma unroll
             for (int k = 16; k; k >>= 1)
                 gm = fmaxf(gm, __shfl_xor_sync(0xFFFFFFFFu, gm, k));
@@ -429,7 +387,9 @@ __global__ void __launch_bounds__(kThreads, kThreads <= 256 ? 2 : 1)
 #pragma unroll
             for (int k = 16; k; k >>= 1)
                 G += __shfl_xor_sync(0xFFFFFFFFu, G, k);
-            const RowScalars r = row_scalars(p, in, gm, G, xt, c);
+            if (nan_target)
+                G = x_t;
+            const RowScalars r = row_scalars(p, now, gm, G, x_t, c);
             if (lane == 0) {
                 const float dz = r.dlp / p.temperature;
                 // -dz * softmax; an empty row's probabilities are 0
@@ -443,32 +403,36 @@ __global__ void __launch_bounds__(kThreads, kThreads <= 256 ? 2 : 1)
                         p.loss[row] = r.loss;
                 }
             }
-        }
-        if (live && dx) {
-            if (!*abort_flag)
-                mbar_wait(smem_u32(&coef_bars[par]), pph, abort_flag, plan.timeout_ns, SITE_LOSS_ROW);
             __syncwarp();
+            ++nlive;
         }
-        T raw[N];
-        int eu = -1;
-        if (more && warp == nw - 1) {
-            const T *xa = logits + ahead * p.ld;
-            eu = edge_unit(xa);
-            if (eu >= 0)
-                load_edge(xa, eu * N - offset(xa), V, raw);
-        }
-        if (live && dx) {
-            const float4 k4 = coef[par];
-            const float2 f2 = make_float2(k4.x, k4.x), ng2 = make_float2(-k4.y, -k4.y);
-            const int te = (int)tgt + off, ut = te / N, jt = te - ut * N;
-#pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const int u = u0 + t + i * (int)blockDim.x;
-                if (u < u1) {
+    } else {
+        // ---------------------------------------------- reducing warps ---
+        const int threads = nw * 32;
+        // The gradient of live row number `n` (row `row`, target `tgt`), behind its factors;
+        // then the row's buffer is free.
+        auto finish = [&](int n, int64_t row, int64_t tgt) {
+            wait(&coef_bars[n & 1], n >> 1);
+            const int buf = n % bufs;
+            if (p.dlogits) {
+                T *dx = reinterpret_cast<T *>(p.dlogits) + row * p.ldd;
+                const T *x = logits + row * p.ld;
+                const int off = offset(x), units = min(cap, (off + V + N - 1) / N - u0);
+                // rows that share the logits' 16-byte phase: whole units leave as one store
+                const bool vec = ((reinterpret_cast<uintptr_t>(dx) ^ reinterpret_cast<uintptr_t>(x)) & 15) == 0;
+                const uint4 *src = reinterpret_cast<const uint4 *>(data) + buf * cap;
+                const float4 k4 = coef[n & 1];
+                const float2 f2 = make_float2(k4.x, k4.x), ng2 = make_float2(-k4.y, -k4.y);
+                const int te = (int)tgt + off, ut = te / N - u0, jt = te % N;
+                const int lo = vec ? (off && u0 == 0 ? 1 : 0) : cap, hi = vec ? (off + V) / N - u0 : 0;
+                T *dst = dx + ((int64_t)u0 * N - off);
+#pragma unroll 4
+                for (int u = t; u < units; u += threads) {
+                    const uint4 v = src[u];
                     float2 f[N / 2];
 #pragma unroll
                     for (int j = 0; j < N / 2; ++j) {
-                        const float2 z = __fmul2_rn(__fadd2_rn(E::get2(v[i], j), ng2), c2);
+                        const float2 z = __fmul2_rn(__fadd2_rn(E::get2(v, j), ng2), c2);
                         f[j] = __fmul2_rn(make_float2(ex2(z.x), ex2(z.y)), f2);
                     }
                     if (u == ut) {
@@ -481,24 +445,89 @@ __global__ void __launch_bounds__(kThreads, kThreads <= 256 ? 2 : 1)
                                     f[j / 2].x += k4.z;
                             }
                     }
-                    store(u, f);
+                    if (u >= lo && u < hi)
+                        *reinterpret_cast<uint4 *>(dst + u * N) = E::pack(f);
+                    else
+                        store_edge(dx, (u0 + u) * N - off, V, E::pack(f));
                 }
             }
-        }
-        if (more) {
-            if (warp == nw - 1) {
-                if (eu >= 0) {
-                    reinterpret_cast<uint4 *>(data)[(ahead_live % bufs) * cap + eu - u0] = join_edge<T>(raw);
-                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                }
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(smem_u32(&bars[ahead_live % bufs]));
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(smem_u32(&empty_bars[buf]));
+        };
+        int64_t last_row = -1, last_target = 0;  // the live row whose gradient is due
+        for (int64_t row = first; row < p.rows; row += clusters) {
+            const int64_t tgt = target;
+            const bool live = live_row(target, weight);
+            if (row + clusters < p.rows) {
+                target = p.targets[row + clusters];
+                weight = p.weight ? p.weight[row + clusters] : 1.0f;
             }
-            ++ahead_live;
-        }
-        if (live)
+            const T *x = logits + row * p.ld;
+            const int off = offset(x), units = min(cap, (off + V + N - 1) / N - u0);
+            if (!live) {
+                if (p.dlogits) {
+                    T *dx = reinterpret_cast<T *>(p.dlogits) + row * p.ldd;
+                    const bool vec = ((reinterpret_cast<uintptr_t>(dx) ^ reinterpret_cast<uintptr_t>(x)) & 15) == 0;
+                    for (int u = t; u < units; u += threads) {
+                        const int e0 = (u0 + u) * N - off;
+                        if (vec && e0 >= 0 && e0 + N <= V)
+                            *reinterpret_cast<uint4 *>(dx + e0) = make_uint4(0, 0, 0, 0);
+                        else
+                            store_edge(dx, e0, V, make_uint4(0, 0, 0, 0));
+                    }
+                }
+                continue;
+            }
+            const int buf = nlive % bufs, par = nlive & 1;
+            wait(&full_bars[buf], nlive / bufs);
+            const uint4 *src = reinterpret_cast<const uint4 *>(data) + buf * cap;
+            float m = -INFINITY;
+#pragma unroll 4
+            for (int u = t; u < units; u += threads)
+                m = E::max_of(m, src[u]);
+            // a part that is all -inf sums zeros against any finite maximum
+            const float mm = m == -INFINITY ? 0.0f : m;
+            const float2 nm2 = make_float2(-mm, -mm);
+            float2 sum = make_float2(0.0f, 0.0f);
+#pragma unroll 4
+            for (int u = t; u < units; u += threads) {
+                const uint4 v = src[u];
+#pragma unroll
+                for (int j = 0; j < N / 2; ++j) {
+                    const float2 f = __fmul2_rn(__fadd2_rn(E::get2(v, j), nm2), c2);
+                    sum = __fadd2_rn(sum, make_float2(ex2(f.x), ex2(f.y)));
+                }
+            }
+            float S = sum.x + sum.y, wm = m;
+#pragma unroll
+            for (int o = 16; o; o >>= 1)
+                wm = fmaxf(wm, __shfl_xor_sync(0xFFFFFFFFu, wm, o));
+            S = S == 0.0f ? 0.0f : S * ex2((m - wm) * c);
+#pragma unroll
+            for (int o = 16; o; o >>= 1)
+                S += __shfl_xor_sync(0xFFFFFFFFu, S, o);
+            // (pairs of this parity were joined before the factors that finish() of the row
+            // two before waited for, in a cluster before the barrier of the row before)
+            if (lane == 0)
+                pairs[par][warp] = make_float2(wm, S);
+            __syncwarp();
+            if (csize > 1)
+                cluster_arrive();
+            else if (lane == 0)
+                mbar_arrive(smem_u32(&pair_bars[par]));
+            if (!lag)
+                finish(nlive, row, tgt);
+            else if (last_row >= 0)
+                finish(nlive - 1, last_row, last_target);
+            last_row = row;
+            last_target = tgt;
+            if (csize > 1)
+                cluster_wait();
             ++nlive;
+        }
+        if (lag && last_row >= 0)
+            finish(nlive - 1, last_row, last_target);
     }
     if (*abort_flag) {  // copies may still be in flight: they have some time to land
         const uint64_t t0 = global_timer_ns();
@@ -560,8 +589,8 @@ cudaError_t resident_ctas(Kernel kernel, const cudaLaunchConfig_t &cfg, int csiz
     return cudaSuccess;
 }
 
-template <typename T, int NV, int kThreads>
-cudaError_t launch_rows(const PolicyLossArgs &p, RowsPlan plan, int threads, cudaStream_t st)
+template <typename T, int kThreads>
+cudaError_t launch_rows(const PolicyLossArgs &p, const RowsPlan &plan, int threads, cudaStream_t st)
 {
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -576,7 +605,7 @@ cudaError_t launch_rows(const PolicyLossArgs &p, RowsPlan plan, int threads, cud
     cfg.stream = st;
     cfg.attrs = attr;
     cfg.numAttrs = plan.csize > 1 ? 2 : 1;
-    auto kernel = k_policy_rows<T, NV, kThreads>;
+    auto kernel = k_policy_rows<T, kThreads>;
     int ctas = 0;
     const cudaError_t e = resident_ctas(kernel, cfg, plan.csize, &ctas);
     if (e != cudaSuccess)
@@ -593,28 +622,24 @@ cudaError_t launch_typed(const PolicyLossArgs &p, cudaStream_t st)
 {
     constexpr int N = Elem<T>::N;
     const int64_t units = (p.V + N - 1) / N + 1;  // one more where the rows start off a boundary
-    // a row in one CTA of at most 256 threads x 8 units (32 KB), else in the smallest
-    // cluster whose CTAs hold that, else in a cluster of 8 with more per CTA
+    // a row in one CTA of at most 32 KB, else in the smallest cluster whose CTAs hold
+    // that, else in a cluster of 8 with more per CTA
     int csize = 1;
-    while (csize < MAX_CLUSTER && units > (int64_t)csize * 256 * 8)
+    while (csize < MAX_CLUSTER && units > (int64_t)csize * 2048)
         csize *= 2;
     RowsPlan plan;
     plan.csize = csize;
     plan.units_cta = (int)((units + csize - 1) / csize);
     plan.timeout_ns = wait_limit_ns();
     const int64_t row = (int64_t)plan.units_cta * 16;
-    // two CTAs per SM where that leaves each two rows at least, else one
-    const int64_t room = 4 * row <= SMEM_CTA ? SMEM_CTA / 2 : SMEM_CTA;
+    // two CTAs per SM where that leaves each three rows, else one
+    const int64_t room = 6 * row <= SMEM_CTA ? SMEM_CTA / 2 : SMEM_CTA;
     plan.bufs = (int)(room / row < MAX_BUFS ? room / row : MAX_BUFS);
-    const int threads = plan.units_cta >= 256 * 16 ? 512 : plan.units_cta >= 256 ? 256 : (plan.units_cta + 31) / 32 * 32;
-    const int nv = (plan.units_cta + threads - 1) / threads;
-    if (threads == 512)
-        return launch_rows<T, 16, 512>(p, plan, threads, st);
-    return nv <= 1   ? launch_rows<T, 1, 256>(p, plan, threads, st)
-           : nv <= 2 ? launch_rows<T, 2, 256>(p, plan, threads, st)
-           : nv <= 4 ? launch_rows<T, 4, 256>(p, plan, threads, st)
-           : nv <= 8 ? launch_rows<T, 8, 256>(p, plan, threads, st)
-                     : launch_rows<T, 16, 256>(p, plan, threads, st);
+    // the reducing warps, the joining and the copying one
+    if (plan.units_cta > 2304)
+        return launch_rows<T, 576>(p, plan, 576, st);
+    const int threads = plan.units_cta >= 256 ? 256 : (plan.units_cta + 31) / 32 * 32;
+    return launch_rows<T, 320>(p, plan, threads + 64, st);
 }
 
 }  // namespace
