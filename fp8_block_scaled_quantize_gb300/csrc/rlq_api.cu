@@ -674,6 +674,8 @@ rlq_status rlq_gemm_gated_fprop(const uint8_t *xq, int64_t ldxq, const float *xs
     a.ldguq = ldguq;
     a.gus = gus;
     a.ld_gus = ldgus;
+    if (M <= GATED_DECODE_MAX)
+        return cuda_status(launch_gated_decode(a, cs(stream)), "gated block (few tokens) launch");
     return launch_gemm(a, cs(stream));
 }
 

@@ -181,6 +181,9 @@ struct GemmArgs {
     int64_t ld_gus;
 };
 rlq_status launch_gemm(const GemmArgs &a, cudaStream_t st);
+// The gated block for at most GATED_DECODE_MAX tokens (rlq_gated_decode.cu); same arguments.
+constexpr int GATED_DECODE_MAX = 8;
+cudaError_t launch_gated_decode(const GemmArgs &a, cudaStream_t st);
 
 // ---- NVFP4 weight-only GEMM (rlq_gemm_nvfp4.cu); arguments already validated ----
 // Y[M, N] = bf16(st * X W^T), X bf16 [M, K] (pitch ldx elements), W from packed
