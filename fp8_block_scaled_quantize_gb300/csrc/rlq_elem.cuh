@@ -133,6 +133,22 @@ __device__ __forceinline__ float half_warp_max(float a)
     return a;
 }
 
+// The maxima of a thread's eight columns over its rows -> over both halves of the warp
+// (lanes l and l ^ 16 hold the same columns), to eight consecutive floats at dst: the
+// lower half keeps columns 0-3, the upper 4-7.
+__device__ __forceinline__ void store_column_maxima(const float2 (&c)[4], bool upper, float *dst)
+{
+    float4 o;
+    float *f = &o.x;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const float2 keep = upper ? c[2 + j] : c[j], send = upper ? c[j] : c[2 + j];
+        f[2 * j] = fmaxf(keep.x, __shfl_xor_sync(0xFFFFFFFFu, send.x, 16));
+        f[2 * j + 1] = fmaxf(keep.y, __shfl_xor_sync(0xFFFFFFFFu, send.y, 16));
+    }
+    *reinterpret_cast<float4 *>(dst + (upper ? 4 : 0)) = o;
+}
+
 // Writes a 128 x 128 tile of codes, held as [column][16 chunks of 8 rows] with chunk
 // index XOR column / 8, as rows of the transposed matrix: 8 threads per column, 16
 // bytes each.  Rows at or past `rows` are not written.  dst: element (column 0, row 0).

@@ -177,20 +177,9 @@ __global__ void __launch_bounds__(THREADS, 1) k_gate_bwd(const GateBwd p)
                                              max3_abs(val[k][0][j].y, val[k][1][j].y, val[k][2][j].y));
                 cmax[k][j] = make_float2(fmaxf(m.x, fabsf(val[k][3][j].x)), fmaxf(m.y, fabsf(val[k][3][j].y)));
             }
-        // the halves of a warp exchange: the lower keeps columns 0-3 of its eight, the upper 4-7
 #pragma unroll
-        for (int k = 0; k < 3; ++k) {
-            float4 c;
-            const bool up = t & 16;
-            float *cc = &c.x;
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const float2 keep = up ? cmax[k][2 + j] : cmax[k][j], send = up ? cmax[k][j] : cmax[k][2 + j];
-                cc[2 * j] = fmaxf(keep.x, __shfl_xor_sync(0xFFFFFFFFu, send.x, 16));
-                cc[2 * j + 1] = fmaxf(keep.y, __shfl_xor_sync(0xFFFFFFFFu, send.y, 16));
-            }
-            *reinterpret_cast<float4 *>(part + (warp * 3 + k) * GRP + 8 * cg + (up ? 4 : 0)) = c;
-        }
+        for (int k = 0; k < 3; ++k)
+            store_column_maxima(cmax[k], t & 16, part + (warp * 3 + k) * GRP + 8 * cg);
         __syncthreads();
         float cs = 1.0f;
         if (t < 3 * GRP) {

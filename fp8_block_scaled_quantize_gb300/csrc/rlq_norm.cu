@@ -128,7 +128,7 @@ __global__ void __launch_bounds__(1024) k_add_rmsnorm_rows(const uint16_t *res, 
 // tile, thread t rows 8 (t / 16) .. + 7 and columns 8 (t % 16) .. + 7.  The codes
 // are turned in shared memory ([column][16 chunks of 8 rows], chunks XOR-swizzled by
 // column / 8: conflict-free both ways) and leave as whole 128-byte lines of qT.
-__global__ void __launch_bounds__(256) k_norm_cols(const uint16_t *__restrict__ h, int64_t ldh,
+__global__ void __launch_bounds__(256, 3) k_norm_cols(const uint16_t *__restrict__ h, int64_t ldh,
                                                    const float *__restrict__ rstd,
                                                    const uint16_t *__restrict__ gamma, int64_t M, int64_t K,
                                                    uint8_t *__restrict__ qT, int64_t ldqT, float *__restrict__ sc,
@@ -136,7 +136,7 @@ __global__ void __launch_bounds__(256) k_norm_cols(const uint16_t *__restrict__ 
 {
     pdl_begin();
     __shared__ __align__(16) uint8_t tile[128 * 128];
-    __shared__ float part[8][128];
+    __shared__ __align__(16) float part[8][128];
     const int t = threadIdx.x, cg = t & 15, rg = t >> 4, warp = t >> 5;
     const int64_t m0 = (int64_t)blockIdx.x * GRP, k0 = (int64_t)blockIdx.y * GRP;
     const int rows = (int)(M - m0 < GRP ? M - m0 : GRP);
@@ -148,46 +148,67 @@ __global__ void __launch_bounds__(256) k_norm_cols(const uint16_t *__restrict__ 
         v[i] = m < rows ? ld_stream(h + (m0 + m) * ldh + k0 + 8 * cg) : make_uint4(0, 0, 0, 0);
         r[i] = m < rows ? rstd[m0 + m] : 0.0f;
     }
-    float g[8], x[8][8], cmax[8];
-    unpack8(*reinterpret_cast<const uint4 *>(gamma + k0 + 8 * cg), g);
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-        cmax[j] = 0.0f;
+    const uint4 gv = *reinterpret_cast<const uint4 *>(gamma + k0 + 8 * cg);
+    const uint32_t gw[4] = {gv.x, gv.y, gv.z, gv.w};
+    float2 x[8][4];  // [row][column pair]
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        unpack8(v[i], x[i]);
+        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            x[i][j] = (x[i][j] * r[i]) * g[j];
-            cmax[j] = fmaxf(cmax[j], fabsf(x[i][j]));
-        }
+        for (int j = 0; j < 4; ++j)
+            x[i][j] = __fmul2_rn(__fmul2_rn(make_float2(bf_lo(w[j]), bf_hi(w[j])), make_float2(r[i], r[i])),
+                                 make_float2(bf_lo(gw[j]), bf_hi(gw[j])));
     }
+    float2 cmax[4];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const float c = fmaxf(cmax[j], __shfl_xor_sync(0xFFFFFFFFu, cmax[j], 16));
-        if ((t & 16) == 0)
-            part[warp][8 * cg + j] = c;
+    for (int j = 0; j < 4; ++j) {
+        cmax[j] = make_float2(max3_abs(x[0][j].x, x[1][j].x, x[2][j].x), max3_abs(x[0][j].y, x[1][j].y, x[2][j].y));
+        cmax[j] = make_float2(max3_abs(cmax[j].x, x[3][j].x, x[4][j].x), max3_abs(cmax[j].y, x[3][j].y, x[4][j].y));
+        cmax[j] = make_float2(max3_abs(cmax[j].x, x[5][j].x, x[6][j].x), max3_abs(cmax[j].y, x[5][j].y, x[6][j].y));
+        cmax[j] = make_float2(fmaxf(cmax[j].x, fabsf(x[7][j].x)), fmaxf(cmax[j].y, fabsf(x[7][j].y)));
     }
+    store_column_maxima(cmax, t & 16, part[warp] + 8 * cg);
     __syncthreads();
+    float cs = 1.0f;
     if (t < 128) {
         float a = part[0][t];
 #pragma unroll
         for (int w = 1; w < 8; ++w)
             a = fmaxf(a, part[w][t]);
-        a = group_scale(a);
-        part[0][t] = a;
-        part[1][t] = scale_rcp(a);
-        sc[(int64_t)blockIdx.x * ldsc + k0 + t] = a;
+        cs = group_scale(a);
+        part[0][t] = scale_rcp(cs);  // (only this thread reads column t of the maxima)
+        sc[(int64_t)blockIdx.x * ldsc + k0 + t] = cs;
     }
-    __syncthreads();
+    // (columns whose scale is below 2^-100 are scaled up first)
+    if (__syncthreads_or(cs < 0x1p-100f)) {
+        if (t < 128)
+            part[1][t] = scale_pre(cs);
+        __syncthreads();
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const int c = 8 * cg + j;
-        float col[8];
+        for (int j = 0; j < 4; ++j) {
+            const float2 f = *reinterpret_cast<const float2 *>(part[1] + 8 * cg + 2 * j);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                x[i][j] = __fmul2_rn(x[i][j], f);
+        }
+    }
+    const float4 r0 = *reinterpret_cast<const float4 *>(part[0] + 8 * cg);
+    const float4 r1 = *reinterpret_cast<const float4 *>(part[0] + 8 * cg + 4);
+    const float2 rc[4] = {make_float2(r0.x, r0.y), make_float2(r0.z, r0.w), make_float2(r1.x, r1.y),
+                          make_float2(r1.z, r1.w)};
+    uint8_t *out = tile + 8 * cg * GRP + 8 * (rg ^ cg);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        float2 y[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            col[i] = x[i][j];
-        *reinterpret_cast<uint2 *>(tile + c * 128 + 8 * (rg ^ cg)) = encode8f(col, part[0][c], part[1][c]);
+            y[i] = __fmul2_rn(x[i][j], rc[j]);
+        *reinterpret_cast<uint2 *>(out + 2 * j * GRP) =
+            make_uint2(e4m3x2(y[0].x, y[1].x) | (e4m3x2(y[2].x, y[3].x) << 16),
+                       e4m3x2(y[4].x, y[5].x) | (e4m3x2(y[6].x, y[7].x) << 16));
+        *reinterpret_cast<uint2 *>(out + (2 * j + 1) * GRP) =
+            make_uint2(e4m3x2(y[0].y, y[1].y) | (e4m3x2(y[2].y, y[3].y) << 16),
+                       e4m3x2(y[4].y, y[5].y) | (e4m3x2(y[6].y, y[7].y) << 16));
     }
     __syncthreads();
     store_tile_T(tile, t, 256, rows, qT + k0 * ldqT + m0, ldqT);
@@ -360,13 +381,16 @@ cudaError_t launch_add_rmsnorm_quant(const uint16_t *res, int64_t ldr, const uin
                                      uint8_t *q, int64_t ldq, float *s, int64_t lds, uint8_t *qT, int64_t ldqT,
                                      float *sc, int64_t ldsc, cudaStream_t st)
 {
-    // Few rows: one vector per thread, the shortest path through a row.  More rows
-    // than SMs: four per thread, more bytes in flight per thread and fewer warps per sum.
+    // Vectors per thread.  As many rows as SMs or fewer: one, the shortest path through a
+    // row.  More: two up to K = 5120 (M = 1001, K = 5120 7.3 us, with four 8.8), four
+    // beyond, where a row's sum over more warps costs more (M = 4096, K = 8192 with the
+    // columns 62 us, with two 68).
     const int nvec = (int)(K / 8);
-    const int nv = (M <= device_sms() && nvec <= 1024) ? 1 : 4;
+    const int nv = (M <= device_sms() && nvec <= 1024) ? 1 : nvec <= 640 ? 2 : 4;
     const int T = ((nvec + nv - 1) / nv + 31) / 32 * 32;
-    auto kernel = nv == 1 ? (delta ? k_add_rmsnorm_rows<1, true> : k_add_rmsnorm_rows<1, false>)
-                          : (delta ? k_add_rmsnorm_rows<4, true> : k_add_rmsnorm_rows<4, false>);
+    auto kernel = nv == 1   ? (delta ? k_add_rmsnorm_rows<1, true> : k_add_rmsnorm_rows<1, false>)
+                  : nv == 2 ? (delta ? k_add_rmsnorm_rows<2, true> : k_add_rmsnorm_rows<2, false>)
+                            : (delta ? k_add_rmsnorm_rows<4, true> : k_add_rmsnorm_rows<4, false>);
     cudaError_t e = launch_pdl(kernel, dim3((unsigned)M), dim3(T), 0, st, res, ldr, delta, ldd, gamma, eps, (int)K, h,
                                ldh, rstd, q, ldq, s, lds);
     if (e != cudaSuccess || !qT)
