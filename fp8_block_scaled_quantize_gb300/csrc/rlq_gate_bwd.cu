@@ -273,7 +273,14 @@ cudaError_t launch_gated_backward(const uint16_t *da, int64_t ldda, const uint8_
         return cudaErrorInvalidValue;
     const GateBwd p = {da, ldda, guq, ldguq, gus, ld_gus, q,  ldq, s, lds, qT,           ldqT,
                        sc, ldsc, aT,  ldaT,  ac,  ldac,   M,  F,   (int)m_tiles, (int)tiles};
-    const cudaError_t e = cudaFuncSetAttribute(k_gate_bwd, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+    // (once per device)
+    static std::atomic<bool> set[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess && !set[dev & 63].load(std::memory_order_relaxed)) {
+        e = cudaFuncSetAttribute(k_gate_bwd, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+        set[dev & 63].store(e == cudaSuccess, std::memory_order_relaxed);
+    }
     if (e != cudaSuccess)
         return e;
     const int64_t sms = device_sms();

@@ -11,6 +11,7 @@ loaded, the first call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -299,7 +300,7 @@ def rlq_version() -> str:
 def _stream(stream) -> int:
     if stream is None:
         # the current stream's handle without building a Stream object around it
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -576,6 +577,12 @@ def _rows_of(name, t, M, K, dtype=torch.bfloat16):
     return ld if M > 1 else max(ld, K)
 
 
+def _codes_T(K: int, M: int, device):
+    """(transposed codes [K, M], their pitch), the pitch a multiple of 16 as the GEMMs' copies take it."""
+    ld = (max(M, 1) + 15) & ~15
+    return torch.empty_strided((K, M), (ld, 1), dtype=torch.uint8, device=device), ld
+
+
 def _vector(name, t, n, dtype=torch.float32):
     """Address of ``t``, a contiguous [n] CUDA tensor of ``dtype``."""
     if t.dtype is not dtype:
@@ -606,13 +613,13 @@ def add_rmsnorm_quant_act_1x128(res: torch.Tensor, delta: torch.Tensor | None, g
     s = torch.empty((K // GRP, M), dtype=torch.float32, device=dev)
     rstd = torch.empty((M,), dtype=torch.float32, device=dev)
     qT = sc = None
+    ldT = 0
     if colwise:
-        qT = empty_codes_T(K, M, dev)
+        qT, ldT = _codes_T(K, M, dev)
         sc = torch.empty(((M + GRP - 1) // GRP, K), dtype=torch.float32, device=dev)
-    rlq_add_rmsnorm_quant_act_1x128(res.data_ptr(), ldr, _ptr(delta), ldd, M, K, g, eps,
-                                    h.data_ptr() if delta is not None else None, _ld(h), rstd.data_ptr(),
-                                    q.data_ptr(), K, s.data_ptr(), max(M, 1), _ptr(qT),
-                                    _ld(qT) if colwise else 0, _ptr(sc), K if colwise else 0, _stream(stream))
+    _call("rlq_add_rmsnorm_quant_act_1x128", res.data_ptr(), ldr, _ptr(delta), ldd, M, K, g, eps,
+          h.data_ptr() if delta is not None else None, ldr if h is res else K, rstd.data_ptr(), q.data_ptr(), K,
+          s.data_ptr(), max(M, 1), _ptr(qT), ldT, _ptr(sc), K if colwise else 0, _stream(stream))
     return h, q, s, qT, sc, rstd
 
 
@@ -630,13 +637,21 @@ def rmsnorm_backward(dx: torch.Tensor, h: torch.Tensor, rstd: torch.Tensor, gamm
     g, r = _vector("gamma", gamma, K, torch.bfloat16), _vector("rstd", rstd, M)
     dh = dres if inplace and dres is not None else torch.empty((M, K), dtype=torch.bfloat16, device=dx.device)
     dgamma = torch.empty((K,), dtype=torch.float32, device=dx.device)
-    nbytes = rlq_rmsnorm_backward_workspace_bytes(M, K)
-    if workspace is None and nbytes:
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=dx.device)
-    rlq_rmsnorm_backward(dx.data_ptr(), lddx, h.data_ptr(), ldh, r, g, _ptr(dres), ldres, dh.data_ptr(), _ld(dh),
-                         dgamma.data_ptr(), M, K, _ptr(workspace),
-                         workspace.numel() * workspace.element_size() if workspace is not None else 0, _stream(stream))
+    if workspace is None:
+        nbytes = _norm_workspace_bytes(M, K, torch._C._cuda_getDevice())
+        if nbytes:
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=dx.device)
+    else:
+        nbytes = workspace.numel() * workspace.element_size()
+    _call("rlq_rmsnorm_backward", dx.data_ptr(), lddx, h.data_ptr(), ldh, r, g, _ptr(dres), ldres, dh.data_ptr(),
+          ldres if dh is dres else K, dgamma.data_ptr(), M, K, _ptr(workspace), nbytes, _stream(stream))
     return dh, dgamma
+
+
+@functools.lru_cache(maxsize=1024)
+def _norm_workspace_bytes(M: int, K: int, device: int) -> int:
+    """The library's workspace size for a shape on a device (its plan depends on nothing else)."""
+    return rlq_rmsnorm_backward_workspace_bytes(M, K)
 
 
 def gemm_gated_fprop(xq, xs, wq, ws, checkpoint: bool = False, stream=None):
@@ -659,9 +674,9 @@ def gemm_gated_fprop(xq, xs, wq, ws, checkpoint: bool = False, stream=None):
     if checkpoint:
         guq = torch.empty((M, 2 * F), dtype=torch.uint8, device=dev)
         gus = torch.empty((2 * F // GRP, M), dtype=torch.float32, device=dev)
-    rlq_gemm_gated_fprop(xq.data_ptr(), ldx, xs.data_ptr(), max(ldxs, 1), wq.data_ptr(), ldw, ws.data_ptr(), ldws,
-                         aq.data_ptr(), F, a_s.data_ptr(), max(M, 1), _ptr(guq), 2 * F, _ptr(gus), max(M, 1), M, F, K,
-                         _stream(stream))
+    _call("rlq_gemm_gated_fprop", xq.data_ptr(), ldx, xs.data_ptr(), max(ldxs, 1), wq.data_ptr(), ldw, ws.data_ptr(),
+          ldws, aq.data_ptr(), F, a_s.data_ptr(), max(M, 1), _ptr(guq), 2 * F, _ptr(gus), max(M, 1), M, F, K,
+          _stream(stream))
     return aq, a_s, guq, gus
 
 
@@ -679,12 +694,12 @@ def gated_backward(da: torch.Tensor, guq, gus, stream=None):
     nb = (M + GRP - 1) // GRP
     q = torch.empty((M, 2 * F), dtype=torch.uint8, device=dev)
     s = torch.empty((2 * F // GRP, M), dtype=torch.float32, device=dev)
-    qT, aT = empty_codes_T(2 * F, M, dev), empty_codes_T(F, M, dev)
+    (qT, ldT), (aT, _) = _codes_T(2 * F, M, dev), _codes_T(F, M, dev)
     sc = torch.empty((nb, 2 * F), dtype=torch.float32, device=dev)
     ac = torch.empty((nb, F), dtype=torch.float32, device=dev)
-    rlq_gated_backward(da.data_ptr(), ldda, guq.data_ptr(), ldgu, gus.data_ptr(), ldgs, q.data_ptr(), 2 * F,
-                       s.data_ptr(), max(M, 1), qT.data_ptr(), _ld(qT), sc.data_ptr(), 2 * F, aT.data_ptr(), _ld(aT),
-                       ac.data_ptr(), F, M, F, _stream(stream))
+    _call("rlq_gated_backward", da.data_ptr(), ldda, guq.data_ptr(), ldgu, gus.data_ptr(), ldgs, q.data_ptr(), 2 * F,
+          s.data_ptr(), max(M, 1), qT.data_ptr(), ldT, sc.data_ptr(), 2 * F, aT.data_ptr(), ldT, ac.data_ptr(), F, M, F,
+          _stream(stream))
     return q, s, qT, sc, aT, ac
 
 
@@ -706,8 +721,8 @@ def token_logprobs(logits: torch.Tensor, targets: torch.Tensor, temperature: flo
     T, V, dt, ld, tg = _logits(logits, targets)
     lp = torch.empty((T,), dtype=torch.float32, device=logits.device)
     lse = torch.empty((T,), dtype=torch.float32, device=logits.device)
-    rlq_token_logprobs(logits.data_ptr(), dt, ld, T, V, tg, temperature, lp.data_ptr(), lse.data_ptr(),
-                       _stream(stream))
+    _call("rlq_token_logprobs", logits.data_ptr(), dt, ld, T, V, tg, temperature, lp.data_ptr(), lse.data_ptr(),
+          _stream(stream))
     return lp, lse
 
 
@@ -731,10 +746,10 @@ def policy_loss(logits: torch.Tensor, targets: torch.Tensor, logp_old: torch.Ten
     elif grad:
         # the logits' own pitch, so that their rows share 16-byte phases
         d = torch.empty_strided((T, V), (ld, 1), dtype=logits.dtype, device=logits.device)
-    rlq_policy_loss(logits.data_ptr(), dt, ld, T, V, tg, temperature, _vector("logp_old", logp_old, T),
-                    _vector("adv", adv, T), _vector("weight", weight, T), opt("logp_behav", logp_behav),
-                    opt("logp_ref", logp_ref), opt("clip_hi", clip_hi), eps_lo, eps_hi, tis_cap, kl_beta,
-                    loss.data_ptr(), lp.data_ptr(), _ptr(d), ld if grad else 0, _stream(stream))
+    _call("rlq_policy_loss", logits.data_ptr(), dt, ld, T, V, tg, temperature, _vector("logp_old", logp_old, T),
+          _vector("adv", adv, T), _vector("weight", weight, T), opt("logp_behav", logp_behav),
+          opt("logp_ref", logp_ref), opt("clip_hi", clip_hi), eps_lo, eps_hi, tis_cap, kl_beta, loss.data_ptr(),
+          lp.data_ptr(), _ptr(d), ld if grad else 0, _stream(stream))
     return loss, lp, d
 
 
