@@ -9,14 +9,15 @@
 //   dloss/dlp = weight (-w A rho [the unclipped branch is the minimum] - beta (exp(d) - 1))
 //   dlogits_v = dloss/dlp (1[v = t] - softmax(z)_v) / temperature
 //
-// Bound by memory: the logits are read once and the gradient written once.  A row is
-// held on chip by one CTA, or by a cluster of 2, 4 or 8 for long rows.  Persistent
-// CTAs: one warp copies the next rows to shared memory (bulk copies), another joins the
-// reducing warps' (maximum, sum) pairs of a row across the cluster and publishes the
-// row's factors, while those warps already reduce the next row; they write a row's
-// gradient after that.  So a row's chain of latencies (cluster barrier, remote reads, logarithm
-// and exponentials) lies beside the work on its neighbours.  The gradient may overwrite
-// the logits: a row is read whole before any of it is written.
+// Bound by memory: the logits are read once and the gradient written once.  Without a
+// gradient a row is streamed (k_token_rows).  With one it is held on chip by one CTA, or
+// by a cluster of 2, 4 or 8 for long rows (k_policy_grad), persistent CTAs: one warp copies
+// the next rows to shared memory (bulk copies), another joins the reducing warps'
+// (maximum, sum) pairs of a row across the cluster and publishes the row's factors, while
+// those warps already reduce the next row; they write a row's gradient after that.  So a
+// row's chain of latencies (cluster barrier, remote reads, logarithm and exponentials)
+// lies beside the work on its neighbours.  The gradient may overwrite the logits: a row
+// is read whole before any of it is written.
 #include <cuda_runtime.h>
 
 #include <mutex>
@@ -121,6 +122,35 @@ struct RowInputs {
     float old, adv, weight, behav, ref, hi;
 };
 
+__device__ __forceinline__ RowInputs row_inputs(const PolicyLossArgs &p, int64_t row)
+{
+    RowInputs in = {};
+    if (p.adv) {
+        in.old = p.lp_old[row];
+        in.adv = p.adv[row];
+        in.weight = p.weight[row];
+        in.behav = p.lp_behav ? p.lp_behav[row] : 0.0f;
+        in.ref = p.lp_ref ? p.lp_ref[row] : 0.0f;
+        in.hi = p.clip_hi ? p.clip_hi[row] : 1.0f + p.eps_hi;
+    }
+    return in;
+}
+
+// (maximum, sum of 2^((x - maximum) c)) pairs of a warp's lanes, joined in every lane.  A
+// pair of -inf only has the sum 0; one of NaN has no maximum but a NaN sum.
+__device__ __forceinline__ float2 join_pairs(float2 v, float c)
+{
+    float m = v.x;
+#pragma unroll
+    for (int o = 16; o; o >>= 1)
+        m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+    float s = v.y == 0.0f ? 0.0f : v.y * ex2((v.x - m) * c);
+#pragma unroll
+    for (int o = 16; o; o >>= 1)
+        s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+    return make_float2(m, s);
+}
+
 // The row's loss and its derivative, from the row's maximum (m, in logits), the sum S
 // of 2^((x - m) c) and the target's logit.
 __device__ __noinline__ RowScalars row_scalars(const PolicyLossArgs &p, const RowInputs in, float m, float S,
@@ -173,7 +203,15 @@ __device__ __forceinline__ uint4 join_edge(const T (&raw)[Elem<T>::N])
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// (out of line: a row has at most one such unit at each end)
+// (both out of line: a row has at most one such unit at each end)
+template <typename T>
+__device__ __noinline__ uint4 load_cut(const T *x, int e0, int V)
+{
+    T raw[Elem<T>::N];
+    load_edge(x, e0, V, raw);
+    return join_edge<T>(raw);
+}
+
 template <typename T>
 __device__ __noinline__ void store_edge(T *dx, int e0, int V, uint4 v)
 {
@@ -182,6 +220,107 @@ __device__ __noinline__ void store_edge(T *dx, int e0, int V, uint4 v)
     for (int j = 0; j < Elem<T>::N; ++j)
         if (e0 + j >= 0 && e0 + j < V)
             dx[e0 + j] = sizeof(T) == 2 ? (T)(w[j / 2] >> (16 * (j & 1))) : (T)w[j & 3];
+}
+
+// Log probabilities, or the loss without its gradient: nothing of the row is needed
+// again, so a CTA streams its part of it once, keeping a running maximum and sum a
+// thread, 8 loads of 16 bytes in flight.  A row is one CTA's, or a cluster's of 2, 4 or 8
+// where there are few rows; unit and rank as below.
+template <typename T>
+__global__ void __launch_bounds__(256, 4) k_token_rows(const PolicyLossArgs p, int csize, int units_cta)
+{
+    pdl_begin();
+    using E = Elem<T>;
+    constexpr int N = E::N, BATCH = 8;
+    constexpr uint32_t NINF = sizeof(T) == 2 ? 0xFF80FF80u : 0xFF800000u;
+    __shared__ float2 pairs[8], mine;
+    const int64_t row = blockIdx.x / csize;
+    const int rank = (int)(blockIdx.x - row * csize), V = (int)p.V;
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5, nw = blockDim.x >> 5;
+    const T *x = reinterpret_cast<const T *>(p.logits) + row * p.ld;
+    const int64_t target = p.targets[row];
+    if (target < 0 || target >= V || (p.weight && p.weight[row] == 0.0f)) {  // an empty row, to the whole cluster
+        if (rank == 0 && t == 0) {
+            p.lp[row] = 0.0f;
+            if (p.lse)
+                p.lse[row] = 0.0f;
+            if (p.loss)
+                p.loss[row] = 0.0f;
+        }
+        return;
+    }
+    float xt = 0.0f;
+    RowInputs in = {};
+    if (rank == 0 && warp == 0) {
+        xt = E::load(x + target);
+        in = row_inputs(p, row);
+    }
+    const int off = (int)((reinterpret_cast<uintptr_t>(x) & 15) / sizeof(T));
+    const int u0 = rank * units_cta, u1 = min(u0 + units_cta, (off + V + N - 1) / N);
+    const int whole0 = off ? 1 : 0, whole1 = (off + V) / N;  // units that the row's ends do not cut
+    const float c = 1.4426950408889634f / p.temperature;
+    const float2 c2 = make_float2(c, c);
+    float m = -INFINITY;
+    float2 sum = make_float2(0.0f, 0.0f);
+    for (int u = u0 + t; u < u1; u += BATCH * blockDim.x) {
+        uint4 v[BATCH];
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i) {
+            const int w = u + i * (int)blockDim.x;
+            v[i] = make_uint4(NINF, NINF, NINF, NINF);
+            if (w < u1 && w >= whole0 && w < whole1)
+                v[i] = ld_stream(reinterpret_cast<const uint16_t *>(x + ((int64_t)w * N - off)));
+            else if (w < u1)
+                v[i] = load_cut(x, w * N - off, V);
+        }
+        float b = m;
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i)
+            b = E::max_of(b, v[i]);
+        // (a thread that has seen -inf only sums zeros against 0)
+        const float ref = b == -INFINITY ? 0.0f : b;
+        if (b > m) {
+            const float k = m == -INFINITY ? (sum.x + sum.y == 0.0f ? 0.0f : 1.0f) : ex2((m - b) * c);
+            sum = __fmul2_rn(sum, make_float2(k, k));
+            m = b;
+        }
+        const float2 nref = make_float2(-ref, -ref);
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i)
+#pragma unroll
+            for (int j = 0; j < N / 2; ++j) {
+                const float2 f = __fmul2_rn(__fadd2_rn(E::get2(v[i], j), nref), c2);
+                sum = __fadd2_rn(sum, make_float2(ex2(f.x), ex2(f.y)));
+            }
+    }
+    float2 o = join_pairs(make_float2(m, sum.x + sum.y), c);
+    if (lane == 0)
+        pairs[warp] = o;
+    __syncthreads();
+    if (warp == 0) {
+        o = join_pairs(lane < nw ? pairs[lane] : make_float2(-INFINITY, 0.0f), c);
+        if (lane == 0)
+            mine = o;
+    }
+    if (csize > 1) {
+        __syncwarp();
+        cluster_sync();
+        if (rank == 0 && warp == 0)
+            o = join_pairs(lane < csize ? ld_cluster2(smem_u32(&mine), lane) : make_float2(-INFINITY, 0.0f), c);
+        __syncwarp();
+    }
+    if (rank == 0 && warp == 0) {
+        const RowScalars r = row_scalars(p, in, o.x, o.y, xt, c);
+        if (lane == 0) {
+            p.lp[row] = r.lp;
+            if (p.lse)
+                p.lse[row] = r.lse;
+            if (p.loss)
+                p.loss[row] = r.loss;
+        }
+    }
+    if (csize > 1)
+        cluster_sync();  // no CTA leaves while another may still read its pair
 }
 
 constexpr int MAX_BUFS = 3;
@@ -211,11 +350,10 @@ struct RowsPlan {
 // a CTA's reducing warps hand their pairs to its joining warp (an mbarrier), whose
 // arrival alone releases them to the cluster.  (A releasing arrival of the reducing
 // warps waits for the gradient's stores at every row: 479 us against 439 for 4096 rows
-// of 128256.  Without a gradient there is nothing to wait for, and they release their
-// pairs themselves, one hand-over less: 174 us against 224 for 2048 rows.)
+// of 128256.)
 template <typename T, int kThreads>
 __global__ void __launch_bounds__(kThreads, kThreads <= 320 ? 2 : 1)
-    k_policy_rows(const PolicyLossArgs p, const RowsPlan plan)
+    k_policy_grad(const PolicyLossArgs p, const RowsPlan plan)
 {
     pdl_begin();
     using E = Elem<T>;
@@ -334,14 +472,7 @@ __global__ void __launch_bounds__(kThreads, kThreads <= 320 ? 2 : 1)
             if (row >= p.rows || !live_row(target, weight))
                 return;
             xt = E::load(logits + row * p.ld + target);
-            if (p.adv) {
-                in.old = p.lp_old[row];
-                in.adv = p.adv[row];
-                in.weight = weight;
-                in.behav = p.lp_behav ? p.lp_behav[row] : 0.0f;
-                in.ref = p.lp_ref ? p.lp_ref[row] : 0.0f;
-                in.hi = p.clip_hi ? p.clip_hi[row] : 1.0f + p.eps_hi;
-            }
+            in = row_inputs(p, row);
         };
         load_inputs(first);
         for (int64_t row = first; row < p.rows; row += clusters) {
@@ -366,8 +497,7 @@ __global__ void __launch_bounds__(kThreads, kThreads <= 320 ? 2 : 1)
             const float x_t = xt;
             const RowInputs now = in;
             const bool nan_target = __any_sync(0xFFFFFFFFu, x_t != x_t);
-            if (csize == 1 || p.dlogits)
-                wait(&pair_bars[par], nlive >> 1);
+            wait(&pair_bars[par], nlive >> 1);
             if (csize > 1) {
                 cluster_arrive();
                 cluster_wait();
@@ -423,42 +553,40 @@ __global__ void __launch_bounds__(kThreads, kThreads <= 320 ? 2 : 1)
         auto finish = [&](int n, int64_t row, int64_t tgt) {
             wait(&coef_bars[n & 1], n >> 1);
             const int buf = n % bufs;
-            if (p.dlogits) {
-                T *dx = reinterpret_cast<T *>(p.dlogits) + row * p.ldd;
-                const T *x = logits + row * p.ld;
-                const int off = offset(x), units = min(cap, (off + V + N - 1) / N - u0);
-                // rows that share the logits' 16-byte phase: whole units leave as one store
-                const bool vec = ((reinterpret_cast<uintptr_t>(dx) ^ reinterpret_cast<uintptr_t>(x)) & 15) == 0;
-                const uint4 *src = reinterpret_cast<const uint4 *>(data) + buf * cap;
-                const float4 k4 = coef[n & 1];
-                const float2 f2 = make_float2(k4.x, k4.x), ng2 = make_float2(-k4.y, -k4.y);
-                const int te = (int)tgt + off, ut = te / N - u0, jt = te % N;
-                const int lo = vec ? (off && u0 == 0 ? 1 : 0) : cap, hi = vec ? (off + V) / N - u0 : 0;
-                T *dst = dx + ((int64_t)u0 * N - off);
+            T *dx = reinterpret_cast<T *>(p.dlogits) + row * p.ldd;
+            const T *x = logits + row * p.ld;
+            const int off = offset(x), units = min(cap, (off + V + N - 1) / N - u0);
+            // rows that share the logits' 16-byte phase: whole units leave as one store
+            const bool vec = ((reinterpret_cast<uintptr_t>(dx) ^ reinterpret_cast<uintptr_t>(x)) & 15) == 0;
+            const uint4 *src = reinterpret_cast<const uint4 *>(data) + buf * cap;
+            const float4 k4 = coef[n & 1];
+            const float2 f2 = make_float2(k4.x, k4.x), ng2 = make_float2(-k4.y, -k4.y);
+            const int te = (int)tgt + off, ut = te / N - u0, jt = te % N;
+            const int lo = vec ? (off && u0 == 0 ? 1 : 0) : cap, hi = vec ? (off + V) / N - u0 : 0;
+            T *dst = dx + ((int64_t)u0 * N - off);
 #pragma unroll 4
-                for (int u = t; u < units; u += threads) {
-                    const uint4 v = src[u];
-                    float2 f[N / 2];
+            for (int u = t; u < units; u += threads) {
+                const uint4 v = src[u];
+                float2 f[N / 2];
 #pragma unroll
-                    for (int j = 0; j < N / 2; ++j) {
-                        const float2 z = __fmul2_rn(__fadd2_rn(E::get2(v, j), ng2), c2);
-                        f[j] = __fmul2_rn(make_float2(ex2(z.x), ex2(z.y)), f2);
-                    }
-                    if (u == ut) {
-#pragma unroll
-                        for (int j = 0; j < N; ++j)
-                            if (j == jt) {
-                                if (j & 1)
-                                    f[j / 2].y += k4.z;
-                                else
-                                    f[j / 2].x += k4.z;
-                            }
-                    }
-                    if (u >= lo && u < hi)
-                        *reinterpret_cast<uint4 *>(dst + u * N) = E::pack(f);
-                    else
-                        store_edge(dx, (u0 + u) * N - off, V, E::pack(f));
+                for (int j = 0; j < N / 2; ++j) {
+                    const float2 z = __fmul2_rn(__fadd2_rn(E::get2(v, j), ng2), c2);
+                    f[j] = __fmul2_rn(make_float2(ex2(z.x), ex2(z.y)), f2);
                 }
+                if (u == ut) {
+#pragma unroll
+                    for (int j = 0; j < N; ++j)
+                        if (j == jt) {
+                            if (j & 1)
+                                f[j / 2].y += k4.z;
+                            else
+                                f[j / 2].x += k4.z;
+                        }
+                }
+                if (u >= lo && u < hi)
+                    *reinterpret_cast<uint4 *>(dst + u * N) = E::pack(f);
+                else
+                    store_edge(dx, (u0 + u) * N - off, V, E::pack(f));
             }
             __syncwarp();
             if (lane == 0)
@@ -475,16 +603,14 @@ __global__ void __launch_bounds__(kThreads, kThreads <= 320 ? 2 : 1)
             const T *x = logits + row * p.ld;
             const int off = offset(x), units = min(cap, (off + V + N - 1) / N - u0);
             if (!live) {
-                if (p.dlogits) {
-                    T *dx = reinterpret_cast<T *>(p.dlogits) + row * p.ldd;
-                    const bool vec = ((reinterpret_cast<uintptr_t>(dx) ^ reinterpret_cast<uintptr_t>(x)) & 15) == 0;
-                    for (int u = t; u < units; u += threads) {
-                        const int e0 = (u0 + u) * N - off;
-                        if (vec && e0 >= 0 && e0 + N <= V)
-                            *reinterpret_cast<uint4 *>(dx + e0) = make_uint4(0, 0, 0, 0);
-                        else
-                            store_edge(dx, e0, V, make_uint4(0, 0, 0, 0));
-                    }
+                T *dx = reinterpret_cast<T *>(p.dlogits) + row * p.ldd;
+                const bool vec = ((reinterpret_cast<uintptr_t>(dx) ^ reinterpret_cast<uintptr_t>(x)) & 15) == 0;
+                for (int u = t; u < units; u += threads) {
+                    const int e0 = (u0 + u) * N - off;
+                    if (vec && e0 >= 0 && e0 + N <= V)
+                        *reinterpret_cast<uint4 *>(dx + e0) = make_uint4(0, 0, 0, 0);
+                    else
+                        store_edge(dx, e0, V, make_uint4(0, 0, 0, 0));
                 }
                 continue;
             }
@@ -508,30 +634,17 @@ __global__ void __launch_bounds__(kThreads, kThreads <= 320 ? 2 : 1)
                     sum = __fadd2_rn(sum, make_float2(ex2(f.x), ex2(f.y)));
                 }
             }
-            float S = sum.x + sum.y, wm = m;
-#pragma unroll
-            for (int o = 16; o; o >>= 1)
-                wm = fmaxf(wm, __shfl_xor_sync(0xFFFFFFFFu, wm, o));
-            S = S == 0.0f ? 0.0f : S * ex2((m - wm) * c);
-#pragma unroll
-            for (int o = 16; o; o >>= 1)
-                S += __shfl_xor_sync(0xFFFFFFFFu, S, o);
+            const float2 pair = join_pairs(make_float2(m, sum.x + sum.y), c);
             // (pairs of this parity were joined before the factors that finish() of the row
             // two before waited for, in a cluster before the barrier of the row before)
             if (lane == 0)
-                pairs[par][warp] = make_float2(wm, S);
+                pairs[par][warp] = pair;
             __syncwarp();
-            if (csize == 1 || p.dlogits) {
-                if (lane == 0)
-                    mbar_arrive(smem_u32(&pair_bars[par]));
-                __syncwarp();
-            }
-            if (csize > 1) {
-                if (p.dlogits)
-                    cluster_arrive_relaxed();
-                else
-                    cluster_arrive();
-            }
+            if (lane == 0)
+                mbar_arrive(smem_u32(&pair_bars[par]));
+            __syncwarp();
+            if (csize > 1)
+                cluster_arrive_relaxed();
             if (!lag)
                 finish(nlive, row, tgt);
             else if (last_row >= 0)
@@ -621,7 +734,7 @@ cudaError_t launch_rows(const PolicyLossArgs &p, const RowsPlan &plan, int threa
     cfg.stream = st;
     cfg.attrs = attr;
     cfg.numAttrs = plan.csize > 1 ? 2 : 1;
-    auto kernel = k_policy_rows<T, kThreads>;
+    auto kernel = k_policy_grad<T, kThreads>;
     int ctas = 0;
     const cudaError_t e = resident_ctas(kernel, cfg, plan.csize, &ctas);
     if (e != cudaSuccess)
@@ -634,10 +747,36 @@ cudaError_t launch_rows(const PolicyLossArgs &p, const RowsPlan &plan, int threa
 constexpr int64_t SMEM_CTA = 220 * 1024;  // of 227 KB, beside the pairs and what the system keeps
 
 template <typename T>
+cudaError_t launch_forward(const PolicyLossArgs &p, int64_t units, cudaStream_t st)
+{
+    // rows over clusters until every SM has four CTAs, while a thread keeps two units
+    int csize = 1;
+    while (csize < MAX_CLUSTER && p.rows * csize < 4 * device_sms() && units >= (int64_t)csize * 2 * 512)
+        csize *= 2;
+    const int units_cta = (int)((units + csize - 1) / csize);
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = csize;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(p.rows * csize));
+    cfg.blockDim = dim3(units_cta >= 256 ? 256 : (units_cta + 31) / 32 * 32);
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = csize > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, k_token_rows<T>, p, csize, units_cta);
+}
+
+template <typename T>
 cudaError_t launch_typed(const PolicyLossArgs &p, cudaStream_t st)
 {
     constexpr int N = Elem<T>::N;
     const int64_t units = (p.V + N - 1) / N + 1;  // one more where the rows start off a boundary
+    if (!p.dlogits)
+        return launch_forward<T>(p, units, st);
     // a row in one CTA of at most 32 KB, else in the smallest cluster whose CTAs hold
     // that, else in a cluster of 8 with more per CTA
     int csize = 1;
