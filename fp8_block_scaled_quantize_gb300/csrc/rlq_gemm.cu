@@ -993,8 +993,6 @@ PFN_cuTensorMapEncodeTiled_v12000 get_encode_fn()
     return fn;
 }
 
-}  // namespace
-
 uint64_t wait_limit_ns()
 {
     static uint64_t ns = [] {
@@ -1008,8 +1006,6 @@ uint64_t wait_limit_ns()
     }();
     return ns;
 }
-
-namespace {
 
 // bf16 output [rows][cols], pitch ld elements; box 64 columns x 32 rows, 128-byte swizzle.
 rlq_status encode_out_map(CUtensorMap *map, uint16_t *base, int64_t cols, int64_t rows, int64_t ld)
@@ -1381,23 +1377,20 @@ rlq_status check_device_errors(cudaStream_t st)
     if (e != cudaSuccess)
         return cuda_status(e, "cudaStreamSynchronize");
     // every translation unit with bounded-wait kernels keeps its own error word
-    unsigned long long words[3] = {0, 0, 0};
+    unsigned long long words[2] = {0, 0};
     e = take_error_word(st, &words[0]);
     if (e == cudaSuccess)
         e = take_nvfp4_error_word(st, &words[1]);
-    if (e == cudaSuccess)
-        e = take_loss_error_word(st, &words[2]);
     if (e != cudaSuccess)
         return cuda_status(e, "reading and clearing the device error words");
-    const unsigned long long word = words[0] ? words[0] : words[1] ? words[1] : words[2];
+    const unsigned long long word = words[0] ? words[0] : words[1];
     if (word == 0)
         return RLQ_OK;
     const uint32_t code = (uint32_t)word, site = (uint32_t)(word >> 32);
     static const char *names[] = {"?", "TMA producer (stage free)", "MMA issuer (TMEM buffer free)",
                                   "MMA issuer (stage loaded)", "epilogue (partial ready)", "teardown", "drain",
-                                  "scale loader (slot free)", "epilogue (scales ready)", "FP4 converter (stage free)",
-                                  "loss (row loaded)"};
-    const char *where = site == SITE_DIAG ? "diagnostic wait" : (site < 11 ? names[site] : "?");
+                                  "scale loader (slot free)", "epilogue (scales ready)", "FP4 converter (stage free)"};
+    const char *where = site == SITE_DIAG ? "diagnostic wait" : (site < 10 ? names[site] : "?");
     return fail((rlq_status)code, "device-side wait ran out at site %u (%s)%s", site, where,
                 words[1] && !words[0] ? " in the NVFP4 GEMM" : "");
 }

@@ -125,12 +125,6 @@ struct PolicyLossArgs {
     void *dlogits;           // NULL: no gradient
     int64_t ldd;
 };
-// The loss's translation unit's error word, read and cleared (0: none).
-cudaError_t take_loss_error_word(cudaStream_t st, unsigned long long *word);
-// Bound of every device-side wait, from RLQ_WAIT_TIMEOUT_MS (rlq_gemm.cu).
-uint64_t wait_limit_ns();
-// Longest row the kernel holds.
-int64_t policy_max_vocab(int dtype);
 cudaError_t launch_policy_rows(const PolicyLossArgs &p, cudaStream_t st);
 
 // ---- block-scaled GEMM (rlq_gemm.cu) ----

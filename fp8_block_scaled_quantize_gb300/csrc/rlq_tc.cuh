@@ -28,7 +28,6 @@ enum : uint32_t {
     SITE_SCALE_EMPTY = 7,
     SITE_EPI_SCALE_FULL = 8,
     SITE_CONVERTER_EMPTY = 9,
-    SITE_LOSS_ROW = 10,
     SITE_DIAG = 99,
 };
 

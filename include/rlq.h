@@ -592,7 +592,7 @@ typedef enum { RLQ_DTYPE_BF16 = 0, RLQ_DTYPE_F32 = 1 } rlq_dtype;
  *           empty: lp and lse are 0 and its logits are not read
  *   lp      f32 [rows]; lse f32 [rows] or NULL           (outputs)
  * Logits of -inf have probability 0; a row of nothing else has lp = lse = -inf.
- * V >= 1, at most 524280 (bf16) or 262136 (fp32); temperature finite, > 0.
+ * V >= 1, below 2^30; rows below 2^28; temperature finite, > 0.
  */
 rlq_status rlq_token_logprobs(const void *logits, rlq_dtype dtype, int64_t ld, int64_t rows, int64_t V,
                               const int64_t *targets, float temperature, float *lp, float *lse,
@@ -623,8 +623,8 @@ rlq_status rlq_token_logprobs(const void *logits, rlq_dtype dtype, int64_t ld, i
  *   dlogits   [rows, V] of `dtype`, pitch ldd >= V, or NULL for the loss alone
  *             (output); may be logits itself (in place, same pitch)
  * eps_lo in [0, 1], eps_hi >= 0, tis_cap > 0, kl_beta >= 0, all finite.  Other
- * arguments and limits as for rlq_token_logprobs.  One read and one write of the
- * logits.
+ * arguments and limits as for rlq_token_logprobs.  The logits are read from memory
+ * once (and again from L2), the gradient written once.
  */
 rlq_status rlq_policy_loss(const void *logits, rlq_dtype dtype, int64_t ld, int64_t rows, int64_t V,
                            const int64_t *targets, float temperature, const float *lp_old, const float *adv,

@@ -82,8 +82,7 @@ def test_loss_refusals():
     lp = rlq.rlq_token_logprobs
     #     logits dt ld   rows V  targets temp lp   lse stream
     ok = (FAKE, 0, 100, 4, 100, FAKE, 1.0, FAKE, FAKE, None)
-    bad = [({1: 2}, INVALID), ({3: -1}, INVALID), ({4: 0}, INVALID), ({4: 524281, 2: 1 << 20}, UNSUPPORTED),
-           ({1: 1, 4: 262137, 2: 1 << 20}, UNSUPPORTED), ({3: 1 << 28}, UNSUPPORTED), ({0: None}, INVALID),
+    bad = [({1: 2}, INVALID), ({3: -1}, INVALID), ({4: 0}, INVALID), ({4: 1 << 30, 2: 1 << 31}, UNSUPPORTED), ({3: 1 << 28}, UNSUPPORTED), ({0: None}, INVALID),
            ({2: 99}, INVALID), ({0: FAKE + 1}, MISALIGNED), ({1: 1, 0: FAKE + 2}, MISALIGNED), ({5: None}, INVALID),
            ({5: FAKE + 4}, MISALIGNED), ({6: 0.0}, INVALID), ({6: float("inf")}, INVALID), ({6: -1.0}, INVALID)]
     refusals(lp, ok, bad + [({7: None}, INVALID), ({8: FAKE + 2}, MISALIGNED)])

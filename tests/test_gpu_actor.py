@@ -394,8 +394,9 @@ def test_policy_loss_options(behav, kl, clip):
         check_loss(loss_inputs(64, 3001, dtype, 9, pitch=7, behav=behav, kl=kl, clip=clip), temperature=1.0)
 
 
-def test_policy_loss_longest_bf16_row():
-    check_loss(loss_inputs(2, 524280, torch.bfloat16, 4))
+@pytest.mark.parametrize("T,V", [(2, 524280), (1, 1200007)])
+def test_policy_loss_long_rows(T, V):
+    check_loss(loss_inputs(T, V, torch.bfloat16, 4))
 
 
 @pytest.mark.parametrize("V", [999, 40000, 140000])
@@ -406,8 +407,14 @@ def test_policy_loss_in_place_and_without_gradient(V):
                            logp_ref=st["logp_ref"], **HYP)
     none = rlq.policy_loss(st["logits"], st["targets"], st["logp_old"], st["adv"], st["weight"],
                            logp_ref=st["logp_ref"], grad=False, **HYP)
-    assert none[2] is None and torch.equal(none[0], want[0]) and torch.equal(none[1], want[1])
-    assert torch.equal(st["logits"], before)
+    # (another launch shape, so another order of the row's sums)
+    assert none[2] is None and torch.equal(st["logits"], before)
+    live, lp, loss, _, elp = loss_reference({**st, "logp_behav": None}, 1.0)
+    eloss, _ = row_sensitivity({**st, "logp_behav": None}, lp, elp, 1.0)
+    rho = (lp - st["logp_old"].to(D)).exp()
+    sure = live & ((rho - 1.28).abs() > 1e-4) & ((rho - 0.8).abs() > 1e-4)
+    assert bool(((none[1].to(D) - lp).abs() <= elp)[live].all())
+    assert bool(((none[0].to(D) - loss).abs() <= eloss)[sure].all())
     over = rlq.policy_loss(st["logits"], st["targets"], st["logp_old"], st["adv"], st["weight"],
                            logp_ref=st["logp_ref"], inplace=True, **HYP)
     assert over[2] is st["logits"] and all(torch.equal(a, b) for a, b in zip(over, want))
@@ -444,7 +451,7 @@ def test_policy_loss_empty_and_masked_rows(V):
         for r in (2, 3):
             assert float(l2[r]) == 0 and float(lse[r]) == 0
         assert math.isnan(float(l2[1])) and float(lse[5]) == -math.inf
-        assert torch.equal(l2[keep], lp[keep])
+        assert bool(((l2[keep].to(D) - ref).abs() <= 1e-5 * (1 + ref.abs())).all())
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
