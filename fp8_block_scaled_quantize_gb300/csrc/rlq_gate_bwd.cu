@@ -9,7 +9,15 @@
 // keeps two bytes per column and no more.  Everything between the loads and the codes
 // is fp32.
 //
-// Bound by memory: 2 + 1 + 1 bytes read and 2 + 2 + 1 written per element of [M, F].
+// Floor: 2 + 1 + 1 bytes read and 2 + 2 + 1 written per element of [M, F], 160 us at 8192
+// x 14336 at the HBM rate.  Measured 294 us: about 48 instructions an element (decoding,
+// the sigmoid, three maxima, five encodings), issued at 55% because the 16 warps that the
+// values' registers leave a SM stand in the same phase of a tile (ncu: 4 warps a
+// scheduler, stalls spread over math throttle, fixed latency and barriers).  Copies that
+// skip work, for timing: arithmetic alone 158 us, without the loads 241, without the
+// transposed stores 248, without the row codes 242.  Slower: forming the values twice at
+// two CTAs a SM (303 us, 75 instructions an element), pairs of half tiles that exchange
+// row maxima across a cluster (335 us).
 #include <cuda_runtime.h>
 
 #include "rlq_elem.cuh"
