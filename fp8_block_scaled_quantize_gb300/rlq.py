@@ -641,6 +641,9 @@ def rmsnorm_backward(dx: torch.Tensor, h: torch.Tensor, rstd: torch.Tensor, gamm
         nbytes = _norm_workspace_bytes(M, K, torch._C._cuda_getDevice())
         if nbytes:
             workspace = torch.empty(nbytes, dtype=torch.uint8, device=dx.device)
+            if stream is not None:  # freed here, used there
+                workspace.record_stream(stream if isinstance(stream, torch.cuda.Stream)
+                                        else torch.cuda.ExternalStream(int(stream)))
     else:
         nbytes = workspace.numel() * workspace.element_size()
     _call("rlq_rmsnorm_backward", dx.data_ptr(), lddx, h.data_ptr(), ldh, r, g, _ptr(dres), ldres, dh.data_ptr(),

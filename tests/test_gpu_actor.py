@@ -497,9 +497,10 @@ def test_policy_loss_against_differences():
 
 # --------------------------------------------------- streams and graphs ---
 
-def test_another_stream_and_a_graph():
+@pytest.mark.parametrize("M", [5, 70, 300])  # the few-token kernel, single CTAs, CTA pairs
+def test_another_stream_and_a_graph(M):
     g = gen(8)
-    M, F, K = 70, 256, 512
+    F, K = 256, 512
     res, delta = normal(g, M, K), normal(g, M, K, std=0.3)
     gamma = torch.ones(K, dtype=torch.bfloat16, device=DEV)
     wq, ws = R.quant_blocks(normal(g, 2 * F, K, std=0.05))
@@ -522,6 +523,12 @@ def test_another_stream_and_a_graph():
     torch.cuda.current_stream().wait_stream(side)
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+    for handle in (side, side.cuda_stream):  # named instead of made current
+        dh, dgamma = rlq.rmsnorm_backward(delta, want[0], want[5], gamma, dres=res, stream=handle)
+        aq, as_, _, _ = rlq.gemm_gated_fprop(want[1], want[2], wq, ws, stream=handle)
+        side.synchronize()
+        assert torch.equal(dh, want[16]) and torch.equal(dgamma, want[17])
+        assert torch.equal(aq, want[6]) and torch.equal(as_, want[7])
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
         got = step()
@@ -577,3 +584,84 @@ def test_policy_loss_many_rows(T, V, pitch, offset, dtype):
     drop = z.amax(1) - z.gather(1, st["targets"].clamp(min=0)[:, None])[:, 0]
     assert bool(((lp.to(D) - want).abs() <= 156 * U + 6 * U * (drop + want.abs()))[keep].all())
     assert bool((lp[~keep] == 0).all()) and bool((lse[~keep] == 0).all())
+
+
+# ------------------------------------------------ offsets past 32 bits ---
+
+def tail_and_head(M, n):
+    return torch.cat((torch.arange(n, device=DEV), torch.arange(M - n, M, device=DEV)))
+
+
+def test_norm_past_32_bits():
+    """M K beyond 2^31: the last rows and their column group against the 64-bit form."""
+    M, K = 300003, 8192
+    g = gen(12)
+    res = torch.randint(-120, 121, (M, K), generator=g, device=DEV, dtype=torch.int8).to(torch.bfloat16)
+    gamma = torch.ones(K, dtype=torch.bfloat16, device=DEV)
+    delta = res.clone()
+    h, q, s, qT, sc, rstd = rlq.add_rmsnorm_quant_act_1x128(res, delta, gamma, 1e-6, colwise=True, inplace=True)
+    assert h is res and M * K > 2 ** 31
+    last = (M - 1) // 128 * 128  # the last column group's first row
+    rows = slice(last, M)
+    assert torch.equal(h[rows], 2 * delta[rows])
+    r, x, rtol, err = norm_reference(h[rows], gamma, 1e-6)
+    assert bool(((rstd[rows].to(D) - r).abs() <= rtol * r).all())
+    R.check_rows(q[rows], s[:, rows].contiguous(), x, err, "rows")
+    R.check_cols(qT[:, rows], sc[-1:], x, err, "columns")
+    del q, qT
+    dh, dgamma = rlq.rmsnorm_backward(delta, h, rstd, gamma)
+    want, e, _, _ = norm_bwd_reference(delta[rows], h[rows], rstd[rows], gamma, None)
+    assert bool(((dh[rows].to(D) - want).abs() <= e).all())
+    sums = torch.zeros(K, dtype=D, device=DEV)
+    mags = torch.zeros(K, dtype=D, device=DEV)
+    for a in range(0, M, 20000):
+        v = delta[a:a + 20000].to(D) * (h[a:a + 20000].to(D) * rstd[a:a + 20000].to(D)[:, None])
+        sums += v.sum(0)
+        mags += v.abs().sum(0)
+    # the sums run over at most 500 rows a team, then over teams and CTAs
+    assert bool(((dgamma.to(D) - sums).abs() <= (M // 500 + 600 + 24) * U * mags).all())
+
+
+def test_loss_past_32_bits():
+    T, V = 17003, 128256
+    g = gen(13)
+    logits = torch.empty((T, V), dtype=torch.bfloat16, device=DEV)
+    logits.normal_(0, 2, generator=g)
+    assert T * V > 2 ** 31
+    st = {"logits": logits, "targets": torch.randint(0, V, (T,), generator=g, device=DEV)}
+    st["logp_old"] = rlq.token_logprobs(logits, st["targets"])[0]
+    st["adv"] = torch.randn(T, generator=g, device=DEV)
+    st["weight"] = torch.ones(T, device=DEV)
+    pick = tail_and_head(T, 6)
+    few = {k: v[pick].clone() for k, v in st.items()} | {"logp_behav": None, "logp_ref": None, "clip_hi": None}
+    loss, lp, d = rlq.policy_loss(logits, st["targets"], st["logp_old"], st["adv"], st["weight"], temperature=1.0,
+                                  inplace=True, **HYP)
+    live, wlp, wloss, grad, elp = loss_reference(few, 1.0)
+    eloss, edlp = row_sensitivity(few, wlp, elp, 1.0)
+    assert bool(((lp[pick].to(D) - wlp).abs() <= elp).all()) and bool(((loss[pick].to(D) - wloss).abs() <= eloss).all())
+    tol = edlp[:, None] + grad.abs() * (512 * U)
+    assert bool(((d[pick].to(D) - grad).abs() <= tol + 2.0 ** -8 * (grad.abs() + tol)).all())
+
+
+def test_gate_past_32_bits():
+    """Codes [M, 2F] of more than 2^31 bytes, forward and backward: the last rows against
+    the same rows alone (each row's codes depend on that row only)."""
+    M, F, K = 75001, 14336, 128
+    g = gen(14)
+    xq, xs = R.quant_rows(normal(g, M, K))
+    wq, ws = R.quant_blocks(normal(g, 2 * F, K, std=0.1))
+    aq, as_, guq, gus = rlq.gemm_gated_fprop(xq, xs, wq, ws, checkpoint=True)
+    rlq.check()
+    assert guq.numel() > 2 ** 31
+    rows = slice((M - 1) // 128 * 128, M)  # the last token group
+    # (through the same tile shape: 300 rows that end with these)
+    part = slice(M - 300, M)
+    one = rlq.gemm_gated_fprop(xq[part], xs[:, part].contiguous(), wq, ws, checkpoint=True)
+    for a, b in ((aq[part], one[0]), (as_[:, part], one[1]), (guq[part], one[2]), (gus[:, part], one[3])):
+        assert torch.equal(a, b)
+    del aq, one
+    da = normal(g, M, F)
+    q, s, qT, sc, aT, ac = rlq.gated_backward(da, guq, gus)
+    two = rlq.gated_backward(da[rows], guq[rows], gus[:, rows].contiguous())
+    assert torch.equal(q[rows], two[0]) and torch.equal(s[:, rows], two[1]) and torch.equal(qT[:, rows], two[2])
+    assert torch.equal(sc[-1:], two[3]) and torch.equal(aT[:, rows], two[4]) and torch.equal(ac[-1:], two[5])
