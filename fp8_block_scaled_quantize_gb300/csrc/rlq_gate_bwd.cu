@@ -10,12 +10,11 @@
 // is fp32.
 //
 // Floor: 2 + 1 + 1 bytes read and 2 + 2 + 1 written per element of [M, F], 160 us at 8192
-// x 14336 at the HBM rate.  Measured 294 us: about 48 instructions an element (decoding,
-// the sigmoid, three maxima, five encodings), issued at 55% because the 16 warps that the
+// x 14336 at the HBM rate.  Measured 265 us (294 with per-thread stores of the transposed
+// codes and 8-byte copies): the instructions of an element (51 before, 17 of them integer;
+// decoding, the sigmoid, three maxima, five encodings), issued at about 55% because the 16 warps that the
 // values' registers leave a SM stand in the same phase of a tile (ncu: 4 warps a
-// scheduler, stalls spread over math throttle, fixed latency and barriers).  Copies that
-// skip work, for timing: arithmetic alone 158 us, without the loads 241, without the
-// transposed stores 248, without the row codes 242.  Slower: forming the values twice at
+// scheduler, stalls spread over math throttle, fixed latency and barriers).  Slower: forming the values twice at
 // two CTAs a SM (303 us, 75 instructions an element), pairs of half tiles that exchange
 // row maxima across a cluster (335 us).
 #include <cuda_runtime.h>
@@ -31,7 +30,10 @@ constexpr int THREADS = 512;
 // Shared memory: two prefetched tiles (per thread four rows of 16 + 8 + 8 bytes) and
 // their 2 x 128 scales, the three transposed code tiles, 16 warps' column maxima.
 constexpr int IN_BYTES = THREADS * 4 * 32;
-constexpr int TILE_BYTES = GRP * GRP;
+// A code tile is 128 slots of 144 bytes, a column's 128 codes each: column 8 c + j in
+// slot 16 j + c, so that the lanes that write one j differ in the bank.
+constexpr int SLOT = GRP + 16;
+constexpr int TILE_BYTES = GRP * SLOT;
 constexpr int OFF_SCALES = 2 * IN_BYTES;
 constexpr int OFF_TILES = OFF_SCALES + 2 * 2 * GRP * 4;
 constexpr int OFF_PART = OFF_TILES + 3 * TILE_BYTES;
@@ -66,13 +68,15 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void *src, uint32_t b
 {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
-__device__ __forceinline__ void copy8(uint32_t dst, const void *src, uint32_t bytes)
-{
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
 __device__ __forceinline__ void copy4(uint32_t dst, const void *src, uint32_t bytes)
 {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+// Shared -> global by the copy engine: both addresses and the size multiples of 16.
+__device__ __forceinline__ void bulk_store(void *dst, uint32_t src, int bytes)
+{
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(bytes)
+                 : "memory");
 }
 
 // 8 E4M3 codes -> fp32, times s (each code is exact in fp16, so the product is the
@@ -113,42 +117,65 @@ __global__ void __launch_bounds__(THREADS, 1) k_gate_bwd(const GateBwd p)
     const int own = (t & 15) >> 1;  // the group maximum this lane ends up with: matrix own / 4, row own % 4
     const int64_t fb = p.F / GRP;   // scale rows of one projection
 
-    auto prefetch = [&](int tile, int buf) {
-        const int mt = tile % p.m_tiles, ft = tile / p.m_tiles;
-        const int64_t m = (int64_t)mt * GRP + 4 * rg, f = (int64_t)ft * GRP + 8 * cg;
+    // Row block and column block of a tile, and the step from one of this CTA's tiles to
+    // the next.
+    int mt = blockIdx.x % p.m_tiles, ft = blockIdx.x / p.m_tiles;
+    const int step_m = gridDim.x % p.m_tiles, step_f = gridDim.x / p.m_tiles;
+    auto prefetch = [&](int pm, int pf, int buf) {
+        const int64_t m = (int64_t)pm * GRP + 4 * rg, f = (int64_t)pf * GRP;
         const int left = (int)(p.M - m < 4 ? p.M - m : 4);  // rows of mine inside the matrix (may be <= 0)
-        const uint16_t *ap = p.da + m * p.ldda + f;
-        const uint8_t *gp = p.guq + m * p.ldguq + f;
-        const uint32_t in = smem0 + buf * IN_BYTES + t * 16, in8 = smem0 + buf * IN_BYTES + THREADS * 64 + t * 8;
+        const uint32_t in = smem0 + buf * IN_BYTES + t * 16;
+        // da: my 8 columns of four rows; the codes: rows cg / 8 and 2 + cg / 8 of the
+        // half-warp's four, 16 columns each
+        const uint16_t *ap = p.da + m * p.ldda + f + 8 * cg;
+        const int r = cg >> 3;
+        const uint8_t *gp = p.guq + (m + r) * p.ldguq + f + 16 * (cg & 7);
+        const uint32_t in8 = smem0 + buf * IN_BYTES + THREADS * 64 + rg * 512 + cg * 16;
+        if (left == 4) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const bool ok = i < left;
-            copy16(in + i * THREADS * 16, ok ? ap : p.da, ok ? 16 : 0);
-            copy8(in8 + i * THREADS * 8, ok ? gp : p.guq, ok ? 8 : 0);
-            copy8(in8 + THREADS * 32 + i * THREADS * 8, ok ? gp + p.F : p.guq, ok ? 8 : 0);
-            ap += p.ldda;
-            gp += p.ldguq;
+            for (int i = 0; i < 4; ++i, ap += p.ldda)
+                copy16(in + i * THREADS * 16, ap, 16);
+            copy16(in8, gp, 16);
+            copy16(in8 + THREADS * 32, gp + p.F, 16);
+            gp += 2 * p.ldguq;
+            copy16(in8 + 256, gp, 16);
+            copy16(in8 + THREADS * 32 + 256, gp + p.F, 16);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                copy16(in + i * THREADS * 16, i < left ? ap + i * p.ldda : p.da, i < left ? 16 : 0);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const bool ok = 2 * i + r < left;
+                const uint8_t *g = ok ? gp + 2 * i * p.ldguq : p.guq;
+                copy16(in8 + i * 256, g, ok ? 16 : 0);
+                copy16(in8 + THREADS * 32 + i * 256, ok ? g + p.F : g, ok ? 16 : 0);
+            }
         }
         if (cg < 8) {  // this half-warp's scales: four rows of g, four of u
             const bool ok = (cg & 3) < left;
             copy4(smem0 + OFF_SCALES + (buf * 2 * GRP + 8 * rg + cg) * 4,
-                  ok ? p.gus + ((cg >> 2) * fb + ft) * p.ld_gus + m + (cg & 3) : p.gus, ok ? 4 : 0);
+                  ok ? p.gus + ((cg >> 2) * fb + pf) * p.ld_gus + m + (cg & 3) : p.gus, ok ? 4 : 0);
         }
     };
 
     int tile = blockIdx.x;
     if (tile < p.tiles)
-        prefetch(tile, 0);
+        prefetch(mt, ft, 0);
     asm volatile("cp.async.commit_group;" ::: "memory");
     for (int buf = 0; tile < p.tiles; tile += gridDim.x, buf ^= 1) {
+        int nm = mt + step_m, nf = ft + step_f;
+        if (nm >= p.m_tiles) {
+            nm -= p.m_tiles;
+            ++nf;
+        }
         if (tile + (int)gridDim.x < p.tiles)
-            prefetch(tile + gridDim.x, buf ^ 1);
+            prefetch(nm, nf, buf ^ 1);
         asm volatile("cp.async.commit_group;" ::: "memory");
         asm volatile("cp.async.wait_group 1;" ::: "memory");
         // A thread reads what its half-warp copied.  The last tile's codes may still be
         // leaving: shared memory that they use is written after the next barrier only.
         __syncwarp();
-        const int mt = tile % p.m_tiles, ft = tile / p.m_tiles;
         const int64_t m0 = (int64_t)mt * GRP, f0 = (int64_t)ft * GRP;
         const int rows = (int)(p.M - m0 < GRP ? p.M - m0 : GRP);
         const uint8_t *in = smem + buf * IN_BYTES;
@@ -160,8 +187,8 @@ __global__ void __launch_bounds__(THREADS, 1) k_gate_bwd(const GateBwd p)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             float2 g[4], u[4];
-            decode8(*reinterpret_cast<const uint2 *>(in + THREADS * 64 + (i * THREADS + t) * 8), sg4[i], g);
-            decode8(*reinterpret_cast<const uint2 *>(in + THREADS * 96 + (i * THREADS + t) * 8), su4[i], u);
+            decode8(*reinterpret_cast<const uint2 *>(in + THREADS * 64 + rg * 512 + i * GRP + 8 * cg), sg4[i], g);
+            decode8(*reinterpret_cast<const uint2 *>(in + THREADS * 96 + rg * 512 + i * GRP + 8 * cg), su4[i], u);
             const uint4 dv = *reinterpret_cast<const uint4 *>(in + (i * THREADS + t) * 16);
             const uint32_t dw[4] = {dv.x, dv.y, dv.z, dv.w};
 #pragma unroll
@@ -188,6 +215,8 @@ __global__ void __launch_bounds__(THREADS, 1) k_gate_bwd(const GateBwd p)
 #pragma unroll
         for (int k = 0; k < 3; ++k)
             store_column_maxima(cmax[k], t & 16, part + (warp * 3 + k) * GRP + 8 * cg);
+        // (the copies of the last tile's codes have read them: waited for by their issuers)
+        asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
         __syncthreads();
         float cs = 1.0f;
         if (t < 3 * GRP) {
@@ -216,15 +245,27 @@ __global__ void __launch_bounds__(THREADS, 1) k_gate_bwd(const GateBwd p)
         const float rs = group_scale(x1), rr = scale_rcp(rs), rp = scale_pre(rs);
         if ((t & 1) == 0 && 4 * rg + (own & 3) < rows)
             p.s[((own >> 2) * fb + ft) * p.lds + m0 + 4 * rg + (own & 3)] = rs;
-        const bool pre_rows = __any_sync(0xFFFFFFFFu, rp != 1.0f);
+        uint8_t *qp = p.q + (m0 + 4 * rg) * p.ldq + f0 + 8 * cg;
+        const int left = rows - 4 * rg;
+        if (__any_sync(0xFFFFFFFFu, rp != 1.0f)) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const int i = k & 3, r = 4 * rg + i, src = (t & 16) + 2 * k;
-            const float q = __shfl_sync(0xFFFFFFFFu, rr, src);
-            const float pre = pre_rows ? __shfl_sync(0xFFFFFFFFu, rp, src) : 1.0f;
-            if (r < rows)
-                *reinterpret_cast<uint2 *>(p.q + (m0 + r) * p.ldq + (k >> 2) * p.F + f0 + 8 * cg) =
-                    encode8f(val[k >> 2][i], pre, q);
+            for (int k = 0; k < 8; ++k) {
+                const int i = k & 3, src = (t & 16) + 2 * k;
+                const float q = __shfl_sync(0xFFFFFFFFu, rr, src), pre = __shfl_sync(0xFFFFFFFFu, rp, src);
+                if (i < left)
+                    *reinterpret_cast<uint2 *>(qp + i * p.ldq + (k >> 2) * p.F) = encode8f(val[k >> 2][i], pre, q);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i, qp += p.ldq) {
+                const float qg = __shfl_sync(0xFFFFFFFFu, rr, (t & 16) + 2 * i);
+                const float qu = __shfl_sync(0xFFFFFFFFu, rr, (t & 16) + 8 + 2 * i);
+                const uint2 cg8 = encode8f(val[0][i], 1.0f, qg), cu8 = encode8f(val[1][i], 1.0f, qu);
+                if (i < left) {
+                    *reinterpret_cast<uint2 *>(qp) = cg8;
+                    *reinterpret_cast<uint2 *>(qp + p.F) = cu8;
+                }
+            }
         }
         // Column groups, with the reciprocals that now stand in the first warp's places.
         // (Columns whose scale is below 2^-100 are scaled up first.)
@@ -248,25 +289,40 @@ __global__ void __launch_bounds__(THREADS, 1) k_gate_bwd(const GateBwd p)
             const float4 r1 = *reinterpret_cast<const float4 *>(part + k * GRP + 8 * cg + 4);
             const float2 r[4] = {make_float2(r0.x, r0.y), make_float2(r0.z, r0.w), make_float2(r1.x, r1.y),
                                  make_float2(r1.z, r1.w)};
-            uint8_t *out = tiles + k * TILE_BYTES + 8 * cg * GRP + 8 * ((rg >> 1) ^ cg) + 4 * (rg & 1);
+            uint8_t *out = tiles + k * TILE_BYTES + cg * SLOT + 4 * rg;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 float2 y[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     y[i] = __fmul2_rn(val[k][i][j], r[j]);
-                *reinterpret_cast<uint32_t *>(out + 2 * j * GRP) =
+                *reinterpret_cast<uint32_t *>(out + 2 * j * 16 * SLOT) =
                     e4m3x2(y[0].x, y[1].x) | (e4m3x2(y[2].x, y[3].x) << 16);
-                *reinterpret_cast<uint32_t *>(out + (2 * j + 1) * GRP) =
+                *reinterpret_cast<uint32_t *>(out + (2 * j + 1) * 16 * SLOT) =
                     e4m3x2(y[0].y, y[1].y) | (e4m3x2(y[2].y, y[3].y) << 16);
             }
         }
+        // A thread a column: its codes leave by the copy engine, which reads shared memory
+        // through the async proxy.  (The last rows past a multiple of 16 by byte stores.)
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncthreads();
-        store_tile_T(tiles, t, THREADS, rows, p.qT + f0 * p.ldqT + m0, p.ldqT);
-        store_tile_T(tiles + TILE_BYTES, t, THREADS, rows, p.qT + (p.F + f0) * p.ldqT + m0, p.ldqT);
-        store_tile_T(tiles + 2 * TILE_BYTES, t, THREADS, rows, p.aT + f0 * p.ldaT + m0, p.ldaT);
+        if (t < 3 * GRP) {
+            const int k = t >> 7, c = t & 127;
+            const int64_t col = f0 + c;
+            uint8_t *dst = (k < 2 ? p.qT + (k * p.F + col) * p.ldqT : p.aT + col * p.ldaT) + m0;
+            const uint8_t *slot = tiles + k * TILE_BYTES + ((c & 7) * 16 + (c >> 3)) * SLOT;
+            const int wide = rows & ~15;
+            if (wide)
+                bulk_store(dst, smem0 + (uint32_t)(slot - smem), wide);
+            for (int i = wide; i < rows; ++i)
+                dst[i] = slot[i];
+            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+        }
+        mt = nm;
+        ft = nf;
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
+    asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
 
 }  // namespace
