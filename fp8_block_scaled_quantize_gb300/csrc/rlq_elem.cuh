@@ -49,6 +49,20 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi)
     return d;
 }
 
+// Four of them in a word, `a` in bits 0..7.  (One block of assembly, so that the pairs
+// meet in the word without being widened first.)
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d)
+{
+    uint32_t w;
+    asm("{\n\t.reg .b16 lo, hi;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n\t"
+        "mov.b32 %0, {lo, hi};\n\t}"
+        : "=r"(w)
+        : "f"(a), "f"(b), "f"(c), "f"(d));
+    return w;
+}
+
 // Scale of a group: fl32(amax / 448), 1 for an all-zero group.
 __device__ __forceinline__ float group_scale(float amax)
 {
@@ -78,8 +92,8 @@ __device__ __forceinline__ uint2 encode8f(const float2 (&v)[4], float pre, float
 #pragma unroll
     for (int i = 0; i < 4; ++i)
         f[i] = __fmul2_rn(f[i], r2);
-    return make_uint2(e4m3x2(f[0].x, f[0].y) | (e4m3x2(f[1].x, f[1].y) << 16),
-                      e4m3x2(f[2].x, f[2].y) | (e4m3x2(f[3].x, f[3].y) << 16));
+    return make_uint2(e4m3x4(f[0].x, f[0].y, f[1].x, f[1].y),
+                      e4m3x4(f[2].x, f[2].y, f[3].x, f[3].y));
 }
 
 __device__ __forceinline__ uint2 encode8f(const float (&v)[8], float s, float rcp)

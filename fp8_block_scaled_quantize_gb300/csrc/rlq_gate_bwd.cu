@@ -84,11 +84,16 @@ __device__ __forceinline__ void bulk_store(void *dst, uint32_t src, int bytes)
 __device__ __forceinline__ void decode8(uint2 c, float s, float2 (&f)[4])
 {
     const uint32_t w[2] = {c.x, c.y};
+    uint32_t h4[4];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+            "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+            : "=r"(h4[2 * i]), "=r"(h4[2 * i + 1])
+            : "r"(w[i]));
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const uint16_t two = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
-        uint32_t h;
-        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(two));
+        const uint32_t h = h4[i];
         float lo, hi;
         asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
             : "=f"(lo), "=f"(hi)
@@ -297,9 +302,9 @@ __global__ void __launch_bounds__(THREADS, 1) k_gate_bwd(const GateBwd p)
                 for (int i = 0; i < 4; ++i)
                     y[i] = __fmul2_rn(val[k][i][j], r[j]);
                 *reinterpret_cast<uint32_t *>(out + 2 * j * 16 * SLOT) =
-                    e4m3x2(y[0].x, y[1].x) | (e4m3x2(y[2].x, y[3].x) << 16);
+                    e4m3x4(y[0].x, y[1].x, y[2].x, y[3].x);
                 *reinterpret_cast<uint32_t *>(out + (2 * j + 1) * 16 * SLOT) =
-                    e4m3x2(y[0].y, y[1].y) | (e4m3x2(y[2].y, y[3].y) << 16);
+                    e4m3x4(y[0].y, y[1].y, y[2].y, y[3].y);
             }
         }
         // A thread a column: its codes leave by the copy engine, which reads shared memory

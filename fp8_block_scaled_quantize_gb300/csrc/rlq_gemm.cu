@@ -311,7 +311,7 @@ __device__ __forceinline__ void store_codes64(uint8_t *__restrict__ dst, uint32_
         for (int i = 0; i < 4; ++i) {
             const float2 a = __fmul2_rn(__fmul2_rn(v[8 * j + 2 * i], pre), r);
             const float2 b = __fmul2_rn(__fmul2_rn(v[8 * j + 2 * i + 1], pre), r);
-            w[i] = e4m3x2(a.x, a.y) | (e4m3x2(b.x, b.y) << 16);
+            w[i] = e4m3x4(a.x, a.y, b.x, b.y);
         }
         if (kStage)
             asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(

@@ -204,11 +204,11 @@ __global__ void __launch_bounds__(256, 3) k_norm_cols(const uint16_t *__restrict
         for (int i = 0; i < 8; ++i)
             y[i] = __fmul2_rn(x[i][j], rc[j]);
         *reinterpret_cast<uint2 *>(out + 2 * j * GRP) =
-            make_uint2(e4m3x2(y[0].x, y[1].x) | (e4m3x2(y[2].x, y[3].x) << 16),
-                       e4m3x2(y[4].x, y[5].x) | (e4m3x2(y[6].x, y[7].x) << 16));
+            make_uint2(e4m3x4(y[0].x, y[1].x, y[2].x, y[3].x),
+                       e4m3x4(y[4].x, y[5].x, y[6].x, y[7].x));
         *reinterpret_cast<uint2 *>(out + (2 * j + 1) * GRP) =
-            make_uint2(e4m3x2(y[0].y, y[1].y) | (e4m3x2(y[2].y, y[3].y) << 16),
-                       e4m3x2(y[4].y, y[5].y) | (e4m3x2(y[6].y, y[7].y) << 16));
+            make_uint2(e4m3x4(y[0].y, y[1].y, y[2].y, y[3].y),
+                       e4m3x4(y[4].y, y[5].y, y[6].y, y[7].y));
     }
     __syncthreads();
     store_tile_T(tile, t, 256, rows, qT + k0 * ldqT + m0, ldqT);
