@@ -698,9 +698,8 @@ rlq_status rlq_gated_backward(const uint16_t *da, int64_t ldda, const uint8_t *g
     RLQ_TRY(check_scales("sc", sc, ldsc, 2 * F));
     RLQ_TRY(check_codes("aT", aT, ldaT, M));
     RLQ_TRY(check_scales("ac", ac, ldac, F));
-    return cuda_status(launch_gated_backward(da, ldda, guq, ldguq, gus, ldgus, q, ldq, s, lds, qT, ldqT, sc, ldsc, aT,
-                                             ldaT, ac, ldac, M, F, cs(stream)),
-                       "gated backward launch");
+    return launch_gated_backward(da, ldda, guq, ldguq, gus, ldgus, q, ldq, s, lds, qT, ldqT, sc, ldsc, aT, ldaT, ac,
+                                 ldac, M, F, cs(stream));
 }
 
 rlq_status rlq_token_logprobs(const void *logits, rlq_dtype dtype, int64_t ld, int64_t rows, int64_t V,

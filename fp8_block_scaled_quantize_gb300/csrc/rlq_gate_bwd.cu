@@ -17,6 +17,7 @@
 // scheduler, stalls spread over math throttle, fixed latency and barriers).  Slower: forming the values twice at
 // two CTAs a SM (303 us, 75 instructions an element), pairs of half tiles that exchange
 // row maxima across a cluster (335 us).
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include "rlq_elem.cuh"
@@ -30,15 +31,16 @@ constexpr int THREADS = 512;
 // Shared memory: two prefetched tiles (per thread four rows of 16 + 8 + 8 bytes) and
 // their 2 x 128 scales, the three transposed code tiles, 16 warps' column maxima.
 constexpr int IN_BYTES = THREADS * 4 * 32;
-// A code tile is 128 slots of 144 bytes, a column's 128 codes each: column 8 c + j in
-// slot 16 j + c, so that the lanes that write one j differ in the bank.
-constexpr int SLOT = GRP + 16;
-constexpr int TILE_BYTES = GRP * SLOT;
+// A code tile is 128 slots of 128 bytes, a column's codes each: column 8 c + j in slot
+// 16 j + c, its eight 16-byte chunks XOR c mod 8 (the 128-byte swizzle), so that the
+// lanes that write one j differ in the bank.
+constexpr int TILE_BYTES = GRP * GRP;
 constexpr int OFF_SCALES = 2 * IN_BYTES;
 constexpr int OFF_TILES = OFF_SCALES + 2 * 2 * GRP * 4;
 constexpr int OFF_PART = OFF_TILES + 3 * TILE_BYTES;
-constexpr int SMEM_BYTES = OFF_PART + 16 * 3 * GRP * 4;
-static_assert(SMEM_BYTES <= 232448, "shared memory budget");
+constexpr int OFF_RCP = OFF_PART + 16 * 3 * GRP * 4;  // 3 x 128 reciprocals, 3 x 128 factors
+constexpr int SMEM_BYTES = OFF_RCP + 2 * 3 * GRP * 4;
+static_assert(SMEM_BYTES <= 232448 && OFF_TILES % 1024 == 0, "shared memory budget; the swizzle's period");
 
 struct GateBwd {
     const uint16_t *da;
@@ -72,10 +74,20 @@ __device__ __forceinline__ void copy4(uint32_t dst, const void *src, uint32_t by
 {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
-// Shared -> global by the copy engine: both addresses and the size multiples of 16.
-__device__ __forceinline__ void bulk_store(void *dst, uint32_t src, int bytes)
+// A barrier of the CTA that some warps wait at and others only pass.
+__device__ __forceinline__ void bar_wait()
 {
-    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(bytes)
+    asm volatile("bar.sync %0, %1;" ::"n"(1), "n"(THREADS) : "memory");
+}
+__device__ __forceinline__ void bar_pass()
+{
+    asm volatile("bar.arrive %0, %1;" ::"n"(1), "n"(THREADS) : "memory");
+}
+// Shared -> global by the copy engine: a box of 16 columns of 128 codes.
+__device__ __forceinline__ void store_box(const CUtensorMap *map, uint32_t src, int x, int y, int z)
+{
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"((uint64_t)map),
+                 "r"(src), "r"(x), "r"(y), "r"(z)
                  : "memory");
 }
 
@@ -110,11 +122,13 @@ __device__ __forceinline__ void decode8(uint2 c, float s, float2 (&f)[4])
 // remaining ones to the partner lane), after which a lane pair holds one group's and
 // computes its scale once.  Column maxima go over the rows of a thread, the two halves
 // of a warp and, in shared memory, the 16 warps.
-__global__ void __launch_bounds__(THREADS, 1) k_gate_bwd(const GateBwd p)
+__global__ void __launch_bounds__(THREADS, 1) k_gate_bwd(const GateBwd p, const __grid_constant__ CUtensorMap tmQ,
+                                                         const __grid_constant__ CUtensorMap tmA)
 {
     pdl_begin();
-    extern __shared__ __align__(16) uint8_t smem[];
+    extern __shared__ __align__(1024) uint8_t smem[];
     float *part = reinterpret_cast<float *>(smem + OFF_PART);  // [warp][3][128]
+    float *rcp = reinterpret_cast<float *>(smem + OFF_RCP);    // [3][128], factors behind them
     uint8_t *tiles = smem + OFF_TILES;
     const uint32_t smem0 = (uint32_t)__cvta_generic_to_shared(smem);
     const int t = threadIdx.x, cg = t & 15, rg = t >> 4, warp = t >> 5;
@@ -222,9 +236,11 @@ __global__ void __launch_bounds__(THREADS, 1) k_gate_bwd(const GateBwd p)
             store_column_maxima(cmax[k], t & 16, part + (warp * 3 + k) * GRP + 8 * cg);
         // (the copies of the last tile's codes have read them: waited for by their issuers)
         asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-        __syncthreads();
         float cs = 1.0f;
-        if (t < 3 * GRP) {
+        if (t >= 3 * GRP) {
+            bar_pass();
+        } else {
+            bar_wait();
             float c = part[t];
 #pragma unroll
             for (int w = 1; w < 16; ++w)
@@ -235,7 +251,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_gate_bwd(const GateBwd p)
                 p.sc[(int64_t)mt * p.ldsc + k * p.F + f0 + cc] = cs;
             else
                 p.ac[(int64_t)mt * p.ldac + f0 + cc] = cs;
-            part[t] = scale_rcp(cs);  // (only this thread reads column t of the maxima)
+            rcp[t] = scale_rcp(cs);
         }
         // row groups
         float x4[4], x2[2], x1;
@@ -272,17 +288,16 @@ __global__ void __launch_bounds__(THREADS, 1) k_gate_bwd(const GateBwd p)
                 }
             }
         }
-        // Column groups, with the reciprocals that now stand in the first warp's places.
-        // (Columns whose scale is below 2^-100 are scaled up first.)
+        // Column groups.  (Columns whose scale is below 2^-100 are scaled up first.)
         if (__syncthreads_or(cs < 0x1p-100f)) {
             if (t < 3 * GRP)
-                part[3 * GRP + t] = scale_pre(cs);
+                rcp[3 * GRP + t] = scale_pre(cs);
             __syncthreads();
 #pragma unroll
             for (int k = 0; k < 3; ++k)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const float2 f = *reinterpret_cast<const float2 *>(part + (3 + k) * GRP + 8 * cg + 2 * j);
+                    const float2 f = *reinterpret_cast<const float2 *>(rcp + (3 + k) * GRP + 8 * cg + 2 * j);
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
                         val[k][i][j] = __fmul2_rn(val[k][i][j], f);
@@ -290,38 +305,54 @@ __global__ void __launch_bounds__(THREADS, 1) k_gate_bwd(const GateBwd p)
         }
 #pragma unroll
         for (int k = 0; k < 3; ++k) {
-            const float4 r0 = *reinterpret_cast<const float4 *>(part + k * GRP + 8 * cg);
-            const float4 r1 = *reinterpret_cast<const float4 *>(part + k * GRP + 8 * cg + 4);
+            const float4 r0 = *reinterpret_cast<const float4 *>(rcp + k * GRP + 8 * cg);
+            const float4 r1 = *reinterpret_cast<const float4 *>(rcp + k * GRP + 8 * cg + 4);
             const float2 r[4] = {make_float2(r0.x, r0.y), make_float2(r0.z, r0.w), make_float2(r1.x, r1.y),
                                  make_float2(r1.z, r1.w)};
-            uint8_t *out = tiles + k * TILE_BYTES + cg * SLOT + 4 * rg;
+            uint8_t *out = tiles + k * TILE_BYTES + cg * GRP + 16 * ((rg >> 2) ^ (cg & 7)) + 4 * (rg & 3);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 float2 y[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     y[i] = __fmul2_rn(val[k][i][j], r[j]);
-                *reinterpret_cast<uint32_t *>(out + 2 * j * 16 * SLOT) =
+                *reinterpret_cast<uint32_t *>(out + 2 * j * 16 * GRP) =
                     e4m3x4(y[0].x, y[1].x, y[2].x, y[3].x);
-                *reinterpret_cast<uint32_t *>(out + (2 * j + 1) * 16 * SLOT) =
+                *reinterpret_cast<uint32_t *>(out + (2 * j + 1) * 16 * GRP) =
                     e4m3x4(y[0].y, y[1].y, y[2].y, y[3].y);
             }
         }
-        // A thread a column: its codes leave by the copy engine, which reads shared memory
-        // through the async proxy.  (The last rows past a multiple of 16 by byte stores.)
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncthreads();
-        if (t < 3 * GRP) {
-            const int k = t >> 7, c = t & 127;
-            const int64_t col = f0 + c;
-            uint8_t *dst = (k < 2 ? p.qT + (k * p.F + col) * p.ldqT : p.aT + col * p.ldaT) + m0;
-            const uint8_t *slot = tiles + k * TILE_BYTES + ((c & 7) * 16 + (c >> 3)) * SLOT;
-            const int wide = rows & ~15;
-            if (wide)
-                bulk_store(dst, smem0 + (uint32_t)(slot - smem), wide);
-            for (int i = wide; i < rows; ++i)
-                dst[i] = slot[i];
-            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+        // The column codes leave by the copy engine, which reads shared memory through the
+        // async proxy: 24 boxes, one or two a warp (all of them from one warp: 253 us at
+        // the size above).  The last row block's by 16-byte and byte stores.
+        if (rows == GRP) {
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncthreads();
+            const int b = warp + 16 * (t & 31);
+            if (b < 24) {
+                const int k = b >> 3, j = b & 7;
+                store_box(k < 2 ? &tmQ : &tmA, smem0 + OFF_TILES + k * TILE_BYTES + j * 16 * GRP, (int)m0, j,
+                          (int)(((k == 1 ? p.F : 0) + f0) >> 3));
+                asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+            }
+        } else {
+            __syncthreads();
+            for (int b = t; b < 3 * GRP * 8; b += THREADS) {
+                const int k = b >> 10, slot = (b >> 3) & 127, i = b & 7;
+                const int64_t col = f0 + 8 * (slot & 15) + (slot >> 4);
+                const uint4 c = *reinterpret_cast<const uint4 *>(tiles + k * TILE_BYTES + slot * GRP +
+                                                                 16 * (i ^ (slot & 7)));
+                uint8_t *dst = (k < 2 ? p.qT + (k * p.F + col) * p.ldqT : p.aT + col * p.ldaT) + m0 + 16 * i;
+                if (16 * i + 16 <= rows) {
+                    *reinterpret_cast<uint4 *>(dst) = c;
+                } else {
+                    const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        if (16 * i + e < rows)
+                            dst[e] = (uint8_t)(w[e >> 2] >> (8 * (e & 3)));
+                }
+            }
         }
         mt = nm;
         ft = nf;
@@ -332,16 +363,22 @@ __global__ void __launch_bounds__(THREADS, 1) k_gate_bwd(const GateBwd p)
 
 }  // namespace
 
-cudaError_t launch_gated_backward(const uint16_t *da, int64_t ldda, const uint8_t *guq, int64_t ldguq, const float *gus,
+rlq_status launch_gated_backward(const uint16_t *da, int64_t ldda, const uint8_t *guq, int64_t ldguq, const float *gus,
                                   int64_t ld_gus, uint8_t *q, int64_t ldq, float *s, int64_t lds, uint8_t *qT,
                                   int64_t ldqT, float *sc, int64_t ldsc, uint8_t *aT, int64_t ldaT, float *ac,
                                   int64_t ldac, int64_t M, int64_t F, cudaStream_t st)
 {
     const int64_t m_tiles = (M + GRP - 1) / GRP, tiles = m_tiles * (F / GRP);
-    if (tiles > INT32_MAX / 2)
-        return cudaErrorInvalidValue;
     const GateBwd p = {da, ldda, guq, ldguq, gus, ld_gus, q,  ldq, s, lds, qT,           ldqT,
                        sc, ldsc, aT,  ldaT,  ac,  ldac,   M,  F,   (int)m_tiles, (int)tiles};
+    CUtensorMap tmQ = {}, tmA = {};
+    if (M >= GRP) {  // (a tile of fewer rows does without)
+        rlq_status r = encode_columns_map(&tmQ, qT, M, 2 * F, ldqT);
+        if (r == RLQ_OK)
+            r = encode_columns_map(&tmA, aT, M, F, ldaT);
+        if (r != RLQ_OK)
+            return r;
+    }
     // (once per device)
     static std::atomic<bool> set[64];
     int dev = 0;
@@ -350,10 +387,11 @@ cudaError_t launch_gated_backward(const uint16_t *da, int64_t ldda, const uint8_
         e = cudaFuncSetAttribute(k_gate_bwd, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
         set[dev & 63].store(e == cudaSuccess, std::memory_order_relaxed);
     }
-    if (e != cudaSuccess)
-        return e;
-    const int64_t sms = device_sms();
-    return launch_pdl(k_gate_bwd, dim3((unsigned)(tiles < sms ? tiles : sms)), dim3(THREADS), SMEM_BYTES, st, p);
+    if (e == cudaSuccess) {
+        const int64_t sms = device_sms();
+        e = launch_pdl(k_gate_bwd, dim3((unsigned)(tiles < sms ? tiles : sms)), dim3(THREADS), SMEM_BYTES, st, p, tmQ, tmA);
+    }
+    return cuda_status(e, "gated backward launch");
 }
 
 }  // namespace rlq

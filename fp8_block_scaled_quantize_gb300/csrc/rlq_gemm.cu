@@ -1098,6 +1098,28 @@ rlq_status encode_codes_out_map(CUtensorMap *map, uint8_t *base, int64_t cols, i
     return RLQ_OK;
 }
 
+}  // namespace
+
+rlq_status encode_columns_map(CUtensorMap_st *map, uint8_t *base, int64_t M, int64_t cols, int64_t ld)
+{
+    auto enc = get_encode_fn();
+    if (!enc)
+        return fail(RLQ_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+    const cuuint64_t dims[3] = {(cuuint64_t)M, 8, (cuuint64_t)(cols / 8)};
+    const cuuint64_t strides[2] = {(cuuint64_t)ld, (cuuint64_t)ld * 8};
+    const cuuint32_t box[3] = {128, 1, 16};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, base, dims, strides, box, estr,
+                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                           CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS)
+        return fail(RLQ_ERR_CUDA, "cuTensorMapEncodeTiled failed (CUresult %d) for %lld columns of %lld codes, pitch %lld",
+                    (int)r, (long long)cols, (long long)M, (long long)ld);
+    return RLQ_OK;
+}
+
+namespace {
+
 struct DevInfo {
     int sms = 0;
     bool attr_set[16] = {};

@@ -106,7 +106,7 @@ cudaError_t launch_rmsnorm_backward(const uint16_t *dx, int64_t lddx, const uint
                                     int64_t lddh, float *dgamma, int64_t M, int64_t K, float *ws, cudaStream_t st);
 
 // ---- backward of the gated block's activation (rlq_gate_bwd.cu) ----
-cudaError_t launch_gated_backward(const uint16_t *da, int64_t ldda, const uint8_t *guq, int64_t ldguq, const float *gus,
+rlq_status launch_gated_backward(const uint16_t *da, int64_t ldda, const uint8_t *guq, int64_t ldguq, const float *gus,
                                   int64_t ld_gus, uint8_t *q, int64_t ldq, float *s, int64_t lds, uint8_t *qT,
                                   int64_t ldqT, float *sc, int64_t ldsc, uint8_t *aT, int64_t ldaT, float *ac,
                                   int64_t ldac, int64_t M, int64_t F, cudaStream_t st);
@@ -128,6 +128,11 @@ struct PolicyLossArgs {
 cudaError_t launch_policy_rows(const PolicyLossArgs &p, cudaStream_t st);
 
 // ---- block-scaled GEMM (rlq_gemm.cu) ----
+// Tensor map of transposed codes [cols][M], pitch ld bytes (a multiple of 16), cols a
+// multiple of 8, seen as [cols / 8][8][M]: a box is 128 codes of every eighth of 128
+// columns, [16][1][128], 128-byte swizzle.
+rlq_status encode_columns_map(struct CUtensorMap_st *map, uint8_t *base, int64_t M, int64_t cols, int64_t ld);
+
 //
 // out[r, c] = bf16( sum_b sa(b, r) * sb(b, c) * sum_{j in block b} A[r, j] * B[c, j] )
 // A: E4M3 [R rows][L contraction], pitch lda bytes; B: E4M3 [C rows][L], pitch ldb.
