@@ -9,7 +9,12 @@
 //   dh = dres + rstd * (dn - xh * mean(dn * xh)),   dgamma = sum_m dx * xh
 //
 // Both are bound by memory: 7.03 bytes per element forward (2 + 2 read, 2 + 1 and a
-// scale per 128 written), 8 backward.
+// scale per 128 written; 8.06 with the 128x1 codes), 8 backward.  Measured at 8192 x 4096:
+// forward 40 us (0.87 of the HBM rate); with the 128x1 codes 58 us, since the column
+// groups need every row's factor first and read h again (2 bytes an element: 10 us, of
+// which L2 saves little); backward 47 us (0.84).  Tried for the second read and slower or
+// equal: row blocks in the order that was written last, both passes over chunks of rows
+// that fit L2 (64-88 us), L2 hints on the inputs (62 us).
 #include <cuda_runtime.h>
 
 #include "rlq_elem.cuh"
@@ -333,25 +338,34 @@ __global__ void __launch_bounds__(512)
 }
 
 // dgamma[c] = sum over p < parts, in a fixed order, of part[p][c]: a CTA takes 32
-// columns, warp w the partial rows w, w + 8, ...; the eight warp sums are added in order.
-__global__ void __launch_bounds__(256) k_dgamma_sum(const float *__restrict__ part, int parts, int K,
-                                                    float *__restrict__ dgamma)
+// columns, warp w the partial rows w, w + 32, ..., all its loads in flight (one partial
+// row a SM: five), and the warps' sums are added as a tree.  With eight warps, each
+// 19 loads a few at a time, the pass took 1.6 us more (8192 x 4096: 48.8 -> 47.2 in all).
+__global__ void __launch_bounds__(1024) k_dgamma_sum(const float *__restrict__ part, int parts, int K,
+                                                     float *__restrict__ dgamma)
 {
     pdl_begin();
-    __shared__ float sh[8][32];
+    __shared__ float sh[32][33];
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     const int c = blockIdx.x * 32 + lane;  // K % 128 == 0: always in range
     float v = 0.0f;
-    for (int p = w; p < parts; p += 8)
-        v += part[(int64_t)p * K + c];
+    for (int p0 = w; p0 < parts; p0 += 8 * 32) {
+        float a[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            a[i] = p0 + 32 * i < parts ? part[(int64_t)(p0 + 32 * i) * K + c] : 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            v += a[i];
+    }
     sh[w][lane] = v;
     __syncthreads();
-    if (w == 0) {
+    v = sh[lane][w];  // column w of this CTA, partial sum `lane`
 #pragma unroll
-        for (int i = 1; i < 8; ++i)
-            v += sh[i][lane];
-        dgamma[c] = v;
-    }
+    for (int o = 16; o; o >>= 1)
+        v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    if (lane == 0)
+        dgamma[blockIdx.x * 32 + w] = v;
 }
 
 // Launch shape of the backward kernel.
@@ -422,7 +436,7 @@ cudaError_t launch_rmsnorm_backward(const uint16_t *dx, int64_t lddx, const uint
                    lddh, p.grid > 1 ? ws : dgamma, (int)M, (int)K, p.T, p.teams);
     if (e != cudaSuccess || p.grid == 1)
         return e;
-    return launch_pdl(k_dgamma_sum, dim3((unsigned)(K / 32)), dim3(256), 0, st, ws, p.grid, (int)K, dgamma);
+    return launch_pdl(k_dgamma_sum, dim3((unsigned)(K / 32)), dim3(1024), 0, st, ws, p.grid, (int)K, dgamma);
 }
 
 }  // namespace rlq
