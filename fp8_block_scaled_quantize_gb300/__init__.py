@@ -2,8 +2,9 @@
 
 Fine-grained FP8 E4M3 quantizers (1x128 groups for activations and gradients,
 128x128 blocks for weights, fused 128x1 groups for WGrad), block-scaled FP8
-GEMMs for FProp / DGrad / WGrad on tcgen05 tensor cores, and the UAQ
-invariant-scaling fold, all in hand-written CUDA for sm_103a behind the C ABI
+GEMMs for FProp / DGrad / WGrad on tcgen05 tensor cores, the UAQ
+invariant-scaling fold, and around the layer the residual norm, the gated
+feed-forward block, their gradients and the policy loss, all in hand-written CUDA for sm_103a behind the C ABI
 declared in ``include/rlq.h`` (``librlq.so``).
 
 ``fp8_block_scaled_quantize_gb300.rlq`` is the thin ctypes binding (it loads

@@ -10,13 +10,18 @@
 // is fp32.
 //
 // Floor: 2 + 1 + 1 bytes read and 2 + 2 + 1 written per element of [M, F], 160 us at 8192
-// x 14336 at the HBM rate.  Measured 265 us (294 with per-thread stores of the transposed
-// codes and 8-byte copies): the instructions of an element (51 before, 17 of them integer;
-// decoding, the sigmoid, three maxima, five encodings), issued at about 55% because the 16 warps that the
-// values' registers leave a SM stand in the same phase of a tile (ncu: 4 warps a
-// scheduler, stalls spread over math throttle, fixed latency and barriers).  Slower: forming the values twice at
-// two CTAs a SM (303 us, 75 instructions an element), pairs of half tiles that exchange
-// row maxima across a cluster (335 us).
+// x 14336 at the HBM rate.  Measured 235 us (0.68): 38 instructions an element (decoding,
+// the sigmoid, three maxima, five encodings), issued at about 55%, because the values'
+// registers leave a SM 16 warps that stand in the same phase of a tile (ncu: stalls spread
+// over fixed latency, loads, shared memory, math throttle and barriers).  What brought it
+// there from 294: the transposed codes stored as TMA boxes rather than by the threads (the
+// stores had held the warps), 16-byte copies of the checkpoint, four codes packed at once.
+// Slower on top of it: each column's 128 codes as a plain bulk copy (265), all boxes from
+// one warp (253), warps that store nothing running ahead of the boxes' issue (285), the row
+// codes as boxes too (238), the next tile's loads after the first barrier (283), column
+// maxima joined by 24 lanes of every warp (248).  L2 hints two tiles ahead: equal.  Earlier:
+// the values formed twice at two CTAs a SM (303, 75 instructions an element), pairs of half
+// tiles that exchange row maxima across a cluster (335).
 #include <cuda.h>
 #include <cuda_runtime.h>
 

@@ -273,6 +273,12 @@ __device__ __forceinline__ Unit unit_of(const Params &p, int u)
 //                of each, as MODE_BLOCK does, forms a = silu(g) * u and leaves a's (and
 //                optionally g's and u's) FP8 codes: a tile's columns are one 1x128 group,
 //                whose maximum its two threads exchange through shared memory.
+//                8192 tokens, 14336 x 4096, with the checkpoint: 800 us, 2.40 PFLOP/s; the
+//                same product as a plain FProp (28672 columns, bf16 out) takes 730-760.
+//                The main loop is the plain mode's and bounds it; the rest is the sigmoids
+//                (two special-function operations an element, 64 a thread and tile: 922 us
+//                with their denormal handling) and the codes, while the MMAs wait.
+//                64 tokens, 18944 x 3584: 27.4 us, 0.74 of the HBM rate.
 enum : int { MODE_BLOCK = 0, MODE_COLS = 1, MODE_ONCE = 2, MODE_GATED = 3 };
 
 // Epilogue outputs.

@@ -16,8 +16,9 @@ namespace rlq {
 // have completed and their memory is visible, and then lets the next kernel in
 // the stream be scheduled as soon as every block of this grid has started.  The
 // next kernel's blocks can then be resident and waiting when this grid ends,
-// instead of being launched only afterwards.  No kernel touches global memory
-// before the wait, so the ordering of the stream is unchanged.
+// instead of being launched only afterwards.  No kernel reads or writes global memory
+// before the wait (one sends L2 prefetch hints for its weights), so the ordering of the
+// stream is unchanged.
 #ifdef __CUDACC__
 __device__ __forceinline__ void pdl_begin()
 {

@@ -11,6 +11,9 @@
  *   - the one-time UAQ invariant-scaling fold WX = (W/s)(sX), s applied per
  *     column of W and per row of the previous activation (QuRL notes,
  *     关键设计 §1).
+ * Around the layer: the residual norm with its gradient, the gated feed-forward
+ * block with its gradient from 8-bit checkpoints, token log probabilities and the
+ * clipped policy loss.
  *
  * Conventions for every call
  *   - Every tensor pointer is a DEVICE pointer owned by the caller.  The library
