@@ -175,10 +175,17 @@ __device__ __noinline__ RowScalars row_scalars(const PolicyLossArgs &p, const Ro
     if (!p.adv)
         return o;
     const float rho = expf(o.lp - in.old);
-    const float isw = p.lp_behav ? fminf(expf(in.old - in.behav), p.tis_cap) : 1.0f;
-    const float plain = rho * in.adv, clipped = fminf(fmaxf(rho, 1.0f - p.eps_lo), in.hi) * in.adv;
-    float loss = -isw * fminf(plain, clipped);
-    float dlp = plain <= clipped ? -isw * plain : 0.0f;
+    // (minima by comparison: a NaN among the row's inputs stays one, fminf would drop it)
+    float isw = 1.0f;
+    if (p.lp_behav) {
+        const float w = expf(in.old - in.behav);
+        isw = w > p.tis_cap ? p.tis_cap : w;
+    }
+    float clip = rho < 1.0f - p.eps_lo ? 1.0f - p.eps_lo : rho;
+    clip = clip > in.hi || in.hi != in.hi ? in.hi : clip;
+    const float plain = rho * in.adv, clipped = clip * in.adv;
+    float loss = -isw * (plain > clipped || clipped != clipped ? clipped : plain);
+    float dlp = plain > clipped ? 0.0f : -isw * plain;
     if (p.lp_ref) {
         const float d = in.ref - o.lp, e = expm1f(d);
         loss = fmaf(p.kl_beta, e - d, loss);

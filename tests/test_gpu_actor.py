@@ -454,6 +454,29 @@ def test_policy_loss_empty_and_masked_rows(V):
         assert bool(((l2[keep].to(D) - ref).abs() <= 1e-5 * (1 + ref.abs())).all())
 
 
+@pytest.mark.parametrize("V", [500, 40001])
+def test_policy_loss_keeps_nan(V):
+    """A NaN among a row's inputs reaches its loss and its gradient, and no other row's."""
+    st = loss_inputs(6, V, torch.bfloat16, 23)
+    st["weight"][:] = 1 / 6
+    nan = float("nan")
+    st["logits"][0, V // 3] = nan
+    st["logp_old"][1] = nan
+    st["adv"][2] = nan
+    behav = st["logp_old"].clone()
+    behav[1] = 0
+    behav[3] = nan
+    hi = torch.full((6,), 1.3, device=DEV)
+    hi[4] = nan
+    loss, _, d = rlq.policy_loss(st["logits"], st["targets"], st["logp_old"], st["adv"], st["weight"],
+                                 logp_behav=behav, clip_hi=hi)
+    for r in range(5):
+        assert math.isnan(float(loss[r])), r
+        if r < 4:
+            assert bool(torch.isnan(d[r]).any()), r
+    assert math.isfinite(float(loss[5])) and bool(torch.isfinite(d[5]).all())
+
+
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("T,V,pitch,offset", [(1, 1, 0, 0), (7, 333, 0, 1), (64, 32001, 0, 0), (3, 128256, 0, 0)])
 def test_token_logprobs(T, V, pitch, offset, dtype):
