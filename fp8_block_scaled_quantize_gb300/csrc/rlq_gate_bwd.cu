@@ -11,7 +11,7 @@
 //
 // Floor: 2 + 1 + 1 bytes read and 2 + 2 + 1 written per element of [M, F], 160 us at 8192
 // x 14336 at the HBM rate.  Measured 235 us (0.68): 38 instructions an element (decoding,
-// the sigmoid, three maxima, five encodings), issued at about 55%, because the values'
+// the sigmoid, three maxima, five encodings), issued at 48%, because the values'
 // registers leave a SM 16 warps that stand in the same phase of a tile (ncu: stalls spread
 // over fixed latency, loads, shared memory, math throttle and barriers).  What brought it
 // there from 294: the transposed codes stored as TMA boxes rather than by the threads (the
