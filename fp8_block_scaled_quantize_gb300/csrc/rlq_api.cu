@@ -109,8 +109,9 @@ rlq_status check_logits(PolicyLossArgs *a, const void *logits, rlq_dtype dtype, 
     RLQ_REQUIRE(V >= 1, RLQ_ERR_INVALID_ARG, "V=%lld: a row has at least one logit", (long long)V);
     RLQ_REQUIRE(V < MAX_DIM / 2, RLQ_ERR_UNSUPPORTED, "V=%lld is beyond 2^30", (long long)V);
     RLQ_REQUIRE(rows < MAX_DIM / 8, RLQ_ERR_UNSUPPORTED, "rows beyond 2^28");
-    RLQ_REQUIRE(std::isfinite(temperature) && temperature > 0.0f, RLQ_ERR_INVALID_ARG,
-                "temperature must be finite and > 0");
+    // (the reciprocal of a subnormal one would overflow)
+    RLQ_REQUIRE(std::isnormal(temperature) && temperature > 0.0f, RLQ_ERR_INVALID_ARG,
+                "temperature must be a finite normal number > 0");
     if (rows == 0)
         return RLQ_OK;
     RLQ_REQUIRE(logits, RLQ_ERR_INVALID_ARG, "logits is NULL");

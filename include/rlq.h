@@ -595,7 +595,8 @@ typedef enum { RLQ_DTYPE_BF16 = 0, RLQ_DTYPE_F32 = 1 } rlq_dtype;
  *           empty: lp and lse are 0 and its logits are not read
  *   lp      f32 [rows]; lse f32 [rows] or NULL           (outputs)
  * Logits of -inf have probability 0; a row of nothing else has lp = lse = -inf.
- * V >= 1, below 2^30; rows below 2^28; temperature finite, > 0.
+ * V >= 1, below 2^30; rows below 2^28; temperature finite,
+ * > 0 and not subnormal.
  */
 rlq_status rlq_token_logprobs(const void *logits, rlq_dtype dtype, int64_t ld, int64_t rows, int64_t V,
                               const int64_t *targets, float temperature, float *lp, float *lse,

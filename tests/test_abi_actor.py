@@ -98,6 +98,12 @@ def test_loss_refusals():
         ({20: 99}, INVALID), ({19: FAKE + 1}, MISALIGNED), ({19: FAKE, 20: 104}, INVALID)])
 
 
+def test_subnormal_temperature_is_refused():
+    """Its reciprocal would overflow."""
+    ok = (FAKE, 0, 100, 4, 100, FAKE, 1.0, FAKE, FAKE, None)
+    refusals(rlq.rlq_token_logprobs, ok, [({6: 1e-40}, INVALID), ({6: -1e-40}, INVALID), ({6: float("nan")}, INVALID)])
+
+
 class OnGpu(torch.Tensor):
     """A CPU tensor that says it is on the GPU, so that the checks behind that one are reached."""
 
