@@ -239,8 +239,6 @@ __global__ void __launch_bounds__(THREADS, 1) k_gate_bwd(const GateBwd p, const 
 #pragma unroll
         for (int k = 0; k < 3; ++k)
             store_column_maxima(cmax[k], t & 16, part + (warp * 3 + k) * GRP + 8 * cg);
-        // (the copies of the last tile's codes have read them: waited for by their issuers)
-        asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
         float cs = 1.0f;
         if (t >= 3 * GRP) {
             bar_pass();
@@ -293,6 +291,8 @@ __global__ void __launch_bounds__(THREADS, 1) k_gate_bwd(const GateBwd p, const 
                 }
             }
         }
+        // (the copies of the last tile's codes have read them: waited for by their issuers)
+        asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
         // Column groups.  (Columns whose scale is below 2^-100 are scaled up first.)
         if (__syncthreads_or(cs < 0x1p-100f)) {
             if (t < 3 * GRP)
