@@ -10,7 +10,7 @@
 // is fp32.
 //
 // Floor: 2 + 1 + 1 bytes read and 2 + 2 + 1 written per element of [M, F], 160 us at 8192
-// x 14336 at the HBM rate.  Measured 235 us (0.68): 38 instructions an element (decoding,
+// x 14336 at the HBM rate.  Measured 211 us (0.76): 38 instructions an element (decoding,
 // the sigmoid, three maxima, five encodings), issued at 48%, because the values'
 // registers leave a SM 16 warps that stand in the same phase of a tile (ncu: stalls spread
 // over fixed latency, loads, shared memory, math throttle and barriers).  What brought it
@@ -27,15 +27,17 @@
 
 #include "rlq_elem.cuh"
 #include "rlq_internal.h"
+#include "rlq_tc.cuh"
 
 namespace rlq {
 namespace {
 
 constexpr int GRP = 128;
 constexpr int THREADS = 512;
-// Shared memory: two prefetched tiles (per thread four rows of 16 + 8 + 8 bytes) and
-// their 2 x 128 scales, the three transposed code tiles, 16 warps' column maxima.
-constexpr int IN_BYTES = THREADS * 4 * 32;
+constexpr int LOADER = THREADS - 32;  // the thread that issues the input copies
+// Shared memory: two input tiles (da's 128 rows of 256 bytes, g's and u's codes) and their
+// 2 x 128 scales, the three transposed code tiles, 16 warps' column maxima.
+constexpr int IN_BYTES = 4 * GRP * GRP;
 // A code tile is 128 slots of 128 bytes, a column's codes each: column 8 c + j in slot
 // 16 j + c, its eight 16-byte chunks XOR c mod 8 (the 128-byte swizzle), so that the
 // lanes that write one j differ in the bank.
@@ -44,7 +46,8 @@ constexpr int OFF_SCALES = 2 * IN_BYTES;
 constexpr int OFF_TILES = OFF_SCALES + 2 * 2 * GRP * 4;
 constexpr int OFF_PART = OFF_TILES + 3 * TILE_BYTES;
 constexpr int OFF_RCP = OFF_PART + 16 * 3 * GRP * 4;  // 3 x 128 reciprocals, 3 x 128 factors
-constexpr int SMEM_BYTES = OFF_RCP + 2 * 3 * GRP * 4;
+constexpr int OFF_BARS = OFF_RCP + 2 * 3 * GRP * 4;  // two mbarriers, the abort flag
+constexpr int SMEM_BYTES = OFF_BARS + 24;
 static_assert(SMEM_BYTES <= 232448 && OFF_TILES % 1024 == 0, "shared memory budget; the swizzle's period");
 
 struct GateBwd {
@@ -68,13 +71,10 @@ struct GateBwd {
     int64_t ldac;
     int64_t M, F;
     int m_tiles, tiles;
+    uint64_t timeout_ns;
 };
 
 // Global -> shared copies; bytes = 0 writes zeros without reading.
-__device__ __forceinline__ void copy16(uint32_t dst, const void *src, uint32_t bytes)
-{
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
 __device__ __forceinline__ void copy4(uint32_t dst, const void *src, uint32_t bytes)
 {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
@@ -121,16 +121,17 @@ __device__ __forceinline__ void decode8(uint2 c, float s, float2 (&f)[4])
 
 // Persistent, one CTA per SM, 128 x 128 tiles of [M, F], row block fastest.  Thread t
 // has rows 4 (t / 16) .. + 3 and columns 8 (t % 16) .. + 7 of a tile, all of it in
-// registers; it copies its own part of the next tile to shared memory meanwhile.  A
+// registers; the next tile arrives in shared memory by TMA meanwhile.  A
 // row's 16 lanes are its 1x128 group: the eight row maxima of a half-warp (four rows of
 // dg, four of du) are reduced in one transposed exchange (each step hands half of the
 // remaining ones to the partner lane), after which a lane pair holds one group's and
 // computes its scale once.  Column maxima go over the rows of a thread, the two halves
 // of a warp and, in shared memory, the 16 warps.
 __global__ void __launch_bounds__(THREADS, 1) k_gate_bwd(const GateBwd p, const __grid_constant__ CUtensorMap tmQ,
-                                                         const __grid_constant__ CUtensorMap tmA)
+                                                         const __grid_constant__ CUtensorMap tmA,
+                                                         const __grid_constant__ CUtensorMap tmDa,
+                                                         const __grid_constant__ CUtensorMap tmGu)
 {
-    pdl_begin();
     extern __shared__ __align__(1024) uint8_t smem[];
     float *part = reinterpret_cast<float *>(smem + OFF_PART);  // [warp][3][128]
     float *rcp = reinterpret_cast<float *>(smem + OFF_RCP);    // [3][128], factors behind them
@@ -145,36 +146,27 @@ __global__ void __launch_bounds__(THREADS, 1) k_gate_bwd(const GateBwd p, const 
     // the next.
     int mt = blockIdx.x % p.m_tiles, ft = blockIdx.x / p.m_tiles;
     const int step_m = gridDim.x % p.m_tiles, step_f = gridDim.x / p.m_tiles;
+    const uint32_t bars = smem0 + OFF_BARS;
+    volatile uint32_t *abort_flag = reinterpret_cast<uint32_t *>(smem + OFF_BARS + 16);
+    if (t == LOADER) {
+        mbar_init(bars, 1);
+        mbar_init(bars + 8, 1);
+        *abort_flag = 0;
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        prefetch_tmap(&tmDa);
+        prefetch_tmap(&tmGu);
+    }
+    __syncthreads();
+    pdl_begin();
     auto prefetch = [&](int pm, int pf, int buf) {
-        const int64_t m = (int64_t)pm * GRP + 4 * rg, f = (int64_t)pf * GRP;
+        const int64_t m = (int64_t)pm * GRP + 4 * rg;
         const int left = (int)(p.M - m < 4 ? p.M - m : 4);  // rows of mine inside the matrix (may be <= 0)
-        const uint32_t in = smem0 + buf * IN_BYTES + t * 16;
-        // da: my 8 columns of four rows; the codes: rows cg / 8 and 2 + cg / 8 of the
-        // half-warp's four, 16 columns each
-        const uint16_t *ap = p.da + m * p.ldda + f + 8 * cg;
-        const int r = cg >> 3;
-        const uint8_t *gp = p.guq + (m + r) * p.ldguq + f + 16 * (cg & 7);
-        const uint32_t in8 = smem0 + buf * IN_BYTES + THREADS * 64 + rg * 512 + cg * 16;
-        if (left == 4) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i, ap += p.ldda)
-                copy16(in + i * THREADS * 16, ap, 16);
-            copy16(in8, gp, 16);
-            copy16(in8 + THREADS * 32, gp + p.F, 16);
-            gp += 2 * p.ldguq;
-            copy16(in8 + 256, gp, 16);
-            copy16(in8 + THREADS * 32 + 256, gp + p.F, 16);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                copy16(in + i * THREADS * 16, i < left ? ap + i * p.ldda : p.da, i < left ? 16 : 0);
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const bool ok = 2 * i + r < left;
-                const uint8_t *g = ok ? gp + 2 * i * p.ldguq : p.guq;
-                copy16(in8 + i * 256, g, ok ? 16 : 0);
-                copy16(in8 + THREADS * 32 + i * 256, ok ? g + p.F : g, ok ? 16 : 0);
-            }
+        if (t == LOADER && !*abort_flag) {  // (rows past the end arrive as zeros)
+            const uint32_t bar = bars + 8 * buf, in = smem0 + buf * IN_BYTES;
+            mbar_arrive_expect_tx(bar, IN_BYTES);
+            tma_load_2d(in, &tmDa, bar, pf * GRP, pm * GRP);
+            tma_load_2d(in + 2 * GRP * GRP, &tmGu, bar, pf * GRP, pm * GRP);
+            tma_load_2d(in + 3 * GRP * GRP, &tmGu, bar, (int)p.F + pf * GRP, pm * GRP);
         }
         if (cg < 8) {  // this half-warp's scales: four rows of g, four of u
             const bool ok = (cg & 3) < left;
@@ -187,7 +179,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_gate_bwd(const GateBwd p, const 
     if (tile < p.tiles)
         prefetch(mt, ft, 0);
     asm volatile("cp.async.commit_group;" ::: "memory");
-    for (int buf = 0; tile < p.tiles; tile += gridDim.x, buf ^= 1) {
+    for (uint32_t buf = 0, phase = 0; tile < p.tiles; tile += gridDim.x, phase ^= buf, buf ^= 1) {
         int nm = mt + step_m, nf = ft + step_f;
         if (nm >= p.m_tiles) {
             nm -= p.m_tiles;
@@ -197,6 +189,9 @@ __global__ void __launch_bounds__(THREADS, 1) k_gate_bwd(const GateBwd p, const 
             prefetch(nm, nf, buf ^ 1);
         asm volatile("cp.async.commit_group;" ::: "memory");
         asm volatile("cp.async.wait_group 1;" ::: "memory");
+        // (Should the wait run out, this tile is formed from what is there, within the
+        // buffers, the error word says so and the CTA leaves after it.)
+        (void)mbar_wait(bars + 8 * buf, phase, abort_flag, p.timeout_ns, SITE_GATE_FULL);
         // A thread reads what its half-warp copied.  The last tile's codes may still be
         // leaving: shared memory that they use is written after the next barrier only.
         __syncwarp();
@@ -211,9 +206,9 @@ __global__ void __launch_bounds__(THREADS, 1) k_gate_bwd(const GateBwd p, const 
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             float2 g[4], u[4];
-            decode8(*reinterpret_cast<const uint2 *>(in + THREADS * 64 + rg * 512 + i * GRP + 8 * cg), sg4[i], g);
-            decode8(*reinterpret_cast<const uint2 *>(in + THREADS * 96 + rg * 512 + i * GRP + 8 * cg), su4[i], u);
-            const uint4 dv = *reinterpret_cast<const uint4 *>(in + (i * THREADS + t) * 16);
+            decode8(*reinterpret_cast<const uint2 *>(in + 2 * GRP * GRP + (4 * rg + i) * GRP + 8 * cg), sg4[i], g);
+            decode8(*reinterpret_cast<const uint2 *>(in + 3 * GRP * GRP + (4 * rg + i) * GRP + 8 * cg), su4[i], u);
+            const uint4 dv = *reinterpret_cast<const uint4 *>(in + (4 * rg + i) * 2 * GRP + 16 * cg);
             const uint32_t dw[4] = {dv.x, dv.y, dv.z, dv.w};
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -330,6 +325,8 @@ __global__ void __launch_bounds__(THREADS, 1) k_gate_bwd(const GateBwd p, const 
         // The column codes leave by the copy engine, which reads shared memory through the
         // async proxy: 24 boxes, one or two a warp (all of them from one warp: 253 us at
         // the size above).  The last row block's by 16-byte and byte stores.
+        // (raised before the last barrier or after the next one only: all threads agree)
+        const bool stop = *abort_flag != 0;
         if (rows == GRP) {
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncthreads();
@@ -359,6 +356,15 @@ __global__ void __launch_bounds__(THREADS, 1) k_gate_bwd(const GateBwd p, const 
                 }
             }
         }
+        if (stop) {
+            if (t == LOADER) {  // copies still in flight land before the CTA's memory is given up
+                uint32_t never = 0;
+                mbar_wait(bars + 8 * buf, phase, &never, 20000000ull, SITE_DRAIN);
+                if (tile + (int)gridDim.x < p.tiles)
+                    mbar_wait(bars + 8 * (buf ^ 1), phase ^ buf, &never, 20000000ull, SITE_DRAIN);
+            }
+            break;
+        }
         mt = nm;
         ft = nf;
     }
@@ -375,8 +381,13 @@ rlq_status launch_gated_backward(const uint16_t *da, int64_t ldda, const uint8_t
 {
     const int64_t m_tiles = (M + GRP - 1) / GRP, tiles = m_tiles * (F / GRP);
     const GateBwd p = {da, ldda, guq, ldguq, gus, ld_gus, q,  ldq, s, lds, qT,           ldqT,
-                       sc, ldsc, aT,  ldaT,  ac,  ldac,   M,  F,   (int)m_tiles, (int)tiles};
-    CUtensorMap tmQ = {}, tmA = {};
+                       sc, ldsc, aT,  ldaT,  ac,  ldac,   M,  F,   (int)m_tiles, (int)tiles, wait_limit_ns()};
+    CUtensorMap tmQ = {}, tmA = {}, tmDa, tmGu;
+    rlq_status rin = encode_tile_map(&tmDa, da, true, M, F, ldda);
+    if (rin == RLQ_OK)
+        rin = encode_tile_map(&tmGu, guq, false, M, 2 * F, ldguq);
+    if (rin != RLQ_OK)
+        return rin;
     if (M >= GRP) {  // (a tile of fewer rows does without)
         rlq_status r = encode_columns_map(&tmQ, qT, M, 2 * F, ldqT);
         if (r == RLQ_OK)
@@ -394,9 +405,11 @@ rlq_status launch_gated_backward(const uint16_t *da, int64_t ldda, const uint8_t
     }
     if (e == cudaSuccess) {
         const int64_t sms = device_sms();
-        e = launch_pdl(k_gate_bwd, dim3((unsigned)(tiles < sms ? tiles : sms)), dim3(THREADS), SMEM_BYTES, st, p, tmQ, tmA);
+        e = launch_pdl(k_gate_bwd, dim3((unsigned)(tiles < sms ? tiles : sms)), dim3(THREADS), SMEM_BYTES, st, p, tmQ, tmA, tmDa, tmGu);
     }
     return cuda_status(e, "gated backward launch");
 }
+
+cudaError_t take_gate_error_word(cudaStream_t st, unsigned long long *word) { return take_error_word(st, word); }
 
 }  // namespace rlq

@@ -1012,20 +1012,6 @@ PFN_cuTensorMapEncodeTiled_v12000 get_encode_fn()
     return fn;
 }
 
-uint64_t wait_limit_ns()
-{
-    static uint64_t ns = [] {
-        const char *e = std::getenv("RLQ_WAIT_TIMEOUT_MS");
-        long long ms = e ? std::atoll(e) : 1000;
-        if (ms < 1)
-            ms = 1;
-        if (ms > 600000)
-            ms = 600000;
-        return (uint64_t)ms * 1000000ull;
-    }();
-    return ns;
-}
-
 // bf16 output [rows][cols], pitch ld elements; box 64 columns x 32 rows, 128-byte swizzle.
 rlq_status encode_out_map(CUtensorMap *map, uint16_t *base, int64_t cols, int64_t rows, int64_t ld)
 {
@@ -1105,6 +1091,39 @@ rlq_status encode_codes_out_map(CUtensorMap *map, uint8_t *base, int64_t cols, i
 }
 
 }  // namespace
+
+uint64_t wait_limit_ns()
+{
+    static uint64_t ns = [] {
+        const char *e = std::getenv("RLQ_WAIT_TIMEOUT_MS");
+        long long ms = e ? std::atoll(e) : 1000;
+        if (ms < 1)
+            ms = 1;
+        if (ms > 600000)
+            ms = 600000;
+        return (uint64_t)ms * 1000000ull;
+    }();
+    return ns;
+}
+
+rlq_status encode_tile_map(CUtensorMap_st *map, const void *base, bool bf16, int64_t rows, int64_t cols, int64_t ld)
+{
+    auto enc = get_encode_fn();
+    if (!enc)
+        return fail(RLQ_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)ld * (bf16 ? 2 : 1)};
+    const cuuint32_t box[2] = {128, 128};
+    const cuuint32_t estr[2] = {1, 1};
+    const CUresult r = enc(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 2,
+                           const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                           CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS)
+        return fail(RLQ_ERR_CUDA, "cuTensorMapEncodeTiled failed (CUresult %d) for the [%lld x %lld] input, pitch %lld",
+                    (int)r, (long long)rows, (long long)cols, (long long)ld);
+    return RLQ_OK;
+}
 
 rlq_status encode_columns_map(CUtensorMap_st *map, uint8_t *base, int64_t M, int64_t cols, int64_t ld)
 {
@@ -1420,20 +1439,23 @@ rlq_status check_device_errors(cudaStream_t st)
     if (e != cudaSuccess)
         return cuda_status(e, "cudaStreamSynchronize");
     // every translation unit with bounded-wait kernels keeps its own error word
-    unsigned long long words[2] = {0, 0};
+    unsigned long long words[3] = {0, 0, 0};
     e = take_error_word(st, &words[0]);
     if (e == cudaSuccess)
         e = take_nvfp4_error_word(st, &words[1]);
+    if (e == cudaSuccess)
+        e = take_gate_error_word(st, &words[2]);
     if (e != cudaSuccess)
         return cuda_status(e, "reading and clearing the device error words");
-    const unsigned long long word = words[0] ? words[0] : words[1];
+    const unsigned long long word = words[0] ? words[0] : words[1] ? words[1] : words[2];
     if (word == 0)
         return RLQ_OK;
     const uint32_t code = (uint32_t)word, site = (uint32_t)(word >> 32);
     static const char *names[] = {"?", "TMA producer (stage free)", "MMA issuer (TMEM buffer free)",
                                   "MMA issuer (stage loaded)", "epilogue (partial ready)", "teardown", "drain",
-                                  "scale loader (slot free)", "epilogue (scales ready)", "FP4 converter (stage free)"};
-    const char *where = site == SITE_DIAG ? "diagnostic wait" : (site < 10 ? names[site] : "?");
+                                  "scale loader (slot free)", "epilogue (scales ready)", "FP4 converter (stage free)",
+                                  "gate backward (tile loaded)"};
+    const char *where = site == SITE_DIAG ? "diagnostic wait" : (site < 11 ? names[site] : "?");
     return fail((rlq_status)code, "device-side wait ran out at site %u (%s)%s", site, where,
                 words[1] && !words[0] ? " in the NVFP4 GEMM" : "");
 }

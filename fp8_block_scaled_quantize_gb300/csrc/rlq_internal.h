@@ -128,12 +128,19 @@ struct PolicyLossArgs {
 };
 cudaError_t launch_policy_rows(const PolicyLossArgs &p, cudaStream_t st);
 
-// ---- block-scaled GEMM (rlq_gemm.cu) ----
+// ---- device-side waits and tensor maps (rlq_gemm.cu) ----
+// Limit of a device-side wait (RLQ_WAIT_TIMEOUT_MS, default one second).
+uint64_t wait_limit_ns();
+// Tensor map of a bf16 or 8-bit matrix [rows][cols], pitch ld elements, for loads of
+// 128 x 128 boxes, unswizzled; what lies outside the matrix arrives as zeros.
+rlq_status encode_tile_map(struct CUtensorMap_st *map, const void *base, bool bf16, int64_t rows, int64_t cols,
+                           int64_t ld);
 // Tensor map of transposed codes [cols][M], pitch ld bytes (a multiple of 16), cols a
 // multiple of 8, seen as [cols / 8][8][M]: a box is 128 codes of every eighth of 128
 // columns, [16][1][128], 128-byte swizzle.
 rlq_status encode_columns_map(struct CUtensorMap_st *map, uint8_t *base, int64_t M, int64_t cols, int64_t ld);
 
+// ---- block-scaled GEMM (rlq_gemm.cu) ----
 //
 // out[r, c] = bf16( sum_b sa(b, r) * sb(b, c) * sum_{j in block b} A[r, j] * B[c, j] )
 // A: E4M3 [R rows][L contraction], pitch lda bytes; B: E4M3 [C rows][L], pitch ldb.
@@ -213,6 +220,8 @@ rlq_status plan_splitk(int64_t R, int64_t C, int64_t L, int64_t ws_cap, int *spl
 rlq_status check_device_errors(cudaStream_t st);
 // The NVFP4 GEMM's translation unit's error word, read and cleared (0: none).
 cudaError_t take_nvfp4_error_word(cudaStream_t st, unsigned long long *word);
+// The gate backward's, likewise.
+cudaError_t take_gate_error_word(cudaStream_t st, unsigned long long *word);
 rlq_status launch_diag_wait(int64_t timeout_us, cudaStream_t st);
 
 // Arms, for the calling thread, a one-shot stall of the next block-scaled GEMM

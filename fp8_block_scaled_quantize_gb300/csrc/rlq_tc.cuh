@@ -28,6 +28,7 @@ enum : uint32_t {
     SITE_SCALE_EMPTY = 7,
     SITE_EPI_SCALE_FULL = 8,
     SITE_CONVERTER_EMPTY = 9,
+    SITE_GATE_FULL = 10,
     SITE_DIAG = 99,
 };
 

@@ -38,7 +38,7 @@
  *   - Errors: arguments are validated on the host before any launch (NULL
  *     pointers, negative sizes, ld smaller than the row, misalignment); on
  *     failure nothing is launched.  A failed launch returns RLQ_ERR_CUDA.  The
- *     GEMM kernels bound every wait on the GPU: a wait that runs out records
+ *     GEMM kernels and rlq_gated_backward bound every wait on the GPU: a wait that runs out records
  *     an error word on the device, and the next rlq_check on that device
  *     returns RLQ_ERR_TIMEOUT.  rlq_last_error() describes the latest failure.
  *   - Inputs must be finite; NaN / Inf inputs are outside the contract.
@@ -571,7 +571,8 @@ rlq_status rlq_gemm_gated_fprop(const uint8_t *xq, int64_t ldxq, const float *xs
  *   q    E4M3 [M, 2F], pitch ldq; s f32, s[fb * lds + m], fb < 2F/128      (outputs)
  *   qT   E4M3 [2F, M], pitch ldqT; sc f32, sc[mb * ldsc + n], ldsc >= 2F   (outputs)
  *   aT   E4M3 [F, M], pitch ldaT;  ac f32, ac[mb * ldac + f], ldac >= F    (outputs)
- * F % 128 == 0; M any value >= 0; the last token group may be partial.
+ * F % 128 == 0; M any value >= 0; the last token group may be partial.  (A bounded
+ * device wait that runs out reports at rlq_check.)
  */
 rlq_status rlq_gated_backward(const uint16_t *da, int64_t ldda, const uint8_t *guq, int64_t ldguq,
                               const float *gus, int64_t ldgus, uint8_t *q, int64_t ldq, float *s, int64_t lds,
