@@ -10,18 +10,18 @@
 // is fp32.
 //
 // Floor: 2 + 1 + 1 bytes read and 2 + 2 + 1 written per element of [M, F], 160 us at 8192
-// x 14336 at the HBM rate.  Measured 211 us (0.76): 38 instructions an element (decoding,
-// the sigmoid, three maxima, five encodings), issued at 48%, because the values'
-// registers leave a SM 16 warps that stand in the same phase of a tile (ncu: stalls spread
-// over fixed latency, loads, shared memory, math throttle and barriers).  What brought it
-// there from 294: the transposed codes stored as TMA boxes rather than by the threads (the
-// stores had held the warps), 16-byte copies of the checkpoint, four codes packed at once.
-// Slower on top of it: each column's 128 codes as a plain bulk copy (265), all boxes from
-// one warp (253), warps that store nothing running ahead of the boxes' issue (285), the row
-// codes as boxes too (238), the next tile's loads after the first barrier (283), column
-// maxima joined by 24 lanes of every warp (248).  L2 hints two tiles ahead: equal.  Earlier:
-// the values formed twice at two CTAs a SM (303, 75 instructions an element), pairs of half
-// tiles that exchange row maxima across a cluster (335).
+// x 14336 at the HBM rate.  Measured 203 us (0.79): instructions (decoding, the sigmoid,
+// three maxima and five encodings an element, 38 before the input copies left the threads;
+// a copy of the kernel without its loads and stores took 188), at 16 warps a SM, which is
+// what the values' registers allow.  What brought it there from 294: the transposed codes
+// stored as TMA boxes rather than by the threads (265 with 16-byte copies and bulk copies
+// of single columns, 235 with boxes), the boxes' reads waited for a barrier later (223),
+// inputs by TMA (211), two tiles ahead (203).  Slower, each on top of the version of its
+// time: all boxes from one warp (253 for 235), warps that store nothing running ahead of
+// the boxes' issue (285), the row codes as boxes too (238), column maxima joined by 24
+// lanes of every warp (248).  Earlier: the values formed twice at two CTAs a SM (303, 75
+// instructions an element), pairs of half tiles that exchange row maxima across a cluster
+// (335).
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -35,7 +35,7 @@ namespace {
 constexpr int GRP = 128;
 constexpr int THREADS = 512;
 constexpr int LOADER = THREADS - 32;  // the thread that issues the input copies
-// Shared memory: two input tiles (da's 128 rows of 256 bytes, g's and u's codes) and their
+// Shared memory: two tiles of input (da's 128 rows of 256 bytes, g's and u's codes) and their
 // 2 x 128 scales, the three transposed code tiles, 16 warps' column maxima.
 constexpr int IN_BYTES = 4 * GRP * GRP;
 // A code tile is 128 slots of 128 bytes, a column's codes each: column 8 c + j in slot
@@ -121,7 +121,7 @@ __device__ __forceinline__ void decode8(uint2 c, float s, float2 (&f)[4])
 
 // Persistent, one CTA per SM, 128 x 128 tiles of [M, F], row block fastest.  Thread t
 // has rows 4 (t / 16) .. + 3 and columns 8 (t % 16) .. + 7 of a tile, all of it in
-// registers; the next tile arrives in shared memory by TMA meanwhile.  A
+// registers; the next two arrive in shared memory by TMA meanwhile.  A
 // row's 16 lanes are its 1x128 group: the eight row maxima of a half-warp (four rows of
 // dg, four of du) are reduced in one transposed exchange (each step hands half of the
 // remaining ones to the partner lane), after which a lane pair holds one group's and
@@ -175,19 +175,24 @@ __global__ void __launch_bounds__(THREADS, 1) k_gate_bwd(const GateBwd p, const 
         }
     };
 
-    int tile = blockIdx.x;
-    if (tile < p.tiles)
-        prefetch(mt, ft, 0);
-    asm volatile("cp.async.commit_group;" ::: "memory");
-    for (uint32_t buf = 0, phase = 0; tile < p.tiles; tile += gridDim.x, phase ^= buf, buf ^= 1) {
-        int nm = mt + step_m, nf = ft + step_f;
-        if (nm >= p.m_tiles) {
-            nm -= p.m_tiles;
-            ++nf;
+    auto step = [&](int &m, int &f) {
+        m += step_m;
+        f += step_f;
+        if (m >= p.m_tiles) {
+            m -= p.m_tiles;
+            ++f;
         }
-        if (tile + (int)gridDim.x < p.tiles)
-            prefetch(nm, nf, buf ^ 1);
-        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    int tile = blockIdx.x, am = mt, af = ft;  // (am, af): the tile to copy next
+    if (tile < p.tiles)
+        prefetch(am, af, 0);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    step(am, af);
+    if (tile + (int)gridDim.x < p.tiles)
+        prefetch(am, af, 1);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    step(am, af);
+    for (uint32_t buf = 0, phase = 0; tile < p.tiles; tile += gridDim.x, phase ^= buf, buf ^= 1) {
         asm volatile("cp.async.wait_group 1;" ::: "memory");
         // (Should the wait run out, this tile is formed from what is there, within the
         // buffers, the error word says so and the CTA leaves after it.)
@@ -289,7 +294,13 @@ __global__ void __launch_bounds__(THREADS, 1) k_gate_bwd(const GateBwd p, const 
         // (the copies of the last tile's codes have read them: waited for by their issuers)
         asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
         // Column groups.  (Columns whose scale is below 2^-100 are scaled up first.)
-        if (__syncthreads_or(cs < 0x1p-100f)) {
+        const int tiny = __syncthreads_or(cs < 0x1p-100f);
+        // every thread has this tile's values: its buffer takes the one after the next
+        if (tile + 2 * (int)gridDim.x < p.tiles)
+            prefetch(am, af, buf);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        step(am, af);
+        if (tiny) {
             if (t < 3 * GRP)
                 rcp[3 * GRP + t] = scale_pre(cs);
             __syncthreads();
@@ -365,8 +376,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_gate_bwd(const GateBwd p, const 
             }
             break;
         }
-        mt = nm;
-        ft = nf;
+        step(mt, ft);
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
     asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
