@@ -89,6 +89,37 @@ def test_add_rmsnorm_tiny_and_large_values():
             assert bool((R.decode(q).abs() <= 448).all())
 
 
+def test_scales_and_codes_are_the_rule_of_the_values():
+    """From the kernel's own rstd the fp32 values are known bit for bit: every scale is the
+    IEEE quotient of its group's maximum, every code that of value * RN(1 / scale)."""
+    g = gen(31)
+    M, K = 1031, 4096
+    h = normal(g, M, K)
+    h[::7] *= torch.exp2(torch.randint(-20, 20, (h[::7].shape[0], 1), generator=g, device=DEV)).to(torch.bfloat16)
+    # weights from 2^-126 to 2^60: scales from far below the normal range's end to large ones
+    step = torch.linspace(-126, 60, K // 128, device=DEV).round().repeat_interleave(128)
+    gamma = (torch.randn(K, generator=g, device=DEV).sign() * (1 + torch.rand(K, generator=g, device=DEV)) *
+             torch.exp2(step)).to(torch.bfloat16)
+    _, q, s, qT, sc, rstd = rlq.add_rmsnorm_quant_act_1x128(h, None, gamma, 1e-6, colwise=True)
+    h, gamma, rstd = h.cpu().float(), gamma.cpu().float(), rstd.cpu()
+    x = (h * rstd[:, None]) * gamma
+
+    def rule(x, dim):  # x with its groups along dim: scales, codes
+        amax = x.abs().amax(dim, keepdim=True)
+        s = torch.where(amax == 0, torch.ones_like(amax), amax / 448)
+        pre = torch.where(s < 2.0 ** -100, torch.full_like(s, 2.0 ** 64), torch.ones_like(s))
+        v = (x * pre) * (1 / (s * pre))
+        return s, v.clamp(-448, 448).to(torch.float8_e4m3fn)
+
+    ws, wq = rule(x.view(M, K // 128, 128), 2)
+    assert torch.equal(s.cpu(), ws[:, :, 0].t())
+    assert torch.equal(q.cpu(), wq.view(M, K).view(torch.uint8))
+    xp = torch.nn.functional.pad(x, (0, 0, 0, -M % 128))
+    ws, wq = rule(xp.view(-1, 128, K), 1)
+    assert torch.equal(sc.cpu(), ws[:, 0])
+    assert torch.equal(qT.cpu(), wq.view(-1, K)[:M].t().contiguous().view(torch.uint8))
+
+
 def norm_bwd_reference(dx, h, rstd, gamma, dres):
     dx, xh, g, r = dx.to(D), h.to(D) * rstd.to(D)[:, None], gamma.to(D), rstd.to(D)[:, None]
     K = dx.shape[1]
