@@ -10,9 +10,10 @@
 //
 // Both are bound by memory: 7.03 bytes per element forward (2 + 2 read, 2 + 1 and a
 // scale per 128 written; 8.06 with the 128x1 codes), 8 backward.  Measured at 8192 x 4096:
-// forward 40 us (0.87 of the HBM rate); with the 128x1 codes 58 us, since the column
-// groups need every row's factor first and read h again (2 bytes an element: 10 us, of
-// which L2 saves little); backward 47 us (0.84).  Tried for the second read and slower or
+// forward 38 us (0.92 of the HBM rate; 40 with unpacked fp32 arithmetic, whose
+// instructions filled 0.72 of the issue slots); with the 128x1 codes 55 us, since the
+// column groups need every row's factor first and read h again (2 bytes an element: 10
+// us, of which L2 saves little); backward 47.5 us (0.83).  Tried for the second read and slower or
 // equal: row blocks in the order that was written last, both passes over chunks of rows
 // that fit L2 (64-88 us), L2 hints on the inputs (62 us).
 #include <cuda_runtime.h>
@@ -37,10 +38,25 @@ __device__ __forceinline__ uint4 ld_once(const uint16_t *p)
     return v;
 }
 
+// Sums of two bf16 pairs, rounded once.  (The same bits as an fp32 sum rounded to bf16:
+// that sum is exact unless the exponents are more than 16 apart, and then both are the
+// larger term.)
 __device__ __forceinline__ uint32_t add_bf16x2(uint32_t a, uint32_t b)
 {
-    return pack_bf16x2(make_float2(bf_lo(a) + bf_lo(b), bf_hi(a) + bf_hi(b)));
+    uint32_t d;
+    asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
 }
+
+// 8 bf16 as four pairs of fp32.
+__device__ __forceinline__ void unpack4x2(const uint4 &v, float2 (&f)[4])
+{
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        f[i] = make_float2(bf_lo(w[i]), bf_hi(w[i]));
+}
+__device__ __forceinline__ float2 both(float a) { return make_float2(a, a); }
 
 // Sum over the threads of one team: warps `w0 ..` of `nw` warps, partials in `sh`
 // (nw floats), named barrier `bar` of 32 * nw threads.  Every thread gets the sum,
@@ -94,19 +110,19 @@ __global__ void __launch_bounds__(1024) k_add_rmsnorm_rows(const uint16_t *res, 
             v[i] = make_uint4(add_bf16x2(v[i].x, d[i].x), add_bf16x2(v[i].y, d[i].y), add_bf16x2(v[i].z, d[i].z),
                               add_bf16x2(v[i].w, d[i].w));
     }
-    float ss = 0.0f;
+    float2 ss2 = both(0.0f);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int c = t + i * T;
         if (h && c < nvec)
             *reinterpret_cast<uint4 *>(h + m * ldh + 8 * c) = v[i];
-        float f[8];
-        unpack8(v[i], f);
+        float2 f[4];
+        unpack4x2(v[i], f);
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            ss = fmaf(f[j], f[j], ss);
+        for (int j = 0; j < 4; ++j)
+            ss2 = __ffma2_rn(f[j], f[j], ss2);
     }
-    ss = team_sum(ss, sh, t >> 5, T >> 5, 0);
+    const float ss = team_sum(ss2.x + ss2.y, sh, t >> 5, T >> 5, 0);
     const float r = __frcp_rn(__fsqrt_rn(ss / (float)K + eps));
     if (t == 0)
         rstd[m] = r;
@@ -114,17 +130,17 @@ __global__ void __launch_bounds__(1024) k_add_rmsnorm_rows(const uint16_t *res, 
     for (int i = 0; i < NV; ++i) {
         const int c = t + i * T;
         const bool in = c < nvec;
-        float f[8], g[8];
-        unpack8(v[i], f);
-        unpack8(in ? *reinterpret_cast<const uint4 *>(gamma + 8 * c) : make_uint4(0, 0, 0, 0), g);
+        float2 f[4], g[4];
+        unpack4x2(v[i], f);
+        unpack4x2(in ? *reinterpret_cast<const uint4 *>(gamma + 8 * c) : make_uint4(0, 0, 0, 0), g);
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            f[j] = (f[j] * r) * g[j];
+        for (int j = 0; j < 4; ++j)
+            f[j] = __fmul2_rn(__fmul2_rn(f[j], both(r)), g[j]);
         const float sc = group_scale(half_warp_max(max_abs8(f)));
         if (in) {
             if ((t & 15) == 0)
                 s[(int64_t)(c >> 4) * lds + m] = sc;
-            *reinterpret_cast<uint2 *>(q + m * ldq + 8 * c) = encode8f(f, sc, scale_rcp(sc));
+            *reinterpret_cast<uint2 *>(q + m * ldq + 8 * c) = encode8f(f, scale_pre(sc), scale_rcp(sc));
         }
     }
 }
@@ -239,12 +255,12 @@ __global__ void __launch_bounds__(512)
     const int team = threadIdx.x / T, t = threadIdx.x - team * T;
     const int nvec = K / 8, nw = T >> 5, wi = t >> 5;
     const int step = gridDim.x * teams;
-    float acc[NV][8];
+    float2 acc[NV][4];
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            acc[i][j] = 0.0f;
+        for (int j = 0; j < 4; ++j)
+            acc[i][j] = both(0.0f);
     uint4 a[NV], b[NV], d[NV];
     float r = 0.0f;
     const uint4 zero = make_uint4(0, 0, 0, 0);
@@ -276,39 +292,40 @@ __global__ void __launch_bounds__(512)
         }
         if (NV == 2)
             load(m + step < M ? m + step : M);
-        float dot = 0.0f;
+        float2 dot2 = both(0.0f);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = t + i * T;
-            float x[8], y[8], g[8];
-            unpack8(ca[i], x);
-            unpack8(cb[i], y);
-            unpack8(c < nvec ? __ldg(reinterpret_cast<const uint4 *>(gamma + 8 * c)) : zero, g);
+            float2 x[4], y[4], g[4];
+            unpack4x2(ca[i], x);
+            unpack4x2(cb[i], y);
+            unpack4x2(c < nvec ? __ldg(reinterpret_cast<const uint4 *>(gamma + 8 * c)) : zero, g);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float xh = y[j] * cr;
-                acc[i][j] = fmaf(x[j], xh, acc[i][j]);
-                dot = fmaf(x[j] * g[j], xh, dot);
+            for (int j = 0; j < 4; ++j) {
+                const float2 xh = __fmul2_rn(y[j], both(cr));
+                acc[i][j] = __ffma2_rn(x[j], xh, acc[i][j]);
+                dot2 = __ffma2_rn(__fmul2_rn(x[j], g[j]), xh, dot2);
             }
         }
         // (the parity keeps a fast warp's next partials apart from the ones being read)
-        dot = team_sum(dot, sh[par] + team * nw, wi, nw, 1 + team) / (float)K;
+        const float dot = team_sum(dot2.x + dot2.y, sh[par] + team * nw, wi, nw, 1 + team) / (float)K;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = t + i * T;
             if (c >= nvec)
                 continue;
-            float x[8], y[8], g[8], e[8];
-            unpack8(ca[i], x);
-            unpack8(cb[i], y);
-            unpack8(__ldg(reinterpret_cast<const uint4 *>(gamma + 8 * c)), g);
-            unpack8(cd[i], e);
+            float2 x[4], y[4], g[4], e[4];
+            unpack4x2(ca[i], x);
+            unpack4x2(cb[i], y);
+            unpack4x2(__ldg(reinterpret_cast<const uint4 *>(gamma + 8 * c)), g);
+            unpack4x2(cd[i], e);
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                e[j] = fmaf(cr, x[j] * g[j] - (y[j] * cr) * dot, e[j]);
+            for (int j = 0; j < 4; ++j) {
+                const float2 xh = __fmul2_rn(y[j], both(cr));
+                e[j] = __ffma2_rn(both(cr), __ffma2_rn(xh, both(-dot), __fmul2_rn(x[j], g[j])), e[j]);
+            }
             *reinterpret_cast<uint4 *>(dh + (int64_t)m * lddh + 8 * c) =
-                make_uint4(pack_bf16x2(make_float2(e[0], e[1])), pack_bf16x2(make_float2(e[2], e[3])),
-                           pack_bf16x2(make_float2(e[4], e[5])), pack_bf16x2(make_float2(e[6], e[7])));
+                make_uint4(pack_bf16x2(e[0]), pack_bf16x2(e[1]), pack_bf16x2(e[2]), pack_bf16x2(e[3]));
         }
     }
     for (int k = 0; k < teams; ++k) {
@@ -319,8 +336,8 @@ __global__ void __launch_bounds__(512)
                 if (c >= nvec)
                     continue;
                 float4 *p = reinterpret_cast<float4 *>(dyn + 8 * c);
-                float4 lo = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
-                float4 hi = make_float4(acc[i][4], acc[i][5], acc[i][6], acc[i][7]);
+                float4 lo = make_float4(acc[i][0].x, acc[i][0].y, acc[i][1].x, acc[i][1].y);
+                float4 hi = make_float4(acc[i][2].x, acc[i][2].y, acc[i][3].x, acc[i][3].y);
                 if (k > 0) {
                     const float4 x = p[0], y = p[1];
                     lo = make_float4(lo.x + x.x, lo.y + x.y, lo.z + x.z, lo.w + x.w);
