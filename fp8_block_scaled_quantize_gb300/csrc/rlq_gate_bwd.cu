@@ -10,13 +10,14 @@
 // is fp32.
 //
 // Floor: 2 + 1 + 1 bytes read and 2 + 2 + 1 written per element of [M, F], 160 us at 8192
-// x 14336 at the HBM rate.  Measured 203 us (0.79): instructions (decoding, the sigmoid,
-// three maxima and five encodings an element, 38 before the input copies left the threads;
-// a copy of the kernel without its loads and stores took 188), at 16 warps a SM, which is
-// what the values' registers allow.  What brought it there from 294: the transposed codes
+// x 14336 at the HBM rate.  Measured 198 us (0.81): instructions (decoding, the sigmoid,
+// three maxima and five encodings an element, 35 in all), issued at 51% by the 16 warps a
+// SM that the values' registers allow; a copy of the kernel without loads and stores was
+// 15 us faster.  What brought it there from 294: the transposed codes
 // stored as TMA boxes rather than by the threads (265 with 16-byte copies and bulk copies
 // of single columns, 235 with boxes), the boxes' reads waited for a barrier later (223),
-// inputs by TMA (211), two tiles ahead (203).  Slower, each on top of the version of its
+// inputs by TMA (211), two tiles ahead (203), scales without the
+// IEEE division's and reciprocal's sequences (198).  Slower, each on top of the version of its
 // time: all boxes from one warp (253 for 235), warps that store nothing running ahead of
 // the boxes' issue (285), the row codes as boxes too (238), column maxima joined by 24
 // lanes of every warp (248).  Earlier: the values formed twice at two CTAs a SM (303, 75
