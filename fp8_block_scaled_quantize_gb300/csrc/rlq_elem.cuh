@@ -114,13 +114,6 @@ __device__ __forceinline__ uint2 encode8f(const float2 (&v)[4], float pre, float
                       e4m3x4(f[2].x, f[2].y, f[3].x, f[3].y));
 }
 
-__device__ __forceinline__ uint2 encode8f(const float (&v)[8], float s, float rcp)
-{
-    const float2 f[4] = {make_float2(v[0], v[1]), make_float2(v[2], v[3]), make_float2(v[4], v[5]),
-                         make_float2(v[6], v[7])};
-    return encode8f(f, scale_pre(s), rcp);
-}
-
 // max(|a|, |b|, |c|) in one instruction.
 __device__ __forceinline__ float max3_abs(float a, float b, float c)
 {
@@ -133,12 +126,6 @@ __device__ __forceinline__ float max_abs8(const float2 (&v)[4])
 {
     const float a = max3_abs(v[0].x, v[0].y, v[1].x), b = max3_abs(v[1].y, v[2].x, v[2].y);
     return max3_abs(max3_abs(a, v[3].x, v[3].y), b, b);
-}
-
-__device__ __forceinline__ float max_abs8(const float (&v)[8])
-{
-    const float a = max3_abs(v[0], v[1], v[2]), b = max3_abs(v[3], v[4], v[5]);
-    return max3_abs(max3_abs(a, v[6], v[7]), b, b);
 }
 
 // 1 / (1 + exp(-g)) of two values, the exponential and the reciprocal on the

@@ -52,11 +52,7 @@ constexpr int SMEM_BYTES = OFF_BARS + 24;
 static_assert(SMEM_BYTES <= 232448 && OFF_TILES % 1024 == 0, "shared memory budget; the swizzle's period");
 
 struct GateBwd {
-    const uint16_t *da;
-    int64_t ldda;
-    const uint8_t *guq;
-    int64_t ldguq;
-    const float *gus;
+    const float *gus;  // (da and the checkpoint's codes come through tensor maps)
     int64_t ld_gus;
     uint8_t *q;
     int64_t ldq;
@@ -75,11 +71,6 @@ struct GateBwd {
     uint64_t timeout_ns;
 };
 
-// Global -> shared copies; bytes = 0 writes zeros without reading.
-__device__ __forceinline__ void copy4(uint32_t dst, const void *src, uint32_t bytes)
-{
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
 // A barrier of the CTA that some warps wait at and others only pass.
 __device__ __forceinline__ void bar_wait()
 {
@@ -171,7 +162,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_gate_bwd(const GateBwd p, const 
         }
         if (cg < 8) {  // this half-warp's scales: four rows of g, four of u
             const bool ok = (cg & 3) < left;
-            copy4(smem0 + OFF_SCALES + (buf * 2 * GRP + 8 * rg + cg) * 4,
+            cp_async4(smem0 + OFF_SCALES + (buf * 2 * GRP + 8 * rg + cg) * 4,
                   ok ? p.gus + ((cg >> 2) * fb + pf) * p.ld_gus + m + (cg & 3) : p.gus, ok ? 4 : 0);
         }
     };
@@ -391,8 +382,8 @@ rlq_status launch_gated_backward(const uint16_t *da, int64_t ldda, const uint8_t
                                   int64_t ldac, int64_t M, int64_t F, cudaStream_t st)
 {
     const int64_t m_tiles = (M + GRP - 1) / GRP, tiles = m_tiles * (F / GRP);
-    const GateBwd p = {da, ldda, guq, ldguq, gus, ld_gus, q,  ldq, s, lds, qT,           ldqT,
-                       sc, ldsc, aT,  ldaT,  ac,  ldac,   M,  F,   (int)m_tiles, (int)tiles, wait_limit_ns()};
+    const GateBwd p = {gus,  ld_gus, q,    ldq, s, lds,          qT,         ldqT,           sc, ldsc, aT,
+                       ldaT, ac,     ldac, M,   F, (int)m_tiles, (int)tiles, wait_limit_ns()};
     CUtensorMap tmQ = {}, tmA = {}, tmDa, tmGu;
     rlq_status rin = encode_tile_map(&tmDa, da, true, M, F, ldda);
     if (rin == RLQ_OK)
@@ -416,7 +407,8 @@ rlq_status launch_gated_backward(const uint16_t *da, int64_t ldda, const uint8_t
     }
     if (e == cudaSuccess) {
         const int64_t sms = device_sms();
-        e = launch_pdl(k_gate_bwd, dim3((unsigned)(tiles < sms ? tiles : sms)), dim3(THREADS), SMEM_BYTES, st, p, tmQ, tmA, tmDa, tmGu);
+        e = launch_pdl(k_gate_bwd, dim3((unsigned)(tiles < sms ? tiles : sms)), dim3(THREADS), SMEM_BYTES, st, p, tmQ, tmA,
+                       tmDa, tmGu);
     }
     return cuda_status(e, "gated backward launch");
 }
