@@ -168,6 +168,29 @@ __device__ __forceinline__ void store_column_maxima(const float2 (&c)[4], bool u
     *reinterpret_cast<float4 *>(dst + (upper ? 4 : 0)) = o;
 }
 
+// The first n bytes (0 .. 15) of a 16-byte piece, p on a 16-byte boundary.
+__device__ __forceinline__ void store_head(uint8_t *p, uint4 v, int n)
+{
+    if (n & 8) {
+        *reinterpret_cast<uint2 *>(p) = make_uint2(v.x, v.y);
+        v.x = v.z;
+        v.y = v.w;
+        p += 8;
+    }
+    if (n & 4) {
+        *reinterpret_cast<uint32_t *>(p) = v.x;
+        v.x = v.y;
+        p += 4;
+    }
+    if (n & 2) {
+        *reinterpret_cast<uint16_t *>(p) = (uint16_t)v.x;
+        v.x >>= 16;
+        p += 2;
+    }
+    if (n & 1)
+        *p = (uint8_t)v.x;
+}
+
 // Writes a 128 x 128 tile of codes, held as [column][16 chunks of 8 rows] with chunk
 // index XOR column / 8, as rows of the transposed matrix: 8 threads per column, 16
 // bytes each.  Rows at or past `rows` are not written.  dst: element (column 0, row 0).
@@ -181,15 +204,10 @@ __device__ __forceinline__ void store_tile_T(const uint8_t *tile, int t, int thr
         if (cg & 1)
             v = make_uint4(v.z, v.w, v.x, v.y);
         uint8_t *p = dst + (int64_t)c * ld + 16 * i;
-        if (16 * i + 16 <= rows) {
+        if (16 * i + 16 <= rows)
             *reinterpret_cast<uint4 *>(p) = v;
-        } else {
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int b = 0; b < 16; ++b)
-                if (16 * i + b < rows)
-                    p[b] = (uint8_t)(w[b >> 2] >> (8 * (b & 3)));
-        }
+        else if (16 * i < rows)
+            store_head(p, v, rows - 16 * i);
     }
 }
 

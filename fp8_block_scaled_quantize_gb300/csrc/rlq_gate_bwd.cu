@@ -348,15 +348,10 @@ __global__ void __launch_bounds__(THREADS, 1) k_gate_bwd(const GateBwd p, const 
                 const uint4 c = *reinterpret_cast<const uint4 *>(tiles + k * TILE_BYTES + slot * GRP +
                                                                  16 * (i ^ (slot & 7)));
                 uint8_t *dst = (k < 2 ? p.qT + (k * p.F + col) * p.ldqT : p.aT + col * p.ldaT) + m0 + 16 * i;
-                if (16 * i + 16 <= rows) {
+                if (16 * i + 16 <= rows)
                     *reinterpret_cast<uint4 *>(dst) = c;
-                } else {
-                    const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-#pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                        if (16 * i + e < rows)
-                            dst[e] = (uint8_t)(w[e >> 2] >> (8 * (e & 3)));
-                }
+                else if (16 * i < rows)
+                    store_head(dst, c, rows - 16 * i);
             }
         }
         if (stop) {

@@ -17,9 +17,9 @@
 // maxima are exchanged across the cluster while the next group's weights arrive.
 //
 // Bound by memory: 2 F K bytes of weight codes.  Measured back to back, one token: F =
-// 14336, K = 4096 22.9 us (0.76 of the HBM rate; the tcgen05 kernel 32.4), 18944 x 3584
-// 24.1 us (0.83), 27648 x 5120 46.5 us (0.90); about 4 us of each are the first copies'
-// and the last group's latency.  One CTA per SM with three times the ring: 25.9, 28.8,
+// 14336, K = 4096 23.5 us (0.74 of the HBM rate; the tcgen05 kernel 24.6), 18944 x 3584
+// 25 us (0.80; the same), 27648 x 5120 46.3 us (0.90; 54.2), 5120 x 5120 13.5 us (23.2);
+// about 4 us of each are the first copies' and the last group's latency.  One CTA per SM with three times the ring: 25.9, 28.8,
 // 48.0 (the GPU holds 36 such clusters, 112 groups take four rounds; with two CTAs per SM
 // a round's stragglers have the SM's bandwidth to themselves).  16 tokens this way were
 // no faster than the tcgen05 kernel, so more than 8 go there.
