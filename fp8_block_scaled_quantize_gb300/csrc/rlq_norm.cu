@@ -11,7 +11,7 @@
 // Both are bound by memory: 7.03 bytes per element forward (2 + 2 read, 2 + 1 and a
 // scale per 128 written; 8.06 with the 128x1 codes), 8 backward.  Measured at 8192 x 4096:
 // forward 38.6 us (0.90 of the HBM rate; 0.95 at 16384 x 5120; 40 us with unpacked fp32 arithmetic, whose
-// instructions filled 0.72 of the issue slots); with the 128x1 codes 55 us, since the
+// instructions filled 0.72 of the issue slots); with the 128x1 codes 54.7 us, since the
 // column groups need every row's factor first and read h again (2 bytes an element: 10
 // us, of which L2 saves little); backward 47.5 us (0.83).  Tried for the second read and slower or
 // equal: row blocks in the order that was written last, both passes over chunks of rows
