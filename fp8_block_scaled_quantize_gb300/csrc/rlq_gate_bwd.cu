@@ -69,6 +69,7 @@ struct GateBwd {
     int64_t M, F;
     int m_tiles, tiles;
     uint64_t timeout_ns;
+    int withhold_first_load;  // diagnostic: nothing arrives for the CTA's first tile
 };
 
 // A barrier of the CTA that some warps wait at and others only pass.
@@ -150,10 +151,10 @@ __global__ void __launch_bounds__(THREADS, 1) k_gate_bwd(const GateBwd p, const 
     }
     __syncthreads();
     pdl_begin();
-    auto prefetch = [&](int pm, int pf, int buf) {
+    auto prefetch = [&](int pm, int pf, int buf, bool inputs = true) {
         const int64_t m = (int64_t)pm * GRP + 4 * rg;
         const int left = (int)(p.M - m < 4 ? p.M - m : 4);  // rows of mine inside the matrix (may be <= 0)
-        if (t == LOADER && !*abort_flag) {  // (rows past the end arrive as zeros)
+        if (t == LOADER && inputs && !*abort_flag) {  // (rows past the end arrive as zeros)
             const uint32_t bar = bars + 8 * buf, in = smem0 + buf * IN_BYTES;
             mbar_arrive_expect_tx(bar, IN_BYTES);
             tma_load_2d(in, &tmDa, bar, pf * GRP, pm * GRP);
@@ -177,7 +178,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_gate_bwd(const GateBwd p, const 
     };
     int tile = blockIdx.x, am = mt, af = ft;  // (am, af): the tile to copy next
     if (tile < p.tiles)
-        prefetch(am, af, 0);
+        prefetch(am, af, 0, !p.withhold_first_load);
     asm volatile("cp.async.commit_group;" ::: "memory");
     step(am, af);
     if (tile + (int)gridDim.x < p.tiles)
@@ -378,7 +379,8 @@ rlq_status launch_gated_backward(const uint16_t *da, int64_t ldda, const uint8_t
 {
     const int64_t m_tiles = (M + GRP - 1) / GRP, tiles = m_tiles * (F / GRP);
     const GateBwd p = {gus,  ld_gus, q,    ldq, s, lds,          qT,         ldqT,           sc, ldsc, aT,
-                       ldaT, ac,     ldac, M,   F, (int)m_tiles, (int)tiles, wait_limit_ns()};
+                       ldaT, ac,     ldac, M,   F, (int)m_tiles, (int)tiles, wait_limit_ns(),
+                       take_stall() ? 1 : 0};
     CUtensorMap tmQ = {}, tmA = {}, tmDa, tmGu;
     rlq_status rin = encode_tile_map(&tmDa, da, true, M, F, ldda);
     if (rin == RLQ_OK)

@@ -1418,6 +1418,13 @@ rlq_status launch_gemm(const GemmArgs &a, cudaStream_t st)
 
 void arm_gemm_stall() { t_stall_armed = true; }
 
+bool take_stall()
+{
+    const bool armed = t_stall_armed;
+    t_stall_armed = false;
+    return armed;
+}
+
 rlq_status plan_splitk(int64_t R, int64_t C, int64_t L, int64_t ws_cap, int *splits, int64_t *ws_bytes)
 {
     int sms = 0;

@@ -228,5 +228,8 @@ rlq_status launch_diag_wait(int64_t timeout_us, cudaStream_t st);
 // launch: it runs on single CTAs and its producer withholds the first stage's
 // loads, so the MMA warp's bounded wait runs out and the CTA takes its abort path.
 void arm_gemm_stall();
+// Whether the calling thread has armed it, which uses it up (the gate's backward pass, whose
+// CTAs then withhold their first tile's copies).
+bool take_stall();
 
 }  // namespace rlq

@@ -38,8 +38,8 @@
  *   - Errors: arguments are validated on the host before any launch (NULL
  *     pointers, negative sizes, ld smaller than the row, misalignment); on
  *     failure nothing is launched.  A failed launch returns RLQ_ERR_CUDA.  The
- *     GEMM kernels and rlq_gated_backward bound every wait on the GPU: a wait that runs out records
- *     an error word on the device, and the next rlq_check on that device
+ *     GEMM kernels and rlq_gated_backward bound every wait on the GPU: a wait that
+ *     runs out records an error word on the device, and the next rlq_check on that device
  *     returns RLQ_ERR_TIMEOUT.  rlq_last_error() describes the latest failure.
  *   - Inputs must be finite; NaN / Inf inputs are outside the contract.
  */
@@ -669,12 +669,14 @@ rlq_status rlq_diag_bounded_wait(int64_t timeout_us, rlq_stream_t stream);
 /*
  * Diagnostic for the block-scaled GEMM's own abort path: arms, for the calling
  * host thread, a one-shot fault in the next GEMM call it makes (any of the
- * FProp / DGrad / WGrad entry points).  That launch runs on single CTAs, and
- * the TMA producer of every CTA withholds the loads of its first pipeline
+ * FProp / DGrad / WGrad entry points, rlq_gemm_gated_fprop of more than 8 tokens) or
+ * in the next rlq_gated_backward, whichever is first.  A GEMM's launch runs on
+ * single CTAs, and the TMA producer of every CTA withholds the loads of its first pipeline
  * stage, so nothing ever arrives on that stage's barrier: the MMA warp's
  * bounded wait runs out (RLQ_WAIT_TIMEOUT_MS, 1 s by default), it records a
  * timeout and raises the CTA's abort flag, and the CTA drains its copies in
- * flight, frees its tensor memory and exits.  The output of that call is
+ * flight, frees its tensor memory and exits.  In rlq_gated_backward no CTA's first
+ * tile arrives, and it leaves after that tile.  The output of that call is
  * undefined; the following rlq_check returns RLQ_ERR_TIMEOUT, and later calls
  * run normally.  Nothing faults, traps or hangs.  Host-only; always RLQ_OK.
  */

@@ -600,6 +600,36 @@ def test_another_stream_and_a_graph(M):
     rlq.check()
 
 
+@pytest.mark.parametrize("call", ["gated", "backward"])
+def test_wait_that_runs_out_is_reported(call):
+    """With the stall diagnostic armed nothing arrives for the first block or tile: the
+    bounded waits run out, the kernel leaves, the check reports it, and the same call then
+    gives the bits that it gave before."""
+    M, F, K = 700, 4096, 1024  # 192 tiles: some CTAs have a second one in flight
+    if call == "gated":
+        g = gen(41)
+        x, w = normal(g, M, K), normal(g, 2 * F, K, std=K ** -0.5)
+        xq, xs, _, _ = rlq.quant_act_1x128(x)
+        wq, ws, _ = rlq.quant_weight_128x128(w)
+        run = lambda: rlq.gemm_gated_fprop(xq, xs, wq, ws, checkpoint=True)  # noqa: E731
+    else:
+        g = gen(42)
+        da = normal(g, M, F, std=1e-3)
+        guq, gus, _, _ = rlq.quant_act_1x128(normal(g, M, 2 * F))
+        run = lambda: rlq.gated_backward(da, guq, gus)  # noqa: E731
+    want = run()
+    rlq.check()
+    rlq.rlq_diag_arm_gemm_stall()
+    run()
+    with pytest.raises(rlq.RlqError) as e:
+        rlq.check()
+    assert e.value.status == 5 and "ran out" in str(e.value)
+    rlq.check()
+    got = run()
+    rlq.check()
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
 @pytest.mark.parametrize("scale", [1e-30, 1e-38])
 def test_gated_backward_tiny_gradients(scale):
     """Groups whose scales are subnormal (their reciprocals overflow) beside ordinary ones."""
