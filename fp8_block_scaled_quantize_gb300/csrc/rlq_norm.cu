@@ -25,6 +25,7 @@ namespace rlq {
 namespace {
 
 constexpr int GRP = 128;
+constexpr int MAX_K = 16384;  // (the entry points refuse more)
 
 // A load that may alias an output of the same kernel (read by the thread that
 // later overwrites it), so not through the read-only path.
@@ -444,9 +445,16 @@ cudaError_t launch_rmsnorm_backward(const uint16_t *dx, int64_t lddx, const uint
     const BwdPlan p = bwd_plan(M, K);
     auto kernel = p.nv == 2 ? k_rmsnorm_bwd<2> : k_rmsnorm_bwd<4>;
     const size_t smem = (size_t)K * 4;
-    cudaError_t e = cudaSuccess;
-    if (smem > 48 * 1024)  // K > 12288
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    // Four vectors a thread (K > 8192) may need more than the 48 KB, static and dynamic,
+    // that a kernel has unasked.  The limit is the process's: raised once per device, to
+    // the largest K's, and never lowered under another thread's launch.
+    static std::atomic<bool> raised[64];
+    int dev = 0;
+    cudaError_t e = p.nv == 2 ? cudaSuccess : cudaGetDevice(&dev);
+    if (e == cudaSuccess && p.nv != 2 && !raised[dev & 63].load(std::memory_order_relaxed)) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, MAX_K * 4);
+        raised[dev & 63].store(e == cudaSuccess, std::memory_order_relaxed);
+    }
     if (e != cudaSuccess)
         return e;
     e = launch_pdl(kernel, dim3(p.grid), dim3(p.T * p.teams), smem, st, dx, lddx, h, ldh, rstd, gamma, dres, lddres, dh,
