@@ -7,6 +7,11 @@ allocate outputs with torch (device memory is PyTorch's plumbing here) and call
 the same entry points; every step of the computation runs in the library's
 CUDA kernels.  There is no fallback: if the library is missing or cannot be
 loaded, the first call raises.
+
+``stream`` names the stream that a helper launches on (a torch stream or a handle); without
+it that is the current one.  Scratch comes from the launching stream's pool, outputs from
+the current stream's.  So where the two differ, the named stream has to have waited for the
+current one, as for any tensor that is made on one stream and used on another.
 """
 from __future__ import annotations
 
@@ -306,6 +311,20 @@ def _stream(stream) -> int:
     return int(stream)
 
 
+def _scratch(nbytes: int, device, stream) -> torch.Tensor:
+    """Workspace of a call on ``stream``, out of that stream's pool.  Nothing that is queued
+    on another stream uses such a block, and once the helper has let go of it, only work
+    behind the call gets it."""
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        # (a stream object made around handle 0 would be a new stream, not the default one)
+        handle = int(stream)
+        stream = torch.cuda.ExternalStream(handle, device) if handle else torch.cuda.default_stream(device)
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
 def _ptr(t) -> int | None:
     return None if t is None else t.data_ptr()
 
@@ -421,21 +440,21 @@ def gemm_fprop_per_channel(xq, xs_rep, wq, ws_rep, out=None, stream=None, split_
     args = (xq.data_ptr(), _ld(xq), xs_rep.data_ptr(), _ld(xs_rep), wq.data_ptr(), _ld(wq), ws_rep.data_ptr(),
             _ld(ws_rep), y.data_ptr(), _ld(y), M, N, K)
     if split_k:
-        rlq_gemm_fprop_per_channel_splitk(*args, *_workspace(GEMM_FPROP, M, N, K, workspace, xq.device),
+        rlq_gemm_fprop_per_channel_splitk(*args, *_workspace(GEMM_FPROP, M, N, K, workspace, xq.device, stream),
                                           _stream(stream))
     else:
         rlq_gemm_fprop_per_channel(*args, _stream(stream))
     return y
 
 
-def _workspace(kind: int, M: int, N: int, K: int, workspace, device):
+def _workspace(kind: int, M: int, N: int, K: int, workspace, device, stream):
     """(pointer, bytes) of the split-K workspace: the caller's uint8 tensor, or
     one allocated with torch for the library's plan (None when it is one pass)."""
     if workspace is None:
         nbytes = rlq_gemm_splitk_workspace_bytes(kind, M, N, K)
         if nbytes == 0:
             return None, 0
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        workspace = _scratch(nbytes, device, stream)
     return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
@@ -450,7 +469,7 @@ def gemm_fprop(xq, xs, wq, ws, out=None, stream=None, split_k: bool = False, wor
     args = (xq.data_ptr(), _ld(xq), xs.data_ptr(), _ld(xs), wq.data_ptr(), _ld(wq), ws.data_ptr(), _ld(ws),
             y.data_ptr(), _ld(y), M, N, K)
     if split_k:
-        rlq_gemm_fprop_splitk(*args, *_workspace(GEMM_FPROP, M, N, K, workspace, xq.device), _stream(stream))
+        rlq_gemm_fprop_splitk(*args, *_workspace(GEMM_FPROP, M, N, K, workspace, xq.device, stream), _stream(stream))
     else:
         rlq_gemm_fprop(*args, _stream(stream))
     return y
@@ -466,7 +485,7 @@ def gemm_dgrad(dyq, dys, w, ws, transposed: bool = True, out=None, stream=None, 
     args = (dyq.data_ptr(), _ld(dyq), dys.data_ptr(), _ld(dys), w.data_ptr(), _ld(w), 1 if transposed else 0,
             ws.data_ptr(), _ld(ws), dx.data_ptr(), _ld(dx), M, N, K)
     if split_k:
-        rlq_gemm_dgrad_splitk(*args, *_workspace(GEMM_DGRAD, M, N, K, workspace, dyq.device), _stream(stream))
+        rlq_gemm_dgrad_splitk(*args, *_workspace(GEMM_DGRAD, M, N, K, workspace, dyq.device, stream), _stream(stream))
     else:
         rlq_gemm_dgrad(*args, _stream(stream))
     return dx
@@ -480,7 +499,7 @@ def gemm_wgrad(dyqT, dysc, xqT, xsc, out=None, stream=None, split_k: bool = Fals
     args = (dyqT.data_ptr(), _ld(dyqT), dysc.data_ptr(), _ld(dysc), xqT.data_ptr(), _ld(xqT),
             xsc.data_ptr(), _ld(xsc), dw.data_ptr(), _ld(dw), M, N, K)
     if split_k:
-        rlq_gemm_wgrad_splitk(*args, *_workspace(GEMM_WGRAD, M, N, K, workspace, dyqT.device), _stream(stream))
+        rlq_gemm_wgrad_splitk(*args, *_workspace(GEMM_WGRAD, M, N, K, workspace, dyqT.device, stream), _stream(stream))
     else:
         rlq_gemm_wgrad(*args, _stream(stream))
     return dw
@@ -494,7 +513,7 @@ def gemm_wgrad_accumulate_(dw_acc: torch.Tensor, dyqT, dysc, xqT, xsc, workspace
         raise TypeError("dw_acc must be float32")
     N, M = dyqT.shape
     K = xqT.shape[0]
-    ptr, nbytes = _workspace(GEMM_WGRAD, M, N, K, workspace, dw_acc.device)
+    ptr, nbytes = _workspace(GEMM_WGRAD, M, N, K, workspace, dw_acc.device, stream)
     rlq_gemm_wgrad_accumulate(dyqT.data_ptr(), _ld(dyqT), dysc.data_ptr(), _ld(dysc), xqT.data_ptr(), _ld(xqT),
                               xsc.data_ptr(), _ld(xsc), dw_acc.data_ptr(), _ld(dw_acc), M, N, K, ptr, nbytes,
                               _stream(stream))
@@ -544,8 +563,8 @@ def gemm_nvfp4_weight_only(x: torch.Tensor, q, sb, st, out=None, stream=None, sp
     args = (x.data_ptr(), _ld(x), q.data_ptr(), q.stride(0), sb.data_ptr(), sb.stride(0), st.data_ptr(),
             y.data_ptr(), _ld(y), M, N, K)
     if split_k:
-        rlq_gemm_nvfp4_weight_only_splitk(*args, *_workspace(GEMM_NVFP4_WEIGHT_ONLY, M, N, K, workspace, x.device),
-                                          _stream(stream))
+        ws = _workspace(GEMM_NVFP4_WEIGHT_ONLY, M, N, K, workspace, x.device, stream)
+        rlq_gemm_nvfp4_weight_only_splitk(*args, *ws, _stream(stream))
     else:
         rlq_gemm_nvfp4_weight_only(*args, _stream(stream))
     return y
@@ -640,10 +659,7 @@ def rmsnorm_backward(dx: torch.Tensor, h: torch.Tensor, rstd: torch.Tensor, gamm
     if workspace is None:
         nbytes = _norm_workspace_bytes(M, K, torch._C._cuda_getDevice())
         if nbytes:
-            workspace = torch.empty(nbytes, dtype=torch.uint8, device=dx.device)
-            if stream is not None:  # freed here, used there
-                workspace.record_stream(stream if isinstance(stream, torch.cuda.Stream)
-                                        else torch.cuda.ExternalStream(int(stream)))
+            workspace = _scratch(nbytes, dx.device, stream)
     else:
         nbytes = workspace.numel() * workspace.element_size()
     _call("rlq_rmsnorm_backward", dx.data_ptr(), lddx, h.data_ptr(), ldh, r, g, _ptr(dres), ldres, dh.data_ptr(),
