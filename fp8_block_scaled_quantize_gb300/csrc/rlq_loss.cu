@@ -174,7 +174,7 @@ __device__ __noinline__ RowScalars row_scalars(const PolicyLossArgs &p, const Ro
     o.loss = o.dlp = 0.0f;
     if (!p.adv)
         return o;
-    const float rho = expf(o.lp - in.old);
+    const float lr = o.lp - in.old, rho = expf(lr);
     // (minima by comparison: a NaN among the row's inputs stays one, fminf would drop it)
     float isw = 1.0f;
     if (p.lp_behav) {
@@ -183,7 +183,8 @@ __device__ __noinline__ RowScalars row_scalars(const PolicyLossArgs &p, const Ro
     }
     float clip = rho < 1.0f - p.eps_lo ? 1.0f - p.eps_lo : rho;
     clip = clip > in.hi || in.hi != in.hi ? in.hi : clip;
-    const float plain = rho * in.adv, clipped = clip * in.adv;
+    // (no advantage: 0, also where a finite ratio's exponential overflows)
+    const float plain = in.adv == 0.0f && lr < INFINITY ? 0.0f : rho * in.adv, clipped = clip * in.adv;
     float loss = -isw * (plain > clipped || clipped != clipped ? clipped : plain);
     float dlp = plain > clipped ? 0.0f : -isw * plain;
     if (p.lp_ref) {
