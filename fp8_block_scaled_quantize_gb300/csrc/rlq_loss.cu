@@ -189,8 +189,10 @@ __device__ __noinline__ RowScalars row_scalars(const PolicyLossArgs &p, const Ro
     float dlp = plain > clipped ? 0.0f : -isw * plain;
     if (p.lp_ref) {
         const float d = in.ref - o.lp, e = expm1f(d);
-        loss = fmaf(p.kl_beta, e - d, loss);
-        dlp = fmaf(-p.kl_beta, e, dlp);
+        if (p.kl_beta > 0.0f || d != d) {  // (0 switches the term off, even where e overflows)
+            loss = fmaf(p.kl_beta, e - d, loss);
+            dlp = fmaf(-p.kl_beta, e, dlp);
+        }
     }
     o.loss = in.weight * loss;
     o.dlp = in.weight * dlp;

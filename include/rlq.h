@@ -613,7 +613,7 @@ rlq_status rlq_token_logprobs(const void *logits, rlq_dtype dtype, int64_t ld, i
  *   w    = min(exp(lp_old - lp_behav), tis_cap)          (1 where lp_behav is NULL)
  *   pg   = -w * min(rho * adv, clip(rho, 1 - eps_lo, hi) * adv),
  *          hi = clip_hi[r], or 1 + eps_hi where clip_hi is NULL
- *   kl   = kl_beta * (exp(d) - 1 - d), d = lp_ref - lp   (0 where lp_ref is NULL)
+ *   kl   = kl_beta * (exp(d) - 1 - d), d = lp_ref - lp   (0 where lp_ref is NULL or kl_beta 0)
  *   loss = weight * (pg + kl)
  *   dlogits[v] = dloss/dlp * (1[v = target] - softmax(z)[v]) / temperature
  *

@@ -30,3 +30,20 @@ def test_no_advantage_and_a_ratio_that_overflows(V):
         assert torch.equal(a, b)
     st["logp_old"][2] = float("nan")
     assert bool(torch.isnan(call(st)[0][2]))
+
+
+@pytest.mark.parametrize("V", [500, 40001])
+def test_no_kl_weight_and_a_reference_far_above(V):
+    """kl_beta = 0 switches the KL term off whatever exp(lp_ref - lp) is, a target of
+    probability 0 included; a NaN in lp_ref is still seen."""
+    st = loss_inputs(6, V, torch.bfloat16, 5)
+    st["weight"][:] = 1 / 6
+    st["logits"][4, st["targets"][4]] = float("-inf")
+    st["logp_ref"][:] = 500.0
+    got = call(st, kl_beta=0.0)
+    st["logp_ref"] = None
+    for a, b in zip(got, call(st)):
+        assert torch.equal(a, b)
+    assert bool(torch.isfinite(got[0]).all()) and bool(torch.isfinite(got[2]).all())
+    st["logp_ref"] = torch.full((6,), float("nan"), device="cuda")
+    assert bool(torch.isnan(call(st, kl_beta=0.0)[0]).all())
