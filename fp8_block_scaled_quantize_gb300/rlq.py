@@ -325,6 +325,15 @@ def _scratch(nbytes: int, device, stream) -> torch.Tensor:
         return torch.empty(nbytes, dtype=torch.uint8, device=device)
 
 
+def _given(workspace: torch.Tensor):
+    """(address, bytes) of a caller's workspace, which the kernels write as plain memory."""
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    if not workspace.is_cuda:
+        raise ValueError("workspace must be a CUDA tensor")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
 def _ptr(t) -> int | None:
     return None if t is None else t.data_ptr()
 
@@ -450,12 +459,12 @@ def gemm_fprop_per_channel(xq, xs_rep, wq, ws_rep, out=None, stream=None, split_
 def _workspace(kind: int, M: int, N: int, K: int, workspace, device, stream):
     """(pointer, bytes) of the split-K workspace: the caller's uint8 tensor, or
     one allocated with torch for the library's plan (None when it is one pass)."""
-    if workspace is None:
-        nbytes = rlq_gemm_splitk_workspace_bytes(kind, M, N, K)
-        if nbytes == 0:
-            return None, 0
-        workspace = _scratch(nbytes, device, stream)
-    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    if workspace is not None:
+        return _given(workspace)
+    nbytes = rlq_gemm_splitk_workspace_bytes(kind, M, N, K)
+    if nbytes == 0:
+        return None, 0
+    return _scratch(nbytes, device, stream).data_ptr(), nbytes
 
 
 def gemm_fprop(xq, xs, wq, ws, out=None, stream=None, split_k: bool = False, workspace=None):
@@ -661,7 +670,7 @@ def rmsnorm_backward(dx: torch.Tensor, h: torch.Tensor, rstd: torch.Tensor, gamm
         if nbytes:
             workspace = _scratch(nbytes, dx.device, stream)
     else:
-        nbytes = workspace.numel() * workspace.element_size()
+        nbytes = _given(workspace)[1]
     _call("rlq_rmsnorm_backward", dx.data_ptr(), lddx, h.data_ptr(), ldh, r, g, _ptr(dres), ldres, dh.data_ptr(),
           ldres if dh is dres else K, dgamma.data_ptr(), M, K, _ptr(workspace), nbytes, _stream(stream))
     return dh, dgamma
