@@ -63,7 +63,9 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d)
     return w;
 }
 
-// Scale of a group: fl32(amax / 448), 1 for an all-zero group.  The quotient by
+// Scale of a group: fl32(amax / 448), 1 for an all-zero group, and 2^-149 where the quotient
+// rounds to zero (amax <= 448 x 2^-150, which no bf16 value is but a product may be: codes
+// by a scale of 0 would be NaN where the value is 0).  The quotient by
 // Markstein's correction (IBM J. Res. Dev. 34(1), 1990): q = amax RN(1/448), then q +
 // (amax - 448 q) RN(1/448), the remainder exact.  It was compared with the IEEE division
 // for every finite amax >= 2^-117, where the quotient is normal, without a difference;
@@ -74,7 +76,8 @@ __device__ __forceinline__ float group_scale(float amax)
         const float r = 1.0f / 448.0f, q = __fmul_rn(amax, r);
         return __fmaf_rn(__fmaf_rn(-q, 448.0f, amax), r, q);
     }
-    return amax == 0.0f ? 1.0f : __fdiv_rn(amax, 448.0f);
+    const float q = __fdiv_rn(amax, 448.0f);
+    return amax == 0.0f ? 1.0f : q == 0.0f ? 0x1p-149f : q;
 }
 
 // A scale as the encoding applies it: codes are of (x * pre) * rcp, with pre = 1, or

@@ -25,7 +25,9 @@
  *   - bf16 tensors are passed as uint16_t bit patterns (IEEE bfloat16).
  *   - "Codes" are FP8 E4M3 bytes (OCP "fn" variant: max 448, no infinities).
  *     Scales are fp32 dequantization multipliers: value ~= decode(code) * scale.
- *     A group's scale is fl32(amax / 448), or 1.0 when the group is all zero;
+ *     A group's scale is fl32(amax / 448), or 1.0 when the group is all zero,
+ *     or 2^-149 where the quotient rounds to zero (amax <= 448 x 2^-150, which only
+ *     the calls that quantize products of theirs can meet);
  *     a code is the round-to-nearest-even, saturating E4M3 encoding of
  *     fl32(x / scale) with IEEE fp32 division.
  *   - Alignment: every code and bf16 base pointer 16-byte aligned and every
