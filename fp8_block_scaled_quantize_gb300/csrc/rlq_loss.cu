@@ -17,12 +17,14 @@
 // overwrite the logits: a thread reads what it overwrites, and a cluster's CTAs read the
 // target's logit before any of them writes.
 //
-// Measured: 4096 rows of 128256 bf16 365 us with the gradient (0.85 of the HBM rate, with
-// 15% of the rows empty), 2048 x 32000 fp32 83 us (0.94), 2048 x 151936 bf16 227 us;
-// without it 2048 x 128256 bf16 83 us (0.93).  Holding rows on chip instead (clusters of up
-// to 8 CTAs, rows copied ahead to shared memory, a joining and a copying warp beside the
-// reducing ones), which reads the logits from L2 once, took 439, 97 and 367 us: a row's
-// chain of barriers and remote reads, with few warps a SM, cost more than the second read.
+// Measured with the gradient, 15% of the rows empty and so not read: 4096 rows of 128256
+// bf16 365 us (0.78 of the HBM rate) or 394 (0.72; which of the two goes with the block of
+// memory that the gradient is written to), 2048 x 32000 fp32 83 us (0.86), 2048 x 151936
+// bf16 227 us (0.75).  Without it, every row read: 2048 x 128256 bf16 83 us (0.93).
+// Holding rows on chip instead (clusters of up to 8 CTAs, rows copied ahead to shared
+// memory, a joining and a copying warp beside the reducing ones), which reads the logits
+// from L2 once, took 439, 97 and 367 us: a row's chain of barriers and remote reads, with
+// few warps a SM, cost more than the second read.
 #include <cuda_runtime.h>
 
 #include "rlq_elem.cuh"

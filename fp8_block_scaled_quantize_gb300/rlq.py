@@ -654,7 +654,8 @@ def add_rmsnorm_quant_act_1x128(res: torch.Tensor, delta: torch.Tensor | None, g
 def rmsnorm_backward(dx: torch.Tensor, h: torch.Tensor, rstd: torch.Tensor, gamma: torch.Tensor,
                      dres: torch.Tensor | None = None, inplace: bool = False, workspace=None, stream=None):
     """Gradient of the residual norm: dh = dres + d rmsnorm(h) * gamma / dh . dx (bf16) and
-    the norm weight's gradient (fp32 [K]).  ``inplace`` writes dh over dres.
+    the norm weight's gradient (fp32 [K]).  ``inplace`` writes dh over dres; without
+    ``dres`` dh is a new tensor either way.
 
     Returns (dh [M, K] bf16, dgamma [K] f32)."""
     if dx.dim() != 2:

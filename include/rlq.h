@@ -29,7 +29,9 @@
  *     or 2^-149 where the quotient rounds to zero (amax <= 448 x 2^-150, which only
  *     the calls that quantize products of theirs can meet);
  *     a code is the round-to-nearest-even, saturating E4M3 encoding of
- *     fl32(x / scale) with IEEE fp32 division.
+ *     fl32(x / scale) with IEEE fp32 division.  (The residual norm, the gated block and
+ *     its gradient, which quantize fp32 values of their own, encode x * RN(1 / scale)
+ *     instead, within 1.5 ulp of that quotient.)
  *   - Alignment: every code and bf16 base pointer 16-byte aligned and every
  *     code / bf16 row pitch a multiple of 16 bytes; fp32 scale pointers 4-byte
  *     aligned.  Violations return RLQ_ERR_MISALIGNED.
@@ -486,7 +488,10 @@ rlq_status rlq_gemm_fprop_splitk_static(const uint8_t *xq, int64_t ldxq, const f
  * is not rounded to bf16 before it is quantized, and the sum of squares is taken
  * in parallel (fp32, in an order fixed by K and by whether M exceeds the number
  * of SMs), so codes may differ in the last place from that call's.  A code is the
- * encoding of x * RN(1 / s), within 1.5 ulp of the quotient x / s.
+ * encoding of x * RN(1 / s), within 1.5 ulp of the quotient x / s.  Which to take: this
+ * one where the norm feeds a quantized layer and nothing else, as between two sublayers;
+ * rlq_rmsnorm_quant_act_1x128 where the codes have to be those of a bf16 activation that
+ * is also used, or made elsewhere, as such.
  *
  *   res    bf16 [M, K], pitch ldr                        (input)
  *   delta  bf16 [M, K], pitch ldd, or NULL (no addition) (input)
