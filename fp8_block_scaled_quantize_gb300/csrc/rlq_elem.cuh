@@ -76,8 +76,8 @@ __device__ __forceinline__ float group_scale(float amax)
         const float r = 1.0f / 448.0f, q = __fmul_rn(amax, r);
         return __fmaf_rn(__fmaf_rn(-q, 448.0f, amax), r, q);
     }
-    const float q = __fdiv_rn(amax, 448.0f);
-    return amax == 0.0f ? 1.0f : q == 0.0f ? 0x1p-149f : q;
+    // (the larger of the quotient's bits and 1: 2^-149 for 0)
+    return amax == 0.0f ? 1.0f : __uint_as_float(max(__float_as_uint(__fdiv_rn(amax, 448.0f)), 1u));
 }
 
 // A scale as the encoding applies it: codes are of (x * pre) * rcp, with pre = 1, or
