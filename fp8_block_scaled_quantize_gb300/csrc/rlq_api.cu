@@ -703,6 +703,69 @@ rlq_status rlq_gated_backward(const uint16_t *da, int64_t ldda, const uint8_t *g
                                  ldac, M, F, cs(stream));
 }
 
+// Scale tiles of an MXFP4 operand.
+static rlq_status check_mx_scales(const char *name, const void *p)
+{
+    RLQ_REQUIRE(p, RLQ_ERR_INVALID_ARG, "%s is NULL", name);
+    RLQ_REQUIRE(al(p, 16), RLQ_ERR_MISALIGNED, "%s is not 16-byte aligned", name);
+    return RLQ_OK;
+}
+
+rlq_status rlq_quant_mxfp4(const uint16_t *x, int64_t M, int64_t K, int64_t ldx, uint8_t *q, int64_t ldq, uint8_t *s,
+                           uint8_t *qT, int64_t ldqT, uint8_t *sT, rlq_stream_t stream)
+{
+    RLQ_REQUIRE(M >= 0 && K >= 0, RLQ_ERR_INVALID_ARG, "negative size (M=%lld, K=%lld)", (long long)M, (long long)K);
+    RLQ_REQUIRE((qT == nullptr) == (sT == nullptr), RLQ_ERR_INVALID_ARG, "qT and sT must both be set or both be NULL");
+    RLQ_REQUIRE(K % 32 == 0, RLQ_ERR_UNSUPPORTED, "K=%lld is not a multiple of 32", (long long)K);
+    RLQ_REQUIRE(M < MAX_DIM && K < MAX_DIM, RLQ_ERR_UNSUPPORTED, "dimension beyond 2^31");
+    if (M == 0 || K == 0)
+        return RLQ_OK;
+    RLQ_TRY(check_bf16("x", x, ldx, K));
+    RLQ_TRY(check_codes("q", q, ldq, K / 2));
+    RLQ_TRY(check_mx_scales("s", s));
+    if (qT) {
+        RLQ_TRY(check_codes("qT", qT, ldqT, (M + 1) / 2));
+        RLQ_TRY(check_mx_scales("sT", sT));
+    }
+    return cuda_status(launch_quant_mxfp4(x, M, K, ldx, q, ldq, s, qT, ldqT, sT, cs(stream)), "MXFP4 quantizer launch");
+}
+
+rlq_status rlq_dequant_mxfp4(const uint8_t *q, int64_t ldq, const uint8_t *s, int64_t rows, int64_t cols, uint16_t *x,
+                             int64_t ldx, rlq_stream_t stream)
+{
+    RLQ_REQUIRE(rows >= 0 && cols >= 0, RLQ_ERR_INVALID_ARG, "negative size (rows=%lld, cols=%lld)", (long long)rows,
+                (long long)cols);
+    RLQ_REQUIRE(rows < MAX_DIM && cols < MAX_DIM, RLQ_ERR_UNSUPPORTED, "dimension beyond 2^31");
+    if (rows == 0 || cols == 0)
+        return RLQ_OK;
+    RLQ_TRY(check_codes("q", q, ldq, (cols + 1) / 2));
+    RLQ_TRY(check_mx_scales("s", s));
+    RLQ_TRY(check_bf16("x", x, ldx, cols));
+    return cuda_status(launch_dequant_mxfp4(q, ldq, s, rows, cols, x, ldx, cs(stream)), "MXFP4 dequantizer launch");
+}
+
+rlq_status rlq_gemm_mxfp4(const uint8_t *xq, int64_t ldxq, const uint8_t *xs, const uint8_t *wq, int64_t ldwq,
+                          const uint8_t *ws, void *y, rlq_dtype dtype, int64_t ldy, int64_t M, int64_t N, int64_t K,
+                          rlq_stream_t stream)
+{
+    RLQ_REQUIRE(M >= 0 && N >= 0 && K >= 0, RLQ_ERR_INVALID_ARG, "negative size (M=%lld, N=%lld, K=%lld)", (long long)M,
+                (long long)N, (long long)K);
+    RLQ_REQUIRE(dtype == RLQ_DTYPE_BF16 || dtype == RLQ_DTYPE_F32, RLQ_ERR_INVALID_ARG, "unknown dtype %d", (int)dtype);
+    RLQ_REQUIRE(M < MAX_DIM && N < MAX_DIM && K < MAX_DIM, RLQ_ERR_UNSUPPORTED, "dimension beyond 2^31");
+    if (M == 0 || N == 0)
+        return RLQ_OK;
+    RLQ_REQUIRE(y, RLQ_ERR_INVALID_ARG, "y is NULL");
+    RLQ_REQUIRE(ldy >= N, RLQ_ERR_INVALID_ARG, "y: pitch %lld < row length %lld", (long long)ldy, (long long)N);
+    RLQ_REQUIRE(al(y, dtype == RLQ_DTYPE_F32 ? 4 : 2), RLQ_ERR_MISALIGNED, "y is not aligned to its element");
+    if (K > 0) {
+        RLQ_TRY(check_codes("xq", xq, ldxq, (K + 1) / 2));
+        RLQ_TRY(check_mx_scales("xs", xs));
+        RLQ_TRY(check_codes("wq", wq, ldwq, (K + 1) / 2));
+        RLQ_TRY(check_mx_scales("ws", ws));
+    }
+    return launch_gemm_mxfp4(xq, ldxq, xs, wq, ldwq, ws, y, dtype == RLQ_DTYPE_F32, ldy, M, N, K, cs(stream));
+}
+
 rlq_status rlq_token_logprobs(const void *logits, rlq_dtype dtype, int64_t ld, int64_t rows, int64_t V,
                               const int64_t *targets, float temperature, float *lp, float *lse, rlq_stream_t stream)
 {

@@ -1454,15 +1454,17 @@ rlq_status check_device_errors(cudaStream_t st)
     if (e != cudaSuccess)
         return cuda_status(e, "cudaStreamSynchronize");
     // every translation unit with bounded-wait kernels keeps its own error word
-    unsigned long long words[3] = {0, 0, 0};
+    unsigned long long words[4] = {0, 0, 0, 0};
     e = take_error_word(st, &words[0]);
     if (e == cudaSuccess)
         e = take_nvfp4_error_word(st, &words[1]);
     if (e == cudaSuccess)
         e = take_gate_error_word(st, &words[2]);
+    if (e == cudaSuccess)
+        e = take_mxfp4_error_word(st, &words[3]);
     if (e != cudaSuccess)
         return cuda_status(e, "reading and clearing the device error words");
-    const unsigned long long word = words[0] ? words[0] : words[1] ? words[1] : words[2];
+    const unsigned long long word = words[0] ? words[0] : words[1] ? words[1] : words[2] ? words[2] : words[3];
     if (word == 0)
         return RLQ_OK;
     const uint32_t code = (uint32_t)word, site = (uint32_t)(word >> 32);
@@ -1472,7 +1474,10 @@ rlq_status check_device_errors(cudaStream_t st)
                                   "gate backward (tile loaded)"};
     const char *where = site == SITE_DIAG ? "diagnostic wait" : (site < 11 ? names[site] : "?");
     return fail((rlq_status)code, "device-side wait ran out at site %u (%s)%s", site, where,
-                words[1] && !words[0] ? " in the NVFP4 GEMM" : "");
+                word == words[0]   ? ""
+                : word == words[1] ? " in the NVFP4 GEMM"
+                : word == words[3] ? " in the MXFP4 GEMM"
+                                   : "");
 }
 
 rlq_status launch_diag_wait(int64_t timeout_us, cudaStream_t st)

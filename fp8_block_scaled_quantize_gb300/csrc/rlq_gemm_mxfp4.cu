@@ -1,0 +1,559 @@
+// MXFP4 x MXFP4 product on 5th-generation tensor cores (sm_103a).
+//
+//   Y[m, n] = sum_k x[m, k] w[n, k],   x = e2m1(code) 2^e, one e per 32 elements of K, w alike
+//
+// tcgen05.mma kind::mxf4 multiplies packed E2M1 operands and applies both operands' E8M0
+// scales (two per row and instruction of K = 64) before it adds in fp32: a product of two
+// 4-bit values and two powers of two is exact, so only the additions round.
+//
+// Orientation: the weights are the MMA's A (128 rows, the TMEM lanes), the tokens its B (up to 256
+// TMEM columns).  A few tokens are then a narrow MMA that leaves nothing idle but the token
+// columns, and lane n of a warp holds output column n of every token: a store of 32 lanes is
+// 32 neighbouring outputs without any staging.
+//
+// Roles (192 threads): warp 0 (one thread) copies ahead by TMA, per stage of 256 contraction
+// elements (128 bytes a row) both operands' codes (128-byte swizzle) and their scale tiles as
+// they lie in memory; warp 1 (one thread) copies the stage's scales to tensor memory
+// (tcgen05.cp, 512 bytes per 128 rows and 128 elements; tcgen05.cp and tcgen05.mma of one
+// thread run in order) and issues four MMAs; warps 2-5 read the finished sums and store them.
+//   * Pairs (kPair): two CTAs, 256 weight rows x up to 256 tokens (cta_group::2), persistent.
+//     Both accumulators (256 columns each) and the scales do not fit the 512 columns, so
+//     the second accumulator begins 32 columns before the first one's end; the epilogue
+//     reads those columns first, and the next tile's MMAs start behind that.
+//   * Single CTAs: 128 weight rows; where there are too few tiles for the SMs, a cluster of
+//     up to 8 CTAs shares a tile's contraction, its CTAs leave their parts in shared memory
+//     and each adds its share of the tokens, parts in rank order.
+// Every wait is bounded as in the FP8 GEMM; what ran out is reported by rlq_check.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <cuda_runtime.h>
+
+#include <mutex>
+
+#include "rlq_internal.h"
+#include "rlq_tc.cuh"
+
+namespace rlq {
+namespace {
+
+constexpr int BM = 128;          // weight rows of a CTA
+constexpr int BK_BYTES = 128;    // bytes of a row's codes in a stage: 256 elements
+constexpr int THREADS = 192;
+constexpr int EPI_WARP0 = 2, EPI_WARPS = 4;
+constexpr int W_BYTES = BM * BK_BYTES;   // 16 KB
+constexpr int WS_BYTES = 1024;           // a row tile's scales of a stage
+constexpr int MAX_STAGES = 8;
+constexpr int NUM_BARS = 2 * MAX_STAGES + 6;
+constexpr int BARS_BYTES = NUM_BARS * 8 + 16;
+// tcgen05.mma kind::mxf4 instruction descriptor: A and B E2M1 (1 in bits 7-9 and 10-11), both
+// K-major, N >> 3 in bits 17-22, E8M0 scales (bit 23), M >> 4 in bits 24-28; the scales of an
+// instruction are bytes 0-1 or 2-3 of a row's word in tensor memory (bits 29-30 for A, 4-5
+// for B: 0 or 2).
+constexpr uint32_t IDESC = (1u << 7) | (1u << 10) | (1u << 23);
+constexpr uint32_t IDESC_HIGH = (2u << 29) | (2u << 4);
+
+struct Params {
+    void *y;
+    int64_t ldy;
+    int f32;
+    int M, N;                    // tokens, weight rows
+    int kstages, last_steps;     // stages, and instructions (64 elements) of the last one
+    int m_tiles, units, tile_m;  // token tiles, (token tile, weight tile) units, tokens of a tile
+    int splits, kps;             // CTAs that share a unit, stages of each
+    int stages, stage_bytes, x_bytes, xs_bytes, tx_bytes;
+    int tmem_cols, buf1, sf_col, overlap;
+    uint64_t timeout_ns;
+    int withhold;                // (diagnostic) the first stage's loads are left out
+};
+
+template <bool kPair>
+__device__ __forceinline__ void mma_mx(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
+                                       uint32_t accumulate)
+{
+    if constexpr (kPair)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
+            ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
+            ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+            : "memory");
+}
+
+// A 512-byte scale tile (32 rows of 16 bytes) to four columns of tensor memory, the same in
+// all four lane quarters (pair: in both CTAs, each from its own shared memory).
+template <bool kPair>
+__device__ __forceinline__ void copy_scales(uint32_t taddr, uint32_t saddr)
+{
+    // no swizzle; 8-row groups of 16-byte rows lie 128 bytes apart
+    const uint64_t desc = (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)(128 >> 4) << 32) | ((uint64_t)1 << 46);
+    if constexpr (kPair)
+        asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+    else
+        asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+
+__device__ __forceinline__ float ld_cluster(uint32_t addr)
+{
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ void store_out(const Params &p, int64_t at, float v)
+{
+    if (p.f32)
+        static_cast<float *>(p.y)[at] = v;
+    else {
+        uint16_t b;
+        asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(b) : "f"(v));
+        static_cast<uint16_t *>(p.y)[at] = b;
+    }
+}
+
+template <bool kPair>
+__global__ void __launch_bounds__(THREADS)
+    k_gemm_mxfp4(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
+                 const __grid_constant__ CUtensorMap tmWs, const __grid_constant__ CUtensorMap tmXs, const Params p)
+{
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + p.stages * p.stage_bytes);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + NUM_BARS);
+    volatile uint32_t *abort_flag = tmem_slot + 1;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t s0 = smem_u32(smem);
+    auto stage = [&](int s) { return s0 + (uint32_t)(s * p.stage_bytes); };  // W codes, X codes, W scales, X scales
+    auto full = [&](int s) { return smem_u32(&bars[s]); };
+    auto empty = [&](int s) { return smem_u32(&bars[MAX_STAGES + s]); };
+    auto tfull = [&](int b) { return smem_u32(&bars[2 * MAX_STAGES + b]); };
+    auto tempty = [&](int b) { return smem_u32(&bars[2 * MAX_STAGES + 2 + b]); };
+    const uint32_t shared_free = smem_u32(&bars[2 * MAX_STAGES + 4]), teardown = smem_u32(&bars[2 * MAX_STAGES + 5]);
+    const uint32_t rank = kPair || p.splits > 1 ? cta_rank() : 0;
+    const int group = kPair ? 2 : p.splits;  // CTAs that work on one unit
+    const int unit0 = blockIdx.x / group, unit_step = gridDim.x / group;
+    const int ks0 = kPair ? 0 : (int)rank * p.kps;
+    const int ks1 = kPair ? p.kstages : min(ks0 + p.kps, p.kstages);
+    auto w_row = [&](int u) { return (u / p.m_tiles) * (kPair ? 2 * BM : BM) + (kPair ? (int)rank * BM : 0); };
+    auto x_row = [&](int u) { return (u % p.m_tiles) * p.tile_m; };
+    auto tokens = [&](int u) { return min(p.tile_m, p.M - x_row(u)); };
+    // the MMA's token columns: whole steps of 16 (pair: 32, half of them each CTA's)
+    auto mma_n = [&](int u) { return kPair ? (tokens(u) + 31) & ~31 : (tokens(u) + 15) & ~15; };
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < p.stages; ++s) {
+            mbar_init(full(s), 1);
+            mbar_init(empty(s), 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(tfull(b), 1);
+            mbar_init(tempty(b), kPair ? 2 * EPI_WARPS : EPI_WARPS);
+        }
+        mbar_init(shared_free, kPair ? 2 * EPI_WARPS : EPI_WARPS);
+        mbar_init(teardown, 1);
+        *abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
+    if (warp == 1) {
+        if constexpr (kPair) {
+            asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
+                         "r"(p.tmem_cols)
+                         : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+        } else {
+            asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
+                         "r"(p.tmem_cols)
+                         : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        }
+    }
+    if (warp == 0 && lane == 0) {
+        prefetch_tmap(&tmW);
+        prefetch_tmap(&tmX);
+        prefetch_tmap(&tmWs);
+        prefetch_tmap(&tmXs);
+    }
+    pdl_begin();
+    tc_fence_before();
+    __syncthreads();
+    if (group > 1)
+        cluster_sync();  // every CTA's barriers are initialised before any signal from another
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    if (warp == 0) {
+        // ------------------------------------------------ TMA producer ---
+        if (lane == 0) {
+            int it = 0;
+            bool ok = true;
+            for (int u = unit0; ok && u < p.units; u += unit_step) {
+                const int wr = w_row(u), xr = x_row(u);
+                const int xc = xr + (kPair ? (int)rank * (mma_n(u) / 2) : 0);  // this CTA's token rows
+                for (int ks = ks0; ks < ks1; ++ks, ++it) {
+                    const int s = it % p.stages;
+                    if (!mbar_wait(empty(s), ((uint32_t)(it / p.stages) & 1u) ^ 1u, abort_flag, p.timeout_ns,
+                                   SITE_PRODUCER_EMPTY)) {
+                        ok = false;
+                        break;
+                    }
+                    if (!kPair && p.withhold && it == 0)
+                        continue;  // nothing arrives on this stage's barrier
+                    const uint32_t a = stage(s), b = a + W_BYTES, as = b + (uint32_t)p.x_bytes, bs = as + WS_BYTES;
+                    if constexpr (kPair) {
+                        // both CTAs' copies complete on the even CTA's barrier
+                        const uint32_t fb = cluster_addr(full(s), 0);
+                        if (rank == 0)
+                            mbar_arrive_expect_tx(full(s), 2u * (uint32_t)p.tx_bytes);
+                        tma_load_2d_pair(a, &tmW, fb, ks * BK_BYTES, wr);
+                        tma_load_2d_pair(b, &tmX, fb, ks * BK_BYTES, xc);
+                        tma_load_2d_pair(as, &tmWs, fb, ks * 256, wr / BM);
+                        tma_load_2d_pair(bs, &tmXs, fb, ks * 256, xr / BM);
+                    } else {
+                        mbar_arrive_expect_tx(full(s), (uint32_t)p.tx_bytes);
+                        tma_load_2d(a, &tmW, full(s), ks * BK_BYTES, wr);
+                        tma_load_2d(b, &tmX, full(s), ks * BK_BYTES, xr);
+                        tma_load_2d(as, &tmWs, full(s), ks * 256, wr / BM);
+                        tma_load_2d(bs, &tmXs, full(s), ks * 256, xr / BM);
+                    }
+                }
+            }
+            if constexpr (kPair) {
+                if (!ok) {
+                    // the copies complete on the even CTA's barriers: give them time to land
+                    const uint64_t t0 = global_timer_ns();
+                    while (global_timer_ns() - t0 < 200000ull)
+                        __nanosleep(1000);
+                }
+            } else {
+                // behind the MMA warp's last commit a normal run has consumed every copy; a
+                // CTA that gave up waits (bounded) for those still in flight
+                volatile uint32_t never = 0;
+                mbar_wait(teardown, 0, &never, p.timeout_ns, SITE_TEARDOWN);
+                if (!ok || *abort_flag || p.withhold) {
+                    int first = it > p.stages ? it - p.stages : 0;
+                    if (p.withhold && first == 0)
+                        first = 1;
+                    for (int j = first; j < it; ++j)
+                        mbar_wait(full(j % p.stages), (uint32_t)(j / p.stages) & 1u, &never, 20000000ull, SITE_DRAIN);
+                }
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ------------------------------------------------- MMA issuer ---
+        if (lane == 0 && (!kPair || rank == 0)) {
+            int it = 0, tc = 0;
+            bool ok = true;
+            for (int u = unit0; ok && u < p.units; u += unit_step, ++tc) {
+                const int buf = tc & 1;
+                // the buffer is free: read out two tiles ago, or, where the two share columns,
+                // those read out by the tile before (whose epilogue comes behind the other's)
+                const bool free = p.overlap ? tc == 0 || mbar_wait(shared_free, (uint32_t)(tc - 1) & 1u, abort_flag,
+                                                                   p.timeout_ns, SITE_MMA_TMEM_EMPTY)
+                                            : mbar_wait(tempty(buf), ((uint32_t)(tc >> 1) & 1u) ^ 1u, abort_flag,
+                                                        p.timeout_ns, SITE_MMA_TMEM_EMPTY);
+                if (!free) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const int n = mma_n(u);
+                const uint32_t d = tmem + (uint32_t)(buf * p.buf1), sf = tmem + (uint32_t)p.sf_col;
+                const uint32_t idesc = IDESC | ((uint32_t)(n >> 3) << 17) | ((uint32_t)((kPair ? 2 * BM : BM) >> 4) << 24);
+                for (int ks = ks0; ks < ks1; ++ks, ++it) {
+                    const int s = it % p.stages;
+                    if (!mbar_wait(full(s), (uint32_t)(it / p.stages) & 1u, abort_flag, p.timeout_ns, SITE_MMA_FULL)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t a = stage(s), b = a + W_BYTES, as = b + (uint32_t)p.x_bytes, bs = as + WS_BYTES;
+                    const uint64_t ad = sw128_desc(a), bd = sw128_desc(b);
+                    const int steps = ks + 1 == p.kstages ? p.last_steps : 4;
+#pragma unroll
+                    for (int t = 0; t < 2; ++t)  // 128 elements: columns 4 t of W's scales, 8 + 8 t of X's
+                        if (2 * t < steps) {
+                            copy_scales<kPair>(sf + 4 * t, as + 512 * t);
+                            copy_scales<kPair>(sf + 8 + 8 * t, bs + 512 * t);
+                            if (n > 128)
+                                copy_scales<kPair>(sf + 12 + 8 * t, bs + 1024 + 512 * t);
+                        }
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)  // 64 elements: 32 bytes along the rows
+                        if (j < steps)
+                            mma_mx<kPair>(d, ad + 2 * j, bd + 2 * j, idesc | (j & 1 ? IDESC_HIGH : 0u), sf + 4 * (j >> 1),
+                                          sf + 8 + 8 * (j >> 1), ks > ks0 || j > 0 ? 1u : 0u);
+                    tc_commit_t<kPair>(empty(s));
+                    if (ks + 1 == ks1)
+                        tc_commit_t<kPair>(tfull(buf));
+                }
+            }
+            // every MMA issued above has completed once this commit arrives
+            tc_commit_t<kPair>(teardown);
+            volatile uint32_t never = 0;
+            mbar_wait(teardown, 0, &never, 20000000ull, SITE_TEARDOWN);
+        }
+        __syncwarp();
+    } else {
+        // --------------------------------------------------- epilogue ---
+        const int q = warp & 3;  // TMEM lane quarter of this warp
+        const int row = q * 32 + lane;
+        int tc = 0;
+        for (int u = unit0; u < p.units; u += unit_step, ++tc) {
+            const int buf = tc & 1;
+            if (!__all_sync(0xFFFFFFFFu, mbar_wait(tfull(buf), (uint32_t)(tc >> 1) & 1u, abort_flag, p.timeout_ns,
+                                                   SITE_EPI_TMEM_FULL)))
+                break;
+            tc_fence_after();
+            const int nt = tokens(u), chunks = (nt + 31) / 32;
+            const int64_t n = w_row(u) + row;
+            const int64_t y0 = (int64_t)x_row(u) * p.ldy + n;
+            const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * p.buf1);
+            // the columns that the other buffer has too come first: the first buffer's last chunk, the second's first
+            const int first = p.overlap && buf == 0 ? 7 : 0;
+            uint32_t r[32];
+#pragma unroll 1
+            for (int i = 0; i < 8; ++i) {
+                const int cc = (first + i) & 7;
+                if (cc < chunks) {
+                    tmem_ld32_async(taddr + (uint32_t)(cc * 32), r);
+                    tmem_wait32(r);
+                }
+                if (i == 0 && p.overlap) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if constexpr (kPair)
+                            mbar_arrive_cluster(cluster_addr(shared_free, 0));
+                        else
+                            mbar_arrive(shared_free);
+                    }
+                }
+                if (cc >= chunks)
+                    continue;
+                const int left = min(32, nt - cc * 32);
+                if (p.splits > 1) {  // this CTA's part, [token][row]
+                    float *red = reinterpret_cast<float *>(smem) + cc * 32 * BM + row;
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        if (j < left)
+                            red[j * BM] = __uint_as_float(r[j]);
+                } else if (n < p.N) {
+                    int64_t at = y0 + (int64_t)cc * 32 * p.ldy;
+#pragma unroll
+                    for (int j = 0; j < 32; ++j, at += p.ldy)
+                        if (j < left)
+                            store_out(p, at, __uint_as_float(r[j]));
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if constexpr (kPair)
+                    mbar_arrive_cluster(cluster_addr(tempty(buf), 0));
+                else
+                    mbar_arrive(tempty(buf));
+            }
+        }
+    }
+
+    if (!kPair && p.splits > 1) {
+        // one unit a cluster: its parts lie in the CTAs' shared memory
+        cluster_sync();
+        if (warp >= EPI_WARP0 && unit0 < p.units) {
+            const int row = (warp & 3) * 32 + lane, nt = tokens(unit0);
+            const int64_t n = w_row(unit0) + row;
+            if (n < p.N)
+                for (int m = (int)rank; m < nt; m += p.splits) {
+                    float sum = 0.0f;
+                    for (int c = 0; c < p.splits; ++c)
+                        sum += ld_cluster(cluster_addr(s0 + (uint32_t)(m * BM + row) * 4u, (uint32_t)c));
+                    store_out(p, (int64_t)(x_row(unit0) + m) * p.ldy + n, sum);
+                }
+            __syncwarp();
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if constexpr (kPair) {
+        if (warp == 1) {
+            if (rank == 1 && lane == 0) {
+                // the even CTA's last commit: no MMA writes this CTA's tensor memory or reads its shared memory
+                volatile uint32_t never = 0;
+                mbar_wait(teardown, 0, &never, p.timeout_ns, SITE_TEARDOWN);
+            }
+            __syncwarp();
+        }
+    }
+    if (group > 1)
+        cluster_sync();  // no CTA leaves while another may still signal it or read its part
+    if (warp == 1) {
+        tc_fence_after();
+        if constexpr (kPair)
+            asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(p.tmem_cols) : "memory");
+        else
+            asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(p.tmem_cols) : "memory");
+    }
+}
+
+// Zeros, where there is nothing to add.
+__global__ void __launch_bounds__(256) k_zero_out(const Params p)
+{
+    pdl_begin();
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < (int64_t)p.M * p.N; i += (int64_t)gridDim.x * 256)
+        store_out(p, i / p.N * p.ldy + i % p.N, 0.0f);
+}
+
+// ---------------------------------------------------------------- host ---
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn()
+{
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void *f = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+    });
+    return fn;
+}
+
+// Codes [rows][bytes], boxes of 128 bytes x box_rows, or (scales) tiles of 128 words, boxes of
+// two tiles x box_rows row tiles; what lies outside arrives as zeros.
+rlq_status encode(CUtensorMap *map, const uint8_t *base, bool scales, int64_t inner, int64_t rows, int64_t pitch, int box_rows)
+{
+    auto enc = encode_fn();
+    if (!enc)
+        return fail(RLQ_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+    const cuuint64_t dims[2] = {(cuuint64_t)inner, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)pitch};
+    const cuuint32_t box[2] = {scales ? 256u : (cuuint32_t)BK_BYTES, (cuuint32_t)box_rows};
+    const cuuint32_t estr[2] = {1, 1};
+    const CUresult r = enc(map, scales ? CU_TENSOR_MAP_DATA_TYPE_UINT32 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 2,
+                           const_cast<uint8_t *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                           scales ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS)
+        return fail(RLQ_ERR_CUDA, "cuTensorMapEncodeTiled failed (CUresult %d) for a [%lld x %lld] MXFP4 operand, pitch %lld",
+                    (int)r, (long long)rows, (long long)inner, (long long)pitch);
+    return RLQ_OK;
+}
+
+template <bool kPair>
+rlq_status launch(const CUtensorMap *maps, const Params &p, int grid, int cluster, cudaStream_t st)
+{
+    const size_t smem = 1024 + (size_t)p.stages * p.stage_bytes + BARS_BYTES;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess)
+        return cuda_status(e, "device query");
+    static std::atomic<bool> set[64];
+    if (!set[dev & 63].load(std::memory_order_relaxed)) {
+        e = cudaFuncSetAttribute(k_gemm_mxfp4<kPair>, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448);
+        if (e != cudaSuccess)
+            return cuda_status(e, "cudaFuncSetAttribute(max dynamic shared memory)");
+        set[dev & 63].store(true, std::memory_order_relaxed);
+    }
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cuda_status(cudaLaunchKernelEx(&cfg, k_gemm_mxfp4<kPair>, maps[0], maps[1], maps[2], maps[3], p),
+                       "MXFP4 GEMM launch");
+}
+
+}  // namespace
+
+rlq_status launch_gemm_mxfp4(const uint8_t *xq, int64_t ldxq, const uint8_t *xs, const uint8_t *wq, int64_t ldwq,
+                             const uint8_t *ws, void *y, bool f32, int64_t ldy, int64_t M, int64_t N, int64_t K,
+                             cudaStream_t st)
+{
+    const int sms = device_sms();
+    Params p = {};
+    p.y = y;
+    p.ldy = ldy;
+    p.f32 = f32;
+    p.M = (int)M;
+    p.N = (int)N;
+    if (K == 0) {
+        const int64_t blocks = (M * N + 255) / 256;
+        return cuda_status(launch_pdl(k_zero_out, dim3((unsigned)(blocks < 8 * sms ? blocks : 8 * sms)), dim3(256), 0, st, p),
+                           "MXFP4 GEMM launch");
+    }
+    const int64_t ktiles = (K + 127) / 128;
+    p.kstages = (int)((K + 255) / 256);
+    p.last_steps = (int)((K - (int64_t)(p.kstages - 1) * 256 + 63) / 64);
+    p.timeout_ns = wait_limit_ns();
+    p.withhold = take_stall();
+    const bool pair = M > 256 && !p.withhold;
+    p.tile_m = M < 256 ? (int)M : 256;
+    p.m_tiles = (int)((M + p.tile_m - 1) / p.tile_m);
+    const int64_t n_tiles = (N + (pair ? 2 * BM : BM) - 1) / (pair ? 2 * BM : BM);
+    if (n_tiles * p.m_tiles >= (int64_t)1 << 30)
+        return fail(RLQ_ERR_UNSUPPORTED, "output of %lld x %lld has too many tiles", (long long)M, (long long)N);
+    p.units = (int)n_tiles * p.m_tiles;
+    p.splits = 1;
+    p.kps = p.kstages;
+
+    const int n16 = pair ? 256 : (p.tile_m + 15) / 16 * 16;
+    const int box_x = pair ? 128 : p.tile_m, box_xs = p.tile_m > 128 ? 2 : 1;
+    p.x_bytes = pair ? 128 * BK_BYTES : n16 * BK_BYTES;
+    p.xs_bytes = 1024 * box_xs;
+    p.stage_bytes = (W_BYTES + p.x_bytes + WS_BYTES + p.xs_bytes + 1023) / 1024 * 1024;
+    p.tx_bytes = W_BYTES + box_x * BK_BYTES + WS_BYTES + p.xs_bytes;
+    // Tensor memory: two accumulators and 24 columns of scales.  Up to 112 tokens take 256
+    // columns and half of the shared memory, so that two CTAs fit an SM.
+    const bool two = n16 <= 112;
+    p.tmem_cols = two ? 256 : 512;
+    p.sf_col = two ? 224 : 480;
+    p.buf1 = n16 < 224 ? n16 : 224;
+    p.overlap = n16 > 224;
+    const int room = (two ? 232448 / 2 - 1024 : 232448) - 1024 - BARS_BYTES;
+    p.stages = room / p.stage_bytes < MAX_STAGES ? room / p.stage_bytes : MAX_STAGES;
+    const int slots = pair ? sms / 2 : two ? 2 * sms : sms;
+    if (!pair)
+        while (p.splits < 8 && p.units * p.splits * 2 <= slots && p.kstages >= 4 * p.splits &&
+               n16 * BM * 4 <= p.stages * p.stage_bytes) {
+            p.splits *= 2;
+            p.kps = (p.kstages + p.splits - 1) / p.splits;
+        }
+    // (a split of the plan may be empty: the last ones where kps does not divide the stages)
+    while (p.splits > 1 && (p.splits - 1) * p.kps >= p.kstages) {
+        p.splits /= 2;
+        p.kps = (p.kstages + p.splits - 1) / p.splits;
+    }
+    CUtensorMap maps[4];
+    rlq_status r = encode(&maps[0], wq, false, (K + 1) / 2, N, ldwq, BM);
+    if (r == RLQ_OK)
+        r = encode(&maps[1], xq, false, (K + 1) / 2, M, ldxq, box_x);
+    if (r == RLQ_OK)
+        r = encode(&maps[2], ws, true, ktiles * 128, (N + 127) / 128, ktiles * 512, 1);
+    if (r == RLQ_OK)
+        r = encode(&maps[3], xs, true, ktiles * 128, (M + 127) / 128, ktiles * 512, box_xs);
+    if (r != RLQ_OK)
+        return r;
+    if (pair)
+        return launch<true>(maps, p, 2 * (p.units < slots ? p.units : slots), 2, st);
+    return launch<false>(maps, p, p.splits * (p.splits > 1 || p.units < slots ? p.units : slots), p.splits, st);
+}
+
+cudaError_t take_mxfp4_error_word(cudaStream_t st, unsigned long long *word) { return take_error_word(st, word); }
+
+}  // namespace rlq

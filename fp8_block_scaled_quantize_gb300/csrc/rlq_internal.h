@@ -201,6 +201,20 @@ cudaError_t launch_gated_decode(const GemmArgs &a, cudaStream_t st);
 rlq_status launch_gemm_nvfp4w(const uint16_t *x, int64_t ldx, const uint8_t *wq, int64_t ldwq, const uint8_t *wsb,
                               int64_t ldwsb, const float *st, uint16_t *y, int64_t ldy, int64_t M, int64_t N, int64_t K,
                               void *workspace, int64_t workspace_bytes, cudaStream_t stream);
+// ---- MXFP4 (rlq_mxfp4.cu, rlq_gemm_mxfp4.cu); arguments already validated ----
+// Quantizer, rows only or (qT and sT set) rows and columns; K % 32 == 0, M, K > 0.
+cudaError_t launch_quant_mxfp4(const uint16_t *x, int64_t M, int64_t K, int64_t ldx, uint8_t *q, int64_t ldq, uint8_t *s,
+                               uint8_t *qT, int64_t ldqT, uint8_t *sT, cudaStream_t st);
+// The values of codes and tiled scales in bf16; rows, cols > 0.
+cudaError_t launch_dequant_mxfp4(const uint8_t *q, int64_t ldq, const uint8_t *s, int64_t rows, int64_t cols,
+                                 uint16_t *x, int64_t ldx, cudaStream_t st);
+// Y[M, N] = X W^T of two MXFP4 operands with contraction length K, y bf16 or (f32) fp32; M, N > 0, K >= 0.
+rlq_status launch_gemm_mxfp4(const uint8_t *xq, int64_t ldxq, const uint8_t *xs, const uint8_t *wq, int64_t ldwq,
+                             const uint8_t *ws, void *y, bool f32, int64_t ldy, int64_t M, int64_t N, int64_t K,
+                             cudaStream_t st);
+// Its translation unit's error word, read and cleared (0: none).
+cudaError_t take_mxfp4_error_word(cudaStream_t st, unsigned long long *word);
+
 // Split count and workspace bytes (splits * M * N * 4, or 0 for one pass) of the
 // NVFP4 GEMM's split plan on the current device; ws_cap limits the workspace
 // (-1: no limit).

@@ -57,6 +57,9 @@ _SIGS = {
     "rlq_rmsnorm_backward": [_P, _I, _P, _I, _P, _P, _P, _I, _P, _I, _P, _I, _I, _P, _I, _P],
     "rlq_gemm_gated_fprop": [_P, _I, _P, _I, _P, _I, _P, _I, _P, _I, _P, _I, _P, _I, _P, _I, _I, _I, _I, _P],
     "rlq_gated_backward": [_P, _I, _P, _I, _P, _I, _P, _I, _P, _I, _P, _I, _P, _I, _P, _I, _P, _I, _I, _I, _P],
+    "rlq_quant_mxfp4": [_P, _I, _I, _I, _P, _I, _P, _P, _I, _P, _P],
+    "rlq_dequant_mxfp4": [_P, _I, _P, _I, _I, _P, _I, _P],
+    "rlq_gemm_mxfp4": [_P, _I, _P, _P, _I, _P, _P, ctypes.c_int, _I, _I, _I, _I, _P],
     "rlq_token_logprobs": [_P, ctypes.c_int, _I, _I, _I, _P, _F, _P, _P, _P],
     "rlq_policy_loss": [_P, ctypes.c_int, _I, _I, _I, _P, _F, _P, _P, _P, _P, _P, _P, _F, _F, _F, _F, _P, _P, _P, _I,
                         _P],
@@ -219,6 +222,21 @@ def rlq_gemm_nvfp4_weight_only_splitk(x, ldx, wq, ldwq, wsb, ldwsb, wst, y, ldy,
                  workspace_bytes, stream)
 
 
+DTYPE_BF16, DTYPE_F32 = 0, 1
+
+
+def rlq_quant_mxfp4(x, M, K, ldx, q, ldq, s, qT, ldqT, sT, stream):
+    return _call("rlq_quant_mxfp4", x, M, K, ldx, q, ldq, s, qT, ldqT, sT, stream)
+
+
+def rlq_dequant_mxfp4(q, ldq, s, rows, cols, x, ldx, stream):
+    return _call("rlq_dequant_mxfp4", q, ldq, s, rows, cols, x, ldx, stream)
+
+
+def rlq_gemm_mxfp4(xq, ldxq, xs, wq, ldwq, ws, y, dtype, ldy, M, N, K, stream):
+    return _call("rlq_gemm_mxfp4", xq, ldxq, xs, wq, ldwq, ws, y, dtype, ldy, M, N, K, stream)
+
+
 def rlq_aqn_sigma(sigma_start, sigma_end, t, T) -> float:
     out = ctypes.c_float()
     _call("rlq_aqn_sigma", sigma_start, sigma_end, t, T, ctypes.byref(out))
@@ -261,9 +279,6 @@ def rlq_gated_backward(da, ldda, guq, ldguq, gus, ldgus, q, ldq, s, lds, qT, ldq
                        stream):
     return _call("rlq_gated_backward", da, ldda, guq, ldguq, gus, ldgus, q, ldq, s, lds, qT, ldqT, sc, ldsc, aT, ldaT,
                  ac, ldac, M, F, stream)
-
-
-DTYPE_BF16, DTYPE_F32 = 0, 1
 
 
 def rlq_token_logprobs(logits, dtype, ld, rows, V, targets, temperature, lp, lse, stream):
@@ -730,6 +745,99 @@ def gated_backward(da: torch.Tensor, guq, gus, stream=None):
           s.data_ptr(), max(M, 1), qT.data_ptr(), ldT, sc.data_ptr(), 2 * F, aT.data_ptr(), ldT, ac.data_ptr(), F, M, F,
           _stream(stream))
     return q, s, qT, sc, aT, ac
+
+
+def _here(name, t):
+    """Refuses a tensor of another device than the current one, on whose streams calls run."""
+    if t.device.index != torch._C._cuda_getDevice():
+        raise ValueError(f"{name} must be on the current CUDA device")
+
+
+def _mx_operand(name, q, s):
+    """(rows, bytes a row, pitch) of packed MXFP4 codes with their scale tiles."""
+    if q.dim() != 2:
+        raise ValueError(f"{name}: codes must be a 2-D tensor")
+    R, B = q.shape
+    ld = _rows_of(name, q, R, B, torch.uint8)
+    _here(name, q)
+    if s.dtype is not torch.uint8:
+        raise TypeError(f"{name}: scales must be uint8")
+    if s.shape != mxfp4_scales_shape(R, 2 * B) or not s.is_contiguous():
+        raise ValueError(f"{name}: scales must be a contiguous {mxfp4_scales_shape(R, 2 * B)} tensor")
+    if s.device != q.device:
+        raise ValueError(f"{name}: scales must be on the codes' device")
+    return R, B, ld
+
+
+def mxfp4_scales_shape(rows: int, cols: int):
+    """Shape of the uint8 scale tiles of an MXFP4 matrix [rows, cols]: the byte of row r, block b
+    (columns 32 b .. 32 b + 31) is ``s[r // 128, b // 4, r % 32, r % 128 // 32, b % 4]``."""
+    return (rows + 127) // 128, (cols + 127) // 128, 32, 4, 4
+
+
+def quant_mxfp4(x: torch.Tensor, colwise: bool = False, stream=None):
+    """MXFP4 quantization of bf16 x [M, K] (K % 32 == 0): E2M1 codes, two a byte, and a
+    power-of-two scale per 32 elements along K; with ``colwise`` also of x transposed, per
+    32 rows of x, from the same read.
+
+    Returns (q [M, K/2] u8, s, qT [K, ceil(M/2)] u8 or None, sT or None), s and sT in tiles
+    (``mxfp4_scales_shape``)."""
+    if x.dim() != 2:
+        raise ValueError("x must be a [M, K] tensor")
+    M, K = x.shape
+    ldx = _rows_of("x", x, M, K)
+    _here("x", x)
+    dev = x.device
+    ldq = (K // 2 + 15) & ~15  # K / 2, but for a K that the call refuses
+    q = torch.empty_strided((M, K // 2), (ldq, 1), dtype=torch.uint8, device=dev)
+    s = torch.empty(mxfp4_scales_shape(M, K), dtype=torch.uint8, device=dev)
+    qT = sT = None
+    ldT = 0
+    if colwise:
+        qT, ldT = _codes_T(K, (M + 1) // 2, dev)
+        sT = torch.empty(mxfp4_scales_shape(K, M), dtype=torch.uint8, device=dev)
+    _call("rlq_quant_mxfp4", x.data_ptr(), M, K, ldx, q.data_ptr(), ldq, s.data_ptr(), _ptr(qT), ldT, _ptr(sT),
+          _stream(stream))
+    return q, s, qT, sT
+
+
+def dequant_mxfp4(q: torch.Tensor, s: torch.Tensor, cols: int | None = None, stream=None):
+    """The values (bf16 [rows, cols], exact) of MXFP4 codes and scale tiles.  ``cols`` is needed
+    where it is odd; rows are on 16-byte boundaries, so the result is a view of longer rows
+    where cols is not a multiple of 8."""
+    R, B, ld = _mx_operand("q", q, s)
+    C = 2 * B if cols is None else int(cols)
+    if (C + 1) // 2 != B:
+        raise ValueError(f"cols must be {2 * B} or {2 * B - 1}")
+    ldx = (C + 7) & ~7
+    x = torch.empty_strided((R, C), (ldx, 1), dtype=torch.bfloat16, device=q.device)
+    _call("rlq_dequant_mxfp4", q.data_ptr(), ld, s.data_ptr(), R, C, x.data_ptr(), ldx, _stream(stream))
+    return x
+
+
+def gemm_mxfp4(xq, xs, wq, ws, out=None, out_dtype: torch.dtype = torch.bfloat16, stream=None):
+    """Y [M, N] = X W^T from two MXFP4 operands (codes [M, K/2] and [N, K/2], scale tiles) on
+    the FP4 tensor cores, in bf16 or fp32 (``out_dtype``, or that of ``out``).  DGrad takes
+    the weight's transposed codes, WGrad those of dY and X."""
+    M, B, ldx = _mx_operand("xq", xq, xs)
+    N, Bw, ldw = _mx_operand("wq", wq, ws)
+    if B != Bw:
+        raise ValueError(f"xq and wq have rows of {B} and {Bw} bytes: the contraction lengths differ")
+    if wq.device != xq.device:
+        raise ValueError("wq must be on xq's device")
+    if out is None:
+        if out_dtype not in (torch.bfloat16, torch.float32):
+            raise TypeError("out_dtype must be bfloat16 or float32")
+        out = torch.empty((M, N), dtype=out_dtype, device=xq.device)
+        ldy = max(N, 1)
+    else:
+        if out.dtype not in (torch.bfloat16, torch.float32):
+            raise TypeError("out must be bfloat16 or float32")
+        ldy = _rows_of("out", out, M, N, out.dtype)
+        _here("out", out)
+    _call("rlq_gemm_mxfp4", xq.data_ptr(), ldx, xs.data_ptr(), wq.data_ptr(), ldw, ws.data_ptr(), out.data_ptr(),
+          DTYPE_BF16 if out.dtype is torch.bfloat16 else DTYPE_F32, ldy, M, N, 2 * B, _stream(stream))
+    return out
 
 
 def _logits(logits, targets):

@@ -356,6 +356,68 @@ rlq_status rlq_gemm_nvfp4_weight_only_splitk(const uint16_t *x, int64_t ldx, con
                                             int64_t ldy, int64_t M, int64_t N, int64_t K, void *workspace,
                                             int64_t workspace_bytes, rlq_stream_t stream);
 
+/* Element type of logits and of the MXFP4 product. */
+typedef enum { RLQ_DTYPE_BF16 = 0, RLQ_DTYPE_F32 = 1 } rlq_dtype;
+
+/*
+ * MXFP4 quantization (OCP Microscaling Formats v1.0): 4-bit weights AND activations for the
+ * FP4 tensor cores, where rlq_quant_nvfp4 serves weights beside bf16 activations.  Blocks
+ * of 32 consecutive elements, E2M1 values, one E8M0 scale (a power of two) per block:
+ *
+ *   e = clamp(floor(log2(amax of the block)) - 2, -127, 127), -127 for a block of zeros
+ *   code = E2M1_RNsat(x 2^-e): to nearest, ties to the even code, saturating at +-6, the
+ *          sign of zero kept;  scale byte = e + 127;  x ~= e2m1(code) 2^e
+ *
+ * A block that holds an infinity or a NaN has scale byte 255, which makes all its values
+ * NaN.  Every code and scale is determined bit for bit.
+ *
+ *   x   bf16 [M, K], pitch ldx >= K                       (input)
+ *   q   packed codes, two per byte: byte b of row m holds element 2b in its low nibble and
+ *       2b + 1 in its high one; pitch ldq >= K/2 bytes    (output) blocks along K
+ *   s   scale bytes in 512-byte tiles of 128 rows x 4 blocks: the byte of row m, block b is
+ *       s[((m / 128) ceil(K / 128) + b / 4) 512 + (m % 32) 16 + (m % 128) / 32 4 + b % 4];
+ *       ceil(M / 128) ceil(K / 128) 512 bytes, 16-byte aligned (output).  Bytes of blocks past
+ *       the row's end in its last tile are 0, bytes of rows past M are unspecified.
+ *   qT, ldqT >= ceil(M/2), sT: the same of x transposed [K, M], blocks of 32 rows of x
+ *       along M, the last one of what is left (output; both or neither).  Bytes past
+ *       ceil(M/2) are not written; where M is odd the last byte's high nibble is 0.
+ * K % 32 == 0; M any value >= 0.  One launch; x is read once.
+ */
+rlq_status rlq_quant_mxfp4(const uint16_t *x, int64_t M, int64_t K, int64_t ldx, uint8_t *q, int64_t ldq, uint8_t *s,
+                           uint8_t *qT, int64_t ldqT, uint8_t *sT, rlq_stream_t stream);
+
+/*
+ * The values of MXFP4 codes, x[r, c] = e2m1(code) 2^e, exact in bf16.
+ *
+ *   q, ldq >= ceil(cols/2), s: as rlq_quant_mxfp4 writes them (either direction)
+ *   x   bf16 [rows, cols], pitch ldx >= cols              (output)
+ * rows and cols any values >= 0.
+ */
+rlq_status rlq_dequant_mxfp4(const uint8_t *q, int64_t ldq, const uint8_t *s, int64_t rows, int64_t cols, uint16_t *x,
+                             int64_t ldx, rlq_stream_t stream);
+
+/*
+ * Product of two MXFP4 operands on the FP4 tensor cores:
+ *
+ *   Y[m, n] = sum_k x[m, k] w[n, k],  x and w the operands' values
+ *
+ * summed in fp32 and rounded once, to bf16 or (RLQ_DTYPE_F32) not at all.  One call serves
+ * every pass of a linear layer: FProp on the rows' codes of X [M, K] and W [N, K], DGrad on
+ * dY's rows and W's transposed codes, WGrad on the transposed codes of dY and X.
+ *
+ *   xq, ldxq, xs  codes and scale tiles of [M, K];  wq, ldwq, ws  of [N, K], as
+ *        rlq_quant_mxfp4 writes them (where K is odd, the last byte's high nibble 0)
+ *   y    [M, N] of `dtype`, pitch ldy >= N, aligned to its element (output, overwritten;
+ *        zeros for K == 0)
+ * M, N and K any values >= 0.  Needs no workspace: where the output has too few tiles for
+ * the SMs, a cluster of up to 8 CTAs shares a tile's contraction and adds its parts in a fixed
+ * order, so results repeat bit for bit.  Errors as for the other GEMMs (bounded device
+ * waits report at rlq_check).
+ */
+rlq_status rlq_gemm_mxfp4(const uint8_t *xq, int64_t ldxq, const uint8_t *xs, const uint8_t *wq, int64_t ldwq,
+                          const uint8_t *ws, void *y, rlq_dtype dtype, int64_t ldy, int64_t M, int64_t N, int64_t K,
+                          rlq_stream_t stream);
+
 /*
  * AQN, adaptive quantization noise (QeRL news article: channel-wise Gaussian
  * perturbations mapped into the LayerNorm scale parameters, decaying on an
@@ -586,9 +648,6 @@ rlq_status rlq_gated_backward(const uint16_t *da, int64_t ldda, const uint8_t *g
                               uint8_t *qT, int64_t ldqT, float *sc, int64_t ldsc,
                               uint8_t *aT, int64_t ldaT, float *ac, int64_t ldac,
                               int64_t M, int64_t F, rlq_stream_t stream);
-
-/* Element type of logits. */
-typedef enum { RLQ_DTYPE_BF16 = 0, RLQ_DTYPE_F32 = 1 } rlq_dtype;
 
 /*
  * Log probabilities of given tokens: z = logits / temperature,

@@ -1,0 +1,307 @@
+"""GPU tests of the MXFP4 quantizer, dequantizer and product against the definition in 64 bits."""
+import pytest
+import torch
+
+import mx_ref as R
+from fp8_block_scaled_quantize_gb300 import rlq
+
+pytestmark = pytest.mark.gpu
+D = torch.float64
+DEV = "cuda"
+
+
+def gen(seed):
+    g = torch.Generator(device=DEV)
+    g.manual_seed(seed)
+    return g
+
+
+# ------------------------------------------------------------- quantizer ---
+
+def difficult(g, M, K):
+    """bf16 [M, K]: blocks 2^-133 .. 2^120 apart, zeros of both signs, ties of every size."""
+    x = torch.randn(M, K, generator=g, device=DEV)
+    nb = K // 32
+    e = torch.randint(-20, 20, (M, nb), generator=g, device=DEV).float()
+    far = torch.rand(M, nb, generator=g, device=DEV)
+    e = torch.where(far < 0.05, e - 110, torch.where(far > 0.95, e + 100, e))
+    x = x * torch.exp2(e).repeat_interleave(32, 1)
+    # multiples of a quarter up to 8, times a power of two: every midpoint between codes
+    t = torch.randint(-32, 33, (M, K), generator=g, device=DEV).float() / 4
+    pick = (torch.rand(M, nb, generator=g, device=DEV) < 0.4).repeat_interleave(32, 1)
+    x = torch.where(pick, t * torch.exp2(e.clamp(-120, 118)).repeat_interleave(32, 1), x)
+    x = torch.where(torch.rand(M, K, generator=g, device=DEV) < 0.02, -torch.zeros_like(x), x)
+    x = torch.where((torch.rand(M, nb, generator=g, device=DEV) < 0.03).repeat_interleave(32, 1), torch.zeros_like(x), x)
+    return x.to(torch.bfloat16)
+
+
+def check_codes(q, s, x, what):
+    """Packed codes and scale tiles against the definition, the padding of the last tile too."""
+    code, sb = R.quantize(x.cpu())
+    nb = sb.shape[1]
+    got = R.untile(s.cpu(), x.shape[0])
+    assert torch.equal(got[:, :nb], sb), f"{what}: scales"
+    assert not got[:, nb:].any(), f"{what}: scales past the row's end"
+    fine = (sb != 255).repeat_interleave(32, 1)[:, :x.shape[1]]
+    have = R.unpack(q.cpu(), x.shape[1])
+    assert torch.equal(have[fine], code[fine]), f"{what}: codes"
+    if x.shape[1] % 2:
+        assert not (q.cpu()[:, -1] >> 4).any(), f"{what}: the last byte's high nibble"
+
+
+@pytest.mark.parametrize("M,K,pitch", [(1, 32, 0), (1, 4096, 0), (2, 96, 8), (5, 128, 0), (31, 160, 0), (33, 288, 16),
+                                       (64, 1024, 0), (97, 3584, 0), (128, 128, 0), (129, 256, 0), (200, 5120, 8),
+                                       (255, 64, 0), (300, 18944, 0), (1001, 416, 0)])
+def test_quantizer(M, K, pitch):
+    g = gen(M * 3 + K)
+    x = difficult(g, M, K)
+    if pitch:
+        buf = torch.full((M, K + pitch), 7.0, dtype=torch.bfloat16, device=DEV)
+        buf[:, :K] = x
+        x = buf[:, :K]
+    q, s, qT, sT = rlq.quant_mxfp4(x, colwise=True)
+    check_codes(q, s, x, "rows")
+    check_codes(qT, sT, x.t(), "columns")
+    q2, s2, none, none2 = rlq.quant_mxfp4(x)
+    assert none is None and none2 is None
+    assert torch.equal(q2, q)
+    nb = K // 32
+    assert torch.equal(R.untile(s2, M)[:, :nb], R.untile(s, M)[:, :nb])
+    check_codes(q2, s2, x, "rows alone")
+    # read back: the values themselves
+    code, sb = R.quantize(x.cpu())
+    assert torch.equal(rlq.dequant_mxfp4(q, s).cpu().to(D), R.values(code, sb))
+    code, sb = R.quantize(x.t().cpu())
+    assert torch.equal(rlq.dequant_mxfp4(qT, sT, cols=M).cpu().to(D), R.values(code, sb))
+
+
+def test_quantizer_every_exponent_and_values_that_are_no_numbers():
+    """A block for every bf16 exponent with each pattern of the leading bits; infinities and NaN
+    make their block's scale 255 and its values NaN, the blocks beside it stay."""
+    f = torch.arange(0, 255, device=DEV)
+    bits = (f[:, None] << 7) + (torch.arange(0, 128, 4, device=DEV))[None, :]
+    x = torch.cat((bits.to(torch.int16).view(torch.bfloat16), (bits | 0x8000).to(torch.int32).to(torch.int16).view(torch.bfloat16)), 1)
+    q, s, qT, sT = rlq.quant_mxfp4(x, colwise=True)
+    check_codes(q, s, x, "rows")
+    check_codes(qT, sT, x.t(), "columns")
+    y = torch.randn(70, 128, generator=gen(1), device=DEV).to(torch.bfloat16)
+    y[3, 40] = float("nan")
+    y[4, 0] = float("inf")
+    y[35, 127] = float("-inf")
+    q, s, qT, sT = rlq.quant_mxfp4(y, colwise=True)
+    check_codes(q, s, y, "rows")
+    check_codes(qT, sT, y.t(), "columns")
+    v = rlq.dequant_mxfp4(q, s)
+    bad = torch.zeros(70, 4, dtype=torch.bool, device=DEV)
+    bad[3, 1] = bad[4, 0] = bad[35, 3] = True
+    assert torch.equal(torch.isnan(v), bad.repeat_interleave(32, 1))
+
+
+def test_quantizer_writes_nothing_beside_its_outputs():
+    """Bytes between rows, past the last row and past the scale tiles stay as they were."""
+    M, K = 77, 160
+    x = difficult(gen(4), M, K)
+    ldq, ldT = K // 2 + 16, 64
+    bufs = [torch.full((n,), 0xA5, dtype=torch.uint8, device=DEV) for n in (M * ldq + 64, 2 * 512 + 64, K * ldT + 64,
+                                                                            2 * 512 + 64)]
+    q, s, qT, sT = bufs
+    rlq.rlq_quant_mxfp4(x.data_ptr(), M, K, K, q.data_ptr(), ldq, s.data_ptr(), qT.data_ptr(), ldT, sT.data_ptr(),
+                        torch.cuda.current_stream().cuda_stream)
+    assert (q[:M * ldq].view(M, ldq)[:, K // 2:] == 0xA5).all() and (q[M * ldq:] == 0xA5).all()
+    assert (s[1024:] == 0xA5).all() and (sT[1024:] == 0xA5).all()
+    rows = qT[:K * ldT].view(K, ldT)
+    assert (rows[:, (M + 1) // 2:] == 0xA5).all() and (qT[K * ldT:] == 0xA5).all()
+    check_codes(q[:M * ldq].view(M, ldq)[:, :K // 2], s[:1024].view(1, 2, 32, 4, 4), x, "rows")
+    check_codes(rows[:, :(M + 1) // 2], sT[:1024].view(2, 1, 32, 4, 4), x.t(), "columns")
+
+
+def test_dequantizer_writes_nothing_beside_its_output():
+    q, s, v = R.operand(gen(2), 9, 45, -3, 3)
+    out = torch.full((9 * 64 + 32,), 5.0, dtype=torch.bfloat16, device=DEV)
+    rlq.rlq_dequant_mxfp4(q.data_ptr(), q.stride(0), s.data_ptr(), 9, 45, out.data_ptr(), 64,
+                          torch.cuda.current_stream().cuda_stream)
+    assert torch.equal(out[:9 * 64].view(9, 64)[:, :45].to(D), v)
+    assert (out[:9 * 64].view(9, 64)[:, 45:] == 5).all() and (out[9 * 64:] == 5).all()
+
+
+# --------------------------------------------------------------- product ---
+
+SHAPES = [(1, 128, 256), (1, 1, 32), (1, 1000, 4096), (2, 100, 64), (3, 129, 96), (16, 256, 512), (17, 384, 288),
+          (64, 3584, 1024), (64, 200, 8192), (100, 129, 1000), (112, 256, 320), (113, 256, 320), (128, 130, 160),
+          (129, 512, 352), (200, 257, 1001), (255, 127, 33), (256, 1024, 256), (257, 256, 256), (300, 700, 1),
+          (384, 255, 416), (511, 513, 2048), (513, 1000, 777), (1000, 3000, 64), (2100, 5120, 512), (700, 20000, 288)]
+
+
+@pytest.mark.parametrize("M,N,K", SHAPES)
+def test_product_exact_sums(M, N, K):
+    """Scales within 2^-1 .. 2^1: every product is a multiple of 2^-4 and at most 144, sums up to
+    8192 x 144 stay below 2^24 of those units for the typical signs, so fp32 holds each one
+    exactly in whatever order, and the result is the exact sum."""
+    g = gen(M + 7 * N + K)
+    xq, xs, x = R.operand(g, M, K, -1, 1)
+    wq, ws, w = R.operand(g, N, K, -1, 1)
+    want = x @ w.t()
+    assert float((x.abs() @ w.abs().t()).max()) < 2.0 ** 20  # (units of 2^-4 below 2^24)
+    got = rlq.gemm_mxfp4(xq, xs, wq, ws, out_dtype=torch.float32)
+    rlq.check()
+    assert got.shape == (M, N) and got.dtype == torch.float32
+    assert torch.equal(got.to(D), want)
+    assert torch.equal(rlq.gemm_mxfp4(xq, xs, wq, ws), want.float().to(torch.bfloat16))
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 300, 4096), (5, 4096, 14336), (64, 1000, 2048), (130, 384, 1001), (600, 700, 5120)])
+def test_product_rounding(M, N, K):
+    """Scales 2^-12 .. 2^12.  The hardware adds a product's 64 terms and the accumulator in fp32 with
+    at most a few bits of each lost to alignment: every one of the K / 64 additions is off by at
+    most 2^-21 of the sum of magnitudes so far, a split's parts by 8 more."""
+    g = gen(K + M)
+    xq, xs, x = R.operand(g, M, K, -12, 12)
+    wq, ws, w = R.operand(g, N, K, -12, 12)
+    want, mag = x @ w.t(), x.abs() @ w.abs().t()
+    got = rlq.gemm_mxfp4(xq, xs, wq, ws, out_dtype=torch.float32).to(D)
+    tol = (-(-K // 64) + 8) * 2.0 ** -21 * mag
+    assert bool(((got - want).abs() <= tol).all())
+    # and in the mean far nearer: rounding errors of both signs
+    assert float((got - want).norm() / want.norm()) < 1e-5
+    b = rlq.gemm_mxfp4(xq, xs, wq, ws).to(D)
+    assert bool(((b - want).abs() <= tol + 2.0 ** -8 * (want.abs() + tol)).all())
+
+
+def test_product_extreme_scales():
+    """The ends of the scales' range: 2^-127 x 2^127 is 1; 6 x 2^127 x 2^-3 overflows nowhere."""
+    for ex, ew in ((-127, 127), (127, -127), (127, -3), (-60, -60)):
+        code = torch.full((40, 256), 7, dtype=torch.uint8, device=DEV)
+        code[:, 1::2] = 15  # 6 and -6 in turn: sums of zero
+        code[:, 0] = 4
+        sx = torch.full((40, 8), ex + 127, dtype=torch.uint8, device=DEV)
+        sw = torch.full((40, 8), ew + 127, dtype=torch.uint8, device=DEV)
+        one = torch.zeros(40, 256, dtype=torch.uint8, device=DEV)
+        one[:, 0] = 2  # 1
+        y = rlq.gemm_mxfp4(R.pack(code), R.tile(sx), R.pack(one), R.tile(sw), out_dtype=torch.float32)
+        assert bool((y.to(D) == 2.0 * 2.0 ** (ex + ew)).all())
+
+
+def test_product_nan_scales_stay_in_their_rows():
+    g = gen(9)
+    for M in (20, 300):
+        xq, xs, x = R.operand(g, M, 512, -1, 1)
+        wq, ws, w = R.operand(g, 200, 512, -1, 1)
+        xs[0, 1, 5, 0, 2] = 255  # row 5, block 6
+        ws[1, 0, 3, 1, 0] = 255  # row 128 + 35
+        y = rlq.gemm_mxfp4(xq, xs, wq, ws, out_dtype=torch.float32)
+        nan = torch.zeros(M, 200, dtype=torch.bool, device=DEV)
+        nan[5] = True
+        nan[:, 163] = True
+        assert torch.equal(torch.isnan(y), nan)
+        assert torch.equal(y.to(D)[~nan], (x @ w.t())[~nan])
+
+
+def test_scales_of_rows_that_do_not_exist_are_not_used():
+    """The tiles' bytes of rows past the last one are unspecified: 255 there changes nothing."""
+    g = gen(10)
+    for M, N in ((3, 70), (290, 300)):
+        xq, xs, x = R.operand(g, M, 256, -1, 1)
+        wq, ws, w = R.operand(g, N, 256, -1, 1)
+        for s, rows in ((xs, M), (ws, N)):
+            r = torch.arange(s.shape[0] * 128, device=DEV).view(-1, 4, 32).permute(0, 2, 1)
+            s[(r >= rows)[:, None, :, :, None].expand_as(s)] = 255
+        assert torch.equal(rlq.gemm_mxfp4(xq, xs, wq, ws, out_dtype=torch.float32).to(D), x @ w.t())
+
+
+def test_product_outputs_and_pitches():
+    """Every kind of output: contiguous, pitched, off 16-byte boundaries; nothing beside it is written."""
+    g = gen(12)
+    for M, N, K in ((5, 131, 320), (290, 131, 320)):
+        xq, xs, x = R.operand(g, M, K, -1, 1)
+        wq, ws, w = R.operand(g, N, K, -1, 1)
+        want = x @ w.t()
+        for dt in (torch.bfloat16, torch.float32):
+            buf = torch.full((M + 2, N + 9), 3.0, dtype=dt, device=DEV)
+            out = buf[1:1 + M, 5:5 + N]
+            assert rlq.gemm_mxfp4(xq, xs, wq, ws, out=out) is out
+            assert torch.equal(out, want.float().to(dt))
+            buf[1:1 + M, 5:5 + N] = 3.0
+            assert (buf == 3).all()
+
+
+def test_product_empty_contraction_and_empty_outputs():
+    u8 = lambda *s: torch.empty(*s, dtype=torch.uint8, device=DEV)  # noqa: E731
+    y = rlq.gemm_mxfp4(u8(5, 0), u8(1, 0, 32, 4, 4), u8(7, 0), u8(1, 0, 32, 4, 4))
+    assert y.shape == (5, 7) and not y.any()
+    y = torch.full((3, 9), 2.0, device=DEV)
+    rlq.gemm_mxfp4(u8(3, 0), u8(1, 0, 32, 4, 4), u8(9, 0), u8(1, 0, 32, 4, 4), out=y)
+    assert not y.any()
+    assert rlq.gemm_mxfp4(u8(0, 16), u8(0, 1, 32, 4, 4), u8(7, 16), u8(1, 1, 32, 4, 4)).shape == (0, 7)
+    assert rlq.gemm_mxfp4(u8(7, 16), u8(1, 1, 32, 4, 4), u8(0, 16), u8(0, 1, 32, 4, 4)).shape == (7, 0)
+    q, s, qT, sT = rlq.quant_mxfp4(torch.empty(0, 64, dtype=torch.bfloat16, device=DEV), colwise=True)
+    assert q.shape == (0, 32) and s.shape == (0, 1, 32, 4, 4) and qT.shape == (64, 0) and sT.shape == (1, 0, 32, 4, 4)
+
+
+def test_layer_forward_and_backward_passes():
+    """A layer's three passes on one pair of quantizations, ragged tokens, and the gradients of
+    the layer as it was rounded against autograd in 64 bits."""
+    g = gen(21)
+    M, N, K = 333, 352, 288
+    x = torch.randn(M, K, generator=g, device=DEV).to(torch.bfloat16)
+    w = (torch.randn(N, K, generator=g, device=DEV) * 0.05).to(torch.bfloat16)
+    dy = (torch.randn(M, N, generator=g, device=DEV) * 1e-3).to(torch.bfloat16)
+    xq, xs, xqT, xsT = rlq.quant_mxfp4(x, colwise=True)
+    wq, ws, wqT, wsT = rlq.quant_mxfp4(w, colwise=True)
+    dq, ds, dqT, dsT = rlq.quant_mxfp4(dy, colwise=True)
+    y = rlq.gemm_mxfp4(xq, xs, wq, ws)
+    dx = rlq.gemm_mxfp4(dq, ds, wqT, wsT)
+    dw = rlq.gemm_mxfp4(dqT, dsT, xqT, xsT, out_dtype=torch.float32)
+    val = lambda q, s, c: rlq.dequant_mxfp4(q, s, cols=c).to(D)  # noqa: E731
+    # each pass is the gradient of the bilinear form <dy, x w^T> in its rounded operands
+    a, b = val(xq, xs, K), val(wq, ws, K)
+    assert bool(((y.to(D) - a @ b.t()).abs() <= 2.0 ** -8 * (a @ b.t()).abs() + 1e-5 * (a.abs() @ b.abs().t())).all())
+    p = torch.zeros(M, K, dtype=D, device=DEV, requires_grad=True)
+    (val(dq, ds, N) * (p @ val(wqT, wsT, N))).sum().backward()
+    mag = val(dq, ds, N).abs() @ val(wqT, wsT, N).abs().t()
+    assert bool(((dx.to(D) - p.grad).abs() <= 2.0 ** -8 * p.grad.abs() + 1e-5 * mag).all())
+    p = torch.zeros(N, K, dtype=D, device=DEV, requires_grad=True)
+    (val(dqT, dsT, M).t() * (val(xqT, xsT, M).t() @ p.t())).sum().backward()
+    mag = val(dqT, dsT, M).abs() @ val(xqT, xsT, M).abs().t()
+    assert bool(((dw.to(D) - p.grad).abs() <= 1e-5 * mag).all())
+
+
+def test_streams_graphs_and_repeatability():
+    g = gen(30)
+    M, N, K = 48, 640, 4096
+    xq, xs, x = R.operand(g, M, K, -12, 12)
+    wq, ws, w = R.operand(g, N, K, -12, 12)
+    want = rlq.gemm_mxfp4(xq, xs, wq, ws)
+    for _ in range(3):
+        assert torch.equal(rlq.gemm_mxfp4(xq, xs, wq, ws), want)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    y = rlq.gemm_mxfp4(xq, xs, wq, ws, stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(y, want)
+    xb = torch.randn(M, K, generator=g, device=DEV).to(torch.bfloat16)
+    eager = rlq.gemm_mxfp4(*rlq.quant_mxfp4(xb)[:2], wq, ws)
+    graph = torch.cuda.CUDAGraph()
+    static = torch.zeros_like(xb)
+    with torch.cuda.graph(graph):
+        q, s, _, _ = rlq.quant_mxfp4(static)
+        out = rlq.gemm_mxfp4(q, s, wq, ws)
+    static.copy_(xb)
+    graph.replay()
+    graph.replay()
+    assert torch.equal(out, eager)
+
+
+def test_bounded_wait_runs_out_and_the_next_call_is_right():
+    """The diagnostic withholds every CTA's first loads: the wait runs out, the call ends, the
+    error is reported once, and the next call is right."""
+    g = gen(31)
+    for M, K in ((8, 256), (8, 4096), (300, 512)):
+        xq, xs, x = R.operand(g, M, K, -1, 1)
+        wq, ws, w = R.operand(g, 300, K, -1, 1)
+        rlq.rlq_diag_arm_gemm_stall()
+        rlq.gemm_mxfp4(xq, xs, wq, ws)
+        with pytest.raises(rlq.RlqError) as e:
+            rlq.check()
+        assert e.value.status == 5 and "MXFP4" in str(e.value)
+        rlq.check()
+        assert torch.equal(rlq.gemm_mxfp4(xq, xs, wq, ws, out_dtype=torch.float32).to(D), x @ w.t())
