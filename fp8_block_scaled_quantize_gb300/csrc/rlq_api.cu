@@ -781,6 +781,79 @@ rlq_status rlq_token_logprobs(const void *logits, rlq_dtype dtype, int64_t ld, i
     return cuda_status(launch_policy_rows(a, cs(stream)), "token log probability launch");
 }
 
+rlq_status rlq_token_logprobs_top(const void *logits, rlq_dtype dtype, int64_t ld, int64_t rows, int64_t V,
+                                  const int64_t *targets, float temperature, int64_t top, float *lp, float *lse,
+                                  float *entropy, int64_t *top_ids, float *top_lp, rlq_stream_t stream)
+{
+    PolicyLossArgs a{};
+    RLQ_TRY(check_logits(&a, logits, dtype, ld, rows, V, targets, temperature));
+    RLQ_REQUIRE(top >= 0 && top <= V, RLQ_ERR_INVALID_ARG, "top=%lld: not in 0 .. V", (long long)top);
+    RLQ_REQUIRE(top <= MAX_TOKEN_TOP, RLQ_ERR_UNSUPPORTED, "top=%lld is beyond %d", (long long)top, MAX_TOKEN_TOP);
+    if (rows == 0)
+        return RLQ_OK;
+    RLQ_TRY(check_scales("lp", lp, rows, rows));
+    RLQ_TRY(check_scales("lse", lse, rows, rows));
+    RLQ_TRY(check_scales("entropy", entropy, rows, rows));
+    if (top > 0) {
+        RLQ_REQUIRE(top_ids, RLQ_ERR_INVALID_ARG, "top_ids is NULL");
+        RLQ_REQUIRE(al(top_ids, 8), RLQ_ERR_MISALIGNED, "top_ids is not 8-byte aligned");
+        RLQ_TRY(check_scales("top_lp", top_lp, top, top));
+    }
+    TokenStatsArgs p{};
+    p.logits = logits;
+    p.dtype = dtype;
+    p.ld = ld;
+    p.rows = rows;
+    p.V = V;
+    p.targets = targets;
+    p.temperature = temperature;
+    p.top = (int)top;
+    p.lp = lp;
+    p.lse = lse;
+    p.entropy = entropy;
+    p.top_ids = top_ids;
+    p.top_lp = top_lp;
+    return cuda_status(launch_token_stats(p, cs(stream)), "token log probability launch");
+}
+
+rlq_status rlq_token_logprobs_backward(const void *logits, rlq_dtype dtype, int64_t ld, int64_t rows, int64_t V,
+                                       const int64_t *targets, float temperature, const float *lse,
+                                       const float *entropy, const float *dlp, const float *dentropy, void *dlogits,
+                                       int64_t ldd, rlq_stream_t stream)
+{
+    PolicyLossArgs a{};
+    RLQ_TRY(check_logits(&a, logits, dtype, ld, rows, V, targets, temperature));
+    if (rows == 0)
+        return RLQ_OK;
+    RLQ_REQUIRE(dlp || dentropy, RLQ_ERR_INVALID_ARG, "dlp and dentropy are both NULL");
+    RLQ_TRY(check_scales("lse", lse, rows, rows));
+    if (dlp)
+        RLQ_TRY(check_scales("dlp", dlp, rows, rows));
+    if (dentropy) {
+        RLQ_TRY(check_scales("dentropy", dentropy, rows, rows));
+        RLQ_TRY(check_scales("entropy", entropy, rows, rows));
+    }
+    RLQ_REQUIRE(dlogits, RLQ_ERR_INVALID_ARG, "dlogits is NULL");
+    RLQ_REQUIRE(ldd >= V, RLQ_ERR_INVALID_ARG, "dlogits: pitch %lld < row length %lld", (long long)ldd, (long long)V);
+    RLQ_REQUIRE(al(dlogits, dtype == RLQ_DTYPE_F32 ? 4 : 2), RLQ_ERR_MISALIGNED, "dlogits is not aligned to its element");
+    RLQ_REQUIRE(dlogits != logits || ldd == ld, RLQ_ERR_INVALID_ARG, "dlogits is logits in place, with another pitch");
+    TokenGradArgs p{};
+    p.logits = logits;
+    p.dtype = dtype;
+    p.ld = ld;
+    p.rows = rows;
+    p.V = V;
+    p.targets = targets;
+    p.temperature = temperature;
+    p.lse = lse;
+    p.entropy = entropy;
+    p.dlp = dlp;
+    p.dentropy = dentropy;
+    p.dlogits = dlogits;
+    p.ldd = ldd;
+    return cuda_status(launch_token_grad(p, cs(stream)), "token log probability gradient launch");
+}
+
 rlq_status rlq_policy_loss(const void *logits, rlq_dtype dtype, int64_t ld, int64_t rows, int64_t V,
                            const int64_t *targets, float temperature, const float *lp_old, const float *adv,
                            const float *weight, const float *lp_behav, const float *lp_ref, const float *clip_hi,

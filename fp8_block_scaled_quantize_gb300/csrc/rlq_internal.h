@@ -128,6 +128,34 @@ struct PolicyLossArgs {
 };
 cudaError_t launch_policy_rows(const PolicyLossArgs &p, cudaStream_t st);
 
+// ---- log probabilities with entropy and alternatives, and their gradient (rlq_logprobs.cu) ----
+struct TokenStatsArgs {
+    const void *logits;  // [rows][V], pitch ld elements
+    int dtype;           // RLQ_DTYPE_BF16 or RLQ_DTYPE_F32
+    int64_t ld, rows, V;
+    const int64_t *targets;
+    float temperature;
+    int top;  // alternatives, 0 .. MAX_TOKEN_TOP
+    float *lp, *lse, *entropy;  // [rows]
+    int64_t *top_ids;           // [rows][top]
+    float *top_lp;              // [rows][top]
+};
+constexpr int MAX_TOKEN_TOP = 64;
+cudaError_t launch_token_stats(const TokenStatsArgs &p, cudaStream_t st);
+
+struct TokenGradArgs {
+    const void *logits;
+    int dtype;  // of logits and dlogits
+    int64_t ld, rows, V;
+    const int64_t *targets;
+    float temperature;
+    const float *lse, *entropy, *dlp, *dentropy;  // [rows]; dlp or (entropy and) dentropy may be NULL
+    void *dlogits;
+    int64_t ldd;
+    float c_hi, c_lo;  // set by the launch: log2(e) / temperature as a sum of two floats
+};
+cudaError_t launch_token_grad(const TokenGradArgs &p, cudaStream_t st);
+
 // ---- device-side waits and tensor maps (rlq_gemm.cu) ----
 // Limit of a device-side wait (RLQ_WAIT_TIMEOUT_MS, default one second).
 uint64_t wait_limit_ns();

@@ -1,0 +1,568 @@
+// Token log probabilities with entropy and the most likely alternatives, and the gradient of any
+// loss of log probabilities and entropy with respect to the logits (sm_103a).
+//
+// Per row of logits x [V] with target t, z = x / temperature, m its maximum:
+//   S = sum_v exp(z_v - m),  lse = m + log S,  lp = z_t - lse
+//   H = -sum_v p_v log p_v = log S - sum_v exp(z_v - m) (z_v - m) / S
+//   the k largest logits, among equal ones the lowest token, and their log probabilities
+//   dx_v = ([v = t] dlp - p_v (dlp + dH (log p_v + H))) / temperature,  p_v = exp(z_v - lse)
+// Both terms of H are >= 0, so nothing cancels; a logit of -inf adds nothing to either sum.
+//
+// Forward, bound by memory (the logits are read once): a CTA (few rows: a cluster, a part each)
+// streams its row with running maximum, sum and weighted sum a thread.  The alternatives cost
+// the loop nothing: it keeps each thread's maximum anyway.  The k-th largest of those T is a
+// lower bound of the row's k-th logit, so every wanted logit is in one of the few threads whose
+// maximum reaches T; a warp reads each such thread's units again (from L2, two loads a lane at
+// 128256 bf16) and puts what reaches T on a list, whose ranks are counted.  A list that
+// overflows (thousands of equal logits) is replaced by a search for the k-th logit over the
+// whole row.
+//
+// Backward, bound by memory (read once, written once): lse and H come from the forward pass, so a
+// unit's gradient needs nothing but the unit and the row's factors.
+#include <cuda_runtime.h>
+
+#include "rlq_internal.h"
+#include "rlq_rows.cuh"
+
+namespace rlq {
+namespace {
+
+constexpr float LN2 = 0.6931471805599453f;
+constexpr float LOWEST = -16384.0f;  // 2^LOWEST is 0, and 0 x LOWEST too
+
+constexpr int THREADS = 256, CTAS_SM = 4, WARPS = THREADS / 32, MAX_CLUSTER = 8;
+constexpr int BATCH = 8;     // 16-byte loads in flight a thread
+constexpr int MAX_TOP = MAX_TOKEN_TOP;
+constexpr int LIST = 1024;   // candidates
+
+struct Sums {
+    float m, s, w;  // maximum, sum of 2^t and of t 2^t, t = (x - m) c
+};
+
+// The lanes' sums, joined in every lane.  Sums of -inf only are 0; one that met a NaN is NaN.
+__device__ __forceinline__ Sums join(Sums v, float c)
+{
+    float m = v.m;
+#pragma unroll
+    for (int o = 16; o; o >>= 1)
+        m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+    float s = 0.0f, w = 0.0f;
+    if (v.s != 0.0f) {
+        const float d = (v.m - m) * c, k = ex2(d);
+        s = v.s * k;
+        w = k == 0.0f ? 0.0f : fmaf(d, v.s, v.w) * k;
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+        w += __shfl_xor_sync(0xFFFFFFFFu, w, o);
+    }
+    return {m, s, w};
+}
+
+// Unsigned integers in the order of the floats, and back (what lies below -inf is -inf).
+__device__ __forceinline__ uint32_t key_of(float x)
+{
+    const uint32_t b = __float_as_uint(x);
+    return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float of_key(uint32_t k)
+{
+    return k <= 0x007FFFFFu ? -INFINITY : __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
+}
+
+// Whether logit a at token i comes before b at token j.
+__device__ __forceinline__ bool before(float a, int i, float b, int j) { return a > b || (a == b && i < j); }
+
+// What a CTA has of its row, and the row's units.
+template <typename T>
+struct Part {
+    const T *x;
+    int V, off, u0, u1, whole0, whole1;  // as in the loss's kernel: unit u is elements u N - off ..
+    __device__ __forceinline__ uint4 load(int u) const
+    {
+        constexpr uint32_t NINF = sizeof(T) == 2 ? 0xFF80FF80u : 0xFF800000u;
+        if (u >= u1)
+            return make_uint4(NINF, NINF, NINF, NINF);
+        return u >= whole0 && u < whole1 ? ld_row(x + ((int64_t)u * Elem<T>::N - off)) : load_cut(x, u * Elem<T>::N - off, V);
+    }
+    // f(value, token) for each of a unit's elements that exists
+    template <typename F>
+    __device__ __forceinline__ void each(int u, F f) const
+    {
+        if (u >= u1)
+            return;
+        const uint4 v = load(u);
+        const int e0 = u * Elem<T>::N - off;
+#pragma unroll
+        for (int j = 0; j < Elem<T>::N; j += 2) {
+            const float2 e = Elem<T>::get2(v, j / 2);
+            if (e0 + j >= 0 && e0 + j < V)
+                f(e.x, e0 + j);
+            if (e0 + j + 1 >= 0 && e0 + j + 1 < V)
+                f(e.y, e0 + j + 1);
+        }
+    }
+};
+
+struct Candidates {
+    float x[LIST];
+    int at[LIST];
+    int n;          // candidates, also those past the list's end
+    int scratch[WARPS + 1];
+    float thread_max[THREADS];
+};
+
+__device__ __forceinline__ void put(Candidates &c, float x, int at)
+{
+    const int i = atomicAdd(&c.n, 1);
+    if (i < LIST) {
+        c.x[i] = x;
+        c.at[i] = at;
+    }
+}
+
+// Sum over the CTA, in every thread.
+__device__ __forceinline__ int cta_sum(Candidates &c, int v)
+{
+    v = __reduce_add_sync(0xFFFFFFFFu, v);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0)
+        c.scratch[threadIdx.x >> 5] = v;
+    __syncthreads();
+    int s = 0;
+    for (int i = 0; i < (int)blockDim.x / 32; ++i)
+        s += c.scratch[i];
+    return s;
+}
+
+// The first `want` tokens, in order, whose logit equals `value`.
+template <typename T>
+__device__ __noinline__ void put_first_equal(const Part<T> &p, Candidates &c, float value, int want)
+{
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5, nw = blockDim.x / 32;
+    int have = 0;
+    for (int base = p.u0; base < p.u1 && have < want; base += blockDim.x) {
+        int mine = 0;
+        p.each(base + t, [&](float x, int) { mine += x == value; });
+        int before_me = mine;  // inclusive scan over the warp
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xFFFFFFFFu, before_me, o);
+            before_me += lane >= o ? y : 0;
+        }
+        __syncthreads();
+        if (lane == 31)
+            c.scratch[warp] = before_me;
+        __syncthreads();
+        int at = have + before_me - mine;
+        for (int i = 0; i < nw; ++i) {
+            at += i < warp ? c.scratch[i] : 0;
+            have += c.scratch[i];
+        }
+        p.each(base + t, [&](float x, int token) {
+            if (x == value && at++ < want)
+                put(c, x, token);
+        });
+    }
+}
+
+// The list overflowed: the k-th largest logit by bisection between `low`, which k logits
+// reach, and `high`, which none exceeds; then the logits above it and the first equal ones.
+template <typename T>
+__device__ __noinline__ void search(const Part<T> &p, Candidates &c, float low, float high, int k)
+{
+    uint32_t lo = key_of(low), hi = key_of(high);
+    while (lo < hi) {
+        const uint32_t mid = lo + (hi - lo + 1) / 2;
+        const float v = of_key(mid);
+        int mine = 0;
+        for (int u = p.u0 + threadIdx.x; u < p.u1; u += blockDim.x)
+            p.each(u, [&](float x, int) { mine += x >= v; });
+        if (cta_sum(c, mine) >= k)
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
+    const float v = of_key(lo);
+    __syncthreads();
+    if (threadIdx.x == 0)
+        c.n = 0;
+    __syncthreads();
+    for (int u = p.u0 + threadIdx.x; u < p.u1; u += blockDim.x)
+        p.each(u, [&](float x, int token) {
+            if (x > v)
+                put(c, x, token);
+        });
+    __syncthreads();
+    const int above = c.n;
+    __syncthreads();
+    put_first_equal(p, c, v, k - above);
+}
+
+// Puts the part's k largest logits on the list, and perhaps more: each thread's maximum m is known.
+template <typename T>
+__device__ __forceinline__ void find_top(const Part<T> &p, Candidates &c, float m, int k)
+{
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+    c.thread_max[t] = m;
+    if (t == 0)
+        c.n = 0;
+    __syncthreads();
+    // T: the upper 16 bits of the k-th largest thread maximum's key (of bf16 logits, all of it)
+    if (warp == 0) {
+        uint32_t key[WARPS];
+#pragma unroll
+        for (int i = 0; i < WARPS; ++i)
+            key[i] = 32 * i + lane < (int)blockDim.x ? key_of(c.thread_max[32 * i + lane]) : 0u;
+        uint32_t prefix = 0;
+#pragma unroll 1
+        for (uint32_t bit = 0x80000000u; bit >= 0x10000u; bit >>= 1) {
+            int n = 0;
+#pragma unroll
+            for (int i = 0; i < WARPS; ++i)
+                n += key[i] >= (prefix | bit);
+            if ((int)__reduce_add_sync(0xFFFFFFFFu, n) >= k)
+                prefix |= bit;
+        }
+        if (lane == 0)
+            c.scratch[WARPS] = (int)prefix;
+    }
+    __syncthreads();
+    const float T0 = of_key((uint32_t)c.scratch[WARPS]);
+    // the units of each thread that reaches T, by its warp
+    uint32_t who = __ballot_sync(0xFFFFFFFFu, m >= T0 && m > -INFINITY);
+    while (who) {
+        const int w = warp * 32 + __ffs(who) - 1;
+        who &= who - 1;
+        for (int u = p.u0 + w + lane * (int)blockDim.x; u < p.u1; u += 32 * blockDim.x)
+            p.each(u, [&](float x, int token) {
+                if (x >= T0 && x > -INFINITY)
+                    put(c, x, token);
+            });
+    }
+    __syncthreads();
+    const int n = c.n;
+    __syncthreads();
+    if (n > LIST) {
+        float high = -INFINITY;
+        for (int i = 0; i < (int)blockDim.x; ++i)
+            high = fmaxf(high, c.thread_max[i]);
+        search(p, c, T0, high, k);
+    } else if (n < k) {  // fewer than k logits above -inf
+        put_first_equal(p, c, -INFINITY, k - n);
+    }
+    __syncthreads();
+}
+
+// f(rank, logit, token) for the candidates of ranks below k.
+template <typename F>
+__device__ __forceinline__ void ranked(const float *x, const int *at, int n, int k, F f)
+{
+    for (int i = threadIdx.x; i < n; i += blockDim.x) {
+        int rank = 0;
+        for (int j = 0; j < n; ++j)
+            rank += before(x[j], at[j], x[i], at[i]);
+        if (rank < k)
+            f(rank, x[i], at[i]);
+    }
+}
+
+template <typename T, bool kTop>
+__global__ void __launch_bounds__(THREADS, CTAS_SM) k_token_stats(const TokenStatsArgs p, int csize, int units_cta)
+{
+    pdl_begin();
+    using E = Elem<T>;
+    constexpr int N = E::N;
+    __shared__ float4 part[WARPS], mine;
+    __shared__ float row_m, row_ls;
+    struct Lists {
+        float x[MAX_TOP];
+        int at[MAX_TOP];
+    };
+    __shared__ Candidates cand;
+    __shared__ Lists own;  // a cluster's CTA: the part's k largest, ranked
+    const int64_t row = blockIdx.x / csize;
+    const int rank = (int)(blockIdx.x - row * csize), V = (int)p.V;
+    const int t = threadIdx.x, threads = blockDim.x, lane = t & 31, warp = t >> 5, nw = threads >> 5;
+    const T *x = reinterpret_cast<const T *>(p.logits) + row * p.ld;
+    const int off = (int)((reinterpret_cast<uintptr_t>(x) & 15) / sizeof(T));
+    const int u0 = rank * units_cta;
+    const Part<T> part_of = {x, V, off, u0, min(u0 + units_cta, (off + V + N - 1) / N), off ? 1 : 0, (off + V) / N};
+    int64_t *ids = kTop ? p.top_ids + row * p.top : nullptr;
+    float *top_lp = kTop ? p.top_lp + row * p.top : nullptr;
+
+    const int64_t target = p.targets[row];
+    if (target < 0 || target >= V) {  // an empty row, to the whole cluster
+        if (rank == 0) {
+            if (t == 0)
+                p.lp[row] = p.lse[row] = p.entropy[row] = 0.0f;
+            if (kTop && t < p.top) {
+                ids[t] = -1;
+                top_lp[t] = 0.0f;
+            }
+        }
+        return;
+    }
+    float xt = 0.0f;
+    if (t == 0)
+        xt = E::load(x + target);
+    const float c = 1.4426950408889634f / p.temperature;
+    const float2 c2 = make_float2(c, c);
+    float m = -INFINITY;
+    float2 sum = make_float2(0.0f, 0.0f), wsum = make_float2(0.0f, 0.0f);
+    for (int u = u0 + t; u < part_of.u1; u += BATCH * threads) {
+        uint4 v[BATCH];
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i)
+            v[i] = part_of.load(u + i * threads);
+        float b = m;
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i)
+            b = E::max_of(b, v[i]);
+        if (b > m) {  // (m = -inf: the sums are 0, or NaN, so far)
+            const float d = m == -INFINITY ? 0.0f : fmaxf((m - b) * c, LOWEST), k = ex2(d);
+            wsum = __fmul2_rn(__ffma2_rn(sum, make_float2(d, d), wsum), make_float2(k, k));
+            sum = __fmul2_rn(sum, make_float2(k, k));
+            m = b;
+        }
+        // (a thread that has seen -inf only sums zeros against 0)
+        const float ref = m == -INFINITY ? 0.0f : m;
+        const float2 nref = make_float2(-ref, -ref);
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i)
+#pragma unroll
+            for (int j = 0; j < N / 2; ++j) {
+                const float2 f = __fmul2_rn(__fadd2_rn(E::get2(v[i], j), nref), c2);
+                const float2 e = make_float2(ex2(f.x), ex2(f.y));
+                sum = __fadd2_rn(sum, e);
+                wsum = __ffma2_rn(make_float2(fmaxf(f.x, LOWEST), fmaxf(f.y, LOWEST)), e, wsum);
+            }
+    }
+    Sums o = join({m, sum.x + sum.y, wsum.x + wsum.y}, c);
+    if (lane == 0)
+        part[warp] = make_float4(o.m, o.s, o.w, 0.0f);
+    const int n_part = max(0, min(V, part_of.u1 * N - off) - max(0, u0 * N - off));
+    const int k = kTop ? min(p.top, n_part) : 0;
+    if (kTop)
+        find_top(part_of, cand, m, k);
+    else
+        __syncthreads();
+    if (warp == 0) {
+        const float4 v = lane < nw ? part[lane] : make_float4(-INFINITY, 0.0f, 0.0f, 0.0f);
+        o = join({v.x, v.y, v.z}, c);
+        if (lane == 0)
+            mine = make_float4(o.m, o.s, o.w, 0.0f);
+        __syncwarp();
+    }
+    if (csize > 1) {
+        if (kTop) {
+            if (t < MAX_TOP)
+                own.at[t] = -1;
+            __syncthreads();
+            ranked(cand.x, cand.at, min(cand.n, LIST), k, [&](int r, float v, int at) {
+                own.x[r] = v;
+                own.at[r] = at;
+            });
+        }
+        cluster_arrive();
+        cluster_wait();
+        if (rank == 0) {
+            if (warp == 0) {
+                const float2 a = lane < csize ? ld_cluster2(reinterpret_cast<const float2 *>(&mine), lane)
+                                              : make_float2(-INFINITY, 0.0f);
+                const float2 b = lane < csize ? ld_cluster2(reinterpret_cast<const float2 *>(&mine) + 1, lane)
+                                              : make_float2(0.0f, 0.0f);
+                o = join({a.x, a.y, b.x}, c);
+                __syncwarp();
+            }
+            if (kTop) {  // the parts' lists, one behind the other
+                __syncthreads();
+                if (t == 0)
+                    cand.n = 0;
+                __syncthreads();
+                for (int i = t; i < csize * p.top; i += threads) {
+                    const int r = i / p.top, j = i - r * p.top;
+                    const float v = ld_cluster1(&own.x[j], r);
+                    const int at = __float_as_int(ld_cluster1(reinterpret_cast<const float *>(&own.at[j]), r));
+                    if (at >= 0)
+                        put(cand, v, at);
+                }
+            }
+        }
+        cluster_arrive_relaxed();  // this CTA has read the others' parts
+    }
+    if (rank == 0) {
+        if (t == 0) {
+            // (quotients: a logit that is the type's lowest value has a finite log probability)
+            const float l2 = log2f(o.s), ls = LN2 * l2;
+            const bool none = o.s == 0.0f;  // every logit is -inf
+            // (NaN targets make their sum NaN; +inf - +inf too)
+            p.lp[row] = none ? -INFINITY : (xt - o.m) / p.temperature - ls;
+            p.lse[row] = none ? -INFINITY : o.m / p.temperature + ls;
+            p.entropy[row] = none ? 0.0f : LN2 * (l2 - o.w / o.s);
+            if (kTop) {
+                row_m = o.m;
+                row_ls = none ? INFINITY : ls;
+            }
+        }
+        if (kTop) {
+            for (int i = t; i < p.top; i += threads) {  // (left so where NaN logits leave fewer)
+                ids[i] = -1;
+                top_lp[i] = NAN;
+            }
+            __syncthreads();
+            const float rm = row_m, ls = row_ls;
+            ranked(cand.x, cand.at, min(cand.n, LIST), p.top, [&](int r, float v, int at) {
+                ids[r] = at;
+                top_lp[r] = v == -INFINITY && ls == ls ? -INFINITY : (v - rm) / p.temperature - ls;
+            });
+        }
+    }
+    if (csize > 1)
+        cluster_wait();  // no CTA leaves while another may still read its part
+}
+
+template <typename T, bool kTop>
+cudaError_t launch_stats(const TokenStatsArgs &p, cudaStream_t st)
+{
+    constexpr int N = Elem<T>::N;
+    const int64_t units = (p.V + N - 1) / N + 1;  // one more where the rows start off a boundary
+    // a row to a cluster under the loss's rule
+    const int64_t slots = (int64_t)CTAS_SM * device_sms();
+    int csize = 1;
+    while (csize < MAX_CLUSTER && 3 * p.rows * csize <= slots && units >= (int64_t)csize * 4 * THREADS)
+        csize *= 2;
+    const int units_cta = (int)((units + csize - 1) / csize);
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = csize;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(p.rows * csize));
+    cfg.blockDim = dim3(units_cta >= THREADS ? THREADS : (units_cta + 31) / 32 * 32);
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = csize > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, k_token_stats<T, kTop>, p, csize, units_cta);
+}
+
+// ---------------------------------------------------------------- backward ---
+
+constexpr int BWD_BATCH = 4, BWD_ROUNDS = 2;  // loads in flight a thread, and batches of them
+
+// A CTA takes BWD_ROUNDS x BWD_BATCH units a thread of one row.  In units of log 2, log2 p =
+// x c - L with c = log2(e) / temperature, L = lse log2(e).  fp32 logits keep both as a sum of
+// two floats: one would put an error of 2^-24 |x c| into the exponent, some 10^-6 of a likely
+// token's probability, which bf16 gradients do not show.
+template <typename T>
+__global__ void __launch_bounds__(THREADS) k_token_grad(const TokenGradArgs p, int parts)
+{
+    pdl_begin();
+    using E = Elem<T>;
+    constexpr int N = E::N;
+    constexpr bool kFine = sizeof(T) == 4;
+    const int64_t row = blockIdx.x / parts;
+    const int partno = (int)(blockIdx.x - row * parts), V = (int)p.V, t = threadIdx.x, threads = blockDim.x;
+    const T *x = reinterpret_cast<const T *>(p.logits) + row * p.ld;
+    T *dx = reinterpret_cast<T *>(p.dlogits) + row * p.ldd;
+    const int off = (int)((reinterpret_cast<uintptr_t>(x) & 15) / sizeof(T));
+    const int span = BWD_BATCH * BWD_ROUNDS * threads;
+    const int u0 = partno * span, u1 = min(u0 + span, (off + V + N - 1) / N);
+    const int whole0 = off ? 1 : 0, whole1 = (off + V) / N;
+    // the gradient's rows share the logits' 16-byte phase: whole units leave as one store
+    const bool vec = ((reinterpret_cast<uintptr_t>(dx) ^ reinterpret_cast<uintptr_t>(x)) & 15) == 0;
+    auto store = [&](int u, uint4 v) {
+        if (vec && u >= whole0 && u < whole1)
+            __stcs(reinterpret_cast<uint4 *>(dx + ((int64_t)u * N - off)), v);
+        else
+            store_cut(dx, u * N - off, V, v);
+    };
+    const int64_t target = p.targets[row];
+    const float dlp = p.dlp ? p.dlp[row] : 0.0f, dH = p.dentropy ? p.dentropy[row] : 0.0f, lse = p.lse[row];
+    if (target < 0 || target >= V || (dlp == 0.0f && dH == 0.0f) || lse == -INFINITY) {  // an empty row
+        for (int u = u0 + t; u < u1; u += threads)
+            store(u, make_uint4(0, 0, 0, 0));
+        return;
+    }
+    const double L = (double)lse * 1.4426950408889634074;
+    const float L_hi = (float)L, L_lo = (float)(L - L_hi);
+    const float inv = 1.0f / p.temperature;
+    // (a row that met a NaN has lse NaN, which the maximum below would drop)
+    const float a = lse != lse ? lse : -(dlp + (dH == 0.0f ? 0.0f : dH * p.entropy[row])) * inv;
+    const float b = -dH * LN2 * inv, at_target = dlp * inv;
+    const float2 a2 = make_float2(a, a), b2 = make_float2(b, b), c2 = make_float2(p.c_hi, p.c_hi),
+                 cl2 = make_float2(p.c_lo, p.c_lo), nL2 = make_float2(-L_hi, -L_hi), nLl2 = make_float2(-L_lo, -L_lo);
+    const int te = (int)target + off, ut = te / N, jt = te - ut * N;
+#pragma unroll 1
+    for (int r = 0; r < BWD_ROUNDS; ++r) {
+        const int u = u0 + t + r * BWD_BATCH * threads;
+        uint4 v[BWD_BATCH];
+#pragma unroll
+        for (int i = 0; i < BWD_BATCH; ++i) {
+            const int w = u + i * threads;
+            if (w < u1)
+                v[i] = w >= whole0 && w < whole1 ? ld_row(x + ((int64_t)w * N - off)) : load_cut(x, w * N - off, V);
+        }
+#pragma unroll
+        for (int i = 0; i < BWD_BATCH; ++i) {
+            const int w = u + i * threads;
+            if (w >= u1)
+                break;
+            float2 f[N / 2];
+#pragma unroll
+            for (int j = 0; j < N / 2; ++j) {
+                const float2 e = E::get2(v[i], j);
+                float2 z = __ffma2_rn(e, c2, nL2);
+                if (kFine)
+                    z = __fadd2_rn(z, __ffma2_rn(e, cl2, nLl2));
+                // (logits of -inf: 2^LOWEST is 0)
+                z = make_float2(fmaxf(z.x, LOWEST), fmaxf(z.y, LOWEST));
+                f[j] = __fmul2_rn(make_float2(ex2(z.x), ex2(z.y)), __ffma2_rn(b2, z, a2));
+            }
+            if (w == ut) {
+#pragma unroll
+                for (int j = 0; j < N; ++j)
+                    if (j == jt) {
+                        if (j & 1)
+                            f[j / 2].y += at_target;
+                        else
+                            f[j / 2].x += at_target;
+                    }
+            }
+            store(w, E::pack(f));
+        }
+    }
+}
+
+template <typename T>
+cudaError_t launch_grad(const TokenGradArgs &p, cudaStream_t st)
+{
+    constexpr int N = Elem<T>::N;
+    const int64_t units = (p.V + N - 1) / N + 1, span = (int64_t)BWD_BATCH * BWD_ROUNDS * THREADS;
+    const int64_t parts = (units + span - 1) / span;
+    return launch_pdl(k_token_grad<T>, dim3((unsigned)(p.rows * parts)), dim3(THREADS), 0, st, p, (int)parts);
+}
+
+}  // namespace
+
+cudaError_t launch_token_stats(const TokenStatsArgs &p, cudaStream_t st)
+{
+    if (p.dtype == RLQ_DTYPE_F32)
+        return p.top ? launch_stats<uint32_t, true>(p, st) : launch_stats<uint32_t, false>(p, st);
+    return p.top ? launch_stats<uint16_t, true>(p, st) : launch_stats<uint16_t, false>(p, st);
+}
+
+cudaError_t launch_token_grad(const TokenGradArgs &args, cudaStream_t st)
+{
+    TokenGradArgs p = args;
+    const double c = 1.4426950408889634074 / (double)p.temperature;
+    p.c_hi = (float)c;
+    p.c_lo = (float)(c - (double)p.c_hi);
+    return p.dtype == RLQ_DTYPE_F32 ? launch_grad<uint32_t>(p, st) : launch_grad<uint16_t>(p, st);
+}
+
+}  // namespace rlq

@@ -61,6 +61,8 @@ _SIGS = {
     "rlq_dequant_mxfp4": [_P, _I, _P, _I, _I, _P, _I, _P],
     "rlq_gemm_mxfp4": [_P, _I, _P, _P, _I, _P, _P, ctypes.c_int, _I, _I, _I, _I, _P],
     "rlq_token_logprobs": [_P, ctypes.c_int, _I, _I, _I, _P, _F, _P, _P, _P],
+    "rlq_token_logprobs_top": [_P, ctypes.c_int, _I, _I, _I, _P, _F, _I, _P, _P, _P, _P, _P, _P],
+    "rlq_token_logprobs_backward": [_P, ctypes.c_int, _I, _I, _I, _P, _F, _P, _P, _P, _P, _P, _I, _P],
     "rlq_policy_loss": [_P, ctypes.c_int, _I, _I, _I, _P, _F, _P, _P, _P, _P, _P, _P, _F, _F, _F, _F, _P, _P, _P, _I,
                         _P],
     "rlq_check": [_P],
@@ -283,6 +285,18 @@ def rlq_gated_backward(da, ldda, guq, ldguq, gus, ldgus, q, ldq, s, lds, qT, ldq
 
 def rlq_token_logprobs(logits, dtype, ld, rows, V, targets, temperature, lp, lse, stream):
     return _call("rlq_token_logprobs", logits, dtype, ld, rows, V, targets, temperature, lp, lse, stream)
+
+
+def rlq_token_logprobs_top(logits, dtype, ld, rows, V, targets, temperature, top, lp, lse, entropy, top_ids, top_lp,
+                           stream):
+    return _call("rlq_token_logprobs_top", logits, dtype, ld, rows, V, targets, temperature, top, lp, lse, entropy,
+                 top_ids, top_lp, stream)
+
+
+def rlq_token_logprobs_backward(logits, dtype, ld, rows, V, targets, temperature, lse, entropy, dlp, dentropy, dlogits,
+                                ldd, stream):
+    return _call("rlq_token_logprobs_backward", logits, dtype, ld, rows, V, targets, temperature, lse, entropy, dlp,
+                 dentropy, dlogits, ldd, stream)
 
 
 def rlq_policy_loss(logits, dtype, ld, rows, V, targets, temperature, lp_old, adv, weight, lp_behav, lp_ref, clip_hi,
@@ -861,6 +875,43 @@ def token_logprobs(logits: torch.Tensor, targets: torch.Tensor, temperature: flo
     _call("rlq_token_logprobs", logits.data_ptr(), dt, ld, T, V, tg, temperature, lp.data_ptr(), lse.data_ptr(),
           _stream(stream))
     return lp, lse
+
+
+def token_logprobs_top(logits: torch.Tensor, targets: torch.Tensor, top: int = 0, temperature: float = 1.0, stream=None):
+    """Log probabilities of the int64 ``targets`` under bf16 or fp32 ``logits`` [rows, V]
+    divided by ``temperature``, each row's log-sum-exp and entropy, and the ``top`` (at most
+    64, or V) most likely tokens with their log probabilities, among equal logits the lowest
+    token first.
+
+    Returns (lp [rows] f32, lse [rows] f32, entropy [rows] f32, ids [rows, top] int64,
+    top_lp [rows, top] f32)."""
+    T, V, dt, ld, tg = _logits(logits, targets)
+    _here("logits", logits)
+    top = min(top, V)
+    dev = logits.device
+    lp, lse, H = (torch.empty((T,), dtype=torch.float32, device=dev) for _ in range(3))
+    ids = torch.empty((T, max(top, 0)), dtype=torch.int64, device=dev)
+    top_lp = torch.empty((T, max(top, 0)), dtype=torch.float32, device=dev)
+    _call("rlq_token_logprobs_top", logits.data_ptr(), dt, ld, T, V, tg, temperature, top, lp.data_ptr(), lse.data_ptr(),
+          H.data_ptr(), ids.data_ptr(), top_lp.data_ptr(), _stream(stream))
+    return lp, lse, H, ids, top_lp
+
+
+def token_logprobs_backward(logits: torch.Tensor, targets: torch.Tensor, lse: torch.Tensor, entropy=None, dlp=None,
+                            dentropy=None, temperature: float = 1.0, inplace: bool = False, stream=None):
+    """Gradient with respect to the logits of a loss whose derivatives by the targets' log
+    probabilities and by the entropies are ``dlp`` and ``dentropy`` (fp32 [rows], one of them
+    may be None), from the forward call's ``lse`` and, with ``dentropy``, ``entropy``.
+    ``inplace`` writes it over the logits.  Returns dlogits, like logits."""
+    T, V, dt, ld, tg = _logits(logits, targets)
+    _here("logits", logits)
+    opt = lambda name, t: None if t is None else _vector(name, t, T)  # noqa: E731
+    args = _vector("lse", lse, T), opt("entropy", entropy), opt("dlp", dlp), opt("dentropy", dentropy)
+    # (the logits' own pitch, so that their rows share 16-byte phases)
+    d = logits if inplace else torch.empty_strided((T, V), (ld, 1), dtype=logits.dtype, device=logits.device)
+    _call("rlq_token_logprobs_backward", logits.data_ptr(), dt, ld, T, V, tg, temperature, *args, d.data_ptr(), ld,
+          _stream(stream))
+    return d
 
 
 def policy_loss(logits: torch.Tensor, targets: torch.Tensor, logp_old: torch.Tensor, adv: torch.Tensor,

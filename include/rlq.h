@@ -670,6 +670,50 @@ rlq_status rlq_token_logprobs(const void *logits, rlq_dtype dtype, int64_t ld, i
                               rlq_stream_t stream);
 
 /*
+ * Log probabilities of given tokens with the distribution's entropy and its most likely
+ * tokens: what a rollout records of a step, and what an entropy bonus needs.
+ *
+ *   lse[r], lp[r] as above;  entropy[r] = -sum_v p_v log p_v, p_v = exp(z[r, v] - lse[r])
+ *   top_ids[r, j], top_lp[r, j]: the token of the j-th largest logit, among equal ones the
+ *   lowest token first, and its log probability z - lse
+ *
+ * in fp32, one read of the logits.
+ *
+ *   top      0 .. min(V, 64)
+ *   lp, lse, entropy  f32 [rows]                          (outputs)
+ *   top_ids  int64 [rows, top], top_lp f32 [rows, top], contiguous (outputs; NULL where top is 0)
+ * A target outside [0, V) makes the row empty: its logits are not read, lp, lse, entropy and
+ * top_lp are 0 and top_ids -1.  Logits of -inf have probability 0 and add nothing to the
+ * entropy; as alternatives they come last, with top_lp -inf.  A row of nothing else has lp =
+ * lse = -inf and entropy 0.  A NaN or +inf among the logits makes lp, lse and entropy NaN.
+ * Other arguments and limits as for rlq_token_logprobs.
+ */
+rlq_status rlq_token_logprobs_top(const void *logits, rlq_dtype dtype, int64_t ld, int64_t rows, int64_t V,
+                                  const int64_t *targets, float temperature, int64_t top, float *lp, float *lse,
+                                  float *entropy, int64_t *top_ids, float *top_lp, rlq_stream_t stream);
+
+/*
+ * Gradient with respect to the logits of any loss of lp and entropy:
+ *
+ *   dlogits[r, v] = ([v = target] dlp - p_v (dlp + dentropy (log p_v + entropy))) / temperature
+ *
+ * with dlp and dentropy the loss's derivatives by lp[r] and entropy[r].
+ *
+ *   lse, entropy  f32 [rows], as the forward call wrote them (entropy only with dentropy)
+ *   dlp, dentropy f32 [rows]; one of them may be NULL (zeros)
+ *   dlogits       [rows, V] of `dtype`, pitch ldd >= V (output); may be logits itself (in
+ *                 place, same pitch)
+ * A row whose target is outside [0, V), or whose derivatives are both 0, is empty: its logits
+ * are not read and its gradient is zeros.  So is that of a row of -inf logits only (lse =
+ * -inf).  A row whose lse is NaN has a gradient of NaN.  Other arguments and limits as for
+ * rlq_token_logprobs.  The logits are read once, the gradient written once.
+ */
+rlq_status rlq_token_logprobs_backward(const void *logits, rlq_dtype dtype, int64_t ld, int64_t rows, int64_t V,
+                                       const int64_t *targets, float temperature, const float *lse,
+                                       const float *entropy, const float *dlp, const float *dentropy, void *dlogits,
+                                       int64_t ldd, rlq_stream_t stream);
+
+/*
  * Clipped policy loss with a KL term, and its gradient with respect to the logits.
  * QuRL notes, 关键设计 (the decoupled objective: the clip ratio on full-precision
  * log probabilities, a truncated importance weight for the quantized rollout, an
