@@ -38,8 +38,11 @@ namespace {
 
 constexpr int BM = 128;          // weight rows of a CTA
 constexpr int BK_BYTES = 128;    // bytes of a row's codes in a stage: 256 elements
-constexpr int THREADS = 192;
-constexpr int EPI_WARP0 = 2, EPI_WARPS = 4;
+constexpr int EPI_WARP0 = 2;
+constexpr int EPI_GROUPS = 2;            // groups of four warps (a warp for each TMEM lane quarter)
+constexpr int EPI_WARPS = 4 * EPI_GROUPS;
+constexpr int THREADS = 32 * (EPI_WARP0 + EPI_WARPS);
+constexpr int GROUP_STAGING = 16384;     // a group's staging: two chunks of 32 tokens x 128 bf16 outputs, one of fp32
 constexpr int W_BYTES = BM * BK_BYTES;   // 16 KB
 constexpr int WS_BYTES = 1024;           // a row tile's scales of a stage
 constexpr int MAX_STAGES = 8;
@@ -55,7 +58,7 @@ constexpr uint32_t IDESC_HIGH = (2u << 29) | (2u << 4);
 struct Params {
     void *y;
     int64_t ldy;
-    int f32;
+    int tma_out;                 // (pairs) y's rows lie on 16-byte boundaries: stores by TMA
     int M, N;                    // tokens, weight rows
     int kstages, last_steps;     // stages, and instructions (64 elements) of the last one
     int m_tiles, units, tile_m;  // token tiles, (token tile, weight tile) units, tokens of a tile
@@ -84,6 +87,26 @@ __device__ __forceinline__ void mma_mx(uint32_t d, uint64_t a, uint64_t b, uint3
             : "memory");
 }
 
+// One lane of a warp whose lanes are together.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
+// mbar_wait by a whole warp, the same answer in every lane.  (The lanes stay together, so
+// what the loops around it compute stays in uniform registers, which tcgen05 and TMA
+// instructions take their operands from: issuing them from a thread of its own cost some
+// 70 cycles each.)
+__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, volatile uint32_t *abort_flag,
+                                               uint64_t limit_ns, uint32_t site)
+{
+    if (__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity)))
+        return true;
+    return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, abort_flag, limit_ns, site));
+}
+
 // A 512-byte scale tile (32 rows of 16 bytes) to four columns of tensor memory, the same in
 // all four lane quarters (pair: in both CTAs, each from its own shared memory).
 template <bool kPair>
@@ -104,9 +127,10 @@ __device__ __forceinline__ float ld_cluster(uint32_t addr)
     return v;
 }
 
+template <bool kF32>
 __device__ __forceinline__ void store_out(const Params &p, int64_t at, float v)
 {
-    if (p.f32)
+    if constexpr (kF32)
         static_cast<float *>(p.y)[at] = v;
     else {
         uint16_t b;
@@ -115,14 +139,49 @@ __device__ __forceinline__ void store_out(const Params &p, int64_t at, float v)
     }
 }
 
-template <bool kPair>
+__device__ __forceinline__ void sts32(uint32_t a, uint32_t v)
+{
+    asm volatile("st.shared.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
+}
+
+// A chunk of sums (lane: output column, register: token) to a TMA box's layout, 128 bytes of
+// outputs a token, 128-byte swizzle.  bf16: lanes 2 i and 2 i + 1 swap the halves of two
+// tokens four apart, so that each stores a pair of neighbouring outputs and the two tokens'
+// pieces fall into different banks.
+template <bool kF32>
+__device__ __forceinline__ void stage_chunk(uint32_t buf, int q, int lane, const uint32_t (&r)[32])
+{
+    if constexpr (kF32) {  // a box to a warp: 32 outputs
+        const uint32_t at = buf + (uint32_t)(q * 4096 + (lane & 3) * 4);
+#pragma unroll
+        for (int t = 0; t < 32; ++t)
+            sts32(at + (uint32_t)(t * 128 + (((lane >> 2) ^ (t & 7)) << 4)), r[t]);
+    } else {  // a box to two warps: 64 outputs
+        const bool odd = lane & 1;
+        const int off = (q & 1) * 64 + (lane & ~1) * 2;
+        const uint32_t at = buf + (uint32_t)((q >> 1) * 4096 + (odd ? 4 * 128 : 0) + (off & 15));
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const int t = (i & 3) + 8 * (i >> 2);  // and t + 4
+            const float a = __uint_as_float(r[t]), b = __uint_as_float(r[t + 4]);
+            const float got = __shfl_xor_sync(0xFFFFFFFFu, odd ? a : b, 1);
+            uint32_t w;
+            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(odd ? b : got), "f"(odd ? got : a));
+            sts32(at + (uint32_t)(t * 128 + (((off >> 4) ^ ((t & 7) + (odd ? 4 : 0))) << 4)), w);
+        }
+    }
+}
+
+template <bool kPair, bool kF32>
 __global__ void __launch_bounds__(THREADS)
     k_gemm_mxfp4(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
-                 const __grid_constant__ CUtensorMap tmWs, const __grid_constant__ CUtensorMap tmXs, const Params p)
+                 const __grid_constant__ CUtensorMap tmWs, const __grid_constant__ CUtensorMap tmXs,
+                 const __grid_constant__ CUtensorMap tmOut, const Params p)
 {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + p.stages * p.stage_bytes);
+    constexpr int STAGING = kPair ? EPI_GROUPS * GROUP_STAGING : 0;
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + p.stages * p.stage_bytes + STAGING);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + NUM_BARS);
     volatile uint32_t *abort_flag = tmem_slot + 1;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -153,7 +212,7 @@ __global__ void __launch_bounds__(THREADS)
             mbar_init(tfull(b), 1);
             mbar_init(tempty(b), kPair ? 2 * EPI_WARPS : EPI_WARPS);
         }
-        mbar_init(shared_free, kPair ? 2 * EPI_WARPS : EPI_WARPS);
+        mbar_init(shared_free, kPair ? 8 : 4);  // the group that reads the shared columns
         mbar_init(teardown, 1);
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -184,25 +243,23 @@ __global__ void __launch_bounds__(THREADS)
     if (group > 1)
         cluster_sync();  // every CTA's barriers are initialised before any signal from another
     tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
+    const uint32_t tmem = __reduce_or_sync(0xFFFFFFFFu, *tmem_slot);  // (in a uniform register)
 
     if (warp == 0) {
         // ------------------------------------------------ TMA producer ---
-        if (lane == 0) {
-            int it = 0;
-            bool ok = true;
-            for (int u = unit0; ok && u < p.units; u += unit_step) {
-                const int wr = w_row(u), xr = x_row(u);
-                const int xc = xr + (kPair ? (int)rank * (mma_n(u) / 2) : 0);  // this CTA's token rows
-                for (int ks = ks0; ks < ks1; ++ks, ++it) {
-                    const int s = it % p.stages;
-                    if (!mbar_wait(empty(s), ((uint32_t)(it / p.stages) & 1u) ^ 1u, abort_flag, p.timeout_ns,
-                                   SITE_PRODUCER_EMPTY)) {
-                        ok = false;
-                        break;
-                    }
-                    if (!kPair && p.withhold && it == 0)
-                        continue;  // nothing arrives on this stage's barrier
+        const bool one = elect_one();
+        int it = 0, s = 0;  // stages so far, and the next one's place in the ring
+        uint32_t phase = 1;
+        bool ok = true;
+        for (int u = unit0; ok && u < p.units; u += unit_step) {
+            const int wr = w_row(u), xr = x_row(u);
+            const int xc = xr + (kPair ? (int)rank * (mma_n(u) / 2) : 0);  // this CTA's token rows
+            for (int ks = ks0; ks < ks1; ++ks, ++it) {
+                if (!mbar_wait_warp(empty(s), phase, abort_flag, p.timeout_ns, SITE_PRODUCER_EMPTY)) {
+                    ok = false;
+                    break;
+                }
+                if (one && !(p.withhold && it == 0)) {  // (withheld: nothing arrives on this stage's barrier)
                     const uint32_t a = stage(s), b = a + W_BYTES, as = b + (uint32_t)p.x_bytes, bs = as + WS_BYTES;
                     if constexpr (kPair) {
                         // both CTAs' copies complete on the even CTA's barrier
@@ -221,7 +278,14 @@ __global__ void __launch_bounds__(THREADS)
                         tma_load_2d(bs, &tmXs, full(s), ks * 256, xr / BM);
                     }
                 }
+                __syncwarp();
+                if (++s == p.stages) {
+                    s = 0;
+                    phase ^= 1u;
+                }
             }
+        }
+        if (one) {
             if constexpr (kPair) {
                 if (!ok) {
                     // the copies complete on the even CTA's barriers: give them time to land
@@ -246,18 +310,19 @@ __global__ void __launch_bounds__(THREADS)
         __syncwarp();
     } else if (warp == 1) {
         // ------------------------------------------------- MMA issuer ---
-        if (lane == 0 && (!kPair || rank == 0)) {
-            int it = 0, tc = 0;
+        if (!kPair || rank == 0) {
+            const bool one = elect_one();
+            int tc = 0, s = 0;
+            uint32_t phase = 0;
             bool ok = true;
             for (int u = unit0; ok && u < p.units; u += unit_step, ++tc) {
                 const int buf = tc & 1;
-                // the buffer is free: read out two tiles ago, or, where the two share columns,
-                // those read out by the tile before (whose epilogue comes behind the other's)
-                const bool free = p.overlap ? tc == 0 || mbar_wait(shared_free, (uint32_t)(tc - 1) & 1u, abort_flag,
-                                                                   p.timeout_ns, SITE_MMA_TMEM_EMPTY)
-                                            : mbar_wait(tempty(buf), ((uint32_t)(tc >> 1) & 1u) ^ 1u, abort_flag,
-                                                        p.timeout_ns, SITE_MMA_TMEM_EMPTY);
-                if (!free) {
+                // the buffer is read out (two tiles ago), and so are the columns that it shares with
+                // the other one (the tile before)
+                if (!mbar_wait_warp(tempty(buf), ((uint32_t)(tc >> 1) & 1u) ^ 1u, abort_flag, p.timeout_ns,
+                                    SITE_MMA_TMEM_EMPTY) ||
+                    (p.overlap && tc > 0 && !mbar_wait_warp(shared_free, (uint32_t)(tc - 1) & 1u, abort_flag,
+                                                            p.timeout_ns, SITE_MMA_TMEM_EMPTY))) {
                     ok = false;
                     break;
                 }
@@ -265,66 +330,88 @@ __global__ void __launch_bounds__(THREADS)
                 const int n = mma_n(u);
                 const uint32_t d = tmem + (uint32_t)(buf * p.buf1), sf = tmem + (uint32_t)p.sf_col;
                 const uint32_t idesc = IDESC | ((uint32_t)(n >> 3) << 17) | ((uint32_t)((kPair ? 2 * BM : BM) >> 4) << 24);
-                for (int ks = ks0; ks < ks1; ++ks, ++it) {
-                    const int s = it % p.stages;
-                    if (!mbar_wait(full(s), (uint32_t)(it / p.stages) & 1u, abort_flag, p.timeout_ns, SITE_MMA_FULL)) {
+                for (int ks = ks0; ks < ks1; ++ks) {
+                    if (!mbar_wait_warp(full(s), phase, abort_flag, p.timeout_ns, SITE_MMA_FULL)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t a = stage(s), b = a + W_BYTES, as = b + (uint32_t)p.x_bytes, bs = as + WS_BYTES;
-                    const uint64_t ad = sw128_desc(a), bd = sw128_desc(b);
-                    const int steps = ks + 1 == p.kstages ? p.last_steps : 4;
+                    if (one) {
+                        const uint32_t a = stage(s), b = a + W_BYTES, as = b + (uint32_t)p.x_bytes, bs = as + WS_BYTES;
+                        const uint64_t ad = sw128_desc(a), bd = sw128_desc(b);
+                        const int steps = ks + 1 == p.kstages ? p.last_steps : 4;
 #pragma unroll
-                    for (int t = 0; t < 2; ++t)  // 128 elements: columns 4 t of W's scales, 8 + 8 t of X's
-                        if (2 * t < steps) {
-                            copy_scales<kPair>(sf + 4 * t, as + 512 * t);
-                            copy_scales<kPair>(sf + 8 + 8 * t, bs + 512 * t);
-                            if (n > 128)
-                                copy_scales<kPair>(sf + 12 + 8 * t, bs + 1024 + 512 * t);
-                        }
+                        for (int t = 0; t < 2; ++t)  // 128 elements: columns 4 t of W's scales, 8 + 8 t of X's
+                            if (2 * t < steps) {
+                                copy_scales<kPair>(sf + 4 * t, as + 512 * t);
+                                copy_scales<kPair>(sf + 8 + 8 * t, bs + 512 * t);
+                                if (n > 128)
+                                    copy_scales<kPair>(sf + 12 + 8 * t, bs + 1024 + 512 * t);
+                            }
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)  // 64 elements: 32 bytes along the rows
-                        if (j < steps)
-                            mma_mx<kPair>(d, ad + 2 * j, bd + 2 * j, idesc | (j & 1 ? IDESC_HIGH : 0u), sf + 4 * (j >> 1),
-                                          sf + 8 + 8 * (j >> 1), ks > ks0 || j > 0 ? 1u : 0u);
-                    tc_commit_t<kPair>(empty(s));
-                    if (ks + 1 == ks1)
-                        tc_commit_t<kPair>(tfull(buf));
+                        for (int j = 0; j < 4; ++j)  // 64 elements: 32 bytes along the rows
+                            if (j < steps)
+                                mma_mx<kPair>(d, ad + 2 * j, bd + 2 * j, idesc | (j & 1 ? IDESC_HIGH : 0u),
+                                              sf + 4 * (j >> 1), sf + 8 + 8 * (j >> 1), ks > ks0 || j > 0 ? 1u : 0u);
+                        tc_commit_t<kPair>(empty(s));
+                        if (ks + 1 == ks1)
+                            tc_commit_t<kPair>(tfull(buf));
+                    }
+                    __syncwarp();
+                    if (++s == p.stages) {
+                        s = 0;
+                        phase ^= 1u;
+                    }
                 }
             }
             // every MMA issued above has completed once this commit arrives
-            tc_commit_t<kPair>(teardown);
-            volatile uint32_t never = 0;
-            mbar_wait(teardown, 0, &never, 20000000ull, SITE_TEARDOWN);
+            if (one) {
+                tc_commit_t<kPair>(teardown);
+                volatile uint32_t never = 0;
+                mbar_wait(teardown, 0, &never, 20000000ull, SITE_TEARDOWN);
+            }
         }
         __syncwarp();
     } else {
         // --------------------------------------------------- epilogue ---
+        // Chunks of 32 tokens, the groups in turn.
         const int q = warp & 3;  // TMEM lane quarter of this warp
-        const int row = q * 32 + lane;
-        int tc = 0;
+        const int g = (warp - EPI_WARP0) >> 2, row = q * 32 + lane;
+        const uint32_t staging = s0 + (uint32_t)(p.stages * p.stage_bytes + g * GROUP_STAGING);
+        const uint64_t policy = l2_policy(false);
+        const bool issuer = lane == 0 && (kF32 || ((warp - EPI_WARP0) & 3) == 0);
+        int tc = 0, stored = 0;
+        bool ok = true;
         for (int u = unit0; u < p.units; u += unit_step, ++tc) {
             const int buf = tc & 1;
-            if (!__all_sync(0xFFFFFFFFu, mbar_wait(tfull(buf), (uint32_t)(tc >> 1) & 1u, abort_flag, p.timeout_ns,
-                                                   SITE_EPI_TMEM_FULL)))
-                break;
-            tc_fence_after();
             const int nt = tokens(u), chunks = (nt + 31) / 32;
+            ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait(tfull(buf), (uint32_t)(tc >> 1) & 1u, abort_flag, p.timeout_ns,
+                                                         SITE_EPI_TMEM_FULL));
+            if (!ok) {
+                // a warp that gave up still meets the others of its group, which may not have
+                if (!kPair || kF32 || !p.tma_out)
+                    break;
+                for (int cc = g; cc < chunks; cc += EPI_GROUPS) {
+                    asm volatile("bar.sync %0, 128;" ::"r"(1 + g) : "memory");
+                    asm volatile("bar.sync %0, 128;" ::"r"(1 + g) : "memory");
+                }
+                continue;
+            }
+            tc_fence_after();
             const int64_t n = w_row(u) + row;
             const int64_t y0 = (int64_t)x_row(u) * p.ldy + n;
             const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * p.buf1);
             // the columns that the other buffer has too come first: the first buffer's last chunk, the second's first
-            const int first = p.overlap && buf == 0 ? 7 : 0;
+            const int first = buf == 0 ? 7 : 0;
             uint32_t r[32];
 #pragma unroll 1
-            for (int i = 0; i < 8; ++i) {
-                const int cc = (first + i) & 7;
+            for (int i = 0; i < 8 / EPI_GROUPS; ++i) {
+                const int cc = p.overlap && g == (first & 1) ? (first + 2 * i) & 7 : g + 2 * i;
                 if (cc < chunks) {
                     tmem_ld32_async(taddr + (uint32_t)(cc * 32), r);
                     tmem_wait32(r);
                 }
-                if (i == 0 && p.overlap) {
+                if (i == 0 && p.overlap && g == (first & 1)) {
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) {
@@ -336,6 +423,41 @@ __global__ void __launch_bounds__(THREADS)
                 }
                 if (cc >= chunks)
                     continue;
+                if (kPair && p.tma_out) {
+                    // (a staging buffer is free once the copy engine has read it)
+                    const uint32_t b = staging + (kF32 ? 0u : (uint32_t)((stored & 1) * 8192));
+                    ++stored;
+                    if (issuer) {
+                        if constexpr (kF32)
+                            asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                        else
+                            asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+                    }
+                    if constexpr (kF32)
+                        __syncwarp();
+                    else
+                        asm volatile("bar.sync %0, 128;" ::"r"(1 + g) : "memory");
+                    stage_chunk<kF32>(b, q, lane, r);
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    if constexpr (kF32)
+                        __syncwarp();
+                    else
+                        asm volatile("bar.sync %0, 128;" ::"r"(1 + g) : "memory");
+                    if (issuer) {
+                        const int x = w_row(u), y = x_row(u) + cc * 32;
+                        if constexpr (kF32) {
+                            if (x + q * 32 < p.N)
+                                tma_store_2d_hint(&tmOut, b + (uint32_t)(q * 4096), x + q * 32, y, policy);
+                        } else {
+                            if (x < p.N)
+                                tma_store_2d_hint(&tmOut, b, x, y, policy);
+                            if (x + 64 < p.N)
+                                tma_store_2d_hint(&tmOut, b + 4096, x + 64, y, policy);
+                        }
+                        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+                    }
+                    continue;
+                }
                 const int left = min(32, nt - cc * 32);
                 if (p.splits > 1) {  // this CTA's part, [token][row]
                     float *red = reinterpret_cast<float *>(smem) + cc * 32 * BM + row;
@@ -348,7 +470,7 @@ __global__ void __launch_bounds__(THREADS)
 #pragma unroll
                     for (int j = 0; j < 32; ++j, at += p.ldy)
                         if (j < left)
-                            store_out(p, at, __uint_as_float(r[j]));
+                            store_out<kF32>(p, at, __uint_as_float(r[j]));
                 }
             }
             tc_fence_before();
@@ -360,20 +482,23 @@ __global__ void __launch_bounds__(THREADS)
                     mbar_arrive(tempty(buf));
             }
         }
+        if (issuer)
+            asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");  // stores complete before exit
+        __syncwarp();
     }
 
     if (!kPair && p.splits > 1) {
         // one unit a cluster: its parts lie in the CTAs' shared memory
         cluster_sync();
         if (warp >= EPI_WARP0 && unit0 < p.units) {
-            const int row = (warp & 3) * 32 + lane, nt = tokens(unit0);
+            const int row = (warp & 3) * 32 + lane, nt = tokens(unit0), g = (warp - EPI_WARP0) >> 2;
             const int64_t n = w_row(unit0) + row;
             if (n < p.N)
-                for (int m = (int)rank; m < nt; m += p.splits) {
+                for (int m = (int)rank + g * p.splits; m < nt; m += EPI_GROUPS * p.splits) {
                     float sum = 0.0f;
                     for (int c = 0; c < p.splits; ++c)
                         sum += ld_cluster(cluster_addr(s0 + (uint32_t)(m * BM + row) * 4u, (uint32_t)c));
-                    store_out(p, (int64_t)(x_row(unit0) + m) * p.ldy + n, sum);
+                    store_out<kF32>(p, (int64_t)(x_row(unit0) + m) * p.ldy + n, sum);
                 }
             __syncwarp();
         }
@@ -402,11 +527,12 @@ __global__ void __launch_bounds__(THREADS)
 }
 
 // Zeros, where there is nothing to add.
+template <bool kF32>
 __global__ void __launch_bounds__(256) k_zero_out(const Params p)
 {
     pdl_begin();
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < (int64_t)p.M * p.N; i += (int64_t)gridDim.x * 256)
-        store_out(p, i / p.N * p.ldy + i % p.N, 0.0f);
+        store_out<kF32>(p, i / p.N * p.ldy + i % p.N, 0.0f);
 }
 
 // ---------------------------------------------------------------- host ---
@@ -446,17 +572,36 @@ rlq_status encode(CUtensorMap *map, const uint8_t *base, bool scales, int64_t in
     return RLQ_OK;
 }
 
-template <bool kPair>
+// Output [rows][cols] of y, boxes of 128 bytes x 32 rows, 128-byte swizzle.
+rlq_status encode_out(CUtensorMap *map, void *y, bool f32, int64_t rows, int64_t cols, int64_t ld)
+{
+    auto enc = encode_fn();
+    if (!enc)
+        return fail(RLQ_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)ld * (f32 ? 4 : 2)};
+    const cuuint32_t box[2] = {f32 ? 32u : 64u, 32};
+    const cuuint32_t estr[2] = {1, 1};
+    const CUresult r = enc(map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, y, dims,
+                           strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                           CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS)
+        return fail(RLQ_ERR_CUDA, "cuTensorMapEncodeTiled failed (CUresult %d) for the [%lld x %lld] output", (int)r,
+                    (long long)rows, (long long)cols);
+    return RLQ_OK;
+}
+
+template <bool kPair, bool kF32>
 rlq_status launch(const CUtensorMap *maps, const Params &p, int grid, int cluster, cudaStream_t st)
 {
-    const size_t smem = 1024 + (size_t)p.stages * p.stage_bytes + BARS_BYTES;
+    const size_t smem = 1024 + (size_t)p.stages * p.stage_bytes + (kPair ? EPI_GROUPS * GROUP_STAGING : 0) + BARS_BYTES;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess)
         return cuda_status(e, "device query");
     static std::atomic<bool> set[64];
     if (!set[dev & 63].load(std::memory_order_relaxed)) {
-        e = cudaFuncSetAttribute(k_gemm_mxfp4<kPair>, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448);
+        e = cudaFuncSetAttribute(k_gemm_mxfp4<kPair, kF32>, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448);
         if (e != cudaSuccess)
             return cuda_status(e, "cudaFuncSetAttribute(max dynamic shared memory)");
         set[dev & 63].store(true, std::memory_order_relaxed);
@@ -475,7 +620,7 @@ rlq_status launch(const CUtensorMap *maps, const Params &p, int grid, int cluste
     cfg.stream = st;
     cfg.attrs = attr;
     cfg.numAttrs = cluster > 1 ? 2 : 1;
-    return cuda_status(cudaLaunchKernelEx(&cfg, k_gemm_mxfp4<kPair>, maps[0], maps[1], maps[2], maps[3], p),
+    return cuda_status(cudaLaunchKernelEx(&cfg, k_gemm_mxfp4<kPair, kF32>, maps[0], maps[1], maps[2], maps[3], maps[4], p),
                        "MXFP4 GEMM launch");
 }
 
@@ -489,12 +634,12 @@ rlq_status launch_gemm_mxfp4(const uint8_t *xq, int64_t ldxq, const uint8_t *xs,
     Params p = {};
     p.y = y;
     p.ldy = ldy;
-    p.f32 = f32;
     p.M = (int)M;
     p.N = (int)N;
     if (K == 0) {
         const int64_t blocks = (M * N + 255) / 256;
-        return cuda_status(launch_pdl(k_zero_out, dim3((unsigned)(blocks < 8 * sms ? blocks : 8 * sms)), dim3(256), 0, st, p),
+        return cuda_status(launch_pdl(f32 ? k_zero_out<true> : k_zero_out<false>,
+                                      dim3((unsigned)(blocks < 8 * sms ? blocks : 8 * sms)), dim3(256), 0, st, p),
                            "MXFP4 GEMM launch");
     }
     const int64_t ktiles = (K + 127) / 128;
@@ -525,7 +670,7 @@ rlq_status launch_gemm_mxfp4(const uint8_t *xq, int64_t ldxq, const uint8_t *xs,
     p.sf_col = two ? 224 : 480;
     p.buf1 = n16 < 224 ? n16 : 224;
     p.overlap = n16 > 224;
-    const int room = (two ? 232448 / 2 - 1024 : 232448) - 1024 - BARS_BYTES;
+    const int room = (two ? 232448 / 2 - 1024 : 232448) - 1024 - BARS_BYTES - (pair ? EPI_GROUPS * GROUP_STAGING : 0);
     p.stages = room / p.stage_bytes < MAX_STAGES ? room / p.stage_bytes : MAX_STAGES;
     const int slots = pair ? sms / 2 : two ? 2 * sms : sms;
     if (!pair)
@@ -539,7 +684,7 @@ rlq_status launch_gemm_mxfp4(const uint8_t *xq, int64_t ldxq, const uint8_t *xs,
         p.splits /= 2;
         p.kps = (p.kstages + p.splits - 1) / p.splits;
     }
-    CUtensorMap maps[4];
+    CUtensorMap maps[5] = {};
     rlq_status r = encode(&maps[0], wq, false, (K + 1) / 2, N, ldwq, BM);
     if (r == RLQ_OK)
         r = encode(&maps[1], xq, false, (K + 1) / 2, M, ldxq, box_x);
@@ -547,11 +692,16 @@ rlq_status launch_gemm_mxfp4(const uint8_t *xq, int64_t ldxq, const uint8_t *xs,
         r = encode(&maps[2], ws, true, ktiles * 128, (N + 127) / 128, ktiles * 512, 1);
     if (r == RLQ_OK)
         r = encode(&maps[3], xs, true, ktiles * 128, (M + 127) / 128, ktiles * 512, box_xs);
+    p.tma_out = pair && ((uintptr_t)y & 15) == 0 && ldy * (f32 ? 4 : 2) % 16 == 0;
+    if (r == RLQ_OK && p.tma_out)
+        r = encode_out(&maps[4], y, f32, M, N, ldy);
     if (r != RLQ_OK)
         return r;
+    const int work = p.units < slots ? p.units : slots;
     if (pair)
-        return launch<true>(maps, p, 2 * (p.units < slots ? p.units : slots), 2, st);
-    return launch<false>(maps, p, p.splits * (p.splits > 1 || p.units < slots ? p.units : slots), p.splits, st);
+        return f32 ? launch<true, true>(maps, p, 2 * work, 2, st) : launch<true, false>(maps, p, 2 * work, 2, st);
+    const int grid = p.splits > 1 ? p.splits * p.units : work;
+    return f32 ? launch<false, true>(maps, p, grid, p.splits, st) : launch<false, false>(maps, p, grid, p.splits, st);
 }
 
 cudaError_t take_mxfp4_error_word(cudaStream_t st, unsigned long long *word) { return take_error_word(st, word); }
