@@ -36,15 +36,15 @@
 namespace rlq {
 namespace {
 
-constexpr int BM = 128;          // weight rows of a CTA
+constexpr int BM = 128;          // rows of A of a CTA
 constexpr int BK_BYTES = 128;    // bytes of a row's codes in a stage: 256 elements
 constexpr int EPI_WARP0 = 2;
 constexpr int EPI_GROUPS = 2;            // groups of four warps (a warp for each TMEM lane quarter)
 constexpr int EPI_WARPS = 4 * EPI_GROUPS;
 constexpr int THREADS = 32 * (EPI_WARP0 + EPI_WARPS);
-constexpr int GROUP_STAGING = 16384;     // a group's staging: two chunks of 32 tokens x 128 bf16 outputs, one of fp32
-constexpr int W_BYTES = BM * BK_BYTES;   // 16 KB
-constexpr int WS_BYTES = 1024;           // a row tile's scales of a stage
+constexpr int STAGING_BYTES = EPI_WARPS * 4096;  // (pairs) 32 rows of 128 bytes a warp
+constexpr int A_BYTES = BM * BK_BYTES;   // 16 KB
+constexpr int AS_BYTES = 1024;           // a row tile's scales of a stage
 constexpr int MAX_STAGES = 8;
 constexpr int NUM_BARS = 2 * MAX_STAGES + 6;
 constexpr int BARS_BYTES = NUM_BARS * 8 + 16;
@@ -58,12 +58,12 @@ constexpr uint32_t IDESC_HIGH = (2u << 29) | (2u << 4);
 struct Params {
     void *y;
     int64_t ldy;
-    int tma_out;                 // (pairs) y's rows lie on 16-byte boundaries: stores by TMA
-    int M, N;                    // tokens, weight rows
+    int staged;                  // A is X, and y is stored by TMA; else A is W, and a lane stores its column of y
+    int a_rows, b_rows;
     int kstages, last_steps;     // stages, and instructions (64 elements) of the last one
-    int m_tiles, units, tile_m;  // token tiles, (token tile, weight tile) units, tokens of a tile
+    int b_tiles, units, tile_b;  // tiles of B, (A tile, B tile) units, rows of a B tile
     int splits, kps;             // CTAs that share a unit, stages of each
-    int stages, stage_bytes, x_bytes, xs_bytes, tx_bytes;
+    int stages, stage_bytes, b_bytes, bs_bytes, tx_bytes;
     int tmem_cols, buf1, sf_col, overlap;
     uint64_t timeout_ns;
     int withhold;                // (diagnostic) the first stage's loads are left out
@@ -139,54 +139,46 @@ __device__ __forceinline__ void store_out(const Params &p, int64_t at, float v)
     }
 }
 
-__device__ __forceinline__ void sts32(uint32_t a, uint32_t v)
-{
-    asm volatile("st.shared.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
-}
-
-// A chunk of sums (lane: output column, register: token) to a TMA box's layout, 128 bytes of
-// outputs a token, 128-byte swizzle.  bf16: lanes 2 i and 2 i + 1 swap the halves of two
-// tokens four apart, so that each stores a pair of neighbouring outputs and the two tokens'
-// pieces fall into different banks.
+// A row's 128 bytes of outputs (32 fp32 or 64 bf16) to its place in a TMA box, 128-byte swizzle:
+// 16-byte pieces, which eight neighbouring lanes spread over all banks.
 template <bool kF32>
-__device__ __forceinline__ void stage_chunk(uint32_t buf, int q, int lane, const uint32_t (&r)[32])
+__device__ __forceinline__ void stage_row(uint32_t box, int lane, const uint32_t *lo, const uint32_t *hi)
 {
-    if constexpr (kF32) {  // a box to a warp: 32 outputs
-        const uint32_t at = buf + (uint32_t)(q * 4096 + (lane & 3) * 4);
 #pragma unroll
-        for (int t = 0; t < 32; ++t)
-            sts32(at + (uint32_t)(t * 128 + (((lane >> 2) ^ (t & 7)) << 4)), r[t]);
-    } else {  // a box to two warps: 64 outputs
-        const bool odd = lane & 1;
-        const int off = (q & 1) * 64 + (lane & ~1) * 2;
-        const uint32_t at = buf + (uint32_t)((q >> 1) * 4096 + (odd ? 4 * 128 : 0) + (off & 15));
+    for (int i = 0; i < 8; ++i) {
+        uint32_t w[4];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const int t = (i & 3) + 8 * (i >> 2);  // and t + 4
-            const float a = __uint_as_float(r[t]), b = __uint_as_float(r[t + 4]);
-            const float got = __shfl_xor_sync(0xFFFFFFFFu, odd ? a : b, 1);
-            uint32_t w;
-            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(odd ? b : got), "f"(odd ? got : a));
-            sts32(at + (uint32_t)(t * 128 + (((off >> 4) ^ ((t & 7) + (odd ? 4 : 0))) << 4)), w);
+        for (int j = 0; j < 4; ++j) {
+            if constexpr (kF32) {
+                w[j] = lo[4 * i + j];
+            } else {
+                const uint32_t *h = i < 4 ? lo + 8 * i : hi + 8 * (i - 4);
+                asm("cvt.rn.bf16x2.f32 %0, %1, %2;"
+                    : "=r"(w[j])
+                    : "f"(__uint_as_float(h[2 * j + 1])), "f"(__uint_as_float(h[2 * j])));
+            }
         }
+        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(box + (uint32_t)(lane * 128 + ((i ^ (lane & 7)) << 4))),
+                     "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
+                     : "memory");
     }
 }
 
 template <bool kPair, bool kF32>
 __global__ void __launch_bounds__(THREADS)
-    k_gemm_mxfp4(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
-                 const __grid_constant__ CUtensorMap tmWs, const __grid_constant__ CUtensorMap tmXs,
+    k_gemm_mxfp4(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                 const __grid_constant__ CUtensorMap tmAs, const __grid_constant__ CUtensorMap tmBs,
                  const __grid_constant__ CUtensorMap tmOut, const Params p)
 {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    constexpr int STAGING = kPair ? EPI_GROUPS * GROUP_STAGING : 0;
+    constexpr int STAGING = kPair ? STAGING_BYTES : 0;
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + p.stages * p.stage_bytes + STAGING);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + NUM_BARS);
     volatile uint32_t *abort_flag = tmem_slot + 1;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t s0 = smem_u32(smem);
-    auto stage = [&](int s) { return s0 + (uint32_t)(s * p.stage_bytes); };  // W codes, X codes, W scales, X scales
+    auto stage = [&](int s) { return s0 + (uint32_t)(s * p.stage_bytes); };  // A codes, B codes, A scales, B scales
     auto full = [&](int s) { return smem_u32(&bars[s]); };
     auto empty = [&](int s) { return smem_u32(&bars[MAX_STAGES + s]); };
     auto tfull = [&](int b) { return smem_u32(&bars[2 * MAX_STAGES + b]); };
@@ -197,11 +189,11 @@ __global__ void __launch_bounds__(THREADS)
     const int unit0 = blockIdx.x / group, unit_step = gridDim.x / group;
     const int ks0 = kPair ? 0 : (int)rank * p.kps;
     const int ks1 = kPair ? p.kstages : min(ks0 + p.kps, p.kstages);
-    auto w_row = [&](int u) { return (u / p.m_tiles) * (kPair ? 2 * BM : BM) + (kPair ? (int)rank * BM : 0); };
-    auto x_row = [&](int u) { return (u % p.m_tiles) * p.tile_m; };
-    auto tokens = [&](int u) { return min(p.tile_m, p.M - x_row(u)); };
-    // the MMA's token columns: whole steps of 16 (pair: 32, half of them each CTA's)
-    auto mma_n = [&](int u) { return kPair ? (tokens(u) + 31) & ~31 : (tokens(u) + 15) & ~15; };
+    auto a_row = [&](int u) { return (u / p.b_tiles) * (kPair ? 2 * BM : BM) + (kPair ? (int)rank * BM : 0); };
+    auto b_row = [&](int u) { return (u % p.b_tiles) * p.tile_b; };
+    auto columns = [&](int u) { return min(p.tile_b, p.b_rows - b_row(u)); };
+    // the MMA's columns: whole steps of 16 (pair: 32, half of them each CTA's)
+    auto mma_n = [&](int u) { return kPair ? (columns(u) + 31) & ~31 : (columns(u) + 15) & ~15; };
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < p.stages; ++s) {
@@ -232,10 +224,10 @@ __global__ void __launch_bounds__(THREADS)
         }
     }
     if (warp == 0 && lane == 0) {
-        prefetch_tmap(&tmW);
-        prefetch_tmap(&tmX);
-        prefetch_tmap(&tmWs);
-        prefetch_tmap(&tmXs);
+        prefetch_tmap(&tmA);
+        prefetch_tmap(&tmB);
+        prefetch_tmap(&tmAs);
+        prefetch_tmap(&tmBs);
     }
     pdl_begin();
     tc_fence_before();
@@ -252,30 +244,30 @@ __global__ void __launch_bounds__(THREADS)
         uint32_t phase = 1;
         bool ok = true;
         for (int u = unit0; ok && u < p.units; u += unit_step) {
-            const int wr = w_row(u), xr = x_row(u);
-            const int xc = xr + (kPair ? (int)rank * (mma_n(u) / 2) : 0);  // this CTA's token rows
+            const int ar = a_row(u), br = b_row(u);
+            const int bc = br + (kPair ? (int)rank * (mma_n(u) / 2) : 0);  // this CTA's part of B
             for (int ks = ks0; ks < ks1; ++ks, ++it) {
                 if (!mbar_wait_warp(empty(s), phase, abort_flag, p.timeout_ns, SITE_PRODUCER_EMPTY)) {
                     ok = false;
                     break;
                 }
                 if (one && !(p.withhold && it == 0)) {  // (withheld: nothing arrives on this stage's barrier)
-                    const uint32_t a = stage(s), b = a + W_BYTES, as = b + (uint32_t)p.x_bytes, bs = as + WS_BYTES;
+                    const uint32_t a = stage(s), b = a + A_BYTES, as = b + (uint32_t)p.b_bytes, bs = as + AS_BYTES;
                     if constexpr (kPair) {
                         // both CTAs' copies complete on the even CTA's barrier
                         const uint32_t fb = cluster_addr(full(s), 0);
                         if (rank == 0)
                             mbar_arrive_expect_tx(full(s), 2u * (uint32_t)p.tx_bytes);
-                        tma_load_2d_pair(a, &tmW, fb, ks * BK_BYTES, wr);
-                        tma_load_2d_pair(b, &tmX, fb, ks * BK_BYTES, xc);
-                        tma_load_2d_pair(as, &tmWs, fb, ks * 256, wr / BM);
-                        tma_load_2d_pair(bs, &tmXs, fb, ks * 256, xr / BM);
+                        tma_load_2d_pair(a, &tmA, fb, ks * BK_BYTES, ar);
+                        tma_load_2d_pair(b, &tmB, fb, ks * BK_BYTES, bc);
+                        tma_load_2d_pair(as, &tmAs, fb, ks * 256, ar / BM);
+                        tma_load_2d_pair(bs, &tmBs, fb, ks * 256, br / BM);
                     } else {
                         mbar_arrive_expect_tx(full(s), (uint32_t)p.tx_bytes);
-                        tma_load_2d(a, &tmW, full(s), ks * BK_BYTES, wr);
-                        tma_load_2d(b, &tmX, full(s), ks * BK_BYTES, xr);
-                        tma_load_2d(as, &tmWs, full(s), ks * 256, wr / BM);
-                        tma_load_2d(bs, &tmXs, full(s), ks * 256, xr / BM);
+                        tma_load_2d(a, &tmA, full(s), ks * BK_BYTES, ar);
+                        tma_load_2d(b, &tmB, full(s), ks * BK_BYTES, br);
+                        tma_load_2d(as, &tmAs, full(s), ks * 256, ar / BM);
+                        tma_load_2d(bs, &tmBs, full(s), ks * 256, br / BM);
                     }
                 }
                 __syncwarp();
@@ -337,11 +329,11 @@ __global__ void __launch_bounds__(THREADS)
                     }
                     tc_fence_after();
                     if (one) {
-                        const uint32_t a = stage(s), b = a + W_BYTES, as = b + (uint32_t)p.x_bytes, bs = as + WS_BYTES;
+                        const uint32_t a = stage(s), b = a + A_BYTES, as = b + (uint32_t)p.b_bytes, bs = as + AS_BYTES;
                         const uint64_t ad = sw128_desc(a), bd = sw128_desc(b);
                         const int steps = ks + 1 == p.kstages ? p.last_steps : 4;
 #pragma unroll
-                        for (int t = 0; t < 2; ++t)  // 128 elements: columns 4 t of W's scales, 8 + 8 t of X's
+                        for (int t = 0; t < 2; ++t)  // 128 elements: columns 4 t of A's scales, 8 + 8 t of B's
                             if (2 * t < steps) {
                                 copy_scales<kPair>(sf + 4 * t, as + 512 * t);
                                 copy_scales<kPair>(sf + 8 + 8 * t, bs + 512 * t);
@@ -374,115 +366,97 @@ __global__ void __launch_bounds__(THREADS)
         __syncwarp();
     } else {
         // --------------------------------------------------- epilogue ---
-        // Chunks of 32 tokens, the groups in turn.
+        // Pieces of 64 columns (single CTAs, which have no registers for them: 32), the two
+        // groups of warps in turn.
+        constexpr int PIECE = kPair ? 64 : 32, PIECES = 256 / PIECE;
         const int q = warp & 3;  // TMEM lane quarter of this warp
         const int g = (warp - EPI_WARP0) >> 2, row = q * 32 + lane;
-        const uint32_t staging = s0 + (uint32_t)(p.stages * p.stage_bytes + g * GROUP_STAGING);
+        const uint32_t box = s0 + (uint32_t)(p.stages * p.stage_bytes + (warp - EPI_WARP0) * 4096);
         const uint64_t policy = l2_policy(false);
-        const bool issuer = lane == 0 && (kF32 || ((warp - EPI_WARP0) & 3) == 0);
-        int tc = 0, stored = 0;
-        bool ok = true;
+        int tc = 0;
         for (int u = unit0; u < p.units; u += unit_step, ++tc) {
             const int buf = tc & 1;
-            const int nt = tokens(u), chunks = (nt + 31) / 32;
-            ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait(tfull(buf), (uint32_t)(tc >> 1) & 1u, abort_flag, p.timeout_ns,
-                                                         SITE_EPI_TMEM_FULL));
-            if (!ok) {
-                // a warp that gave up still meets the others of its group, which may not have
-                if (!kPair || kF32 || !p.tma_out)
-                    break;
-                for (int cc = g; cc < chunks; cc += EPI_GROUPS) {
-                    asm volatile("bar.sync %0, 128;" ::"r"(1 + g) : "memory");
-                    asm volatile("bar.sync %0, 128;" ::"r"(1 + g) : "memory");
-                }
-                continue;
-            }
+            if (!__all_sync(0xFFFFFFFFu, mbar_wait(tfull(buf), (uint32_t)(tc >> 1) & 1u, abort_flag, p.timeout_ns,
+                                                   SITE_EPI_TMEM_FULL)))
+                break;
             tc_fence_after();
-            const int64_t n = w_row(u) + row;
-            const int64_t y0 = (int64_t)x_row(u) * p.ldy + n;
+            const int nc = columns(u);
+            const int64_t ar = a_row(u) + row, br = b_row(u);
             const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * p.buf1);
-            // the columns that the other buffer has too come first: the first buffer's last chunk, the second's first
-            const int first = buf == 0 ? 7 : 0;
-            uint32_t r[32];
+            // the columns that the other buffer has too come first: the first buffer's last piece, the second's first
+            const int first = buf == 0 ? PIECES - 1 : 0;
+            const bool shares = p.overlap && g == (first & 1);
+            uint32_t r[PIECE / 32][32];
 #pragma unroll 1
-            for (int i = 0; i < 8 / EPI_GROUPS; ++i) {
-                const int cc = p.overlap && g == (first & 1) ? (first + 2 * i) & 7 : g + 2 * i;
-                if (cc < chunks) {
-                    tmem_ld32_async(taddr + (uint32_t)(cc * 32), r);
-                    tmem_wait32(r);
+            for (int i = 0; i < PIECES / EPI_GROUPS; ++i) {
+                const int c0 = PIECE * (shares ? (first + EPI_GROUPS * i) & (PIECES - 1) : g + EPI_GROUPS * i);
+                if (c0 < nc) {
+#pragma unroll
+                    for (int h = 0; h < PIECE / 32; ++h)
+                        tmem_ld32_async(taddr + (uint32_t)(c0 + 32 * h), r[h]);
+#pragma unroll
+                    for (int h = 0; h < PIECE / 32; ++h)
+                        tmem_wait32(r[h]);
                 }
-                if (i == 0 && p.overlap && g == (first & 1)) {
+                const bool last = i + 1 == PIECES / EPI_GROUPS;
+                if (last || (i == 0 && shares)) {  // the accumulator, or what the other buffer has of it, is read out
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) {
-                        if constexpr (kPair)
-                            mbar_arrive_cluster(cluster_addr(shared_free, 0));
-                        else
-                            mbar_arrive(shared_free);
-                    }
-                }
-                if (cc >= chunks)
-                    continue;
-                if (kPair && p.tma_out) {
-                    // (a staging buffer is free once the copy engine has read it)
-                    const uint32_t b = staging + (kF32 ? 0u : (uint32_t)((stored & 1) * 8192));
-                    ++stored;
-                    if (issuer) {
-                        if constexpr (kF32)
-                            asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-                        else
-                            asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-                    }
-                    if constexpr (kF32)
-                        __syncwarp();
-                    else
-                        asm volatile("bar.sync %0, 128;" ::"r"(1 + g) : "memory");
-                    stage_chunk<kF32>(b, q, lane, r);
-                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                    if constexpr (kF32)
-                        __syncwarp();
-                    else
-                        asm volatile("bar.sync %0, 128;" ::"r"(1 + g) : "memory");
-                    if (issuer) {
-                        const int x = w_row(u), y = x_row(u) + cc * 32;
-                        if constexpr (kF32) {
-                            if (x + q * 32 < p.N)
-                                tma_store_2d_hint(&tmOut, b + (uint32_t)(q * 4096), x + q * 32, y, policy);
-                        } else {
-                            if (x < p.N)
-                                tma_store_2d_hint(&tmOut, b, x, y, policy);
-                            if (x + 64 < p.N)
-                                tma_store_2d_hint(&tmOut, b + 4096, x + 64, y, policy);
+                        if (i == 0 && shares) {
+                            if constexpr (kPair)
+                                mbar_arrive_cluster(cluster_addr(shared_free, 0));
+                            else
+                                mbar_arrive(shared_free);
                         }
-                        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+                        if (last) {
+                            if constexpr (kPair)
+                                mbar_arrive_cluster(cluster_addr(tempty(buf), 0));
+                            else
+                                mbar_arrive(tempty(buf));
+                        }
+                    }
+                }
+                if (c0 >= nc)
+                    continue;
+                if (kPair && p.staged) {
+#pragma unroll
+                    for (int h = 0; h < (kF32 ? 2 : 1); ++h) {
+                        if (lane == 0)  // the copy engine has read the box
+                            asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                        __syncwarp();
+                        stage_row<kF32>(box, lane, r[h], r[PIECE / 32 - 1]);
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                        __syncwarp();
+                        const int x = (int)br + c0 + 32 * h, y = (int)ar - lane;
+                        if (lane == 0 && x < p.b_rows && y < p.a_rows) {
+                            tma_store_2d_hint(&tmOut, box, x, y, policy);
+                            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+                        }
                     }
                     continue;
                 }
-                const int left = min(32, nt - cc * 32);
-                if (p.splits > 1) {  // this CTA's part, [token][row]
-                    float *red = reinterpret_cast<float *>(smem) + cc * 32 * BM + row;
+                // lane: a column of y, registers: its rows
 #pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        if (j < left)
-                            red[j * BM] = __uint_as_float(r[j]);
-                } else if (n < p.N) {
-                    int64_t at = y0 + (int64_t)cc * 32 * p.ldy;
+                for (int h = 0; h < PIECE / 32; ++h) {
+                    const int c = c0 + 32 * h, left = min(32, nc - c);
+                    if (p.splits > 1) {  // this CTA's part, [token][column]
+                        float *red = reinterpret_cast<float *>(smem) + c * BM + row;
 #pragma unroll
-                    for (int j = 0; j < 32; ++j, at += p.ldy)
-                        if (j < left)
-                            store_out<kF32>(p, at, __uint_as_float(r[j]));
+                        for (int j = 0; j < 32; ++j)
+                            if (j < left)
+                                red[j * BM] = __uint_as_float(r[h][j]);
+                    } else if (ar < p.a_rows) {
+                        int64_t at = (br + c) * p.ldy + ar;
+#pragma unroll
+                        for (int j = 0; j < 32; ++j, at += p.ldy)
+                            if (j < left)
+                                store_out<kF32>(p, at, __uint_as_float(r[h][j]));
+                    }
                 }
-            }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-                if constexpr (kPair)
-                    mbar_arrive_cluster(cluster_addr(tempty(buf), 0));
-                else
-                    mbar_arrive(tempty(buf));
             }
         }
-        if (issuer)
+        if (kPair && lane == 0)
             asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");  // stores complete before exit
         __syncwarp();
     }
@@ -491,14 +465,14 @@ __global__ void __launch_bounds__(THREADS)
         // one unit a cluster: its parts lie in the CTAs' shared memory
         cluster_sync();
         if (warp >= EPI_WARP0 && unit0 < p.units) {
-            const int row = (warp & 3) * 32 + lane, nt = tokens(unit0), g = (warp - EPI_WARP0) >> 2;
-            const int64_t n = w_row(unit0) + row;
-            if (n < p.N)
-                for (int m = (int)rank + g * p.splits; m < nt; m += EPI_GROUPS * p.splits) {
+            const int row = (warp & 3) * 32 + lane, nc = columns(unit0), g = (warp - EPI_WARP0) >> 2;
+            const int64_t ar = a_row(unit0) + row;
+            if (ar < p.a_rows)
+                for (int m = (int)rank + g * p.splits; m < nc; m += EPI_GROUPS * p.splits) {
                     float sum = 0.0f;
                     for (int c = 0; c < p.splits; ++c)
                         sum += ld_cluster(cluster_addr(s0 + (uint32_t)(m * BM + row) * 4u, (uint32_t)c));
-                    store_out<kF32>(p, (int64_t)(x_row(unit0) + m) * p.ldy + n, sum);
+                    store_out<kF32>(p, (int64_t)(b_row(unit0) + m) * p.ldy + ar, sum);
                 }
             __syncwarp();
         }
@@ -531,8 +505,9 @@ template <bool kF32>
 __global__ void __launch_bounds__(256) k_zero_out(const Params p)
 {
     pdl_begin();
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < (int64_t)p.M * p.N; i += (int64_t)gridDim.x * 256)
-        store_out<kF32>(p, i / p.N * p.ldy + i % p.N, 0.0f);
+    const int64_t M = p.b_rows, N = p.a_rows;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < M * N; i += (int64_t)gridDim.x * 256)
+        store_out<kF32>(p, i / N * p.ldy + i % N, 0.0f);
 }
 
 // ---------------------------------------------------------------- host ---
@@ -594,7 +569,7 @@ rlq_status encode_out(CUtensorMap *map, void *y, bool f32, int64_t rows, int64_t
 template <bool kPair, bool kF32>
 rlq_status launch(const CUtensorMap *maps, const Params &p, int grid, int cluster, cudaStream_t st)
 {
-    const size_t smem = 1024 + (size_t)p.stages * p.stage_bytes + (kPair ? EPI_GROUPS * GROUP_STAGING : 0) + BARS_BYTES;
+    const size_t smem = 1024 + (size_t)p.stages * p.stage_bytes + (kPair ? STAGING_BYTES : 0) + BARS_BYTES;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess)
@@ -634,9 +609,9 @@ rlq_status launch_gemm_mxfp4(const uint8_t *xq, int64_t ldxq, const uint8_t *xs,
     Params p = {};
     p.y = y;
     p.ldy = ldy;
-    p.M = (int)M;
-    p.N = (int)N;
     if (K == 0) {
+        p.a_rows = (int)N;
+        p.b_rows = (int)M;
         const int64_t blocks = (M * N + 255) / 256;
         return cuda_status(launch_pdl(f32 ? k_zero_out<true> : k_zero_out<false>,
                                       dim3((unsigned)(blocks < 8 * sms ? blocks : 8 * sms)), dim3(256), 0, st, p),
@@ -648,29 +623,40 @@ rlq_status launch_gemm_mxfp4(const uint8_t *xq, int64_t ldxq, const uint8_t *xs,
     p.timeout_ns = wait_limit_ns();
     p.withhold = take_stall();
     const bool pair = M > 256 && !p.withhold;
-    p.tile_m = M < 256 ? (int)M : 256;
-    p.m_tiles = (int)((M + p.tile_m - 1) / p.tile_m);
-    const int64_t n_tiles = (N + (pair ? 2 * BM : BM) - 1) / (pair ? 2 * BM : BM);
-    if (n_tiles * p.m_tiles >= (int64_t)1 << 30)
+    p.staged = pair && ((uintptr_t)y & 15) == 0 && ldy * (f32 ? 4 : 2) % 16 == 0;
+    struct Operand {
+        const uint8_t *q;
+        int64_t ld;
+        const uint8_t *s;
+        int64_t rows;
+    };
+    const Operand x = {xq, ldxq, xs, M}, w = {wq, ldwq, ws, N};
+    const Operand &A = p.staged ? x : w, &B = p.staged ? w : x;
+    p.a_rows = (int)A.rows;
+    p.b_rows = (int)B.rows;
+    p.tile_b = B.rows < 256 ? (int)B.rows : 256;
+    p.b_tiles = (int)((B.rows + p.tile_b - 1) / p.tile_b);
+    const int64_t a_tiles = (A.rows + (pair ? 2 * BM : BM) - 1) / (pair ? 2 * BM : BM);
+    if (a_tiles * p.b_tiles >= (int64_t)1 << 30)
         return fail(RLQ_ERR_UNSUPPORTED, "output of %lld x %lld has too many tiles", (long long)M, (long long)N);
-    p.units = (int)n_tiles * p.m_tiles;
+    p.units = (int)a_tiles * p.b_tiles;
     p.splits = 1;
     p.kps = p.kstages;
 
-    const int n16 = pair ? 256 : (p.tile_m + 15) / 16 * 16;
-    const int box_x = pair ? 128 : p.tile_m, box_xs = p.tile_m > 128 ? 2 : 1;
-    p.x_bytes = pair ? 128 * BK_BYTES : n16 * BK_BYTES;
-    p.xs_bytes = 1024 * box_xs;
-    p.stage_bytes = (W_BYTES + p.x_bytes + WS_BYTES + p.xs_bytes + 1023) / 1024 * 1024;
-    p.tx_bytes = W_BYTES + box_x * BK_BYTES + WS_BYTES + p.xs_bytes;
-    // Tensor memory: two accumulators and 24 columns of scales.  Up to 112 tokens take 256
-    // columns and half of the shared memory, so that two CTAs fit an SM.
-    const bool two = n16 <= 112;
+    const int n16 = pair ? 256 : (p.tile_b + 15) / 16 * 16;
+    const int box_b = pair ? 128 : p.tile_b, box_bs = p.tile_b > 128 ? 2 : 1;
+    p.b_bytes = pair ? 128 * BK_BYTES : n16 * BK_BYTES;
+    p.bs_bytes = 1024 * box_bs;
+    p.stage_bytes = (A_BYTES + p.b_bytes + AS_BYTES + p.bs_bytes + 1023) / 1024 * 1024;
+    p.tx_bytes = A_BYTES + box_b * BK_BYTES + AS_BYTES + p.bs_bytes;
+    // Tensor memory: two accumulators and 24 columns of scales.  Up to 112 columns take 256
+    // of it and half of the shared memory, so that two CTAs fit an SM.
+    const bool two = !pair && n16 <= 112;
     p.tmem_cols = two ? 256 : 512;
     p.sf_col = two ? 224 : 480;
     p.buf1 = n16 < 224 ? n16 : 224;
     p.overlap = n16 > 224;
-    const int room = (two ? 232448 / 2 - 1024 : 232448) - 1024 - BARS_BYTES - (pair ? EPI_GROUPS * GROUP_STAGING : 0);
+    const int room = (two ? 232448 / 2 - 1024 : 232448) - 1024 - BARS_BYTES - (pair ? STAGING_BYTES : 0);
     p.stages = room / p.stage_bytes < MAX_STAGES ? room / p.stage_bytes : MAX_STAGES;
     const int slots = pair ? sms / 2 : two ? 2 * sms : sms;
     if (!pair)
@@ -685,15 +671,14 @@ rlq_status launch_gemm_mxfp4(const uint8_t *xq, int64_t ldxq, const uint8_t *xs,
         p.kps = (p.kstages + p.splits - 1) / p.splits;
     }
     CUtensorMap maps[5] = {};
-    rlq_status r = encode(&maps[0], wq, false, (K + 1) / 2, N, ldwq, BM);
+    rlq_status r = encode(&maps[0], A.q, false, (K + 1) / 2, A.rows, A.ld, BM);
     if (r == RLQ_OK)
-        r = encode(&maps[1], xq, false, (K + 1) / 2, M, ldxq, box_x);
+        r = encode(&maps[1], B.q, false, (K + 1) / 2, B.rows, B.ld, box_b);
     if (r == RLQ_OK)
-        r = encode(&maps[2], ws, true, ktiles * 128, (N + 127) / 128, ktiles * 512, 1);
+        r = encode(&maps[2], A.s, true, ktiles * 128, (A.rows + 127) / 128, ktiles * 512, 1);
     if (r == RLQ_OK)
-        r = encode(&maps[3], xs, true, ktiles * 128, (M + 127) / 128, ktiles * 512, box_xs);
-    p.tma_out = pair && ((uintptr_t)y & 15) == 0 && ldy * (f32 ? 4 : 2) % 16 == 0;
-    if (r == RLQ_OK && p.tma_out)
+        r = encode(&maps[3], B.s, true, ktiles * 128, (B.rows + 127) / 128, ktiles * 512, box_bs);
+    if (r == RLQ_OK && p.staged)
         r = encode_out(&maps[4], y, f32, M, N, ldy);
     if (r != RLQ_OK)
         return r;
