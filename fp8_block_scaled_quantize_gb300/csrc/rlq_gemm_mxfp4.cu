@@ -46,7 +46,7 @@ constexpr int STAGING_BYTES = EPI_WARPS * 4096;  // (pairs) 32 rows of 128 bytes
 constexpr int A_BYTES = BM * BK_BYTES;   // 16 KB
 constexpr int AS_BYTES = 1024;           // a row tile's scales of a stage
 constexpr int MAX_STAGES = 8;
-constexpr int NUM_BARS = 2 * MAX_STAGES + 6;
+constexpr int NUM_BARS = 2 * MAX_STAGES + 7;
 constexpr int BARS_BYTES = NUM_BARS * 8 + 16;
 // tcgen05.mma kind::mxf4 instruction descriptor: A and B E2M1 (1 in bits 7-9 and 10-11), both
 // K-major, N >> 3 in bits 17-22, E8M0 scales (bit 23), M >> 4 in bits 24-28; the scales of an
@@ -120,12 +120,19 @@ __device__ __forceinline__ void copy_scales(uint32_t taddr, uint32_t saddr)
         asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
 }
 
-__device__ __forceinline__ float ld_cluster(uint32_t addr)
+// 16 bytes to a CTA of the cluster, counted by the barrier beside them.
+__device__ __forceinline__ void st_async4(uint32_t addr, uint32_t bar, const uint32_t *v)
 {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-    return v;
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];"
+                 ::"r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(bar)
+                 : "memory");
 }
+
+// The cluster's barrier without an order of memory (a release would wait for this thread's
+// part of a saturated memory system): what has to be seen behind it is either the
+// initialisation of barriers, which has a fence of its own, or comes with a barrier's count.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
 template <bool kF32>
 __device__ __forceinline__ void store_out(const Params &p, int64_t at, float v)
@@ -184,6 +191,7 @@ __global__ void __launch_bounds__(THREADS)
     auto tfull = [&](int b) { return smem_u32(&bars[2 * MAX_STAGES + b]); };
     auto tempty = [&](int b) { return smem_u32(&bars[2 * MAX_STAGES + 2 + b]); };
     const uint32_t shared_free = smem_u32(&bars[2 * MAX_STAGES + 4]), teardown = smem_u32(&bars[2 * MAX_STAGES + 5]);
+    const uint32_t parts_bar = smem_u32(&bars[2 * MAX_STAGES + 6]);
     const uint32_t rank = kPair || p.splits > 1 ? cta_rank() : 0;
     const int group = kPair ? 2 : p.splits;  // CTAs that work on one unit
     const int unit0 = blockIdx.x / group, unit_step = gridDim.x / group;
@@ -206,6 +214,7 @@ __global__ void __launch_bounds__(THREADS)
         }
         mbar_init(shared_free, kPair ? 8 : 4);  // the group that reads the shared columns
         mbar_init(teardown, 1);
+        mbar_init(parts_bar, 1);
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -233,10 +242,13 @@ __global__ void __launch_bounds__(THREADS)
     tc_fence_before();
     __syncthreads();
     if (group > 1)
-        cluster_sync();  // every CTA's barriers are initialised before any signal from another
+        cluster_arrive();  // this CTA's barriers are initialised
+    if (kPair)
+        cluster_wait();  // and the other's
     tc_fence_after();
     const uint32_t tmem = __reduce_or_sync(0xFFFFFFFFu, *tmem_slot);  // (in a uniform register)
 
+    bool met = false;  // (a shared contraction) has seen every CTA's stages used up
     if (warp == 0) {
         // ------------------------------------------------ TMA producer ---
         const bool one = elect_one();
@@ -321,6 +333,8 @@ __global__ void __launch_bounds__(THREADS)
                 tc_fence_after();
                 const int n = mma_n(u);
                 const uint32_t d = tmem + (uint32_t)(buf * p.buf1), sf = tmem + (uint32_t)p.sf_col;
+                // (a tile of B that starts in the middle of a scale tile: 32 rows a column)
+                const int skip = (b_row(u) & 127) >> 5;
                 const uint32_t idesc = IDESC | ((uint32_t)(n >> 3) << 17) | ((uint32_t)((kPair ? 2 * BM : BM) >> 4) << 24);
                 for (int ks = ks0; ks < ks1; ++ks) {
                     if (!mbar_wait_warp(full(s), phase, abort_flag, p.timeout_ns, SITE_MMA_FULL)) {
@@ -337,14 +351,14 @@ __global__ void __launch_bounds__(THREADS)
                             if (2 * t < steps) {
                                 copy_scales<kPair>(sf + 4 * t, as + 512 * t);
                                 copy_scales<kPair>(sf + 8 + 8 * t, bs + 512 * t);
-                                if (n > 128)
+                                if (n + 32 * skip > 128)
                                     copy_scales<kPair>(sf + 12 + 8 * t, bs + 1024 + 512 * t);
                             }
 #pragma unroll
                         for (int j = 0; j < 4; ++j)  // 64 elements: 32 bytes along the rows
                             if (j < steps)
                                 mma_mx<kPair>(d, ad + 2 * j, bd + 2 * j, idesc | (j & 1 ? IDESC_HIGH : 0u),
-                                              sf + 4 * (j >> 1), sf + 8 + 8 * (j >> 1), ks > ks0 || j > 0 ? 1u : 0u);
+                                              sf + 4 * (j >> 1), sf + 8 + 8 * (j >> 1) + skip, ks > ks0 || j > 0 ? 1u : 0u);
                         tc_commit_t<kPair>(empty(s));
                         if (ks + 1 == ks1)
                             tc_commit_t<kPair>(tfull(buf));
@@ -381,6 +395,14 @@ __global__ void __launch_bounds__(THREADS)
                 break;
             tc_fence_after();
             const int nc = columns(u);
+            if (!kPair && p.splits > 1) {
+                // every CTA's stages are used up: their memory takes the parts
+                cluster_wait();
+                cluster_arrive();
+                cluster_wait();
+                met = true;
+            }
+            const int slots_max = ((nc + 3) / 4 + p.splits - 1) / p.splits;
             const int64_t ar = a_row(u) + row, br = b_row(u);
             const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * p.buf1);
             // the columns that the other buffer has too come first: the first buffer's last piece, the second's first
@@ -440,12 +462,17 @@ __global__ void __launch_bounds__(THREADS)
 #pragma unroll
                 for (int h = 0; h < PIECE / 32; ++h) {
                     const int c = c0 + 32 * h, left = min(32, nc - c);
-                    if (p.splits > 1) {  // this CTA's part, [token][column]
-                        float *red = reinterpret_cast<float *>(smem) + c * BM + row;
+                    if (p.splits > 1) {
+                        // this CTA's part, four tokens of a column at a time, to the CTA that adds
+                        // those tokens: [part][four tokens][column]
 #pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            if (j < left)
-                                red[j * BM] = __uint_as_float(r[h][j]);
+                        for (int j = 0; j < 8; ++j)
+                            if (4 * j < left) {
+                                const int four = c / 4 + j, slot = four / p.splits;
+                                const uint32_t to = (uint32_t)(four - slot * p.splits);
+                                st_async4(cluster_addr(s0 + (uint32_t)((((int)rank * slots_max + slot) * BM + row) * 16), to),
+                                          cluster_addr(parts_bar, to), &r[h][4 * j]);
+                            }
                     } else if (ar < p.a_rows) {
                         int64_t at = (br + c) * p.ldy + ar;
 #pragma unroll
@@ -462,18 +489,45 @@ __global__ void __launch_bounds__(THREADS)
     }
 
     if (!kPair && p.splits > 1) {
-        // one unit a cluster: its parts lie in the CTAs' shared memory
-        cluster_sync();
-        if (warp >= EPI_WARP0 && unit0 < p.units) {
-            const int row = (warp & 3) * 32 + lane, nc = columns(unit0), g = (warp - EPI_WARP0) >> 2;
+        // One unit a cluster.  The warps that have met the others' barrier add the parts.
+        if (!met) {
+            cluster_wait();
+            cluster_arrive();
+            cluster_wait();
+        }
+        if (warp >= EPI_WARP0) {
+            const int nc = columns(unit0), fours = (nc + 3) / 4, slots_max = (fours + p.splits - 1) / p.splits;
+            const int slots = (fours - (int)rank + p.splits - 1) / p.splits;  // of this CTA
+            if (threadIdx.x == EPI_WARP0 * 32)
+                mbar_arrive_expect_tx(parts_bar, (uint32_t)(slots * p.splits * BM * 16));
+            bool ok = met && __all_sync(0xFFFFFFFFu, mbar_wait(parts_bar, 0, abort_flag, p.timeout_ns, SITE_EPI_TMEM_FULL));
+            const int row = (warp & 3) * 32 + lane;
             const int64_t ar = a_row(unit0) + row;
-            if (ar < p.a_rows)
-                for (int m = (int)rank + g * p.splits; m < nc; m += EPI_GROUPS * p.splits) {
-                    float sum = 0.0f;
-                    for (int c = 0; c < p.splits; ++c)
-                        sum += ld_cluster(cluster_addr(s0 + (uint32_t)(m * BM + row) * 4u, (uint32_t)c));
-                    store_out<kF32>(p, (int64_t)(b_row(unit0) + m) * p.ldy + ar, sum);
+            if (ok && ar < p.a_rows)
+                for (int i = (warp - EPI_WARP0) >> 2; i < slots; i += EPI_GROUPS) {
+                    const float4 *part = reinterpret_cast<const float4 *>(smem) + i * BM + row;
+                    float4 v[8];
+#pragma unroll
+                    for (int c = 0; c < 8; ++c)
+                        if (c < p.splits)
+                            v[c] = part[c * slots_max * BM];
+                    float4 sum = v[0];
+#pragma unroll
+                    for (int c = 1; c < 8; ++c)
+                        if (c < p.splits)
+                            sum = make_float4(sum.x + v[c].x, sum.y + v[c].y, sum.z + v[c].z, sum.w + v[c].w);
+                    const int m = 4 * ((int)rank + i * p.splits);
+                    const float f[4] = {sum.x, sum.y, sum.z, sum.w};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (m + j < nc)
+                            store_out<kF32>(p, (int64_t)(b_row(unit0) + m + j) * p.ldy + ar, f[j]);
                 }
+            if (!ok) {  // parts may still be on their way here: give them time to land
+                const uint64_t t0 = global_timer_ns();
+                while (global_timer_ns() - t0 < 200000ull)
+                    __nanosleep(1000);
+            }
             __syncwarp();
         }
     }
@@ -489,8 +543,10 @@ __global__ void __launch_bounds__(THREADS)
             __syncwarp();
         }
     }
-    if (group > 1)
-        cluster_sync();  // no CTA leaves while another may still signal it or read its part
+    if (group > 1) {  // no CTA leaves while another may still signal it
+        cluster_arrive();
+        cluster_wait();
+    }
     if (warp == 1) {
         tc_fence_after();
         if constexpr (kPair)
@@ -661,7 +717,7 @@ rlq_status launch_gemm_mxfp4(const uint8_t *xq, int64_t ldxq, const uint8_t *xs,
     const int slots = pair ? sms / 2 : two ? 2 * sms : sms;
     if (!pair)
         while (p.splits < 8 && p.units * p.splits * 2 <= slots && p.kstages >= 4 * p.splits &&
-               n16 * BM * 4 <= p.stages * p.stage_bytes) {
+               (n16 / 4 + 8) * BM * 16 <= p.stages * p.stage_bytes) {
             p.splits *= 2;
             p.kps = (p.kstages + p.splits - 1) / p.splits;
         }
