@@ -62,7 +62,7 @@ struct Params {
     int a_rows, b_rows;
     int kstages, last_steps;     // stages, and instructions (64 elements) of the last one
     int b_tiles, units, tile_b;  // tiles of B, (A tile, B tile) units, rows of a B tile
-    int splits, kps;             // CTAs that share a unit, stages of each
+    int splits, log2_splits, kps;  // CTAs that share a unit (a power of two), stages of each
     int stages, stage_bytes, b_bytes, bs_bytes, tx_bytes;
     int tmem_cols, buf1, sf_col, overlap;
     uint64_t timeout_ns;
@@ -402,7 +402,7 @@ __global__ void __launch_bounds__(THREADS)
                 cluster_wait();
                 met = true;
             }
-            const int slots_max = ((nc + 3) / 4 + p.splits - 1) / p.splits;
+            const int slots_max = ((nc + 3) / 4 + p.splits - 1) >> p.log2_splits;
             const int64_t ar = a_row(u) + row, br = b_row(u);
             const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * p.buf1);
             // the columns that the other buffer has too come first: the first buffer's last piece, the second's first
@@ -465,12 +465,13 @@ __global__ void __launch_bounds__(THREADS)
                     if (p.splits > 1) {
                         // this CTA's part, four tokens of a column at a time, to the CTA that adds
                         // those tokens: [part][four tokens][column]
+                        const uint32_t at = s0 + (uint32_t)(((int)rank * slots_max * BM + row) * 16);
 #pragma unroll
                         for (int j = 0; j < 8; ++j)
                             if (4 * j < left) {
-                                const int four = c / 4 + j, slot = four / p.splits;
-                                const uint32_t to = (uint32_t)(four - slot * p.splits);
-                                st_async4(cluster_addr(s0 + (uint32_t)((((int)rank * slots_max + slot) * BM + row) * 16), to),
+                                const int four = c / 4 + j;
+                                const uint32_t to = (uint32_t)(four & (p.splits - 1));
+                                st_async4(cluster_addr(at + (uint32_t)((four >> p.log2_splits) * (BM * 16)), to),
                                           cluster_addr(parts_bar, to), &r[h][4 * j]);
                             }
                     } else if (ar < p.a_rows) {
@@ -496,16 +497,20 @@ __global__ void __launch_bounds__(THREADS)
             cluster_wait();
         }
         if (warp >= EPI_WARP0) {
-            const int nc = columns(unit0), fours = (nc + 3) / 4, slots_max = (fours + p.splits - 1) / p.splits;
-            const int slots = (fours - (int)rank + p.splits - 1) / p.splits;  // of this CTA
+            const int nc = columns(unit0), fours = (nc + 3) / 4, slots_max = (fours + p.splits - 1) >> p.log2_splits;
+            const int slots = (fours - (int)rank + p.splits - 1) >> p.log2_splits;  // of this CTA
             if (threadIdx.x == EPI_WARP0 * 32)
                 mbar_arrive_expect_tx(parts_bar, (uint32_t)(slots * p.splits * BM * 16));
             bool ok = met && __all_sync(0xFFFFFFFFu, mbar_wait(parts_bar, 0, abort_flag, p.timeout_ns, SITE_EPI_TMEM_FULL));
             const int row = (warp & 3) * 32 + lane;
             const int64_t ar = a_row(unit0) + row;
-            if (ok && ar < p.a_rows)
-                for (int i = (warp - EPI_WARP0) >> 2; i < slots; i += EPI_GROUPS) {
-                    const float4 *part = reinterpret_cast<const float4 *>(smem) + i * BM + row;
+            if (ok && ar < p.a_rows) {
+                const int g = (warp - EPI_WARP0) >> 2;
+                const float4 *part = reinterpret_cast<const float4 *>(smem) + g * BM + row;
+                int m = 4 * ((int)rank + g * p.splits);
+                int64_t at = (int64_t)(b_row(unit0) + m) * p.ldy + ar;
+                for (int i = g; i < slots; i += EPI_GROUPS, part += EPI_GROUPS * BM, m += 4 * EPI_GROUPS * p.splits,
+                         at += 4 * EPI_GROUPS * p.splits * p.ldy) {
                     float4 v[8];
 #pragma unroll
                     for (int c = 0; c < 8; ++c)
@@ -516,13 +521,15 @@ __global__ void __launch_bounds__(THREADS)
                     for (int c = 1; c < 8; ++c)
                         if (c < p.splits)
                             sum = make_float4(sum.x + v[c].x, sum.y + v[c].y, sum.z + v[c].z, sum.w + v[c].w);
-                    const int m = 4 * ((int)rank + i * p.splits);
-                    const float f[4] = {sum.x, sum.y, sum.z, sum.w};
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        if (m + j < nc)
-                            store_out<kF32>(p, (int64_t)(b_row(unit0) + m + j) * p.ldy + ar, f[j]);
+                    store_out<kF32>(p, at, sum.x);
+                    if (m + 1 < nc)
+                        store_out<kF32>(p, at + p.ldy, sum.y);
+                    if (m + 2 < nc)
+                        store_out<kF32>(p, at + 2 * p.ldy, sum.z);
+                    if (m + 3 < nc)
+                        store_out<kF32>(p, at + 3 * p.ldy, sum.w);
                 }
+            }
             if (!ok) {  // parts may still be on their way here: give them time to land
                 const uint64_t t0 = global_timer_ns();
                 while (global_timer_ns() - t0 < 200000ull)
@@ -655,6 +662,57 @@ rlq_status launch(const CUtensorMap *maps, const Params &p, int grid, int cluste
                        "MXFP4 GEMM launch");
 }
 
+// How a product is cut: CTA pairs with 256 x 256 tiles, or single CTAs with 128 output columns x
+// tile_b tokens, a cluster of `splits` to a tile; `two` of them on an SM.
+struct Plan {
+    bool pair, two;
+    int tile_b, splits;
+};
+
+// The cheapest by a model of a launch's microseconds, fitted to single waves of it: a start and an
+// end that grow with the tile, per wave the stages one after the other (or, if that is
+// longer, the operands and the output at 6.2 TB/s), and the joining of a shared contraction.  Measured
+// (us): 1 token, 14336 x 4096: 9.3 alone, 9.4 in twos, 13.6 in fours; 1, 4096 x 14336: 20.1, 12.7,
+// 9.5, 9.6 in eights; 256, 4096 x 4096: 8.7 in tiles of 64, 9.5 of 128, 11.3 of 256, 9.6 in
+// pairs; 300, 1024 x 4096: 7.1 in tiles of 128 in fours, 8.9 in pairs; 1001, 5120 x 5120: 17.6 in
+// pairs, 21.4 in tiles of 256.
+Plan make_plan(int64_t M, int64_t N, int64_t K, bool f32, int sms, bool pairs)
+{
+    const int64_t kstages = (K + 255) / 256;
+    const double bytes = ((double)(M + N) * (double)K * 17 / 32 + (double)M * (double)N * (f32 ? 4 : 2)) / 6.2e6;
+    auto longer = [&](double waves, double per_wave) { return waves * per_wave > bytes ? waves * per_wave : bytes; };
+    Plan best = {};
+    double least = 1e300;
+    if (pairs) {
+        const int64_t units = ((M + 255) / 256) * ((N + 255) / 256), slots = sms / 2;
+        least = 4.4 + longer((double)((units + slots - 1) / slots), (double)kstages * 0.2775);
+        best = {true, false, 256, 1};
+    }
+    for (int tile = 64;; tile *= 2) {
+        const int b = M < tile ? (int)M : tile;
+        const int64_t units = (N + BM - 1) / BM * ((M + b - 1) / b);
+        for (int s = 1; s <= 8; s *= 2) {
+            // (every CTA has a part: the last one's begins before the stages end)
+            const int64_t kps = (kstages + s - 1) / s;
+            if (s > 1 && (kps < 2 || (s - 1) * kps >= kstages))
+                break;
+            const bool two = b <= 112 && (units * s > sms || kps <= 12);
+            const int64_t slots = two ? 2 * sms : sms;
+            if (s > 1 && units * s > slots)
+                break;
+            const double cost = 3.6 + 0.0075 * b + longer((double)((units * s + sms - 1) / sms), (double)kps * (0.26 + 0.0003 * b)) +
+                                (s > 1 ? 0.6 + 0.008 * b : 0.0);
+            if (cost < least) {
+                least = cost;
+                best = {false, two, b, s};
+            }
+        }
+        if (M <= tile || tile == 256)
+            break;
+    }
+    return best;
+}
+
 }  // namespace
 
 rlq_status launch_gemm_mxfp4(const uint8_t *xq, int64_t ldxq, const uint8_t *xs, const uint8_t *wq, int64_t ldwq,
@@ -678,7 +736,8 @@ rlq_status launch_gemm_mxfp4(const uint8_t *xq, int64_t ldxq, const uint8_t *xs,
     p.last_steps = (int)((K - (int64_t)(p.kstages - 1) * 256 + 63) / 64);
     p.timeout_ns = wait_limit_ns();
     p.withhold = take_stall();
-    const bool pair = M > 256 && !p.withhold;
+    const Plan plan = make_plan(M, N, K, f32, sms, !p.withhold);
+    const bool pair = plan.pair;
     p.staged = pair && ((uintptr_t)y & 15) == 0 && ldy * (f32 ? 4 : 2) % 16 == 0;
     struct Operand {
         const uint8_t *q;
@@ -690,24 +749,29 @@ rlq_status launch_gemm_mxfp4(const uint8_t *xq, int64_t ldxq, const uint8_t *xs,
     const Operand &A = p.staged ? x : w, &B = p.staged ? w : x;
     p.a_rows = (int)A.rows;
     p.b_rows = (int)B.rows;
-    p.tile_b = B.rows < 256 ? (int)B.rows : 256;
+    p.tile_b = pair ? (B.rows < 256 ? (int)B.rows : 256) : plan.tile_b;
     p.b_tiles = (int)((B.rows + p.tile_b - 1) / p.tile_b);
     const int64_t a_tiles = (A.rows + (pair ? 2 * BM : BM) - 1) / (pair ? 2 * BM : BM);
     if (a_tiles * p.b_tiles >= (int64_t)1 << 30)
         return fail(RLQ_ERR_UNSUPPORTED, "output of %lld x %lld has too many tiles", (long long)M, (long long)N);
     p.units = (int)a_tiles * p.b_tiles;
-    p.splits = 1;
-    p.kps = p.kstages;
+    p.splits = plan.splits;
+    p.kps = (p.kstages + p.splits - 1) / p.splits;
 
     const int n16 = pair ? 256 : (p.tile_b + 15) / 16 * 16;
+    // scale tiles that a B tile reaches into (one of 192 rows may begin in the middle of one)
     const int box_b = pair ? 128 : p.tile_b, box_bs = p.tile_b > 128 ? 2 : 1;
     p.b_bytes = pair ? 128 * BK_BYTES : n16 * BK_BYTES;
     p.bs_bytes = 1024 * box_bs;
     p.stage_bytes = (A_BYTES + p.b_bytes + AS_BYTES + p.bs_bytes + 1023) / 1024 * 1024;
     p.tx_bytes = A_BYTES + box_b * BK_BYTES + AS_BYTES + p.bs_bytes;
-    // Tensor memory: two accumulators and 24 columns of scales.  Up to 112 columns take 256
-    // of it and half of the shared memory, so that two CTAs fit an SM.
-    const bool two = !pair && n16 <= 112;
+    // Tensor memory: two accumulators and 24 columns of scales.  Up to 112 columns fit in 256
+    // of it and half of the shared memory, two CTAs to an SM: where there are more CTAs than
+    // SMs (64 tokens, 128256 x 4096: 50.2 us, 51.5 with one an SM), and for short
+    // contractions, whose next call then starts beside this one (1001 tokens, 1024 x 2048: 6.0
+    // us back to back, 7.9 with one).  Long ones gain by the larger ring (64 tokens, 14336 x
+    // 4096: 9.7 us, 10.3 with two).
+    const bool two = plan.two;
     p.tmem_cols = two ? 256 : 512;
     p.sf_col = two ? 224 : 480;
     p.buf1 = n16 < 224 ? n16 : 224;
@@ -715,17 +779,8 @@ rlq_status launch_gemm_mxfp4(const uint8_t *xq, int64_t ldxq, const uint8_t *xs,
     const int room = (two ? 232448 / 2 - 1024 : 232448) - 1024 - BARS_BYTES - (pair ? STAGING_BYTES : 0);
     p.stages = room / p.stage_bytes < MAX_STAGES ? room / p.stage_bytes : MAX_STAGES;
     const int slots = pair ? sms / 2 : two ? 2 * sms : sms;
-    if (!pair)
-        while (p.splits < 8 && p.units * p.splits * 2 <= slots && p.kstages >= 4 * p.splits &&
-               (n16 / 4 + 8) * BM * 16 <= p.stages * p.stage_bytes) {
-            p.splits *= 2;
-            p.kps = (p.kstages + p.splits - 1) / p.splits;
-        }
-    // (a split of the plan may be empty: the last ones where kps does not divide the stages)
-    while (p.splits > 1 && (p.splits - 1) * p.kps >= p.kstages) {
-        p.splits /= 2;
-        p.kps = (p.kstages + p.splits - 1) / p.splits;
-    }
+    while (1 << p.log2_splits < p.splits)
+        ++p.log2_splits;
     CUtensorMap maps[5] = {};
     rlq_status r = encode(&maps[0], A.q, false, (K + 1) / 2, A.rows, A.ld, BM);
     if (r == RLQ_OK)
