@@ -46,6 +46,7 @@ constexpr int STAGING_BYTES = EPI_WARPS * 4096;  // (pairs) 32 rows of 128 bytes
 constexpr int A_BYTES = BM * BK_BYTES;   // 16 KB
 constexpr int AS_BYTES = 1024;           // a row tile's scales of a stage
 constexpr int MAX_STAGES = 8;
+constexpr int PREFETCH = 16;             // stages of weights that a CTA hints to L2 ahead
 constexpr int NUM_BARS = 2 * MAX_STAGES + 7;
 constexpr int BARS_BYTES = NUM_BARS * 8 + 16;
 // tcgen05.mma kind::mxf4 instruction descriptor: A and B E2M1 (1 in bits 7-9 and 10-11), both
@@ -85,6 +86,13 @@ __device__ __forceinline__ void mma_mx(uint32_t d, uint64_t a, uint64_t b, uint3
             "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
             ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
             : "memory");
+}
+
+// A box on its way to L2 (a hint: no completion to wait for).
+__device__ __forceinline__ void tma_prefetch_l2(const CUtensorMap *map, int x, int y)
+{
+    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global [%0, {%1, %2}];" ::"l"((uint64_t)map), "r"(x), "r"(y)
+                 : "memory");
 }
 
 // One lane of a warp whose lanes are together.
@@ -237,6 +245,15 @@ __global__ void __launch_bounds__(THREADS)
         prefetch_tmap(&tmB);
         prefetch_tmap(&tmAs);
         prefetch_tmap(&tmBs);
+        if (!kPair && unit0 < p.units) {
+            // The weights' first stages start their way to L2 before the kernels in front (as a
+            // rule the tokens' quantizer) have finished: a hint, nothing is read until the wait below.
+            const int ar = a_row(unit0), ahead = min(ks1, ks0 + PREFETCH);
+            for (int ks = ks0; ks < ahead; ++ks) {
+                tma_prefetch_l2(&tmA, ks * BK_BYTES, ar);
+                tma_prefetch_l2(&tmAs, ks * 256, ar / BM);
+            }
+        }
     }
     pdl_begin();
     tc_fence_before();
