@@ -12,8 +12,8 @@
 // streams its row with running maximum, sum and weighted sum a thread.  The alternatives cost
 // the loop nothing: it keeps each thread's maximum anyway.  The k-th largest of those T is a
 // lower bound of the row's k-th logit, so every wanted logit is in one of the few threads whose
-// maximum reaches T; a warp reads each such thread's units again (from L2, two loads a lane at
-// 128256 bf16) and puts what reaches T on a list, whose ranks are counted.  A list that
+// maximum reaches T, as a rule in the batch of loads that the maximum is in; those batches are
+// read again, and what reaches T goes on a list, whose ranks are counted.  A list that
 // overflows (thousands of equal logits) is replaced by a search for the k-th logit over the
 // whole row.
 //
@@ -34,6 +34,7 @@ constexpr int THREADS = 256, CTAS_SM = 4, WARPS = THREADS / 32, MAX_CLUSTER = 8;
 constexpr int BATCH = 8;     // 16-byte loads in flight a thread
 constexpr int MAX_TOP = MAX_TOKEN_TOP;
 constexpr int LIST = 1024;   // candidates
+constexpr int CHOSEN = 1024; // batches read again
 
 struct Sums {
     float m, s, w;  // maximum, sum of 2^t and of t 2^t, t = (x - m) c
@@ -90,9 +91,14 @@ struct Part {
     template <typename F>
     __device__ __forceinline__ void each(int u, F f) const
     {
+        if (u < u1)
+            each_of(load(u), u, f);
+    }
+    template <typename F>
+    __device__ __forceinline__ void each_of(const uint4 &v, int u, F f) const
+    {
         if (u >= u1)
             return;
-        const uint4 v = load(u);
         const int e0 = u * Elem<T>::N - off;
 #pragma unroll
         for (int j = 0; j < Elem<T>::N; j += 2) {
@@ -109,6 +115,8 @@ struct Candidates {
     float x[LIST];
     int at[LIST];
     int n;          // candidates, also those past the list's end
+    int n_chosen;
+    int chosen[CHOSEN];  // batch x THREADS + thread
     int scratch[WARPS + 1];
     float thread_max[THREADS];
 };
@@ -200,71 +208,116 @@ __device__ __noinline__ void search(const Part<T> &p, Candidates &c, float low, 
     put_first_equal(p, c, v, k - above);
 }
 
-// Puts the part's k largest logits on the list, and perhaps more: each thread's maximum m is known.
-template <typename T>
-__device__ __forceinline__ void find_top(const Part<T> &p, Candidates &c, float m, int k)
+// T, a value that at least k of the threads' maxima reach and, unless equal ones stand in the
+// way, at most 2 k + 8 (by one warp): bisection of the keys between the smallest and the largest.
+__device__ __forceinline__ float threshold(const float *thread_max, int lane, int k)
 {
-    const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-    c.thread_max[t] = m;
-    if (t == 0)
-        c.n = 0;
-    __syncthreads();
-    // T: the upper 16 bits of the k-th largest thread maximum's key (of bf16 logits, all of it)
-    if (warp == 0) {
-        uint32_t key[WARPS];
+    uint32_t key[WARPS], lo = 0xFFFFFFFFu, hi = 0u;
+#pragma unroll
+    for (int i = 0; i < WARPS; ++i) {
+        const bool in = 32 * i + lane < (int)blockDim.x;
+        key[i] = in ? key_of(thread_max[32 * i + lane]) : 0u;
+        lo = min(lo, in ? key[i] : 0xFFFFFFFFu);
+        hi = max(hi, key[i]);
+    }
+    lo = (int)blockDim.x < k ? 0u : __reduce_min_sync(0xFFFFFFFFu, lo);
+    hi = __reduce_max_sync(0xFFFFFFFFu, hi);
+    while (lo < hi) {
+        const uint32_t mid = lo + (hi - lo + 1) / 2;
+        int n = 0;
 #pragma unroll
         for (int i = 0; i < WARPS; ++i)
-            key[i] = 32 * i + lane < (int)blockDim.x ? key_of(c.thread_max[32 * i + lane]) : 0u;
-        uint32_t prefix = 0;
-#pragma unroll 1
-        for (uint32_t bit = 0x80000000u; bit >= 0x10000u; bit >>= 1) {
-            int n = 0;
-#pragma unroll
-            for (int i = 0; i < WARPS; ++i)
-                n += key[i] >= (prefix | bit);
-            if ((int)__reduce_add_sync(0xFFFFFFFFu, n) >= k)
-                prefix |= bit;
+            n += key[i] >= mid;
+        n = __reduce_add_sync(0xFFFFFFFFu, n);
+        if (n >= k) {
+            lo = mid;
+            if (n <= 2 * k + 8)
+                break;
+        } else {
+            hi = mid - 1;
         }
+    }
+    return of_key(lo);
+}
+
+// Puts the part's k largest logits on the list, and perhaps more.  c.thread_max is written and
+// c.n 0; `finder` is the warp that looks for T while warp 0 may be about the row's sums.
+template <typename T>
+__device__ __forceinline__ void find_top(const Part<T> &p, Candidates &c, float m, float others, int at_batch, int k,
+                                         int finder)
+{
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5, threads = blockDim.x;
+    if (warp == finder) {
+        const float v = threshold(c.thread_max, lane, k);
         if (lane == 0)
-            c.scratch[WARPS] = (int)prefix;
+            c.scratch[WARPS] = __float_as_int(v);
     }
     __syncthreads();
-    const float T0 = of_key((uint32_t)c.scratch[WARPS]);
-    // the units of each thread that reaches T, by its warp
-    uint32_t who = __ballot_sync(0xFFFFFFFFu, m >= T0 && m > -INFINITY);
-    while (who) {
-        const int w = warp * 32 + __ffs(who) - 1;
-        who &= who - 1;
-        for (int u = p.u0 + w + lane * (int)blockDim.x; u < p.u1; u += 32 * blockDim.x)
-            p.each(u, [&](float x, int token) {
-                if (x >= T0 && x > -INFINITY)
-                    put(c, x, token);
-            });
+    const float T0 = __int_as_float(c.scratch[WARPS]);
+    // the batches that reach T (a thread knows the one of its maximum; if another of its
+    // batches reaches T too, all of them are read), their units among all threads
+    if (m >= T0 && m > -INFINITY) {
+        const int batches = (p.u1 - p.u0 - t + BATCH * threads - 1) / (BATCH * threads);
+        const bool all = others >= T0 && others > -INFINITY;
+        const int n = all ? batches : 1, first = atomicAdd(&c.n_chosen, n);
+        for (int i = 0; i < n && first + i < CHOSEN; ++i)
+            c.chosen[first + i] = (all ? i : at_batch) * THREADS + t;
+    }
+    __syncthreads();
+    if (c.n_chosen <= CHOSEN) {
+        const int items = c.n_chosen * BATCH;
+        for (int i0 = t; i0 < items; i0 += 2 * threads) {
+            uint4 v[2];
+            int u[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int i = i0 + j * threads, e = i < items ? c.chosen[i / BATCH] : 0;
+                u[j] = i < items ? p.u0 + (e & (THREADS - 1)) + (e / THREADS * BATCH + i % BATCH) * threads : p.u1;
+                v[j] = p.load(u[j]);
+            }
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                p.each_of(v[j], u[j], [&](float x, int token) {
+                    if (x >= T0 && x > -INFINITY)
+                        put(c, x, token);
+                });
+        }
+    } else if (t == 0) {
+        c.n = LIST + 1;
     }
     __syncthreads();
     const int n = c.n;
-    __syncthreads();
     if (n > LIST) {
         float high = -INFINITY;
-        for (int i = 0; i < (int)blockDim.x; ++i)
+        for (int i = 0; i < threads; ++i)
             high = fmaxf(high, c.thread_max[i]);
+        __syncthreads();
         search(p, c, T0, high, k);
+        __syncthreads();
     } else if (n < k) {  // fewer than k logits above -inf
+        __syncthreads();
         put_first_equal(p, c, -INFINITY, k - n);
+        __syncthreads();
     }
-    __syncthreads();
 }
 
-// f(rank, logit, token) for the candidates of ranks below k.
+// f(rank, logit, token) for the candidates of ranks below k, eight lanes to a candidate.
 template <typename F>
 __device__ __forceinline__ void ranked(const float *x, const int *at, int n, int k, F f)
 {
-    for (int i = threadIdx.x; i < n; i += blockDim.x) {
+    const int part = threadIdx.x & 7;
+    for (int base = 0; base < n; base += blockDim.x / 8) {  // (all lanes take part in the sums)
+        const int i = base + threadIdx.x / 8;
+        const float v = i < n ? x[i] : 0.0f;
+        const int token = i < n ? at[i] : 0;
         int rank = 0;
-        for (int j = 0; j < n; ++j)
-            rank += before(x[j], at[j], x[i], at[i]);
-        if (rank < k)
-            f(rank, x[i], at[i]);
+        for (int j = part; j < n; j += 8)
+            rank += before(x[j], at[j], v, token);
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1)
+            rank += __shfl_xor_sync(0xFFFFFFFFu, rank, o);
+        if (part == 0 && i < n && rank < k)
+            f(rank, v, token);
     }
 }
 
@@ -310,16 +363,22 @@ __global__ void __launch_bounds__(THREADS, CTAS_SM) k_token_stats(const TokenSta
     const float c = 1.4426950408889634f / p.temperature;
     const float2 c2 = make_float2(c, c);
     float m = -INFINITY;
+    float others = -INFINITY;  // (kTop) the largest logit outside the batch of the thread's maximum
+    int at_batch = 0, batch = 0;
     float2 sum = make_float2(0.0f, 0.0f), wsum = make_float2(0.0f, 0.0f);
-    for (int u = u0 + t; u < part_of.u1; u += BATCH * threads) {
+    for (int u = u0 + t; u < part_of.u1; u += BATCH * threads, ++batch) {
         uint4 v[BATCH];
 #pragma unroll
         for (int i = 0; i < BATCH; ++i)
             v[i] = part_of.load(u + i * threads);
-        float b = m;
+        float b = kTop ? -INFINITY : m;
 #pragma unroll
         for (int i = 0; i < BATCH; ++i)
             b = E::max_of(b, v[i]);
+        if (kTop) {
+            others = fmaxf(others, fminf(b, m));
+            at_batch = b > m ? batch : at_batch;
+        }
         if (b > m) {  // (m = -inf: the sums are 0, or NaN, so far)
             const float d = m == -INFINITY ? 0.0f : fmaxf((m - b) * c, LOWEST), k = ex2(d);
             wsum = __fmul2_rn(__ffma2_rn(sum, make_float2(d, d), wsum), make_float2(k, k));
@@ -342,21 +401,43 @@ __global__ void __launch_bounds__(THREADS, CTAS_SM) k_token_stats(const TokenSta
     Sums o = join({m, sum.x + sum.y, wsum.x + wsum.y}, c);
     if (lane == 0)
         part[warp] = make_float4(o.m, o.s, o.w, 0.0f);
-    const int n_part = max(0, min(V, part_of.u1 * N - off) - max(0, u0 * N - off));
-    const int k = kTop ? min(p.top, n_part) : 0;
-    if (kTop)
-        find_top(part_of, cand, m, k);
-    else
-        __syncthreads();
+    if (kTop) {
+        cand.thread_max[t] = m;
+        if (t == 0)
+            cand.n = cand.n_chosen = 0;
+    }
+    __syncthreads();
+    // the row's scalars, by lane 0 of warp 0
+    auto finish = [&](const Sums &o) {
+        // (quotients: a logit that is the type's lowest value has a finite log probability)
+        const float l2 = log2f(o.s), ls = LN2 * l2;
+        const bool none = o.s == 0.0f;  // every logit is -inf
+        // (NaN targets make their sum NaN; +inf - +inf too)
+        p.lp[row] = none ? -INFINITY : (xt - o.m) / p.temperature - ls;
+        p.lse[row] = none ? -INFINITY : o.m / p.temperature + ls;
+        p.entropy[row] = none ? 0.0f : LN2 * (l2 - o.w / o.s);
+        if (kTop) {
+            row_m = o.m;
+            row_ls = none ? INFINITY : ls;
+        }
+    };
     if (warp == 0) {
         const float4 v = lane < nw ? part[lane] : make_float4(-INFINITY, 0.0f, 0.0f, 0.0f);
         o = join({v.x, v.y, v.z}, c);
-        if (lane == 0)
-            mine = make_float4(o.m, o.s, o.w, 0.0f);
+        if (lane == 0) {
+            if (csize > 1)
+                mine = make_float4(o.m, o.s, o.w, 0.0f);
+            else
+                finish(o);
+        }
         __syncwarp();
     }
-    if (csize > 1) {
-        if (kTop) {
+    if (kTop) {
+        const int n_part = max(0, min(V, part_of.u1 * N - off) - max(0, u0 * N - off));
+        const int k = min(p.top, n_part);
+        if (k > 0)
+            find_top(part_of, cand, m, others, at_batch, k, nw > 1 ? 1 : 0);
+        if (csize > 1) {
             if (t < MAX_TOP)
                 own.at[t] = -1;
             __syncthreads();
@@ -365,6 +446,8 @@ __global__ void __launch_bounds__(THREADS, CTAS_SM) k_token_stats(const TokenSta
                 own.at[r] = at;
             });
         }
+    }
+    if (csize > 1) {
         cluster_arrive();
         cluster_wait();
         if (rank == 0) {
@@ -374,12 +457,13 @@ __global__ void __launch_bounds__(THREADS, CTAS_SM) k_token_stats(const TokenSta
                 const float2 b = lane < csize ? ld_cluster2(reinterpret_cast<const float2 *>(&mine) + 1, lane)
                                               : make_float2(0.0f, 0.0f);
                 o = join({a.x, a.y, b.x}, c);
+                if (lane == 0) {
+                    finish(o);
+                    cand.n = 0;
+                }
                 __syncwarp();
             }
             if (kTop) {  // the parts' lists, one behind the other
-                __syncthreads();
-                if (t == 0)
-                    cand.n = 0;
                 __syncthreads();
                 for (int i = t; i < csize * p.top; i += threads) {
                     const int r = i / p.top, j = i - r * p.top;
@@ -388,36 +472,24 @@ __global__ void __launch_bounds__(THREADS, CTAS_SM) k_token_stats(const TokenSta
                     if (at >= 0)
                         put(cand, v, at);
                 }
+                __syncthreads();
             }
         }
         cluster_arrive_relaxed();  // this CTA has read the others' parts
     }
-    if (rank == 0) {
-        if (t == 0) {
-            // (quotients: a logit that is the type's lowest value has a finite log probability)
-            const float l2 = log2f(o.s), ls = LN2 * l2;
-            const bool none = o.s == 0.0f;  // every logit is -inf
-            // (NaN targets make their sum NaN; +inf - +inf too)
-            p.lp[row] = none ? -INFINITY : (xt - o.m) / p.temperature - ls;
-            p.lse[row] = none ? -INFINITY : o.m / p.temperature + ls;
-            p.entropy[row] = none ? 0.0f : LN2 * (l2 - o.w / o.s);
-            if (kTop) {
-                row_m = o.m;
-                row_ls = none ? INFINITY : ls;
-            }
-        }
-        if (kTop) {
-            for (int i = t; i < p.top; i += threads) {  // (left so where NaN logits leave fewer)
+    if (kTop && rank == 0) {
+        const int n = min(cand.n, LIST);
+        if (n < p.top) {  // (NaN logits)
+            for (int i = n + t; i < p.top; i += threads) {
                 ids[i] = -1;
                 top_lp[i] = NAN;
             }
-            __syncthreads();
-            const float rm = row_m, ls = row_ls;
-            ranked(cand.x, cand.at, min(cand.n, LIST), p.top, [&](int r, float v, int at) {
-                ids[r] = at;
-                top_lp[r] = v == -INFINITY && ls == ls ? -INFINITY : (v - rm) / p.temperature - ls;
-            });
         }
+        const float rm = row_m, ls = row_ls;
+        ranked(cand.x, cand.at, n, p.top, [&](int r, float v, int at) {
+            ids[r] = at;
+            top_lp[r] = v == -INFINITY && ls == ls ? -INFINITY : (v - rm) / p.temperature - ls;
+        });
     }
     if (csize > 1)
         cluster_wait();  // no CTA leaves while another may still read its part
