@@ -209,7 +209,7 @@ __device__ __noinline__ void search(const Part<T> &p, Candidates &c, float low, 
 }
 
 // T, a value that at least k of the threads' maxima reach and, unless equal ones stand in the
-// way, at most 2 k + 8 (by one warp): bisection of the keys between the smallest and the largest.
+// way, at most 5/4 k + 2 (by one warp): bisection of the keys between the smallest and the largest.
 __device__ __forceinline__ float threshold(const float *thread_max, int lane, int k)
 {
     uint32_t key[WARPS], lo = 0xFFFFFFFFu, hi = 0u;
@@ -231,7 +231,7 @@ __device__ __forceinline__ float threshold(const float *thread_max, int lane, in
         n = __reduce_add_sync(0xFFFFFFFFu, n);
         if (n >= k) {
             lo = mid;
-            if (n <= 2 * k + 8)
+            if (n <= k + k / 4 + 2)
                 break;
         } else {
             hi = mid - 1;
@@ -266,17 +266,17 @@ __device__ __forceinline__ void find_top(const Part<T> &p, Candidates &c, float 
     __syncthreads();
     if (c.n_chosen <= CHOSEN) {
         const int items = c.n_chosen * BATCH;
-        for (int i0 = t; i0 < items; i0 += 2 * threads) {
-            uint4 v[2];
-            int u[2];
+        for (int i0 = t; i0 < items; i0 += 4 * threads) {
+            uint4 v[4];
+            int u[4];
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
+            for (int j = 0; j < 4; ++j) {
                 const int i = i0 + j * threads, e = i < items ? c.chosen[i / BATCH] : 0;
                 u[j] = i < items ? p.u0 + (e & (THREADS - 1)) + (e / THREADS * BATCH + i % BATCH) * threads : p.u1;
                 v[j] = p.load(u[j]);
             }
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
+            for (int j = 0; j < 4; ++j)
                 p.each_of(v[j], u[j], [&](float x, int token) {
                     if (x >= T0 && x > -INFINITY)
                         put(c, x, token);
@@ -360,7 +360,7 @@ __global__ void __launch_bounds__(THREADS, CTAS_SM) k_token_stats(const TokenSta
     float xt = 0.0f;
     if (t == 0)
         xt = E::load(x + target);
-    const float c = 1.4426950408889634f / p.temperature;
+    const float c = 1.4426950408889634f / p.temperature, inv_t = 1.0f / p.temperature;
     const float2 c2 = make_float2(c, c);
     float m = -INFINITY;
     float others = -INFINITY;  // (kTop) the largest logit outside the batch of the thread's maximum
@@ -395,6 +395,7 @@ __global__ void __launch_bounds__(THREADS, CTAS_SM) k_token_stats(const TokenSta
                 const float2 f = __fmul2_rn(__fadd2_rn(E::get2(v[i], j), nref), c2);
                 const float2 e = make_float2(ex2(f.x), ex2(f.y));
                 sum = __fadd2_rn(sum, e);
+                // (a logit of -inf adds 0 x LOWEST)
                 wsum = __ffma2_rn(make_float2(fmaxf(f.x, LOWEST), fmaxf(f.y, LOWEST)), e, wsum);
             }
     }
@@ -409,12 +410,12 @@ __global__ void __launch_bounds__(THREADS, CTAS_SM) k_token_stats(const TokenSta
     __syncthreads();
     // the row's scalars, by lane 0 of warp 0
     auto finish = [&](const Sums &o) {
-        // (quotients: a logit that is the type's lowest value has a finite log probability)
+        // (not in units of log 2: the type's lowest value has a finite log probability)
         const float l2 = log2f(o.s), ls = LN2 * l2;
         const bool none = o.s == 0.0f;  // every logit is -inf
         // (NaN targets make their sum NaN; +inf - +inf too)
-        p.lp[row] = none ? -INFINITY : (xt - o.m) / p.temperature - ls;
-        p.lse[row] = none ? -INFINITY : o.m / p.temperature + ls;
+        p.lp[row] = none ? -INFINITY : (xt - o.m) * inv_t - ls;
+        p.lse[row] = none ? -INFINITY : fmaf(o.m, inv_t, ls);
         p.entropy[row] = none ? 0.0f : LN2 * (l2 - o.w / o.s);
         if (kTop) {
             row_m = o.m;
@@ -488,7 +489,7 @@ __global__ void __launch_bounds__(THREADS, CTAS_SM) k_token_stats(const TokenSta
         const float rm = row_m, ls = row_ls;
         ranked(cand.x, cand.at, n, p.top, [&](int r, float v, int at) {
             ids[r] = at;
-            top_lp[r] = v == -INFINITY && ls == ls ? -INFINITY : (v - rm) / p.temperature - ls;
+            top_lp[r] = v == -INFINITY && ls == ls ? -INFINITY : (v - rm) * inv_t - ls;
         });
     }
     if (csize > 1)
