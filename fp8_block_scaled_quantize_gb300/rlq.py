@@ -761,26 +761,34 @@ def gated_backward(da: torch.Tensor, guq, gus, stream=None):
     return q, s, qT, sc, aT, ac
 
 
+def _current(t):
+    """The current CUDA device's number (no tensor's number where there is none)."""
+    return torch._C._cuda_getDevice() if t.is_cuda else -2
+
+
 def _here(name, t):
     """Refuses a tensor of another device than the current one, on whose streams calls run."""
-    if t.device.index != torch._C._cuda_getDevice():
+    if t.get_device() != _current(t):
         raise ValueError(f"{name} must be on the current CUDA device")
 
 
-def _mx_operand(name, q, s):
-    """(rows, bytes a row, pitch) of packed MXFP4 codes with their scale tiles."""
+def _mx_operand(name, q, s, dev):
+    """(rows, bytes a row, pitch) of packed MXFP4 codes with their scale tiles on device ``dev``."""
+    if q.dim() == 2 and q.dtype is torch.uint8 and s.dtype is torch.uint8 and q.get_device() == dev == s.get_device():
+        R, B = q.shape
+        ld, inner = q.stride()
+        if (inner == 1 or B <= 1) and s.shape == ((R + 127) >> 7, (B + 63) >> 6, 32, 4, 4) and s.is_contiguous():
+            return R, B, ld if R > 1 else max(ld, B)
+    # which of it is not so
     if q.dim() != 2:
         raise ValueError(f"{name}: codes must be a 2-D tensor")
     R, B = q.shape
-    ld = _rows_of(name, q, R, B, torch.uint8)
-    _here(name, q)
+    _rows_of(name, q, R, B, torch.uint8)
     if s.dtype is not torch.uint8:
         raise TypeError(f"{name}: scales must be uint8")
     if s.shape != mxfp4_scales_shape(R, 2 * B) or not s.is_contiguous():
         raise ValueError(f"{name}: scales must be a contiguous {mxfp4_scales_shape(R, 2 * B)} tensor")
-    if s.device != q.device:
-        raise ValueError(f"{name}: scales must be on the codes' device")
-    return R, B, ld
+    raise ValueError(f"{name}: codes and scales must be on the current CUDA device")
 
 
 def mxfp4_scales_shape(rows: int, cols: int):
@@ -802,16 +810,16 @@ def quant_mxfp4(x: torch.Tensor, colwise: bool = False, stream=None):
     ldx = _rows_of("x", x, M, K)
     _here("x", x)
     dev = x.device
-    ldq = (K // 2 + 15) & ~15  # K / 2, but for a K that the call refuses
-    q = torch.empty_strided((M, K // 2), (ldq, 1), dtype=torch.uint8, device=dev)
-    s = torch.empty(mxfp4_scales_shape(M, K), dtype=torch.uint8, device=dev)
-    qT = sT = None
-    ldT = 0
-    if colwise:
-        qT, ldT = _codes_T(K, (M + 1) // 2, dev)
-        sT = torch.empty(mxfp4_scales_shape(K, M), dtype=torch.uint8, device=dev)
-    _call("rlq_quant_mxfp4", x.data_ptr(), M, K, ldx, q.data_ptr(), ldq, s.data_ptr(), _ptr(qT), ldT, _ptr(sT),
-          _stream(stream))
+    # (K / 2 is a multiple of 16, but for a K that the call refuses)
+    q = torch.empty((M, K >> 1), dtype=torch.uint8, device=dev)
+    s = torch.empty(((M + 127) >> 7, (K + 127) >> 7, 32, 4, 4), dtype=torch.uint8, device=dev)
+    if not colwise:
+        _call("rlq_quant_mxfp4", x.data_ptr(), M, K, ldx, q.data_ptr(), K >> 1, s.data_ptr(), None, 0, None, _stream(stream))
+        return q, s, None, None
+    qT, ldT = _codes_T(K, (M + 1) // 2, dev)
+    sT = torch.empty(mxfp4_scales_shape(K, M), dtype=torch.uint8, device=dev)
+    _call("rlq_quant_mxfp4", x.data_ptr(), M, K, ldx, q.data_ptr(), K >> 1, s.data_ptr(), qT.data_ptr(), ldT,
+          sT.data_ptr(), _stream(stream))
     return q, s, qT, sT
 
 
@@ -819,7 +827,7 @@ def dequant_mxfp4(q: torch.Tensor, s: torch.Tensor, cols: int | None = None, str
     """The values (bf16 [rows, cols], exact) of MXFP4 codes and scale tiles.  ``cols`` is needed
     where it is odd; rows are on 16-byte boundaries, so the result is a view of longer rows
     where cols is not a multiple of 8."""
-    R, B, ld = _mx_operand("q", q, s)
+    R, B, ld = _mx_operand("q", q, s, _current(q))
     C = 2 * B if cols is None else int(cols)
     if (C + 1) // 2 != B:
         raise ValueError(f"cols must be {2 * B} or {2 * B - 1}")
@@ -833,24 +841,23 @@ def gemm_mxfp4(xq, xs, wq, ws, out=None, out_dtype: torch.dtype = torch.bfloat16
     """Y [M, N] = X W^T from two MXFP4 operands (codes [M, K/2] and [N, K/2], scale tiles) on
     the FP4 tensor cores, in bf16 or fp32 (``out_dtype``, or that of ``out``).  DGrad takes
     the weight's transposed codes, WGrad those of dY and X."""
-    M, B, ldx = _mx_operand("xq", xq, xs)
-    N, Bw, ldw = _mx_operand("wq", wq, ws)
+    dev = _current(xq)
+    M, B, ldx = _mx_operand("xq", xq, xs, dev)
+    N, Bw, ldw = _mx_operand("wq", wq, ws, dev)
     if B != Bw:
         raise ValueError(f"xq and wq have rows of {B} and {Bw} bytes: the contraction lengths differ")
-    if wq.device != xq.device:
-        raise ValueError("wq must be on xq's device")
     if out is None:
-        if out_dtype not in (torch.bfloat16, torch.float32):
-            raise TypeError("out_dtype must be bfloat16 or float32")
         out = torch.empty((M, N), dtype=out_dtype, device=xq.device)
-        ldy = max(N, 1)
+        ldy = N or 1
     else:
-        if out.dtype not in (torch.bfloat16, torch.float32):
-            raise TypeError("out must be bfloat16 or float32")
-        ldy = _rows_of("out", out, M, N, out.dtype)
+        out_dtype = out.dtype
+        ldy = _rows_of("out", out, M, N, out_dtype)
         _here("out", out)
-    _call("rlq_gemm_mxfp4", xq.data_ptr(), ldx, xs.data_ptr(), wq.data_ptr(), ldw, ws.data_ptr(), out.data_ptr(),
-          DTYPE_BF16 if out.dtype is torch.bfloat16 else DTYPE_F32, ldy, M, N, 2 * B, _stream(stream))
+    dt = DTYPE_BF16 if out_dtype is torch.bfloat16 else DTYPE_F32 if out_dtype is torch.float32 else None
+    if dt is None:
+        raise TypeError("the output must be bfloat16 or float32")
+    _call("rlq_gemm_mxfp4", xq.data_ptr(), ldx, xs.data_ptr(), wq.data_ptr(), ldw, ws.data_ptr(), out.data_ptr(), dt,
+          ldy, M, N, 2 * B, _stream(stream))
     return out
 
 
@@ -889,7 +896,9 @@ def token_logprobs_top(logits: torch.Tensor, targets: torch.Tensor, top: int = 0
     _here("logits", logits)
     top = min(top, V)
     dev = logits.device
-    lp, lse, H = (torch.empty((T,), dtype=torch.float32, device=dev) for _ in range(3))
+    lp = torch.empty((T,), dtype=torch.float32, device=dev)
+    lse = torch.empty((T,), dtype=torch.float32, device=dev)
+    H = torch.empty((T,), dtype=torch.float32, device=dev)
     ids = torch.empty((T, max(top, 0)), dtype=torch.int64, device=dev)
     top_lp = torch.empty((T, max(top, 0)), dtype=torch.float32, device=dev)
     _call("rlq_token_logprobs_top", logits.data_ptr(), dt, ld, T, V, tg, temperature, top, lp.data_ptr(), lse.data_ptr(),
