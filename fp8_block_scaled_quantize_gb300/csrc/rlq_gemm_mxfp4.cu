@@ -679,8 +679,8 @@ rlq_status launch(const CUtensorMap *maps, const Params &p, int grid, int cluste
                        "MXFP4 GEMM launch");
 }
 
-// How a product is cut: CTA pairs with 256 x 256 tiles, or single CTAs with 128 output columns x
-// tile_b tokens, a cluster of `splits` to a tile; `two` of them on an SM.
+// How a product is cut: CTA pairs with tiles of 256 rows of A x tile_b rows of B, or single CTAs with
+// 128 output columns x tile_b tokens, a cluster of `splits` to a tile; `two` of them on an SM.
 struct Plan {
     bool pair, two;
     int tile_b, splits;
@@ -691,19 +691,25 @@ struct Plan {
 // longer, the operands and the output at 6.2 TB/s), and the joining of a shared contraction.  Measured
 // (us): 1 token, 14336 x 4096: 9.3 alone, 9.4 in twos, 13.6 in fours; 1, 4096 x 14336: 20.1, 12.7,
 // 9.5, 9.6 in eights; 256, 4096 x 4096: 8.7 in tiles of 64, 9.5 of 128, 11.3 of 256, 9.6 in
-// pairs; 300, 1024 x 4096: 7.1 in tiles of 128 in fours, 8.9 in pairs; 1001, 5120 x 5120: 17.6 in
-// pairs, 21.4 in tiles of 256.
-Plan make_plan(int64_t M, int64_t N, int64_t K, bool f32, int sms, bool pairs)
+// pairs; 300, 1024 x 4096: 7.1 in tiles of 128 in fours, 8.9 in pairs; 1001, 5120 x 5120: 18.6 in
+// pairs, 17.4 in pairs with tiles of 192, 21.4 alone; 1001, 3584 x 18944: 27.3, 24.8; 8192, 14336 x
+// 4096: 147, 160.
+Plan make_plan(int64_t M, int64_t N, int64_t K, bool f32, int sms, bool pairs, bool staged)
 {
     const int64_t kstages = (K + 255) / 256;
     const double bytes = ((double)(M + N) * (double)K * 17 / 32 + (double)M * (double)N * (f32 ? 4 : 2)) / 6.2e6;
     auto longer = [&](double waves, double per_wave) { return waves * per_wave > bytes ? waves * per_wave : bytes; };
     Plan best = {};
     double least = 1e300;
-    if (pairs) {
-        const int64_t units = ((M + 255) / 256) * ((N + 255) / 256), slots = sms / 2;
-        least = 4.4 + longer((double)((units + slots - 1) / slots), (double)kstages * 0.2775);
-        best = {true, false, 256, 1};
+    for (int tile = 256; pairs && tile >= 128; tile -= 64) {  // (256 first: it wins ties)
+        const int64_t rows = staged ? M : N, cols = staged ? N : M;
+        const int64_t units = ((rows + 255) / 256) * ((cols + tile - 1) / tile), slots = sms / 2;
+        const double cost = 4.4 + longer((double)((units + slots - 1) / slots),
+                                         (double)kstages * (tile == 256 ? 0.35 : tile == 192 ? 0.30 : 0.28));
+        if (cost < least) {
+            least = cost;
+            best = {true, false, tile, 1};
+        }
     }
     for (int tile = 64;; tile *= 2) {
         const int b = M < tile ? (int)M : tile;
@@ -753,9 +759,10 @@ rlq_status launch_gemm_mxfp4(const uint8_t *xq, int64_t ldxq, const uint8_t *xs,
     p.last_steps = (int)((K - (int64_t)(p.kstages - 1) * 256 + 63) / 64);
     p.timeout_ns = wait_limit_ns();
     p.withhold = take_stall();
-    const Plan plan = make_plan(M, N, K, f32, sms, !p.withhold);
+    const bool aligned = ((uintptr_t)y & 15) == 0 && ldy * (f32 ? 4 : 2) % 16 == 0;
+    const Plan plan = make_plan(M, N, K, f32, sms, !p.withhold, aligned);
     const bool pair = plan.pair;
-    p.staged = pair && ((uintptr_t)y & 15) == 0 && ldy * (f32 ? 4 : 2) % 16 == 0;
+    p.staged = pair && aligned;
     struct Operand {
         const uint8_t *q;
         int64_t ld;
@@ -766,7 +773,7 @@ rlq_status launch_gemm_mxfp4(const uint8_t *xq, int64_t ldxq, const uint8_t *xs,
     const Operand &A = p.staged ? x : w, &B = p.staged ? w : x;
     p.a_rows = (int)A.rows;
     p.b_rows = (int)B.rows;
-    p.tile_b = pair ? (B.rows < 256 ? (int)B.rows : 256) : plan.tile_b;
+    p.tile_b = B.rows < plan.tile_b ? (int)B.rows : plan.tile_b;
     p.b_tiles = (int)((B.rows + p.tile_b - 1) / p.tile_b);
     const int64_t a_tiles = (A.rows + (pair ? 2 * BM : BM) - 1) / (pair ? 2 * BM : BM);
     if (a_tiles * p.b_tiles >= (int64_t)1 << 30)
@@ -775,10 +782,10 @@ rlq_status launch_gemm_mxfp4(const uint8_t *xq, int64_t ldxq, const uint8_t *xs,
     p.splits = plan.splits;
     p.kps = (p.kstages + p.splits - 1) / p.splits;
 
-    const int n16 = pair ? 256 : (p.tile_b + 15) / 16 * 16;
+    const int n16 = pair ? (p.tile_b + 31) / 32 * 32 : (p.tile_b + 15) / 16 * 16;
     // scale tiles that a B tile reaches into (one of 192 rows may begin in the middle of one)
-    const int box_b = pair ? 128 : p.tile_b, box_bs = p.tile_b > 128 ? 2 : 1;
-    p.b_bytes = pair ? 128 * BK_BYTES : n16 * BK_BYTES;
+    const int box_b = pair ? n16 / 2 : p.tile_b, box_bs = p.tile_b > 128 ? 2 : 1;
+    p.b_bytes = (pair ? n16 / 2 : n16) * BK_BYTES;
     p.bs_bytes = 1024 * box_bs;
     p.stage_bytes = (A_BYTES + p.b_bytes + AS_BYTES + p.bs_bytes + 1023) / 1024 * 1024;
     p.tx_bytes = A_BYTES + box_b * BK_BYTES + AS_BYTES + p.bs_bytes;

@@ -129,7 +129,8 @@ def test_dequantizer_writes_nothing_beside_its_output():
 SHAPES = [(1, 128, 256), (1, 1, 32), (1, 1000, 4096), (2, 100, 64), (3, 129, 96), (16, 256, 512), (17, 384, 288),
           (64, 3584, 1024), (64, 200, 8192), (100, 129, 1000), (112, 256, 320), (113, 256, 320), (128, 130, 160),
           (129, 512, 352), (200, 257, 1001), (255, 127, 33), (256, 1024, 256), (257, 256, 256), (300, 700, 1),
-          (384, 255, 416), (511, 513, 2048), (513, 1000, 777), (1000, 3000, 64), (2100, 5120, 512), (700, 20000, 288)]
+          (384, 255, 416), (511, 513, 2048), (513, 1000, 777), (1000, 3000, 64), (2100, 5120, 512), (700, 20000, 288),
+          (1001, 3584, 352), (600, 14300, 160), (450, 1024, 2048), (1001, 1024, 2048), (520, 900, 1120), (5000, 130, 96)]
 
 
 @pytest.mark.parametrize("M,N,K", SHAPES)
