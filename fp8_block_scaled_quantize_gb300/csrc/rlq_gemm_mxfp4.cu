@@ -723,7 +723,9 @@ Plan make_plan(int64_t M, int64_t N, int64_t K, bool f32, int sms, bool pairs, b
             const int64_t slots = two ? 2 * sms : sms;
             if (s > 1 && units * s > slots)
                 break;
-            const double cost = 3.6 + 0.0075 * b + longer((double)((units * s + sms - 1) / sms), (double)kps * (0.26 + 0.0003 * b)) +
+            // (waves behind the first one share the memory system with others throughout: 1.35 of its time)
+            const double waves = 1.35 * (double)((units * s + sms - 1) / sms) - 0.35;
+            const double cost = 3.6 + 0.0075 * b + longer(waves, (double)kps * (0.26 + 0.0003 * b)) +
                                 (s > 1 ? 0.6 + 0.008 * b : 0.0);
             if (cost < least) {
                 least = cost;
