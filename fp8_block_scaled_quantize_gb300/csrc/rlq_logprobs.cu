@@ -220,7 +220,15 @@ __device__ __forceinline__ float threshold(const float *thread_max, int lane, in
         lo = min(lo, in ? key[i] : 0xFFFFFFFFu);
         hi = max(hi, key[i]);
     }
-    lo = (int)blockDim.x < k ? 0u : __reduce_min_sync(0xFFFFFFFFu, lo);
+    // (fewer than k maxima above -inf, as where a mask leaves little: T is -inf)
+    constexpr uint32_t NONE = 0x007FFFFFu;
+    int finite = 0;
+#pragma unroll
+    for (int i = 0; i < WARPS; ++i)
+        finite += key[i] > NONE;
+    if ((int)__reduce_add_sync(0xFFFFFFFFu, finite) < k)
+        return -INFINITY;
+    lo = max(__reduce_min_sync(0xFFFFFFFFu, lo), NONE + 1);
     hi = __reduce_max_sync(0xFFFFFFFFu, hi);
     while (lo < hi) {
         const uint32_t mid = lo + (hi - lo + 1) / 2;
@@ -439,8 +447,10 @@ __global__ void __launch_bounds__(THREADS, CTAS_SM) k_token_stats(const TokenSta
         if (k > 0)
             find_top(part_of, cand, m, others, at_batch, k, nw > 1 ? 1 : 0);
         if (csize > 1) {
-            if (t < MAX_TOP)
+            if (t < MAX_TOP) {
+                own.x[t] = -INFINITY;
                 own.at[t] = -1;
+            }
             __syncthreads();
             ranked(cand.x, cand.at, min(cand.n, LIST), k, [&](int r, float v, int at) {
                 own.x[r] = v;
@@ -466,11 +476,17 @@ __global__ void __launch_bounds__(THREADS, CTAS_SM) k_token_stats(const TokenSta
             }
             if (kTop) {  // the parts' lists, one behind the other
                 __syncthreads();
+                // (of which ceil(top / csize) each reach the least of those lists' elements: the rest is left out)
+                const int mth = (p.top - 1) / csize;
+                float least = lane < csize ? ld_cluster1(&own.x[mth], lane) : INFINITY;
+#pragma unroll
+                for (int o = 16; o; o >>= 1)
+                    least = fminf(least, __shfl_xor_sync(0xFFFFFFFFu, least, o));
                 for (int i = t; i < csize * p.top; i += threads) {
                     const int r = i / p.top, j = i - r * p.top;
                     const float v = ld_cluster1(&own.x[j], r);
                     const int at = __float_as_int(ld_cluster1(reinterpret_cast<const float *>(&own.at[j]), r));
-                    if (at >= 0)
+                    if (at >= 0 && v >= least)
                         put(cand, v, at);
                 }
                 __syncthreads();
