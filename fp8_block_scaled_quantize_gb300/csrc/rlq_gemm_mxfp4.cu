@@ -686,26 +686,32 @@ struct Plan {
     int tile_b, splits;
 };
 
-// The cheapest by a model of a launch's microseconds, fitted to single waves of it: a start and an
-// end that grow with the tile, per wave the stages one after the other (or, if that is
-// longer, the operands and the output at 6.2 TB/s), and the joining of a shared contraction.  Measured
-// (us): 1 token, 14336 x 4096: 9.3 alone, 9.4 in twos, 13.6 in fours; 1, 4096 x 14336: 20.1, 12.7,
+// The cheapest by a model of a launch's microseconds, fitted to measurements: a start and an
+// end that grow with the tile, per wave the stages one after the other (or, if that is longer, the
+// operands and the outputs at the rates that they reach), and the joining of a shared contraction.
+// Measured (us): 1 token, 14336 x 4096: 9.3 alone, 9.4 in twos, 13.6 in fours; 1, 4096 x 14336: 20.1, 12.7,
 // 9.5, 9.6 in eights; 256, 4096 x 4096: 8.7 in tiles of 64, 9.5 of 128, 11.3 of 256, 9.6 in
 // pairs; 300, 1024 x 4096: 7.1 in tiles of 128 in fours, 8.9 in pairs; 1001, 5120 x 5120: 18.6 in
 // pairs, 17.4 in pairs with tiles of 192, 21.4 alone; 1001, 3584 x 18944: 27.3, 24.8; 8192, 14336 x
-// 4096: 147, 160.
+// 4096: 147, 160; 8192, 8192 x 256: 22.6 in pairs, 43.8 alone (outputs not staged).
 Plan make_plan(int64_t M, int64_t N, int64_t K, bool f32, int sms, bool pairs, bool staged)
 {
     const int64_t kstages = (K + 255) / 256;
-    const double bytes = ((double)(M + N) * (double)K * 17 / 32 + (double)M * (double)N * (f32 ? 4 : 2)) / 6.2e6;
-    auto longer = [&](double waves, double per_wave) { return waves * per_wave > bytes ? waves * per_wave : bytes; };
+    const double operands = (double)(M + N) * (double)K * 17 / 32 / 6.2e6, out = (double)M * (double)N * (f32 ? 4 : 2);
+    auto longer = [&](double waves, double per_wave, double out_rate) {
+        const double moved = operands + out / out_rate;
+        return waves * per_wave > moved ? waves * per_wave : moved;
+    };
+    const double direct = f32 ? 4.5e6 : 2.9e6;  // bytes a microsecond of outputs stored by the lanes
     Plan best = {};
     double least = 1e300;
-    for (int tile = 256; pairs && tile >= 128; tile -= 64) {  // (256 first: it wins ties)
+    // (a pair's ring is too short for few tokens: 1, 38912 x 1600: 9.4 alone, 14.1)
+    for (int tile = 256; pairs && M > 128 && tile >= 128; tile -= 64) {
         const int64_t rows = staged ? M : N, cols = staged ? N : M;
         const int64_t units = ((rows + 255) / 256) * ((cols + tile - 1) / tile), slots = sms / 2;
         const double cost = 4.4 + longer((double)((units + slots - 1) / slots),
-                                         (double)kstages * (tile == 256 ? 0.35 : tile == 192 ? 0.30 : 0.28));
+                                         (double)kstages * (tile == 256 ? 0.35 : tile == 192 ? 0.30 : 0.28),
+                                         !staged ? direct : tile == 256 ? 5.8e6 : 5.0e6);
         if (cost < least) {
             least = cost;
             best = {true, false, tile, 1};
@@ -725,7 +731,7 @@ Plan make_plan(int64_t M, int64_t N, int64_t K, bool f32, int sms, bool pairs, b
                 break;
             // (waves behind the first one share the memory system with others throughout: 1.35 of its time)
             const double waves = 1.35 * (double)((units * s + sms - 1) / sms) - 0.35;
-            const double cost = 3.6 + 0.0075 * b + longer(waves, (double)kps * (0.26 + 0.0003 * b)) +
+            const double cost = 3.6 + 0.0075 * b + longer(waves, (double)kps * (0.26 + 0.0003 * b), direct) +
                                 (s > 1 ? 0.6 + 0.008 * b : 0.0);
             if (cost < least) {
                 least = cost;

@@ -133,11 +133,25 @@ SHAPES = [(1, 128, 256), (1, 1, 32), (1, 1000, 4096), (2, 100, 64), (3, 129, 96)
           (1001, 3584, 352), (600, 14300, 160), (450, 1024, 2048), (1001, 1024, 2048), (520, 900, 1120), (5000, 130, 96)]
 
 
-@pytest.mark.parametrize("M,N,K", SHAPES)
+# One shape for every way in which a product is cut: pairs with tiles of 128, 192 and 256, their
+# outputs by TMA or by the lanes, one tile a pair or several; single CTAs with tiles of up to 64,
+# 128 and 256 tokens, one tile each or several, alone or in clusters of 2, 4 and 8, one or two an SM.
+CUTS = [(270, 10029, 1034), (5117, 130, 266), (129, 6636, 849), (6970, 568, 779), (5192, 136, 36), (134, 7144, 282),
+        (263, 10138, 808), (129, 19471, 1328), (6007, 129, 258), (130, 7085, 520), (273, 10544, 258), (143, 19704, 836),
+        (5738, 136, 36), (136, 7984, 286), (271, 11771, 281), (129, 21211, 263), (6132, 133, 269), (132, 6473, 257),
+        (281, 10768, 38), (130, 22960, 35), (1377, 712, 33), (196, 5448, 35), (115, 19509, 567), (119, 10181, 524),
+        (122, 4949, 3936), (4872, 1, 4353), (115, 2537, 2810), (2464, 1, 3664), (132, 1555, 3682), (1248, 1, 7334),
+        (601, 12877, 2816), (226, 10333, 10550), (6643, 523, 1801), (225, 5604, 7753), (4923, 129, 9780),
+        (226, 2709, 6165), (4930, 1, 12051), (229, 1340, 12052), (1238, 133, 15595), (1, 39803, 35), (65, 23684, 33),
+        (1, 9981, 3124), (4947, 1, 3169), (67, 1, 33), (1, 5022, 6214), (1, 1, 1281), (4737, 1, 6527), (67, 1, 2079),
+        (1, 1, 12291), (1, 1, 1565), (68, 1, 12354), (68, 1, 1537), (1, 1, 3586), (67, 1, 3627)]
+
+
+@pytest.mark.parametrize("M,N,K", SHAPES + CUTS)
 def test_product_exact_sums(M, N, K):
-    """Scales within 2^-1 .. 2^1: every product is a multiple of 2^-4 and at most 144, sums up to
-    8192 x 144 stay below 2^24 of those units for the typical signs, so fp32 holds each one
-    exactly in whatever order, and the result is the exact sum."""
+    """Scales within 2^-1 .. 2^1: every product is a multiple of 2^-4 and at most 144, and
+    where the magnitudes' sum stays below 2^24 of those units, as it is checked to, fp32 holds
+    every partial sum exactly in whatever order: the result is the exact sum."""
     g = gen(M + 7 * N + K)
     xq, xs, x = R.operand(g, M, K, -1, 1)
     wq, ws, w = R.operand(g, N, K, -1, 1)
