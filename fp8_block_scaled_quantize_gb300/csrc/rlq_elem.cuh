@@ -41,6 +41,47 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float2 v)
     return d;
 }
 
+__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel)
+{
+    uint32_t d;
+    asm("prmt.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(sel));
+    return d;
+}
+
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b)
+{
+    uint32_t d;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
+// Eight E2M1 codes (one 32-bit word, element 0 in the lowest nibble) times one
+// bf16 scale (in both halves of s2): four bf16x2 words, element 0 lowest.
+// Magnitude bytes of 0, 0.5, 1, 1.5, 2, 3, 4, 6 in bf16: high bytes 00 3F 3F 3F 40
+// 40 40 40, low bytes 00 00 80 C0 00 40 80 C0.  Signs: element 2k's sign is bit 7
+// of byte k of (w << 4), element 2k+1's bit 7 of byte k of w; a prmt selector with
+// bit 3 set replicates the selected byte's bit 7, so one prmt gives the sign bytes
+// of four elements, which are merged into their high bytes before the interleave.
+__device__ __forceinline__ uint4 e2m1x8_to_bf16(uint32_t w, uint32_t s2)
+{
+    constexpr uint32_t HI0 = 0x3F3F3F00u, HI1 = 0x40404040u;
+    constexpr uint32_t LO0 = 0xC0800000u, LO1 = 0xC0804000u;
+    const uint32_t m = w & 0x77777777u;  // magnitudes: prmt selectors in plain (not sign) mode
+    const uint32_t m2 = m >> 16;
+    const uint32_t we = w << 4;
+    const uint32_t s03 = prmt(we, w, 0xD9C8u);  // signs of elements 0, 1, 2, 3 as 00 / FF bytes
+    const uint32_t s47 = prmt(we, w, 0xFBEAu);  // elements 4 .. 7
+    const uint32_t h03 = prmt(HI0, HI1, m) | (s03 & 0x80808080u);
+    const uint32_t h47 = prmt(HI0, HI1, m2) | (s47 & 0x80808080u);
+    const uint32_t l03 = prmt(LO0, LO1, m), l47 = prmt(LO0, LO1, m2);
+    uint4 out;
+    out.x = mul_bf16x2(prmt(l03, h03, 0x5140u), s2);  // elements 0, 1
+    out.y = mul_bf16x2(prmt(l03, h03, 0x7362u), s2);  // elements 2, 3
+    out.z = mul_bf16x2(prmt(l47, h47, 0x5140u), s2);
+    out.w = mul_bf16x2(prmt(l47, h47, 0x7362u), s2);
+    return out;
+}
+
 // Two E4M3 codes, RN-even with saturation to +-448: `lo` in bits 0..7.
 __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi)
 {

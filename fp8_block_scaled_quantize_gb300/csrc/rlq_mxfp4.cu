@@ -54,10 +54,11 @@ __device__ __forceinline__ uint32_t scale_byte(uint32_t amax)
 // 2^-e of a scale byte (255: any value, the scale itself is the NaN).
 __device__ __forceinline__ float rcp_of(uint32_t s) { return __uint_as_float((254u - min(s, 253u)) << 23); }
 
-// 2^e of a scale byte, a NaN for 255.
-__device__ __forceinline__ float value_of(uint32_t s)
+// 2^e of a scale byte in bf16, twice; NaNs for 255.
+__device__ __forceinline__ uint32_t value2_of(uint32_t s)
 {
-    return __uint_as_float(s == 255u ? 0x7FC00000u : s == 0u ? 0x00400000u : s << 23);
+    const uint32_t b = s == 255u ? 0x7FC0u : s == 0u ? 0x0040u : s << 7;
+    return b | (b << 16);
 }
 
 // E2M1 codes of eight values, the first in the lowest four bits: RN-even, saturating at
@@ -101,50 +102,89 @@ __device__ __forceinline__ uint32_t row_scales(uint32_t s, int lane)
     return w | __shfl_xor_sync(0xFFFFFFFFu, w, 8);
 }
 
-// Rows: a warp takes the four rows of a row tile that share 16 scale bytes, U column
-// tiles of them, half a warp to a row: 16 bytes a lane and load, 2 U loads in flight.
+// What a warp of the rows' kernels works on: the four rows of a row tile that share 16 scale
+// bytes, U column tiles of them, half a warp to a row: 16 bytes of values a lane and tile.
+struct RowItem {
+    int64_t row, rt, ct0, ctiles;  // this lane's first row (the other: row + 64), the tiles
+    int r, l, half;
+    int left;     // columns from this lane's first one, at most those of the U tiles
+    bool in[2];   // the rows exist
+    bool whole;   // nothing of the warp's is cut
+};
+
 template <int U>
-__global__ void __launch_bounds__(THREADS)
-    k_mx_rows(const uint16_t *__restrict__ x, int64_t M, int64_t K, int64_t ldx, uint8_t *__restrict__ q, int64_t ldq,
-              uint8_t *__restrict__ s, int rv, int64_t items)
+__device__ __forceinline__ RowItem row_item(uint32_t id, int64_t M, int64_t K, uint32_t rv)
 {
-    pdl_begin();
-    const int lane = threadIdx.x & 31, half = lane >> 4, l = lane & 15;
-    const int64_t id = (int64_t)blockIdx.x * WARPS + (threadIdx.x >> 5);
-    if (id >= items)
-        return;
-    const int64_t ctiles = (K + 127) / 128, chunks = (ctiles + U - 1) / U;
+    RowItem it;
+    const int lane = threadIdx.x & 31;
+    it.half = lane >> 4;
+    it.l = lane & 15;
+    it.ctiles = (K + 127) / 128;
+    const uint32_t chunks = (uint32_t)(it.ctiles + U - 1) / U;
     // (neighbouring warps: neighbouring rows, whose scale pieces are neighbours too)
-    const int64_t rest = id / rv, rt = rest / chunks, ct0 = (rest - rt * chunks) * U;
-    const int r = (int)(id - rest * rv);
-    const int64_t row0 = rt * 128 + r + 32 * half;
+    const uint32_t rest = id / rv, rt = rest / chunks;
+    it.r = (int)(id - rest * rv);
+    it.rt = rt;
+    it.ct0 = (int64_t)(rest - rt * chunks) * U;
+    it.row = it.rt * 128 + it.r + 32 * it.half;
+    it.in[0] = it.row < M;
+    it.in[1] = it.row + 64 < M;
+    it.left = (int)min(K - it.ct0 * 128, (int64_t)(U * 128)) - it.l * 8;
+    it.whole = __all_sync(0xFFFFFFFFu, it.in[1] && it.left + it.l * 8 == U * 128);
+    return it;
+}
+
+template <int U, bool kEdge>
+__device__ __forceinline__ void quantize_rows(const RowItem &it, const uint16_t *__restrict__ x, int64_t ldx,
+                                              uint8_t *__restrict__ q, int64_t ldq, uint8_t *__restrict__ s)
+{
+    const uint16_t *const first = x;
+    x += it.row * ldx + it.ct0 * 128 + it.l * 8;
+    q += it.row * ldq + it.ct0 * 64 + it.l * 4;
+    s += (it.rt * it.ctiles + it.ct0) * 512 + it.r * 16 + it.half * 4;
     uint4 v[U][2];
+    // (what is cut reads the matrix's first values, so that all loads are in flight together)
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+            v[u][j] = ld_stream(!kEdge || (it.in[j] && 128 * u < it.left) ? x + 64 * j * ldx + 128 * u : first);
+    if (kEdge) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                if (!(it.in[j] && 128 * u < it.left))
+                    v[u][j] = make_uint4(0, 0, 0, 0);
+    }
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            const int64_t row = row0 + 64 * j, col = (ct0 + u) * 128 + l * 8;
-            v[u][j] = row < M && col < K ? ld_stream(x + row * ldx + col) : make_uint4(0, 0, 0, 0);
-        }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-        const int64_t ct = ct0 + u;
-        if (ct >= ctiles)
-            break;
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
             uint32_t sb;
             const uint32_t codes = row_codes(v[u][j], &sb);
-            const uint32_t sw = row_scales(sb, lane);
-            const int64_t row = row0 + 64 * j, col = ct * 128 + l * 8;
-            if (row < M) {
-                if (col < K)
-                    *reinterpret_cast<uint32_t *>(q + row * ldq + col / 2) = codes;
-                if (l == 0)
-                    *reinterpret_cast<uint32_t *>(s + (rt * ctiles + ct) * 512 + r * 16 + (half + 2 * j) * 4) = sw;
-            }
+            const uint32_t sw = row_scales(sb, threadIdx.x & 31);
+            if (!kEdge || (it.in[j] && 128 * u < it.left))
+                *reinterpret_cast<uint32_t *>(q + 64 * j * ldq + 64 * u) = codes;
+            if (it.l == 0 && (!kEdge || (it.in[j] && it.ct0 + u < it.ctiles)))
+                *reinterpret_cast<uint32_t *>(s + 512 * u + 8 * j) = sw;
         }
-    }
+}
+
+template <int U>
+__global__ void __launch_bounds__(THREADS)
+    k_mx_rows(const uint16_t *__restrict__ x, int64_t M, int64_t K, int64_t ldx, uint8_t *__restrict__ q, int64_t ldq,
+              uint8_t *__restrict__ s, uint32_t rv, uint32_t items)
+{
+    pdl_begin();
+    const uint32_t id = blockIdx.x * WARPS + (threadIdx.x >> 5);
+    if (id >= items)
+        return;
+    const RowItem it = row_item<U>(id, M, K, rv);
+    if (it.whole)
+        quantize_rows<U, false>(it, x, ldx, q, ldq, s);
+    else
+        quantize_rows<U, true>(it, x, ldx, q, ldq, s);
 }
 
 // Rows and columns from one read: a CTA takes a 128 x 128 tile, quantizes its rows as
@@ -259,70 +299,58 @@ __device__ __forceinline__ uint32_t load_cut(const uint8_t *p, int n)
     return w;
 }
 
-// Values of packed codes: the rows' kernel the other way round.  Every value is exact in bf16.
-template <int U>
-__global__ void __launch_bounds__(THREADS)
-    k_mx_values(const uint8_t *__restrict__ q, int64_t ldq, const uint8_t *__restrict__ s, int64_t M, int64_t K,
-                uint16_t *__restrict__ x, int64_t ldx, int rv, int64_t items)
+// Values of packed codes: the rows' kernel the other way round.  Every value is exact in bf16, and
+// so is the product of a code's magnitude and its power of two there.
+template <int U, bool kEdge>
+__device__ __forceinline__ void row_values(const RowItem &it, const uint8_t *__restrict__ q, int64_t ldq,
+                                           const uint8_t *__restrict__ s, uint16_t *__restrict__ x, int64_t ldx)
 {
-    pdl_begin();
-    const int lane = threadIdx.x & 31, half = lane >> 4, l = lane & 15;
-    const int64_t id = (int64_t)blockIdx.x * WARPS + (threadIdx.x >> 5);
-    if (id >= items)
-        return;
-    const int64_t ctiles = (K + 127) / 128, chunks = (ctiles + U - 1) / U;
-    const int64_t rest = id / rv, rt = rest / chunks, ct0 = (rest - rt * chunks) * U;
-    const int r = (int)(id - rest * rv);
-    const int64_t row0 = rt * 128 + r + 32 * half;
-    uint32_t v[U][2];
-    uint32_t sb[U][2];
+    x += it.row * ldx + it.ct0 * 128 + it.l * 8;
+    q += it.row * ldq + it.ct0 * 64 + it.l * 4;
+    s += (it.rt * it.ctiles + it.ct0) * 512 + it.r * 16 + it.half * 4 + (it.l >> 2);
+    uint32_t v[U][2], sb[U][2];
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            const int64_t row = row0 + 64 * j, ct = ct0 + u, col = ct * 128 + l * 8;
-            const bool in = row < M && col < K;
-            v[u][j] = !in ? 0u
-                      : col + 8 <= K ? __ldg(reinterpret_cast<const uint32_t *>(q + row * ldq + col / 2))
-                                     : load_cut(q + row * ldq + col / 2, (int)(K - col + 1) / 2);
-            sb[u][j] = in ? __ldg(s + (rt * ctiles + ct) * 512 + r * 16 + (half + 2 * j) * 4 + (l >> 2)) : 0u;
+            const int n = it.left - 128 * u;
+            const uint8_t *p = q + 64 * j * ldq + 64 * u;
+            const bool in = !kEdge || (it.in[j] && n > 0);
+            v[u][j] = !in ? 0u : !kEdge || n >= 8 ? __ldg(reinterpret_cast<const uint32_t *>(p)) : load_cut(p, (n + 1) / 2);
+            sb[u][j] = in ? __ldg(s + 512 * u + 8 * j) : 0u;
         }
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            const int64_t row = row0 + 64 * j, col = (ct0 + u) * 128 + l * 8;
-            if (row >= M || col >= K)
-                continue;
-            uint32_t h[4];
-            asm("{\n\t.reg .b8 a, b, c, d;\n\t"
-                "mov.b32 {a, b, c, d}, %4;\n\t"
-                "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
-                "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
-                "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
-                "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
-                : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
-                : "r"(v[u][j]));
-            const float sc = value_of(sb[u][j]);
-            uint32_t o[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                float lo, hi;
-                asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
-                    : "=f"(lo), "=f"(hi)
-                    : "r"(h[i]));
-                o[i] = pack_bf16x2(__fmul2_rn(make_float2(lo, hi), make_float2(sc, sc)));
-            }
-            uint16_t *p = x + row * ldx + col;
-            if (col + 8 <= K)
-                *reinterpret_cast<uint4 *>(p) = make_uint4(o[0], o[1], o[2], o[3]);
-            else
-                store_head(reinterpret_cast<uint8_t *>(p), make_uint4(o[0], o[1], o[2], o[3]), (int)(K - col) * 2);
+            const int n = it.left - 128 * u;
+            const uint4 o = e2m1x8_to_bf16(v[u][j], value2_of(sb[u][j]));
+            uint16_t *p = x + 64 * j * ldx + 128 * u;
+            if (!kEdge || (it.in[j] && n >= 8))
+                *reinterpret_cast<uint4 *>(p) = o;
+            else if (it.in[j] && n > 0)
+                store_head(reinterpret_cast<uint8_t *>(p), o, n * 2);
         }
 }
 
+template <int U>
+__global__ void __launch_bounds__(THREADS)
+    k_mx_values(const uint8_t *__restrict__ q, int64_t ldq, const uint8_t *__restrict__ s, int64_t M, int64_t K,
+                uint16_t *__restrict__ x, int64_t ldx, uint32_t rv, uint32_t items)
+{
+    pdl_begin();
+    const uint32_t id = blockIdx.x * WARPS + (threadIdx.x >> 5);
+    if (id >= items)
+        return;
+    const RowItem it = row_item<U>(id, M, K, rv);
+    if (it.whole)
+        row_values<U, false>(it, q, ldq, s, x, ldx);
+    else
+        row_values<U, true>(it, q, ldq, s, x, ldx);
+}
+
 // Warps of a rows' kernel with U column tiles a warp: row tiles x chunks x the rows of a
-// row tile's first 32 that exist.
+// row tile's first 32 that exist.  (Below 2^32 for every matrix below 2^41 values.)
 int64_t row_items(int64_t M, int64_t K, int U, int *rv)
 {
     const int64_t ctiles = (K + 127) / 128;
@@ -339,8 +367,8 @@ cudaError_t launch_quant_mxfp4(const uint16_t *x, int64_t M, int64_t K, int64_t 
         const BothArgs p = {x, M, K, ldx, q, ldq, s, qT, ldqT, sT, (int)((K + 127) / 128), (int)((M + 127) / 128)};
         return launch_pdl(k_mx_both, dim3((unsigned)((int64_t)p.ctiles * p.rtiles)), dim3(THREADS), 0, st, p);
     }
-    // Four column tiles a warp where they make a full wave of warps, else two (8192 x 14336: 50.3
-    // and 52.3 us; 333 x 18944: 6.1 and 5.1).
+    // Four column tiles a warp where they make a full wave of warps, else two (8192 x 14336: 48.2
+    // and 51.6 us; 333 x 18944: 6.1 and 4.6).
     int rv;
     int64_t items = row_items(M, K, 4, &rv);
     const bool four = items >= (int64_t)64 * device_sms();

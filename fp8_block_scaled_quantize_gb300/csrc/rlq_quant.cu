@@ -574,13 +574,6 @@ __device__ __forceinline__ uint2 ld_stream8(const uint16_t *p)
     return v;
 }
 
-__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel)
-{
-    uint32_t d;
-    asm("prmt.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(sel));
-    return d;
-}
-
 // Four rows of four bytes (r[i] = row i, column c in byte c) to four columns
 // (c[k] = column k, row i in byte i).
 __device__ __forceinline__ void transpose4x4(const uint32_t (&r)[4], uint32_t (&c)[4])
