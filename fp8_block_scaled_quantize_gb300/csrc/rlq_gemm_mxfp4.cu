@@ -6,23 +6,31 @@
 // scales (two per row and instruction of K = 64) before it adds in fp32: a product of two
 // 4-bit values and two powers of two is exact, so only the additions round.
 //
-// Orientation: the weights are the MMA's A (128 rows, the TMEM lanes), the tokens its B (up to 256
-// TMEM columns).  A few tokens are then a narrow MMA that leaves nothing idle but the token
-// columns, and lane n of a warp holds output column n of every token: a store of 32 lanes is
-// 32 neighbouring outputs without any staging.
-//
-// Roles (192 threads): warp 0 (one thread) copies ahead by TMA, per stage of 256 contraction
-// elements (128 bytes a row) both operands' codes (128-byte swizzle) and their scale tiles as
-// they lie in memory; warp 1 (one thread) copies the stage's scales to tensor memory
-// (tcgen05.cp, 512 bytes per 128 rows and 128 elements; tcgen05.cp and tcgen05.mma of one
-// thread run in order) and issues four MMAs; warps 2-5 read the finished sums and store them.
-//   * Pairs (kPair): two CTAs, 256 weight rows x up to 256 tokens (cta_group::2), persistent.
-//     Both accumulators (256 columns each) and the scales do not fit the 512 columns, so
-//     the second accumulator begins 32 columns before the first one's end; the epilogue
-//     reads those columns first, and the next tile's MMAs start behind that.
-//   * Single CTAs: 128 weight rows; where there are too few tiles for the SMs, a cluster of
-//     up to 8 CTAs shares a tile's contraction, its CTAs leave their parts in shared memory
-//     and each adds its share of the tokens, parts in rank order.
+// Roles (320 threads): warp 0 copies ahead by TMA, per stage of 256 contraction elements (128
+// bytes a row) both operands' codes (128-byte swizzle) and their scale tiles as they lie in
+// memory; warp 1 copies the stage's scales to tensor memory (tcgen05.cp, 512 bytes per 128 rows
+// and 128 elements; tcgen05.cp and tcgen05.mma of one thread run in order) and issues four MMAs;
+// warps 2-9, two groups of four, read the finished sums and store them.  Warps 0 and 1 stay
+// converged and elect the lane that issues: from a thread of its own every copy and MMA
+// took its operands to uniform registers first, and 8192 x 14336 x 4096 247 us instead of 143.
+//   * Pairs (kPair): two CTAs, 256 rows of A x up to 256 of B (cta_group::2), persistent.  The tokens
+//     are A, so a lane holds neighbouring outputs of one token, which go to a swizzled box of
+//     its warp's in shared memory by 16-byte stores and leave by TMA (the lanes of a column
+//     apart, and swapped pairs, had 18944 x 3584 x 1001 take 88 and 44 us; it takes 35).  Where y's rows
+//     are not on 16-byte boundaries, the weights are A, and a lane stores its column of y.
+//     Two accumulators of 256 columns and the scales do not fit the 512 columns of tensor
+//     memory, so the second one begins 32 columns before the first one's end; the epilogue reads
+//     those columns first, and the next tile's MMAs start behind that.
+//   * Single CTAs: 128 weight rows as A, the tokens as B: a few tokens are a narrow MMA, and a
+//     store of 32 lanes is 32 neighbouring outputs of a token.  Where there are too few tiles for the
+//     SMs, a cluster of up to 8 CTAs shares a tile's contraction; each CTA sends its part, 16 bytes
+//     at a time, to the CTA that adds those tokens, parts in rank order (read from the
+//     others' memory instead, 256 x 4096 x 4096 took 16.2 us for 11.8).
+// Bound by: few tokens, the weights' bytes (64 tokens, 128256 x 4096, fp32 out: 52 us, 0.89 of HBM; one
+// token, 14336 x 4096: 9.5 us, 0.49: start, first loads and end are half of it); many tokens,
+// shared memory, which the copies fill with 35 KB a stage while the MMAs read both operands from
+// it (8192 x 14336 x 4096: 145 us, 6.6 PFLOP/s, 0.86 of four times the bf16 rate; without
+// the copies 132, with a quarter of the MMAs 120); short contractions, the outputs.
 // Every wait is bounded as in the FP8 GEMM; what ran out is reported by rlq_check.
 #include <cuda.h>
 #include <cudaTypedefs.h>

@@ -17,8 +17,15 @@
 // overflows (thousands of equal logits) is replaced by a search for the k-th logit over the
 // whole row.
 //
+// Measured: 2048 x 128256 bf16 with 20 alternatives 102 us (0.76 of HBM; without them 88, a row's
+// end and the batches read again, some of which L2 no longer has, are the rest), 1000 x
+// 128256 fp32 88 (0.86), 64 x 151936 bf16 12.8, 1 x 128256 7.6 (3.4 without alternatives: a
+// chain of barriers and loads).  Reading all units of a chosen thread again took 133 and 125 us
+// for the first two.  512 threads a CTA: 113 us; a bound on the maxima of 2 k + 8 threads: 104.
+//
 // Backward, bound by memory (read once, written once): lse and H come from the forward pass, so a
-// unit's gradient needs nothing but the unit and the row's factors.
+// unit's gradient needs nothing but the unit and the row's factors.  4096 x 128256 bf16, 15% of
+// the rows empty and not read: 281 us (1.02 of the copy rate); 600 x 32001 fp32 25 (0.90).
 #include <cuda_runtime.h>
 
 #include "rlq_internal.h"
