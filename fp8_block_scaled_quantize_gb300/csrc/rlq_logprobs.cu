@@ -551,16 +551,15 @@ cudaError_t launch_stats(const TokenStatsArgs &p, cudaStream_t st)
 constexpr int BWD_BATCH = 4, BWD_ROUNDS = 2;  // loads in flight a thread, and batches of them
 
 // A CTA takes BWD_ROUNDS x BWD_BATCH units a thread of one row.  In units of log 2, log2 p =
-// x c - L with c = log2(e) / temperature, L = lse log2(e).  fp32 logits keep both as a sum of
-// two floats: one would put an error of 2^-24 |x c| into the exponent, some 10^-6 of a likely
-// token's probability, which bf16 gradients do not show.
+// x c - L with c = log2(e) / temperature, L = lse log2(e), each a sum of two floats: one would
+// put an error of 2^-24 |x c| into the exponent, some 10^-6 of a likely token's probability, and
+// powers of two where a mask of -10^9 leaves a row nothing else.
 template <typename T>
 __global__ void __launch_bounds__(THREADS) k_token_grad(const TokenGradArgs p, int parts)
 {
     pdl_begin();
     using E = Elem<T>;
     constexpr int N = E::N;
-    constexpr bool kFine = sizeof(T) == 4;
     const int64_t row = blockIdx.x / parts;
     const int partno = (int)(blockIdx.x - row * parts), V = (int)p.V, t = threadIdx.x, threads = blockDim.x;
     const T *x = reinterpret_cast<const T *>(p.logits) + row * p.ld;
@@ -612,9 +611,7 @@ __global__ void __launch_bounds__(THREADS) k_token_grad(const TokenGradArgs p, i
 #pragma unroll
             for (int j = 0; j < N / 2; ++j) {
                 const float2 e = E::get2(v[i], j);
-                float2 z = __ffma2_rn(e, c2, nL2);
-                if (kFine)
-                    z = __fadd2_rn(z, __ffma2_rn(e, cl2, nLl2));
+                float2 z = __fadd2_rn(__ffma2_rn(e, c2, nL2), __ffma2_rn(e, cl2, nLl2));
                 // (logits of -inf: 2^LOWEST is 0)
                 z = make_float2(fmaxf(z.x, LOWEST), fmaxf(z.y, LOWEST));
                 f[j] = __fmul2_rn(make_float2(ex2(z.x), ex2(z.y)), __ffma2_rn(b2, z, a2));

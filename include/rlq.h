@@ -13,7 +13,8 @@
  *     关键设计 §1).
  * Around the layer: the residual norm with its gradient, the gated feed-forward
  * block with its gradient from 8-bit checkpoints, token log probabilities and the
- * clipped policy loss.
+ * clipped policy loss.  And the rollout in 4 bits: microscaled (MXFP4) layers, log
+ * probabilities with entropy and the most likely alternatives, and their gradients.
  *
  * Conventions for every call
  *   - Every tensor pointer is a DEVICE pointer owned by the caller.  The library
@@ -685,7 +686,8 @@ rlq_status rlq_token_logprobs(const void *logits, rlq_dtype dtype, int64_t ld, i
  * A target outside [0, V) makes the row empty: its logits are not read, lp, lse, entropy and
  * top_lp are 0 and top_ids -1.  Logits of -inf have probability 0 and add nothing to the
  * entropy; as alternatives they come last, with top_lp -inf.  A row of nothing else has lp =
- * lse = -inf and entropy 0.  A NaN or +inf among the logits makes lp, lse and entropy NaN.
+ * lse = -inf and entropy 0.  A NaN or +inf among the logits makes lp, lse, entropy and top_lp
+ * NaN; its alternatives are those of the logits that are no NaN, -1 where there are fewer.
  * Other arguments and limits as for rlq_token_logprobs.
  */
 rlq_status rlq_token_logprobs_top(const void *logits, rlq_dtype dtype, int64_t ld, int64_t rows, int64_t V,
@@ -703,6 +705,8 @@ rlq_status rlq_token_logprobs_top(const void *logits, rlq_dtype dtype, int64_t l
  *   dlp, dentropy f32 [rows]; one of them may be NULL (zeros)
  *   dlogits       [rows, V] of `dtype`, pitch ldd >= V (output); may be logits itself (in
  *                 place, same pitch)
+ * p_v is that of the lse given: an lse far from 0 carries its own rounding into every
+ * probability of the row (|lse| 100: 4e-6 of it; 10^4: 5e-4).
  * A row whose target is outside [0, V), or whose derivatives are both 0, is empty: its logits
  * are not read and its gradient is zeros.  So is that of a row of -inf logits only (lse =
  * -inf).  A row whose lse is NaN has a gradient of NaN.  Other arguments and limits as for
@@ -779,7 +783,8 @@ rlq_status rlq_diag_bounded_wait(int64_t timeout_us, rlq_stream_t stream);
 /*
  * Diagnostic for the block-scaled GEMM's own abort path: arms, for the calling
  * host thread, a one-shot fault in the next GEMM call it makes (any of the
- * FProp / DGrad / WGrad entry points, rlq_gemm_gated_fprop of more than 8 tokens) or
+ * FProp / DGrad / WGrad entry points, rlq_gemm_gated_fprop of more than 8 tokens,
+ * rlq_gemm_mxfp4) or
  * in the next rlq_gated_backward, whichever is first.  A GEMM's launch runs on
  * single CTAs, and the TMA producer of every CTA withholds the loads of its first pipeline
  * stage, so nothing ever arrives on that stage's barrier: the MMA warp's

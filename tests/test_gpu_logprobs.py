@@ -33,8 +33,11 @@ def fp32(temperature):
 
 def reference(x, targets, top, temperature):
     z = x.to(D) / fp32(temperature)
-    lse = torch.logsumexp(z, 1)
-    lg = z - lse[:, None]
+    # (from the maximum: next to a logit of 1e38 a log-sum is nothing in 64 bits either)
+    m = z.amax(1)
+    log_s = torch.logsumexp(z - m[:, None], 1)
+    lse = m + log_s
+    lg = (z - m[:, None]) - log_s[:, None]
     p = lg.exp()
     H = -torch.where(p == 0, torch.zeros_like(p), p * lg).sum(1)
     ids = torch.sort(x, dim=1, descending=True, stable=True)[1][:, :top]
@@ -73,7 +76,8 @@ def check_forward(x, targets, top, temperature, got, rows=slice(None)):
     if top:
         dt = (x.to(D).amax(1, keepdim=True) - x.to(D).gather(1, ids)) / temperature
         tol = b_s[:, None] + 4 * U * dt
-        assert bool(((top_lp.to(D) == want[4]) | ((top_lp.to(D) - want[4]).abs() <= tol)).all())
+        # (equal infinities; a value beyond fp32's range is one)
+        assert bool(((top_lp == want[4].float()) | ((top_lp.to(D) - want[4]).abs() <= tol)).all())
     assert bool((H >= 0).all())
 
 
@@ -175,6 +179,28 @@ def test_forward_empty_rows_and_values_that_are_no_numbers():
     check_forward(x, targets, 6, 1.0, (lp, lse, H, ids, top_lp), fine)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_forward_rows_of_masks_only(dtype):
+    """Masks that are numbers: a row of nothing else is uniform, with -inf beside them too."""
+    V = 5000
+    x = torch.zeros(4, V, dtype=DTYPES[dtype], device=DEV)
+    x[0] = torch.finfo(x.dtype).min
+    x[1] = -1e9
+    x[2] = torch.finfo(x.dtype).min
+    x[2, ::2] = -math.inf
+    x[3] = torch.finfo(x.dtype).max
+    targets = torch.full((4,), 7, device=DEV)
+    got = rlq.token_logprobs_top(x, targets, top=5)
+    check_forward(x, targets, 5, 1.0, got)
+    n = torch.tensor([V, V, V / 2, V], device=DEV)
+    assert bool(((got[2] - n.log()).abs() <= 1e-5).all())
+    # the gradient is of the lse that it is given, which holds no log V next to 1e9
+    one = torch.ones(4, device=DEV)
+    d = rlq.token_logprobs_backward(x, targets, got[1], got[2], dlp=one, dentropy=one)
+    want, tol = gradient(x[1:2], targets[1:2], got[1][1:2], got[2][1:2], one[1:2], one[1:2], 1.0)
+    assert bool(((d[1:2].to(D) - want).abs() <= tol).all())
+
+
 def test_forward_far_offsets():
     """Rows beyond 2^31 elements from the first one."""
     ld, V, T = (1 << 30) + 8, 3000, 4
@@ -204,12 +230,12 @@ def gradient(x, targets, lse, H, dlp, dH, temperature):
     Hc = zero if H is None else H.to(D)[:, None]
     d = -p * (a + h * (lg + Hc)) * c
     at = torch.zeros_like(p).scatter_(1, targets[:, None], 1.0) * a * c
-    # log2 p: one rounding of the multiply-add and one each of c and L (fp32 logits: two of the
-    # result, the others 2^-24 of that); the exponential 2 ulp; four roundings behind
+    # log2 p: two roundings of the result, and c and L as sums of two floats 2^-48 off; the
+    # exponential 2 ulp; four roundings behind
     # (a logit of -inf has p = 0, and p times its part of the bound is 0: not 0 x inf)
     far = torch.where(p == 0, torch.zeros_like(p), (z.abs() + lse.to(D).abs()[:, None]) * 1.4427)
     t = lg.abs() * 1.4427
-    err_t = (U * (t + 2 * far)) if x.dtype == torch.bfloat16 else (4 * U * t + 8 * U * U * far)
+    err_t = 4 * U * t + 8 * U * U * far
     size = (a.abs() + h.abs() * (lg.abs() + Hc.abs())) * c
     tol = p * (size * (0.7 * err_t + 12 * U) + h.abs() * c * 0.7 * err_t) + 4 * U * at.abs()
     # probabilities below 2^-126 are zero
@@ -314,6 +340,60 @@ def test_streams_and_graphs():
     graph.replay()
     graph.replay()
     assert all(torch.equal(a, b) for a, b in zip(out, want)) and torch.equal(dg, d)
+
+
+def test_nothing_to_do_and_refusals():
+    x, targets = torch.zeros(0, 9, device=DEV), torch.zeros(0, dtype=torch.int64, device=DEV)
+    lp, lse, H, ids, top_lp = rlq.token_logprobs_top(x, targets, top=3)
+    assert lp.shape == lse.shape == H.shape == (0,) and ids.shape == top_lp.shape == (0, 3)
+    assert rlq.token_logprobs_backward(x, targets, lse, H, dlp=lp).shape == (0, 9)
+    x, targets = torch.zeros(2, 100, device=DEV), torch.zeros(2, dtype=torch.int64, device=DEV)
+    assert rlq.token_logprobs_top(x[:, :5], targets, top=64)[3].shape == (2, 5)  # no more than there are
+    for top in (-1, 65):
+        with pytest.raises(rlq.RlqError):
+            rlq.token_logprobs_top(x, targets, top=top)
+    lp, lse, H, _, _ = rlq.token_logprobs_top(x, targets)
+    with pytest.raises(rlq.RlqError):
+        rlq.token_logprobs_backward(x, targets, lse, H)  # neither derivative
+    with pytest.raises(rlq.RlqError):
+        rlq.token_logprobs_backward(x, targets, lse, dentropy=lp)  # no entropy
+    with pytest.raises(TypeError):
+        rlq.token_logprobs_top(x, targets.int())
+    with pytest.raises(ValueError):
+        rlq.token_logprobs_backward(x, targets, lse[:1], H, dlp=lp)
+
+
+def test_calls_on_two_streams_and_repeats():
+    """Lists are filled in any order; what comes of them is the same every time."""
+    g = gen(70)
+    x, targets = logits_of(g, 96, 40000, "bf16")
+    want = rlq.token_logprobs_top(x, targets, top=64)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        got = []
+        for st in streams:
+            with torch.cuda.stream(st):
+                got.append(rlq.token_logprobs_top(x, targets, top=64))
+        torch.cuda.synchronize()
+        for per in got:
+            assert all(torch.equal(a, b) for a, b in zip(per, want))
+
+
+@pytest.mark.parametrize("temperature", [1e-3, 0.05, 50.0, 1e4])
+def test_temperatures(temperature):
+    """From nearly one token to nearly uniform, with a mask."""
+    g = gen(71)
+    x, targets = logits_of(g, 20, 3001, "f32")
+    x[3, 100:] = -math.inf
+    x[4, 5:] = torch.finfo(torch.float32).min
+    targets[3:5] = 2
+    got = rlq.token_logprobs_top(x, targets, top=7, temperature=temperature)
+    check_forward(x, targets, 7, temperature, got)
+    a, h = torch.randn(20, generator=g, device=DEV), torch.randn(20, generator=g, device=DEV)
+    d = rlq.token_logprobs_backward(x, targets, got[1], got[2], dlp=a, dentropy=h, temperature=temperature)
+    want, tol = gradient(x, targets, got[1], got[2], a, h, temperature)
+    assert bool(((d.to(D) - want).abs() <= tol).all())
 
 
 # ------------------------------------------------------------ the 4-bit head ---

@@ -320,3 +320,91 @@ def test_bounded_wait_runs_out_and_the_next_call_is_right():
         assert e.value.status == 5 and "MXFP4" in str(e.value)
         rlq.check()
         assert torch.equal(rlq.gemm_mxfp4(xq, xs, wq, ws, out_dtype=torch.float32).to(D), x @ w.t())
+
+
+def test_far_offsets():
+    """Rows of every matrix beyond 2^31 bytes and elements from the first one."""
+    g = gen(40)
+    ld = (1 << 30) + 64
+    rows, K = 4, 352
+    big = torch.empty(rows * ld, dtype=torch.bfloat16, device=DEV)
+    x = big.as_strided((rows, K), (ld, 1))
+    x.copy_(difficult(g, rows, K))
+    q, s, qT, sT = rlq.quant_mxfp4(x, colwise=True)
+    check_codes(q, s, x, "rows")
+    check_codes(qT, sT, x.t(), "columns")
+    code, sb = R.quantize(x.cpu())
+    rlq.rlq_dequant_mxfp4(q.data_ptr(), q.stride(0), s.data_ptr(), rows, K, x.data_ptr(), ld,
+                          torch.cuda.current_stream().cuda_stream)
+    assert torch.equal(x.cpu().to(D), R.values(code, sb))
+    # codes and outputs in the same rows, a quarter apart
+    bytes_ = big.view(torch.uint8)
+    far = bytes_[1 << 20:].as_strided((rows, K // 2), (2 * ld, 1))
+    rlq.rlq_quant_mxfp4(x.data_ptr(), rows, K, ld, far.data_ptr(), 2 * ld, s.data_ptr(), None, 0, None,
+                        torch.cuda.current_stream().cuda_stream)
+    xq, xs, xv = R.operand(g, rows, K, -1, 1)
+    far.copy_(xq)
+    wq, ws, w = R.operand(g, 300, K, -1, 1)
+    y = big[1 << 20:].as_strided((rows, 300), (ld, 1))
+    assert rlq.gemm_mxfp4(far, xs, wq, ws, out=y) is y
+    assert torch.equal(y, (xv @ w.t()).float().to(torch.bfloat16))
+    yT = rlq.gemm_mxfp4(wq, ws, far, xs)  # the far codes as the second operand
+    assert torch.equal(yT, (w @ xv.t()).float().to(torch.bfloat16))
+
+
+def test_operands_in_longer_rows():
+    """Codes as views of longer rows, for single CTAs and pairs."""
+    g = gen(41)
+    for M, N, K in ((20, 200, 512), (700, 600, 1000)):
+        xq, xs, x = R.operand(g, M, K, -1, 1)
+        wq, ws, w = R.operand(g, N, K, -1, 1)
+        bx = torch.randint(0, 255, (M, xq.shape[1] // 16 * 16 + 64), generator=g, device=DEV).to(torch.uint8)
+        bw = torch.randint(0, 255, (N, wq.shape[1] // 16 * 16 + 48), generator=g, device=DEV).to(torch.uint8)
+        bx[:, :xq.shape[1]], bw[:, :wq.shape[1]] = xq, wq
+        got = rlq.gemm_mxfp4(bx[:, :xq.shape[1]], xs, bw[:, :wq.shape[1]], ws, out_dtype=torch.float32)
+        assert torch.equal(got.to(D), x @ w.t())
+
+
+def test_calls_on_two_streams_at_once():
+    """Products of every kind of cut side by side: nothing is shared between calls."""
+    g = gen(42)
+    shapes = [(4, 1024, 4096), (64, 640, 8192), (300, 1024, 2048), (600, 2000, 512)]
+    ops = [(R.operand(g, M, K, -1, 1), R.operand(g, N, K, -1, 1)) for M, N, K in shapes]
+    want = [(a[2] @ b[2].t()).float() for a, b in ops]
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    torch.cuda.synchronize()
+    got = [[] for _ in streams]
+    for i in range(12):
+        for j, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                a, b = ops[(i + j) % len(ops)]
+                got[j].append(((i + j) % len(ops), rlq.gemm_mxfp4(a[0], a[1], b[0], b[1], out_dtype=torch.float32)))
+    torch.cuda.synchronize()
+    rlq.check()
+    for per in got:
+        for k, y in per:
+            assert torch.equal(y, want[k])
+
+
+def test_helpers_refuse_wrong_operands():
+    g = gen(43)
+    xq, xs, _ = R.operand(g, 5, 64, -1, 1)
+    wq, ws, _ = R.operand(g, 7, 64, -1, 1)
+    with pytest.raises(ValueError, match="contraction"):
+        rlq.gemm_mxfp4(xq, xs, wq[:, :16], ws)
+    with pytest.raises(ValueError, match="scales"):
+        rlq.gemm_mxfp4(xq, xs[:, :, :16], wq, ws)
+    with pytest.raises(TypeError):
+        rlq.gemm_mxfp4(xq, xs.int(), wq, ws)
+    with pytest.raises(TypeError):
+        rlq.gemm_mxfp4(xq, xs, wq, ws, out_dtype=torch.float16)
+    with pytest.raises(ValueError, match="out"):
+        rlq.gemm_mxfp4(xq, xs, wq, ws, out=torch.empty(5, 8, device=DEV))
+    with pytest.raises(ValueError):
+        rlq.gemm_mxfp4(xq, xs.cpu(), wq, ws)
+    with pytest.raises(ValueError, match="contiguous rows"):
+        rlq.quant_mxfp4(torch.zeros(64, 64, dtype=torch.bfloat16, device=DEV).t()[:, :32])
+    with pytest.raises(rlq.RlqError):
+        rlq.quant_mxfp4(torch.zeros(4, 48, dtype=torch.bfloat16, device=DEV))
+    with pytest.raises(ValueError, match="cols"):
+        rlq.dequant_mxfp4(xq, xs, cols=62)
