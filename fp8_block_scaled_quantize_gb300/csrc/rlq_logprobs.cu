@@ -38,6 +38,7 @@ constexpr float LN2 = 0.6931471805599453f;
 constexpr float LOWEST = -16384.0f;  // 2^LOWEST is 0, and 0 x LOWEST too
 
 constexpr int THREADS = 256, CTAS_SM = 4, WARPS = THREADS / 32, MAX_CLUSTER = 8;
+static_assert((THREADS & (THREADS - 1)) == 0, "a batch's number and a thread's share a word");
 constexpr int BATCH = 8;     // 16-byte loads in flight a thread
 constexpr int MAX_TOP = MAX_TOKEN_TOP;
 constexpr int LIST = 1024;   // candidates
@@ -637,7 +638,8 @@ cudaError_t launch_grad(const TokenGradArgs &p, cudaStream_t st)
     constexpr int N = Elem<T>::N;
     const int64_t units = (p.V + N - 1) / N + 1, span = (int64_t)BWD_BATCH * BWD_ROUNDS * THREADS;
     const int64_t parts = (units + span - 1) / span;
-    return launch_pdl(k_token_grad<T>, dim3((unsigned)(p.rows * parts)), dim3(THREADS), 0, st, p, (int)parts);
+    const int threads = units < THREADS ? (int)(units + 31) / 32 * 32 : THREADS;
+    return launch_pdl(k_token_grad<T>, dim3((unsigned)(p.rows * parts)), dim3(threads), 0, st, p, (int)parts);
 }
 
 }  // namespace
