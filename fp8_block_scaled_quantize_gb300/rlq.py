@@ -772,23 +772,21 @@ def _here(name, t):
         raise ValueError(f"{name} must be on the current CUDA device")
 
 
-def _mx_operand(name, q, s, dev):
-    """(rows, bytes a row, pitch) of packed MXFP4 codes with their scale tiles on device ``dev``."""
-    if q.dim() == 2 and q.dtype is torch.uint8 and s.dtype is torch.uint8 and q.get_device() == dev == s.get_device():
-        R, B = q.shape
-        ld, inner = q.stride()
-        if (inner == 1 or B <= 1) and s.shape == ((R + 127) >> 7, (B + 63) >> 6, 32, 4, 4) and s.is_contiguous():
-            return R, B, ld if R > 1 else max(ld, B)
-    # which of it is not so
+def _mx_operand(name, q, s):
+    """(rows, bytes a row, pitch) of packed MXFP4 codes with their scale tiles; an error that names
+    what is wrong with them otherwise."""
     if q.dim() != 2:
         raise ValueError(f"{name}: codes must be a 2-D tensor")
     R, B = q.shape
-    _rows_of(name, q, R, B, torch.uint8)
+    ld = _rows_of(name, q, R, B, torch.uint8)
+    _here(name, q)
     if s.dtype is not torch.uint8:
         raise TypeError(f"{name}: scales must be uint8")
     if s.shape != mxfp4_scales_shape(R, 2 * B) or not s.is_contiguous():
         raise ValueError(f"{name}: scales must be a contiguous {mxfp4_scales_shape(R, 2 * B)} tensor")
-    raise ValueError(f"{name}: codes and scales must be on the current CUDA device")
+    if s.device != q.device:
+        raise ValueError(f"{name}: scales must be on the codes' device")
+    return R, B, ld
 
 
 def mxfp4_scales_shape(rows: int, cols: int):
@@ -807,14 +805,20 @@ def quant_mxfp4(x: torch.Tensor, colwise: bool = False, stream=None):
     if x.dim() != 2:
         raise ValueError("x must be a [M, K] tensor")
     M, K = x.shape
-    ldx = _rows_of("x", x, M, K)
-    _here("x", x)
+    ldx, inner = x.stride()
+    d = x.get_device()
+    if x.dtype is not torch.bfloat16 or (inner != 1 and K > 1) or d != _current(x):
+        _rows_of("x", x, M, K)  # says which of it
+        _here("x", x)
+    if M <= 1 and ldx < K:
+        ldx = K
     dev = x.device
     # (K / 2 is a multiple of 16, but for a K that the call refuses)
     q = torch.empty((M, K >> 1), dtype=torch.uint8, device=dev)
     s = torch.empty(((M + 127) >> 7, (K + 127) >> 7, 32, 4, 4), dtype=torch.uint8, device=dev)
     if not colwise:
-        _call("rlq_quant_mxfp4", x.data_ptr(), M, K, ldx, q.data_ptr(), K >> 1, s.data_ptr(), None, 0, None, _stream(stream))
+        _call("rlq_quant_mxfp4", x.data_ptr(), M, K, ldx, q.data_ptr(), K >> 1, s.data_ptr(), None, 0, None,
+              _stream(stream) if stream is not None else torch._C._cuda_getCurrentRawStream(d))
         return q, s, None, None
     qT, ldT = _codes_T(K, (M + 1) // 2, dev)
     sT = torch.empty(mxfp4_scales_shape(K, M), dtype=torch.uint8, device=dev)
@@ -827,7 +831,7 @@ def dequant_mxfp4(q: torch.Tensor, s: torch.Tensor, cols: int | None = None, str
     """The values (bf16 [rows, cols], exact) of MXFP4 codes and scale tiles.  ``cols`` is needed
     where it is odd; rows are on 16-byte boundaries, so the result is a view of longer rows
     where cols is not a multiple of 8."""
-    R, B, ld = _mx_operand("q", q, s, _current(q))
+    R, B, ld = _mx_operand("q", q, s)
     C = 2 * B if cols is None else int(cols)
     if (C + 1) // 2 != B:
         raise ValueError(f"cols must be {2 * B} or {2 * B - 1}")
@@ -841,11 +845,29 @@ def gemm_mxfp4(xq, xs, wq, ws, out=None, out_dtype: torch.dtype = torch.bfloat16
     """Y [M, N] = X W^T from two MXFP4 operands (codes [M, K/2] and [N, K/2], scale tiles) on
     the FP4 tensor cores, in bf16 or fp32 (``out_dtype``, or that of ``out``).  DGrad takes
     the weight's transposed codes, WGrad those of dY and X."""
-    dev = _current(xq)
-    M, B, ldx = _mx_operand("xq", xq, xs, dev)
-    N, Bw, ldw = _mx_operand("wq", wq, ws, dev)
-    if B != Bw:
-        raise ValueError(f"xq and wq have rows of {B} and {Bw} bytes: the contraction lengths differ")
+    u8, d = torch.uint8, xq.get_device()
+    # (one condition for a pass, the checks one by one for what is wrong)
+    if (xq.dtype is u8 and xs.dtype is u8 and wq.dtype is u8 and ws.dtype is u8 and xq.dim() == 2 and wq.dim() == 2 and
+            d == _current(xq) and d == xs.get_device() == wq.get_device() == ws.get_device() and xs.is_contiguous() and
+            ws.is_contiguous()):
+        M, B = xq.shape
+        N, Bw = wq.shape
+        ldx, ix = xq.stride()
+        ldw, iw = wq.stride()
+        tiles = (B + 63) >> 6
+        fine = (ix == 1 == iw and B == Bw and xs.shape == ((M + 127) >> 7, tiles, 32, 4, 4) and
+                ws.shape == ((N + 127) >> 7, tiles, 32, 4, 4))
+        # (the stride of a dimension of size 1 is arbitrary)
+        ldx, ldw = ldx if M > 1 else max(ldx, B), ldw if N > 1 else max(ldw, B)
+    else:
+        fine = False
+    if not fine:
+        M, B, ldx = _mx_operand("xq", xq, xs)
+        N, Bw, ldw = _mx_operand("wq", wq, ws)
+        if B != Bw:
+            raise ValueError(f"xq and wq have rows of {B} and {Bw} bytes: the contraction lengths differ")
+        if wq.device != xq.device:
+            raise ValueError("wq must be on xq's device")
     if out is None:
         out = torch.empty((M, N), dtype=out_dtype, device=xq.device)
         ldy = N or 1
@@ -857,7 +879,7 @@ def gemm_mxfp4(xq, xs, wq, ws, out=None, out_dtype: torch.dtype = torch.bfloat16
     if dt is None:
         raise TypeError("the output must be bfloat16 or float32")
     _call("rlq_gemm_mxfp4", xq.data_ptr(), ldx, xs.data_ptr(), wq.data_ptr(), ldw, ws.data_ptr(), out.data_ptr(), dt,
-          ldy, M, N, 2 * B, _stream(stream))
+          ldy, M, N, 2 * B, _stream(stream) if stream is not None else torch._C._cuda_getCurrentRawStream(d))
     return out
 
 
