@@ -14,8 +14,8 @@
 // columns of each at a time: their 16 scale bytes are one piece.
 //
 // Bound by memory (2 bytes a value read once, 17/32 written per direction) where there is enough
-// of it: rows of 8192 x 14336 in 48.4 us (0.91 of HBM), both ways 14336 x 4096 in 33.1 (0.80;
-// instructions, 63% of the issue slots, and the phases of a tile), read back 25.8 (0.85).
+// of it: rows of 8192 x 14336 in 48.4 us (0.91 of HBM), both ways 14336 x 4096 in 30.3 (0.87;
+// the phases of a tile), read back 25.7 (0.86).
 // Small ones are bound by launch and load latency (333 x 18944: 4.6 us, 1 x 4096: 2.0).
 #include <cuda_runtime.h>
 
@@ -27,6 +27,14 @@ namespace {
 
 constexpr int THREADS = 256, WARPS = THREADS / 32;
 constexpr int BOTH_CTAS_SM = 5;
+
+// 16-byte global -> shared copy; src_bytes = 0 writes zeros.
+__device__ __forceinline__ void cp_async16_zfill(void *dst, const void *src, uint32_t src_bytes)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src),
+                 "r"(src_bytes)
+                 : "memory");
+}
 
 // The larger magnitude in each half of two bf16 pairs, with a sign that means nothing; a NaN if
 // either is one.
@@ -40,7 +48,7 @@ __device__ __forceinline__ uint32_t max_abs2(uint32_t a, uint32_t b)
 template <int N>
 __device__ __forceinline__ uint32_t max_halves(const uint32_t (&w)[N])
 {
-    uint32_t m[4] = {w[0], w[1], w[2], w[3]};  // (four chains: N is 4 or 32)
+    uint32_t m[4] = {w[0], w[1], w[2], w[3]};  // (four chains: N is 4, 16 or 32)
 #pragma unroll
     for (int i = 4; i < N; ++i)
         m[i & 3] = max_abs2(m[i & 3], w[i]);
@@ -190,11 +198,12 @@ __global__ void __launch_bounds__(THREADS)
         quantize_rows<U, true>(it, x, ldx, q, ldq, s);
 }
 
-// Rows and columns from one read: a CTA takes a 128 x 128 tile, quantizes its rows as
-// above while it puts the values to shared memory, then its columns from there, two
-// columns of 32 rows a thread (both halves of a word at once).  Row r of the tile lies at
-// word 64 r + 8 (r / 32): the four row blocks that a warp reads fall into different banks.
-// kEdge: the tile is cut by the matrix's end.
+// Rows and columns from one read: a CTA copies a 128 x 128 tile to shared memory, quantizes its
+// rows from there, a block a thread and turn, and its columns, two columns of 32 rows a thread
+// (both halves of a word at once).  Row r of the tile lies at word 68 r + 8 (r / 32): eight lanes'
+// 16-byte reads of four rows' neighbouring blocks, and the words that a warp reads of four row
+// blocks, fall into different banks.  (Rows as above, straight from their registers, with four lanes
+// to a block, took 33.1 us for 14336 x 4096; so 30.3.)
 struct BothArgs {
     const uint16_t *x;
     int64_t M, K, ldx;
@@ -206,46 +215,60 @@ struct BothArgs {
     int ctiles, rtiles;
 };
 
+__device__ __forceinline__ int tile_word(int r) { return 68 * r + 8 * (r >> 5); }
+
+// kEdge: the tile is cut by the matrix's end.
 template <bool kEdge>
-__device__ __forceinline__ void both_tile(const BothArgs &p, uint32_t *tile, uint8_t *col_scales)
+__device__ __forceinline__ void both_tile(const BothArgs &p, uint32_t *tile, uint8_t *row_scale, uint8_t *col_scale)
 {
-    const int t = threadIdx.x, lane = t & 31, warp = t >> 5, half = lane >> 4, l = lane & 15;
+    const int t = threadIdx.x;
     const int rt = blockIdx.x / p.ctiles, ct = blockIdx.x - rt * p.ctiles;
     const int rows = kEdge ? (int)min(p.M - (int64_t)rt * 128, (int64_t)128) : 128;
     const int cols = kEdge ? (int)min(p.K - (int64_t)ct * 128, (int64_t)128) : 128;
-    const int row0 = warp + 32 * half;  // this lane's rows: row0 + 8 i + 64 j
-    const uint16_t *x = p.x + ((int64_t)rt * 128 + row0) * p.ldx + ct * 128 + l * 8;
-    uint4 v[4][2];
+    {
+        const int l = t & 15, r0 = t >> 4;
+        const uint16_t *x = p.x + ((int64_t)rt * 128 + r0) * p.ldx + ct * 128 + l * 8;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-            v[i][j] = !kEdge || (row0 + 8 * i + 64 * j < rows && l * 8 < cols) ? ld_stream(x + (8 * i + 64 * j) * p.ldx)
-                                                                                : make_uint4(0, 0, 0, 0);
-    uint8_t *q = p.q + ((int64_t)rt * 128 + row0) * p.ldq + ct * 64 + l * 4;
-    uint8_t *s = p.s + ((int64_t)rt * p.ctiles + ct) * 512 + warp * 16 + half * 4;
-    uint32_t *mine = tile + row0 * 64 + 8 * half + 4 * l;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            *reinterpret_cast<uint4 *>(mine + (8 * i + 64 * j) * 64 + 16 * j) = v[i][j];
-            uint32_t sb;
-            const uint32_t codes = row_codes(v[i][j], &sb);
-            const uint32_t sw = row_scales(sb, lane);
-            if (!kEdge || row0 + 8 * i + 64 * j < rows) {
-                if (!kEdge || l * 8 < cols)
-                    *reinterpret_cast<uint32_t *>(q + (8 * i + 64 * j) * p.ldq) = codes;
-                if (l == 0)
-                    *reinterpret_cast<uint32_t *>(s + 128 * i + 8 * j) = sw;
-            }
+        for (int i = 0; i < 8; ++i) {
+            const bool in = !kEdge || (r0 + 16 * i < rows && l * 8 < cols);
+            cp_async16_zfill(tile + tile_word(r0 + 16 * i) + 4 * l, in ? x + (int64_t)16 * i * p.ldx : p.x, in ? 16u : 0u);
         }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+    }
     __syncthreads();
+    {
+        const int b = (t >> 2) & 3;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int r = (t & 3) + 4 * ((t >> 4) + 16 * k);
+            uint32_t w[16];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                *reinterpret_cast<uint4 *>(w + 4 * i) = *reinterpret_cast<const uint4 *>(tile + tile_word(r) + 16 * b + 4 * i);
+            const uint32_t m = max_halves(w);
+            const uint32_t sb = scale_byte(max(m & 0x7FFFu, m >> 16 & 0x7FFFu));
+            const float rc = rcp_of(sb);
+            uint32_t o[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float2 f[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    f[j] = __fmul2_rn(make_float2(bf_lo(w[4 * i + j]), bf_hi(w[4 * i + j])), make_float2(rc, rc));
+                o[i] = e2m1x8(f);
+            }
+            row_scale[(r & 31) * 16 + (r >> 5) * 4 + b] = (uint8_t)sb;
+            // (32 columns are a block's: K % 32 == 0)
+            if (!kEdge || (r < rows && 32 * b < cols))
+                *reinterpret_cast<uint4 *>(p.q + ((int64_t)rt * 128 + r) * p.ldq + ct * 64 + 16 * b) =
+                    make_uint4(o[0], o[1], o[2], o[3]);
+        }
+    }
     const int b = t & 3, cp = t >> 2;  // rows 32 b .., columns 2 cp and 2 cp + 1
     uint32_t w[32];
 #pragma unroll
     for (int i = 0; i < 32; ++i)
-        w[i] = tile[(32 * b + i) * 64 + 8 * b + cp];
+        w[i] = tile[tile_word(32 * b) + 68 * i + cp];
     const uint32_t m = max_halves(w);
     const int left = (rows + 1) / 2 - 16 * b;  // bytes that the transposed row has of the thread's 16
     uint8_t *qT = p.qT + ((int64_t)ct * 128 + 2 * cp) * p.ldqT + rt * 64 + 16 * b;
@@ -266,7 +289,7 @@ __device__ __forceinline__ void both_tile(const BothArgs &p, uint32_t *tile, uin
             o[i] = e2m1x8(f);
         }
         const int c = 2 * cp + h;
-        col_scales[(c & 31) * 16 + (c >> 5) * 4 + b] = (uint8_t)sb;
+        col_scale[(c & 31) * 16 + (c >> 5) * 4 + b] = (uint8_t)sb;
         if (!kEdge || (c < cols && left > 0)) {
             const uint4 o4 = make_uint4(o[0], o[1], o[2], o[3]);
             if (!kEdge || left >= 16)
@@ -276,21 +299,23 @@ __device__ __forceinline__ void both_tile(const BothArgs &p, uint32_t *tile, uin
         }
     }
     __syncthreads();
-    if (t < 32)
-        *reinterpret_cast<uint4 *>(p.sT + ((int64_t)ct * p.rtiles + rt) * 512 + t * 16) =
-            *reinterpret_cast<const uint4 *>(&col_scales[t * 16]);
+    if (t < 64) {
+        uint8_t *to = t < 32 ? p.s + ((int64_t)rt * p.ctiles + ct) * 512 : p.sT + ((int64_t)ct * p.rtiles + rt) * 512;
+        const uint8_t *from = t < 32 ? row_scale : col_scale;
+        *reinterpret_cast<uint4 *>(to + (t & 31) * 16) = *reinterpret_cast<const uint4 *>(from + (t & 31) * 16);
+    }
 }
 
 __global__ void __launch_bounds__(THREADS, BOTH_CTAS_SM) k_mx_both(const BothArgs p)
 {
     pdl_begin();
-    __shared__ __align__(16) uint32_t tile[128 * 64 + 3 * 8 + 8];
-    __shared__ __align__(16) uint8_t col_scales[512];
+    __shared__ __align__(16) uint32_t tile[128 * 68 + 3 * 8];
+    __shared__ __align__(16) uint8_t row_scale[512], col_scale[512];
     const int rt = blockIdx.x / p.ctiles, ct = blockIdx.x - rt * p.ctiles;
     if ((int64_t)(rt + 1) * 128 <= p.M && (int64_t)(ct + 1) * 128 <= p.K)
-        both_tile<false>(p, tile, col_scales);
+        both_tile<false>(p, tile, row_scale, col_scale);
     else
-        both_tile<true>(p, tile, col_scales);
+        both_tile<true>(p, tile, row_scale, col_scale);
 }
 
 // The n (1 .. 4) bytes that a row still has.
