@@ -15,8 +15,8 @@
 //
 // Bound by memory (2 bytes a value read once, 17/32 written per direction) where there is enough
 // of it: rows of 8192 x 14336 in 48.4 us (0.91 of HBM), both ways 14336 x 4096 in 30.3 (0.87;
-// the phases of a tile), read back 25.7 (0.86).
-// Small ones are bound by launch and load latency (333 x 18944: 4.6 us, 1 x 4096: 2.0).
+// the phases of a tile), read back 25.7 (0.86).  Small ones are bound by launch and load latency
+// (333 x 18944: 4.6 us, 1 x 4096: 2.0).
 #include <cuda_runtime.h>
 
 #include "rlq_elem.cuh"
@@ -203,7 +203,7 @@ __global__ void __launch_bounds__(THREADS)
 // (both halves of a word at once).  Row r of the tile lies at word 68 r + 8 (r / 32): eight lanes'
 // 16-byte reads of four rows' neighbouring blocks, and the words that a warp reads of four row
 // blocks, fall into different banks.  (Rows as above, straight from their registers, with four lanes
-// to a block, took 33.1 us for 14336 x 4096; so 30.3.)
+// to a block, took 33.1 us for 14336 x 4096, this 30.3.)
 struct BothArgs {
     const uint16_t *x;
     int64_t M, K, ldx;
