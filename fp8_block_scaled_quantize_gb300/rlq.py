@@ -933,14 +933,18 @@ def token_logprobs_backward(logits: torch.Tensor, targets: torch.Tensor, lse: to
     """Gradient with respect to the logits of a loss whose derivatives by the targets' log
     probabilities and by the entropies are ``dlp`` and ``dentropy`` (fp32 [rows], one of them
     may be None), from the forward call's ``lse`` and, with ``dentropy``, ``entropy``.
-    ``inplace`` writes it over the logits.  Returns dlogits, like logits."""
+    ``inplace`` writes it over the logits.  Returns dlogits, of the logits' shape and type."""
     T, V, dt, ld, tg = _logits(logits, targets)
     _here("logits", logits)
     opt = lambda name, t: None if t is None else _vector(name, t, T)  # noqa: E731
     args = _vector("lse", lse, T), opt("entropy", entropy), opt("dlp", dlp), opt("dentropy", dentropy)
-    # (the logits' own pitch, so that their rows share 16-byte phases)
-    d = logits if inplace else torch.empty_strided((T, V), (ld, 1), dtype=logits.dtype, device=logits.device)
-    _call("rlq_token_logprobs_backward", logits.data_ptr(), dt, ld, T, V, tg, temperature, *args, d.data_ptr(), ld,
+    if inplace:
+        d, ldd = logits, ld
+    else:
+        # (the least pitch whose rows share the logits' 16-byte phases: a part of wide rows gets no wide rows)
+        ldd = V + (ld - V) % (4 if dt == DTYPE_F32 else 8)
+        d = torch.empty_strided((T, V), (ldd, 1), dtype=logits.dtype, device=logits.device)
+    _call("rlq_token_logprobs_backward", logits.data_ptr(), dt, ld, T, V, tg, temperature, *args, d.data_ptr(), ldd,
           _stream(stream))
     return d
 

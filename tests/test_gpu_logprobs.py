@@ -279,6 +279,27 @@ def test_gradient(T, V, dtype, which):
     assert torch.equal(far[:, :V], d) and bool((far[:, V:] == 9).all())
 
 
+@pytest.mark.parametrize("dtype,left,V,ld", [("bf16", 0, 1000, 4096), ("bf16", 3, 1001, 4099), ("f32", 1, 37, 2050)])
+def test_gradient_of_a_part_of_wide_rows(dtype, left, V, ld):
+    """The gradient's rows are no wider than their phases need, and the columns beside the part are not read."""
+    g = gen(51)
+    T = 9
+    wide = torch.full((T, ld), float("nan"), dtype=DTYPES[dtype], device=DEV)
+    x = wide[:, left:left + V]
+    x.copy_(torch.randn(T, V, generator=g, device=DEV) * 3)
+    targets = torch.randint(0, V, (T,), generator=g, device=DEV)
+    a, h = torch.randn(T, generator=g, device=DEV), torch.randn(T, generator=g, device=DEV)
+    lp, lse, H, _, _ = rlq.token_logprobs_top(x, targets)
+    d = rlq.token_logprobs_backward(x, targets, lse, H, dlp=a, dentropy=h)
+    n = 16 // x.element_size()
+    assert d.shape == x.shape and d.stride(1) == 1
+    assert V <= d.stride(0) < V + n and (d.stride(0) - ld) % n == 0
+    want, tol = gradient(x, targets, lse, H, a, h, 1.0)
+    assert bool(((d.to(D) - want).abs() <= tol).all())
+    y = x.contiguous()
+    assert torch.equal(rlq.token_logprobs_backward(y, targets, lse, H, dlp=a, dentropy=h), d)
+
+
 def test_gradient_against_differences():
     """A loss of both outputs, differentiated numerically in 64 bits."""
     g = gen(50)
