@@ -71,7 +71,8 @@ struct Params {
     int a_rows, b_rows;
     int kstages, last_steps;     // stages, and instructions (64 elements) of the last one
     int b_tiles, units, tile_b;  // tiles of B, (A tile, B tile) units, rows of a B tile
-    int splits, log2_splits, kps;  // CTAs that share a unit (a power of two), stages of each
+    int splits, kps;             // CTAs that share a unit, stages of each
+    uint32_t splits_inv;         // 2^16 / splits, rounded up
     int stages, stage_bytes, b_bytes, bs_bytes, tx_bytes;
     int tmem_cols, buf1, sf_col, overlap;
     uint64_t timeout_ns;
@@ -215,6 +216,8 @@ __global__ void __launch_bounds__(THREADS)
     const int ks1 = kPair ? p.kstages : min(ks0 + p.kps, p.kstages);
     auto a_row = [&](int u) { return (u / p.b_tiles) * (kPair ? 2 * BM : BM) + (kPair ? (int)rank * BM : 0); };
     auto b_row = [&](int u) { return (u % p.b_tiles) * p.tile_b; };
+    // n / splits (exact below 2^16 / splits; four tokens of at most 256 are counted)
+    auto over_splits = [&](int n) { return (int)((uint32_t)n * p.splits_inv >> 16); };
     auto columns = [&](int u) { return min(p.tile_b, p.b_rows - b_row(u)); };
     // the MMA's columns: whole steps of 16 (pair: 32, half of them each CTA's)
     auto mma_n = [&](int u) { return kPair ? (columns(u) + 31) & ~31 : (columns(u) + 15) & ~15; };
@@ -427,7 +430,7 @@ __global__ void __launch_bounds__(THREADS)
                 cluster_wait();
                 met = true;
             }
-            const int slots_max = ((nc + 3) / 4 + p.splits - 1) >> p.log2_splits;
+            const int slots_max = over_splits((nc + 3) / 4 + p.splits - 1);
             const int64_t ar = a_row(u) + row, br = b_row(u);
             const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * p.buf1);
             // the columns that the other buffer has too come first: the first buffer's last piece, the second's first
@@ -494,9 +497,9 @@ __global__ void __launch_bounds__(THREADS)
 #pragma unroll
                         for (int j = 0; j < 8; ++j)
                             if (4 * j < left) {
-                                const int four = c / 4 + j;
-                                const uint32_t to = (uint32_t)(four & (p.splits - 1));
-                                st_async4(cluster_addr(at + (uint32_t)((four >> p.log2_splits) * (BM * 16)), to),
+                                const int four = c / 4 + j, slot = over_splits(four);
+                                const uint32_t to = (uint32_t)(four - slot * p.splits);
+                                st_async4(cluster_addr(at + (uint32_t)(slot * (BM * 16)), to),
                                           cluster_addr(parts_bar, to), &r[h][4 * j]);
                             }
                     } else if (ar < p.a_rows) {
@@ -522,8 +525,8 @@ __global__ void __launch_bounds__(THREADS)
             cluster_wait();
         }
         if (warp >= EPI_WARP0) {
-            const int nc = columns(unit0), fours = (nc + 3) / 4, slots_max = (fours + p.splits - 1) >> p.log2_splits;
-            const int slots = (fours - (int)rank + p.splits - 1) >> p.log2_splits;  // of this CTA
+            const int nc = columns(unit0), fours = (nc + 3) / 4, slots_max = over_splits(fours + p.splits - 1);
+            const int slots = over_splits(fours - (int)rank + p.splits - 1);  // of this CTA
             if (threadIdx.x == EPI_WARP0 * 32)
                 mbar_arrive_expect_tx(parts_bar, (uint32_t)(slots * p.splits * BM * 16));
             bool ok = met && __all_sync(0xFFFFFFFFu, mbar_wait(parts_bar, 0, abort_flag, p.timeout_ns, SITE_EPI_TMEM_FULL));
@@ -590,11 +593,11 @@ __global__ void __launch_bounds__(THREADS)
 
 // Zeros, where there is nothing to add.
 template <bool kF32>
-__global__ void __launch_bounds__(256) k_zero_out(const Params p)
+__global__ void __launch_bounds__(THREADS) k_zero_out(const Params p)
 {
     pdl_begin();
     const int64_t M = p.b_rows, N = p.a_rows;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < M * N; i += (int64_t)gridDim.x * 256)
+    for (int64_t i = (int64_t)blockIdx.x * THREADS + threadIdx.x; i < M * N; i += (int64_t)gridDim.x * THREADS)
         store_out<kF32>(p, i / N * p.ldy + i % N, 0.0f);
 }
 
@@ -667,6 +670,12 @@ rlq_status launch(const CUtensorMap *maps, const Params &p, int grid, int cluste
         e = cudaFuncSetAttribute(k_gemm_mxfp4<kPair, kF32>, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448);
         if (e != cudaSuccess)
             return cuda_status(e, "cudaFuncSetAttribute(max dynamic shared memory)");
+        // All of the SM's memory as shared memory, so that the next call's quantizer finds a CTA's room
+        // beside this one whatever its ring takes (40 tokens, 2560 x 10240: 9.2 us; 11.2 with a split for 196 KB).
+        e = cudaFuncSetAttribute(k_gemm_mxfp4<kPair, kF32>, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                 cudaSharedmemCarveoutMaxShared);
+        if (e != cudaSuccess)
+            return cuda_status(e, "cudaFuncSetAttribute(carve-out)");
         set[dev & 63].store(true, std::memory_order_relaxed);
     }
     cudaLaunchAttribute attr[2];
@@ -687,6 +696,49 @@ rlq_status launch(const CUtensorMap *maps, const Params &p, int grid, int cluste
                        "MXFP4 GEMM launch");
 }
 
+// Clusters of `s` single CTAs, one or two CTAs to an SM, that the current device runs at once: fewer
+// than their CTAs would fit, since a cluster stays within a group of SMs (one GB300, alone on an SM: 76,
+// 46, 36, 28, 23, 15 and 15 of 2 .. 8; others differ by one or two).
+int clusters_at_once(int s, bool two)
+{
+    static std::atomic<int> known[64][2][9];
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess)
+        return 0;
+    std::atomic<int> &k = known[dev & 63][two][s];
+    if ((n = k.load(std::memory_order_relaxed)) > 0)
+        return n - 1;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = s;
+    attr.val.clusterDim.y = 1;
+    attr.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)s);
+    cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = two ? 232448 / 2 - 1024 : 232448;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    // (asked of a kernel that takes no tensor memory: of the others the query allows one CTA to an SM)
+    if (cudaFuncSetAttribute(k_zero_out<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, k_zero_out<false>, &cfg) != cudaSuccess) {
+        cudaGetLastError();  // (not this call's: a contraction that is not shared)
+        return 0;
+    }
+    k.store(n + 1, std::memory_order_relaxed);
+    return n;
+}
+
+// Whether so many clusters run at once beside the kernels around them, which may keep some of the SMs: not
+// the last tenth of the clusters, of five CTAs and more not the last sixth (16 tokens, 3584 x
+// 18944 in 28 of 28 clusters of five 16.8 us, in fours 14.3; 100 tokens, 2560 x 10240 in 20 of
+// 23 of six 12.8, in as many of two CTAs an SM 11.1).
+bool at_once(int64_t units, int s, bool two)
+{
+    const int64_t n = clusters_at_once(s, two);
+    return s < 3 ? units <= n : s < 5 ? 10 * units <= 9 * n : 20 * units <= 17 * n;
+}
+
 // How a product is cut: CTA pairs with tiles of 256 rows of A x tile_b rows of B, or single CTAs with
 // 128 output columns x tile_b tokens, a cluster of `splits` to a tile; `two` of them on an SM.
 struct Plan {
@@ -697,8 +749,9 @@ struct Plan {
 // The cheapest by a model of a launch's microseconds, fitted to measurements: a start and an
 // end that grow with the tile, per wave the stages one after the other (or, if that is longer, the
 // operands and the outputs at the rates that they reach), and the joining of a shared contraction.
-// Measured (us): 1 token, 14336 x 4096: 9.3 alone, 9.4 in twos, 13.6 in fours; 1, 4096 x 14336: 20.1, 12.7,
-// 9.5, 9.6 in eights; 256, 4096 x 4096: 8.7 in tiles of 64, 9.5 of 128, 11.3 of 256, 9.6 in
+// Measured (us), the tokens' quantizer in front: 1 token, 14336 x 4096: 10.9 alone, 10.9 in twos, 14.5 in
+// fours; 1, 5120 x 25600: 21.8 in twos, 17.8 in threes; 64, 2048 x 8192: 11.6 in twos, 9.3 in fours,
+// 9.1 in fives; 100, 4096 x 4096: 10.1 in twos, 9.8 in fours.  The product alone: 256, 4096 x 4096: 8.7 in tiles of 64, 9.5 of 128, 11.3 of 256, 9.6 in
 // pairs; 300, 1024 x 4096: 7.1 in tiles of 128 in fours, 8.9 in pairs; 1001, 5120 x 5120: 18.6 in
 // pairs, 17.4 in pairs with tiles of 192, 21.4 alone; 1001, 3584 x 18944: 27.3, 24.8; 8192, 14336 x
 // 4096: 147, 160; 8192, 8192 x 256: 22.6 in pairs, 43.8 alone (outputs not staged).
@@ -708,7 +761,9 @@ Plan make_plan(int64_t M, int64_t N, int64_t K, bool f32, int sms, bool pairs, b
     const double operands = (double)(M + N) * (double)K * 17 / 32 / 6.2e6, out = (double)M * (double)N * (f32 ? 4 : 2);
     auto longer = [&](double waves, double per_wave, double out_rate) {
         const double moved = operands + out / out_rate;
-        return waves * per_wave > moved ? waves * per_wave : moved;
+        const double stages = waves * per_wave;
+        // (where the bytes are the bound, the shorter chain of stages: 1, 4096 x 14336 by 8: 11.2, by 3: 12.1)
+        return stages > moved ? stages : moved + 0.02 * stages;
     };
     const double direct = f32 ? 4.5e6 : 2.9e6;  // bytes a microsecond of outputs stored by the lanes
     Plan best = {};
@@ -728,15 +783,16 @@ Plan make_plan(int64_t M, int64_t N, int64_t K, bool f32, int sms, bool pairs, b
     for (int tile = 64;; tile *= 2) {
         const int b = M < tile ? (int)M : tile;
         const int64_t units = (N + BM - 1) / BM * ((M + b - 1) / b);
-        for (int s = 1; s <= 8; s *= 2) {
+        for (int s = 1; s <= 8; ++s) {
             // (every CTA has a part: the last one's begins before the stages end)
             const int64_t kps = (kstages + s - 1) / s;
             if (s > 1 && (kps < 2 || (s - 1) * kps >= kstages))
-                break;
-            const bool two = b <= 112 && (units * s > sms || kps <= 12);
-            const int64_t slots = two ? 2 * sms : sms;
-            if (s > 1 && units * s > slots)
-                break;
+                continue;
+            // (clusters, two CTAs on an SM: 1 token, 4608 x 8192 in fours: 8.9, in threes alone 9.6; but 2 tokens, 3584 x
+            // 18944 in fives: 13.6, in fours alone 12.5, and 64, 2560 x 10240 in eights: 11.5, in fives alone 10.0)
+            const bool two = s == 1 ? b <= 112 && (units > sms || kps <= 12) : b == 1 && !at_once(units, s, false);
+            if (s > 1 && !at_once(units, s, two))
+                continue;
             // (waves behind the first one share the memory system with others throughout: 1.35 of its time)
             const double waves = 1.35 * (double)((units * s + sms - 1) / sms) - 0.35;
             const double cost = 3.6 + 0.0075 * b + longer(waves, (double)kps * (0.26 + 0.0003 * b), direct) +
@@ -765,9 +821,9 @@ rlq_status launch_gemm_mxfp4(const uint8_t *xq, int64_t ldxq, const uint8_t *xs,
     if (K == 0) {
         p.a_rows = (int)N;
         p.b_rows = (int)M;
-        const int64_t blocks = (M * N + 255) / 256;
+        const int64_t blocks = (M * N + THREADS - 1) / THREADS;
         return cuda_status(launch_pdl(f32 ? k_zero_out<true> : k_zero_out<false>,
-                                      dim3((unsigned)(blocks < 8 * sms ? blocks : 8 * sms)), dim3(256), 0, st, p),
+                                      dim3((unsigned)(blocks < 6 * sms ? blocks : 6 * sms)), dim3(THREADS), 0, st, p),
                            "MXFP4 GEMM launch");
     }
     const int64_t ktiles = (K + 127) / 128;
@@ -819,8 +875,7 @@ rlq_status launch_gemm_mxfp4(const uint8_t *xq, int64_t ldxq, const uint8_t *xs,
     const int room = (two ? 232448 / 2 - 1024 : 232448) - 1024 - BARS_BYTES - (pair ? STAGING_BYTES : 0);
     p.stages = room / p.stage_bytes < MAX_STAGES ? room / p.stage_bytes : MAX_STAGES;
     const int slots = pair ? sms / 2 : two ? 2 * sms : sms;
-    while (1 << p.log2_splits < p.splits)
-        ++p.log2_splits;
+    p.splits_inv = (uint32_t)((65536 + p.splits - 1) / p.splits);
     CUtensorMap maps[5] = {};
     rlq_status r = encode(&maps[0], A.q, false, (K + 1) / 2, A.rows, A.ld, BM);
     if (r == RLQ_OK)

@@ -147,7 +147,16 @@ CUTS = [(270, 10029, 1034), (5117, 130, 266), (129, 6636, 849), (6970, 568, 779)
         (1, 1, 12291), (1, 1, 1565), (68, 1, 12354), (68, 1, 1537), (1, 1, 3586), (67, 1, 3627)]
 
 
-@pytest.mark.parametrize("M,N,K", SHAPES + CUTS)
+# clusters of 2 .. 8 CTAs: one or two tokens (also with two CTAs on an SM), a narrow tile, several of them, a wide one
+CLUSTERS = [(2, 6410, 1350), (67, 5467, 2331), (270, 1111, 1873), (2, 10, 1124), (129, 4044, 3140), (67, 2948, 2155),
+            (200, 2554, 2840), (67, 5, 1519), (1, 5266, 1054), (5, 26, 1177), (129, 2462, 4050), (270, 1025, 3629),
+            (2, 4103, 1592), (3, 27, 1833), (129, 1805, 3222), (67, 1589, 2255), (200, 1386, 3076), (300, 11, 2498),
+            (2, 2956, 2113), (2, 18, 2261), (129, 1746, 2872), (67, 1153, 2808), (256, 1063, 5411), (200, 2, 2913),
+            (2, 2537, 2628), (64, 5, 2731), (129, 1426, 4695), (67, 770, 3365), (200, 686, 8226), (2, 1554, 3180),
+            (67, 1, 3172), (17, 1, 3345), (129, 1374, 4014), (256, 649, 7574), (1, 1549, 3607), (115, 3, 5457)]
+
+
+@pytest.mark.parametrize("M,N,K", SHAPES + CUTS + CLUSTERS)
 def test_product_exact_sums(M, N, K):
     """Scales within 2^-1 .. 2^1: every product is a multiple of 2^-4 and at most 144, and
     where the magnitudes' sum stays below 2^24 of those units, as it is checked to, fp32 holds
