@@ -696,46 +696,54 @@ rlq_status launch(const CUtensorMap *maps, const Params &p, int grid, int cluste
                        "MXFP4 GEMM launch");
 }
 
-// Clusters of `s` single CTAs, one or two CTAs to an SM, that the current device runs at once: fewer
-// than their CTAs would fit, since a cluster stays within a group of SMs (one GB300, alone on an SM: 76,
-// 46, 36, 28, 23, 15 and 15 of 2 .. 8; others differ by one or two).
-int clusters_at_once(int s, bool two)
+// Clusters of s single CTAs, one ([0][s]) or two ([1][s]) CTAs to an SM, that the current device runs at
+// once: fewer than their CTAs would fit, since a cluster stays within a group of SMs (one GB300, alone on
+// an SM: 76, 46, 36, 28, 23, 15 and 15 of 2 .. 8; others differ by one or two).
+struct AtOnce {
+    int n[2][9];
+};
+
+const AtOnce &clusters_at_once()
 {
-    static std::atomic<int> known[64][2][9];
-    int dev = 0, n = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess)
-        return 0;
-    std::atomic<int> &k = known[dev & 63][two][s];
-    if ((n = k.load(std::memory_order_relaxed)) > 0)
-        return n - 1;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = s;
-    attr.val.clusterDim.y = 1;
-    attr.val.clusterDim.z = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)s);
-    cfg.blockDim = dim3(THREADS);
-    cfg.dynamicSmemBytes = two ? 232448 / 2 - 1024 : 232448;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    // (asked of a kernel that takes no tensor memory: of the others the query allows one CTA to an SM)
-    if (cudaFuncSetAttribute(k_zero_out<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448) != cudaSuccess ||
-        cudaOccupancyMaxActiveClusters(&n, k_zero_out<false>, &cfg) != cudaSuccess) {
-        cudaGetLastError();  // (not this call's: a contraction that is not shared)
-        return 0;
-    }
-    k.store(n + 1, std::memory_order_relaxed);
-    return n;
+    static AtOnce known[64];
+    static std::once_flag once[64];
+    int dev = 0;
+    cudaGetDevice(&dev);
+    std::call_once(once[dev & 63], [dev] {
+        for (int two = 0; two < 2; ++two)
+            for (int s = 1; s <= 8; ++s) {
+                cudaLaunchAttribute attr;
+                attr.id = cudaLaunchAttributeClusterDimension;
+                attr.val.clusterDim.x = s;
+                attr.val.clusterDim.y = 1;
+                attr.val.clusterDim.z = 1;
+                cudaLaunchConfig_t cfg = {};
+                cfg.gridDim = dim3((unsigned)s);
+                cfg.blockDim = dim3(THREADS);
+                cfg.dynamicSmemBytes = two ? 232448 / 2 - 1024 : 232448;
+                cfg.attrs = &attr;
+                cfg.numAttrs = 1;
+                // (asked of a kernel that takes no tensor memory: of the others the query allows one CTA to an SM)
+                int n = 0;
+                if (cudaFuncSetAttribute(k_zero_out<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448) !=
+                        cudaSuccess ||
+                    cudaOccupancyMaxActiveClusters(&n, k_zero_out<false>, &cfg) != cudaSuccess) {
+                    cudaGetLastError();  // (not this call's: contractions are not shared)
+                    n = 0;
+                }
+                known[dev & 63].n[two][s] = n;
+            }
+    });
+    return known[dev & 63];
 }
 
 // Whether so many clusters run at once beside the kernels around them, which may keep some of the SMs: not
 // the last tenth of the clusters, of five CTAs and more not the last sixth (16 tokens, 3584 x
 // 18944 in 28 of 28 clusters of five 16.8 us, in fours 14.3; 100 tokens, 2560 x 10240 in 20 of
 // 23 of six 12.8, in as many of two CTAs an SM 11.1).
-bool at_once(int64_t units, int s, bool two)
+bool at_once(const AtOnce &c, int64_t units, int s, bool two)
 {
-    const int64_t n = clusters_at_once(s, two);
+    const int64_t n = c.n[two][s];
     return s < 3 ? units <= n : s < 5 ? 10 * units <= 9 * n : 20 * units <= 17 * n;
 }
 
@@ -765,6 +773,7 @@ Plan make_plan(int64_t M, int64_t N, int64_t K, bool f32, int sms, bool pairs, b
         // (where the bytes are the bound, the shorter chain of stages: 1, 4096 x 14336 by 8: 11.2, by 3: 12.1)
         return stages > moved ? stages : moved + 0.02 * stages;
     };
+    const AtOnce &clusters = clusters_at_once();
     const double direct = f32 ? 4.5e6 : 2.9e6;  // bytes a microsecond of outputs stored by the lanes
     Plan best = {};
     double least = 1e300;
@@ -790,8 +799,8 @@ Plan make_plan(int64_t M, int64_t N, int64_t K, bool f32, int sms, bool pairs, b
                 continue;
             // (clusters, two CTAs on an SM: 1 token, 4608 x 8192 in fours: 8.9, in threes alone 9.6; but 2 tokens, 3584 x
             // 18944 in fives: 13.6, in fours alone 12.5, and 64, 2560 x 10240 in eights: 11.5, in fives alone 10.0)
-            const bool two = s == 1 ? b <= 112 && (units > sms || kps <= 12) : b == 1 && !at_once(units, s, false);
-            if (s > 1 && !at_once(units, s, two))
+            const bool two = s == 1 ? b <= 112 && (units > sms || kps <= 12) : b == 1 && !at_once(clusters, units, s, false);
+            if (s > 1 && !at_once(clusters, units, s, two))
                 continue;
             // (waves behind the first one share the memory system with others throughout: 1.35 of its time)
             const double waves = 1.35 * (double)((units * s + sms - 1) / sms) - 0.35;
