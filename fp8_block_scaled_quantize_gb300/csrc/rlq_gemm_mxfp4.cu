@@ -68,6 +68,7 @@ struct Params {
     void *y;
     int64_t ldy;
     int staged;                  // A is X, and y is stored by TMA; else A is W, and a lane stores its column of y
+    int ragged;                  // (staged) y's rows end inside 16 bytes, the unit in which a TMA store is cut off
     int a_rows, b_rows;
     int kstages, last_steps;     // stages, and instructions (64 elements) of the last one
     int b_tiles, units, tile_b;  // tiles of B, (A tile, B tile) units, rows of a B tile
@@ -472,13 +473,24 @@ __global__ void __launch_bounds__(THREADS)
                 if (kPair && p.staged) {
 #pragma unroll
                     for (int h = 0; h < (kF32 ? 2 : 1); ++h) {
+                        const int x = (int)br + c0 + 32 * h, y = (int)ar - lane;
+                        if (p.ragged && x + (kF32 ? 32 : 64) > p.b_rows) {
+                            // the box that the end of y's rows cuts inside 16 bytes: element by element
+                            if (ar < p.a_rows) {
+                                const int64_t at = ar * p.ldy + x;
+#pragma unroll
+                                for (int j = 0; j < (kF32 ? 32 : 64); ++j)
+                                    if (x + j < p.b_rows)
+                                        store_out<kF32>(p, at + j, __uint_as_float(r[(kF32 ? h : j / 32) % (PIECE / 32)][j % 32]));
+                            }
+                            continue;
+                        }
                         if (lane == 0)  // the copy engine has read the box
                             asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
                         __syncwarp();
                         stage_row<kF32>(box, lane, r[h], r[PIECE / 32 - 1]);
                         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                         __syncwarp();
-                        const int x = (int)br + c0 + 32 * h, y = (int)ar - lane;
                         if (lane == 0 && x < p.b_rows && y < p.a_rows) {
                             tma_store_2d_hint(&tmOut, box, x, y, policy);
                             asm volatile("cp.async.bulk.commit_group;" ::: "memory");
@@ -844,6 +856,7 @@ rlq_status launch_gemm_mxfp4(const uint8_t *xq, int64_t ldxq, const uint8_t *xs,
     const Plan plan = make_plan(M, N, K, f32, sms, !p.withhold, aligned);
     const bool pair = plan.pair;
     p.staged = pair && aligned;
+    p.ragged = N * (f32 ? 4 : 2) % 16 != 0;
     struct Operand {
         const uint8_t *q;
         int64_t ld;

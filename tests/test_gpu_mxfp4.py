@@ -248,6 +248,22 @@ def test_product_outputs_and_pitches():
             assert (buf == 3).all()
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("M,N,K,ldy", [(300, 5681, 64, 5696), (300, 5682, 64, 5688), (300, 5683, 64, 5692), (301, 5685, 33, 5688),
+                                       (300, 5687, 64, 5688), (300, 5684, 64, 5688), (700, 2499, 40, 2504), (261, 4100, 600, 4104),
+                                       (129, 8129, 90, 8136), (200, 4893, 494, 4896), (200, 4909, 594, 4912)])
+def test_product_leaves_the_elements_beside_its_rows(M, N, K, ldy, dtype):
+    """Rows that end anywhere inside 16 bytes, at pitches that are multiples of them (and of 8 bytes only)."""
+    g = gen(M + N)
+    xq, xs, x = R.operand(g, M, K, -1, 1)
+    wq, ws, w = R.operand(g, N, K, -1, 1)
+    buf = torch.full((M + 1, ldy), 7.0, dtype=dtype, device=DEV)
+    rlq.gemm_mxfp4(xq, xs, wq, ws, out=buf[:M, :N])
+    rlq.check()
+    assert torch.equal(buf[:M, :N], (x @ w.t()).float().to(dtype))
+    assert bool((buf[:, N:] == 7).all()) and bool((buf[M] == 7).all())
+
+
 def test_product_empty_contraction_and_empty_outputs():
     u8 = lambda *s: torch.empty(*s, dtype=torch.uint8, device=DEV)  # noqa: E731
     y = rlq.gemm_mxfp4(u8(5, 0), u8(1, 0, 32, 4, 4), u8(7, 0), u8(1, 0, 32, 4, 4))
