@@ -366,10 +366,11 @@ __global__ void __launch_bounds__(THREADS, CTAS_SM) k_token_stats(const TokenSta
         if (rank == 0) {
             if (t == 0)
                 p.lp[row] = p.lse[row] = p.entropy[row] = 0.0f;
-            if (kTop && t < p.top) {
-                ids[t] = -1;
-                top_lp[t] = 0.0f;
-            }
+            if (kTop)
+                for (int i = t; i < p.top; i += threads) {  // (a short row has fewer threads than alternatives)
+                    ids[i] = -1;
+                    top_lp[i] = 0.0f;
+                }
         }
         return;
     }

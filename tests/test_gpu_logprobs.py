@@ -279,6 +279,22 @@ def test_gradient(T, V, dtype, which):
     assert torch.equal(far[:, :V], d) and bool((far[:, V:] == 9).all())
 
 
+@pytest.mark.parametrize("dtype,V,top", [("bf16", 64, 64), ("bf16", 115, 64), ("bf16", 249, 33), ("f32", 64, 64), ("f32", 130, 50),
+                                         ("bf16", 700, 64), ("f32", 40000, 64)])
+def test_empty_rows_have_every_alternative_empty(dtype, V, top):
+    """Also where a short row has fewer threads than alternatives."""
+    g = gen(52)
+    x, targets = logits_of(g, 6, V, dtype)
+    targets[::2] = torch.tensor([-1, V, -100], device=DEV)
+    for _ in range(2):  # (what an output's memory held before is not what is found there)
+        junk = [torch.full((6, top), 77, dtype=torch.int64, device=DEV), torch.full((6, top), 77.0, device=DEV)]
+        del junk
+        lp, lse, H, ids, top_lp = rlq.token_logprobs_top(x, targets, top=top)
+        assert bool((ids[::2] == -1).all()) and not top_lp[::2].any()
+        assert not lp[::2].any() and not lse[::2].any() and not H[::2].any()
+        assert torch.equal(ids[1::2], torch.sort(x.float(), dim=1, descending=True, stable=True)[1][1::2, :top])
+
+
 @pytest.mark.parametrize("dtype,left,V,ld", [("bf16", 0, 1000, 4096), ("bf16", 3, 1001, 4099), ("f32", 1, 37, 2050)])
 def test_gradient_of_a_part_of_wide_rows(dtype, left, V, ld):
     """The gradient's rows are no wider than their phases need, and the columns beside the part are not read."""
