@@ -552,12 +552,58 @@ cudaError_t launch_stats(const TokenStatsArgs &p, cudaStream_t st)
 
 constexpr int BWD_BATCH = 4, BWD_ROUNDS = 2;  // loads in flight a thread, and batches of them
 
+// From here on an lse has too little of fp32 left for what it is subtracted from (2^-17 of a probability).
+constexpr float FAR = 256.0f;
+
+// Maximum and log2 of the sum of a row, read by one CTA, in every thread; the maximum is -inf where
+// every logit is, and the sum NaN where one is a NaN or +inf.
+template <typename T>
+__device__ __forceinline__ float2 row_sums(const T *x, int V, int off, float c)
+{
+    using E = Elem<T>;
+    constexpr int N = E::N;
+    __shared__ float part[WARPS + 1];
+    const int t = threadIdx.x, threads = blockDim.x, lane = t & 31, warp = t >> 5, nw = threads >> 5;
+    const Part<T> row = {x, V, off, 0, (off + V + N - 1) / N, off ? 1 : 0, (off + V) / N};
+    float m = -INFINITY;
+#pragma unroll 1
+    for (int u = t; u < row.u1; u += threads)
+        m = E::max_of(m, row.load(u));
+    for (int o = 16; o; o >>= 1)
+        m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+    if (lane == 0)
+        part[warp] = m;
+    __syncthreads();
+    for (int i = 0; i < nw; ++i)
+        m = fmaxf(m, part[i]);
+    __syncthreads();
+    if (m == -INFINITY)
+        return make_float2(m, 0.0f);
+    float s = 0.0f;
+#pragma unroll 1
+    for (int u = t; u < row.u1; u += threads)
+        row.each(u, [&](float v, int) { s += ex2((v - m) * c); });
+    for (int o = 16; o; o >>= 1)
+        s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+    if (lane == 0)
+        part[warp] = s;
+    __syncthreads();
+    s = 0.0f;
+    for (int i = 0; i < nw; ++i)
+        s += part[i];
+    return make_float2(m, log2f(s));
+}
+
 // A CTA takes BWD_ROUNDS x BWD_BATCH units a thread of one row.  In units of log 2, log2 p =
 // x c - L with c = log2(e) / temperature, L = lse log2(e), each a sum of two floats: one would
 // put an error of 2^-24 |x c| into the exponent, some 10^-6 of a likely token's probability, and
-// powers of two where a mask of -10^9 leaves a row nothing else.
+// powers of two where a mask of -10^9 leaves a row nothing else.  There the lse itself has lost the
+// sum's logarithm: of a row with such an lse the first CTA forms the sum again, and takes all of the
+// row, since in place the others would overwrite what it reads.
+// (Five CTAs an SM: without that bound the far rows' part costs the bf16 kernel 10 registers and
+// 4096 x 128256 4%.)
 template <typename T>
-__global__ void __launch_bounds__(THREADS) k_token_grad(const TokenGradArgs p, int parts)
+__global__ void __launch_bounds__(THREADS, 5) k_token_grad(const TokenGradArgs p, int parts)
 {
     pdl_begin();
     using E = Elem<T>;
@@ -568,7 +614,7 @@ __global__ void __launch_bounds__(THREADS) k_token_grad(const TokenGradArgs p, i
     T *dx = reinterpret_cast<T *>(p.dlogits) + row * p.ldd;
     const int off = (int)((reinterpret_cast<uintptr_t>(x) & 15) / sizeof(T));
     const int span = BWD_BATCH * BWD_ROUNDS * threads;
-    const int u0 = partno * span, u1 = min(u0 + span, (off + V + N - 1) / N);
+    const int units = (off + V + N - 1) / N, u0 = partno * span, u1 = min(u0 + span, units);
     const int whole0 = off ? 1 : 0, whole1 = (off + V) / N;
     // the gradient's rows share the logits' 16-byte phase: whole units leave as one store
     const bool vec = ((reinterpret_cast<uintptr_t>(dx) ^ reinterpret_cast<uintptr_t>(x)) & 15) == 0;
@@ -580,20 +626,67 @@ __global__ void __launch_bounds__(THREADS) k_token_grad(const TokenGradArgs p, i
     };
     const int64_t target = p.targets[row];
     const float dlp = p.dlp ? p.dlp[row] : 0.0f, dH = p.dentropy ? p.dentropy[row] : 0.0f, lse = p.lse[row];
-    if (target < 0 || target >= V || (dlp == 0.0f && dH == 0.0f) || lse == -INFINITY) {  // an empty row
+    if (target < 0 || target >= V || (dlp == 0.0f && dH == 0.0f)) {  // an empty row
         for (int u = u0 + t; u < u1; u += threads)
             store(u, make_uint4(0, 0, 0, 0));
         return;
     }
     const double L = (double)lse * 1.4426950408889634074;
-    const float L_hi = (float)L, L_lo = (float)(L - L_hi);
     const float inv = 1.0f / p.temperature;
     // (a row that met a NaN has lse NaN, which the maximum below would drop)
     const float a = lse != lse ? lse : -(dlp + (dH == 0.0f ? 0.0f : dH * p.entropy[row])) * inv;
     const float b = -dH * LN2 * inv, at_target = dlp * inv;
     const float2 a2 = make_float2(a, a), b2 = make_float2(b, b), c2 = make_float2(p.c_hi, p.c_hi),
-                 cl2 = make_float2(p.c_lo, p.c_lo), nL2 = make_float2(-L_hi, -L_hi), nLl2 = make_float2(-L_lo, -L_lo);
+                 cl2 = make_float2(p.c_lo, p.c_lo);
     const int te = (int)target + off, ut = te / N, jt = te - ut * N;
+    // unit w's gradient, from logits less `ref` with log2 of their sum L_hi + L_lo
+    auto unit = [&](int w, const uint4 &v, auto minus_ref, float L_hi, float L_lo) {
+        const float2 nL2 = make_float2(-L_hi, -L_hi), nLl2 = make_float2(-L_lo, -L_lo);
+        float2 f[N / 2];
+#pragma unroll
+        for (int j = 0; j < N / 2; ++j) {
+            const float2 e = minus_ref(E::get2(v, j));
+            float2 z = __fadd2_rn(__ffma2_rn(e, c2, nL2), __ffma2_rn(e, cl2, nLl2));
+            // (logits of -inf: 2^LOWEST is 0)
+            z = make_float2(fmaxf(z.x, LOWEST), fmaxf(z.y, LOWEST));
+            f[j] = __fmul2_rn(make_float2(ex2(z.x), ex2(z.y)), __ffma2_rn(b2, z, a2));
+        }
+        if (w == ut) {
+#pragma unroll
+            for (int j = 0; j < N; ++j)
+                if (j == jt) {
+                    if (j & 1)
+                        f[j / 2].y += at_target;
+                    else
+                        f[j / 2].x += at_target;
+                }
+        }
+        store(w, E::pack(f));
+    };
+    float L_hi = (float)L, L_lo = (float)(L - L_hi);
+    if (fabsf(lse) > FAR) {
+        if (partno > 0)
+            return;
+        const float2 own = row_sums(x, V, off, p.c_hi);
+        const float own_lse = fmaf(own.x, inv, LN2 * own.y);
+        // (an lse that is not these logits' stays what it is; without logits above -inf all is 0)
+        const bool same = own_lse == lse || fabsf(own_lse - lse) <= fabsf(lse) * 0x1p-22f;
+        const bool none = own.x == -INFINITY && lse == -INFINITY;
+        const float ref = same && !none ? own.x : 0.0f;
+        if (same) {
+            L_hi = own.y;
+            L_lo = 0.0f;
+        }
+        const Part<T> all = {x, V, off, 0, units, whole0, whole1};
+#pragma unroll 1
+        for (int w = t; w < units; w += threads) {
+            if (none)
+                store(w, make_uint4(0, 0, 0, 0));
+            else
+                unit(w, all.load(w), [&](float2 e) { return __fadd2_rn(e, make_float2(-ref, -ref)); }, L_hi, L_lo);
+        }
+        return;
+    }
 #pragma unroll 1
     for (int r = 0; r < BWD_ROUNDS; ++r) {
         const int u = u0 + t + r * BWD_BATCH * threads;
@@ -609,26 +702,7 @@ __global__ void __launch_bounds__(THREADS) k_token_grad(const TokenGradArgs p, i
             const int w = u + i * threads;
             if (w >= u1)
                 break;
-            float2 f[N / 2];
-#pragma unroll
-            for (int j = 0; j < N / 2; ++j) {
-                const float2 e = E::get2(v[i], j);
-                float2 z = __fadd2_rn(__ffma2_rn(e, c2, nL2), __ffma2_rn(e, cl2, nLl2));
-                // (logits of -inf: 2^LOWEST is 0)
-                z = make_float2(fmaxf(z.x, LOWEST), fmaxf(z.y, LOWEST));
-                f[j] = __fmul2_rn(make_float2(ex2(z.x), ex2(z.y)), __ffma2_rn(b2, z, a2));
-            }
-            if (w == ut) {
-#pragma unroll
-                for (int j = 0; j < N; ++j)
-                    if (j == jt) {
-                        if (j & 1)
-                            f[j / 2].y += at_target;
-                        else
-                            f[j / 2].x += at_target;
-                    }
-            }
-            store(w, E::pack(f));
+            unit(w, v[i], [](float2 e) { return e; }, L_hi, L_lo);
         }
     }
 }

@@ -705,8 +705,10 @@ rlq_status rlq_token_logprobs_top(const void *logits, rlq_dtype dtype, int64_t l
  *   dlp, dentropy f32 [rows]; one of them may be NULL (zeros)
  *   dlogits       [rows, V] of `dtype`, pitch ldd >= V (output); may be logits itself (in
  *                 place, same pitch)
- * p_v is that of the lse given: an lse far from 0 carries its own rounding into every
- * probability of the row (|lse| 100: 4e-6 of it; 10^4: 5e-4).
+ * p_v is that of the lse given, whose rounding every probability of the row has (|lse| 100: 4e-6
+ * of it).  Where |lse| is above 256, or it is infinite since fp32 does not reach so far, and is
+ * that of the row's logits, the row's sum is formed again: a row of masks of -10^9 only has
+ * probabilities 1 / V.
  * A row whose target is outside [0, V), or whose derivatives are both 0, is empty: its logits
  * are not read and its gradient is zeros.  So is that of a row of -inf logits only (lse =
  * -inf).  A row whose lse is NaN has a gradient of NaN.  Other arguments and limits as for

@@ -194,11 +194,11 @@ def test_forward_rows_of_masks_only(dtype):
     check_forward(x, targets, 5, 1.0, got)
     n = torch.tensor([V, V, V / 2, V], device=DEV)
     assert bool(((got[2] - n.log()).abs() <= 1e-5).all())
-    # the gradient is of the lse that it is given, which holds no log V next to 1e9
+    # the gradient's probabilities are uniform too, although the lse holds no log V next to 1e9
     one = torch.ones(4, device=DEV)
     d = rlq.token_logprobs_backward(x, targets, got[1], got[2], dlp=one, dentropy=one)
-    want, tol = gradient(x[1:2], targets[1:2], got[1][1:2], got[2][1:2], one[1:2], one[1:2], 1.0)
-    assert bool(((d[1:2].to(D) - want).abs() <= tol).all())
+    want, tol = gradient_of_rows(x, targets, got[2], one, one, 1.0)
+    assert bool(((d.to(D) - want).abs() <= tol).all())
 
 
 def test_forward_far_offsets():
@@ -316,6 +316,77 @@ def test_gradient_of_a_part_of_wide_rows(dtype, left, V, ld):
     assert torch.equal(rlq.token_logprobs_backward(y, targets, lse, H, dlp=a, dentropy=h), d)
 
 
+def gradient_of_rows(x, targets, H, dlp, dH, temperature):
+    """The gradient in 64 bits from the rows' own sums (H as given), and the bound where the kernel forms them."""
+    c = 1 / fp32(temperature)
+    V = x.shape[1]
+    m = x.to(D).amax(1, keepdim=True).clamp(min=-3.5e38)
+    z = (x.to(D) - m) * c
+    lg = z - z.exp().sum(1, keepdim=True).log()
+    p = lg.exp()
+    lg = torch.where(p < 2.0 ** -200, torch.zeros_like(lg), lg)
+    a, h, Hc = dlp.to(D)[:, None], dH.to(D)[:, None], H.to(D)[:, None]
+    at = torch.zeros_like(p).scatter_(1, targets[:, None], 1.0) * a * c
+    d = at - p * (a + h * (lg + Hc)) * c
+    # log2 p: the difference to the maximum, its product, the sum's logarithm and their sum; the sum: at
+    # most V / 256 + 16 terms one after the other, 13 joined, each an exponential 2 ulp off
+    t = lg.abs() * 1.4427
+    err_t = 6 * U * t + 4 * U * math.log2(V + 1) + 1.4427 * (V / 256 + 35) * U
+    size = (a.abs() + h.abs() * (lg.abs() + Hc.abs())) * c
+    tol = p * (size * (0.7 * err_t + 12 * U) + h.abs() * c * 0.7 * err_t) + 4 * U * at.abs()
+    tol = tol + 2.0 ** -125 * (a.abs() + h.abs() * (100 + Hc.abs())) * c
+    half = 2.0 ** -8 if x.dtype == torch.bfloat16 else 2.0 ** -23
+    return d, tol + half * (d.abs() + tol) + 2.0 ** -133
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("V,temperature", [(1, 1.0), (6, 0.3), (47, 0.3), (1000, 1.0), (5000, 0.3), (40000, 2.0), (40001, 0.3)])
+def test_gradient_of_rows_far_from_zero(V, temperature, dtype):
+    """Logits whose lse, or whose lse's logarithm of a sum, fp32 does not hold."""
+    g = gen(53)
+    T = 10
+    x, targets = logits_of(g, T, V, dtype)
+    low = torch.finfo(x.dtype).min
+    x[0] = -1e9
+    x[1] = low
+    x[2, 1:] = low
+    x[3] = torch.finfo(x.dtype).max
+    x[4] = (x[4].float() + 1e6).to(x.dtype)
+    x[5] *= 1e4
+    x[6] = -1e9
+    x[6, 1::2] = -math.inf
+    x[7] -= 700
+    x[8] = -math.inf
+    targets[6] = 0
+    a, h = torch.randn(T, generator=g, device=DEV), torch.randn(T, generator=g, device=DEV) * 0.1
+    lp, lse, H, _, _ = rlq.token_logprobs_top(x, targets, temperature=temperature)
+    d = rlq.token_logprobs_backward(x, targets, lse, H, dlp=a, dentropy=h, temperature=temperature)
+    want, tol = gradient_of_rows(x, targets, H, a, h, temperature)
+    rows = [r for r in range(T) if r != 8 and float(lse[r].abs()) > 256]
+    off = (d.to(D) - want).abs()[rows]
+    assert len(rows) >= 5 and bool((off <= tol[rows]).all())
+    assert not d[8].any()
+    y = x.clone()
+    rlq.token_logprobs_backward(y, targets, lse, H, dlp=a, dentropy=h, temperature=temperature, inplace=True)
+    assert torch.equal(y, d)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_gradient_takes_an_lse_that_is_not_the_rows(dtype):
+    """A part of a vocabulary has the lse of the whole one, near to 0 or far from it."""
+    g = gen(54)
+    T, V = 5, 3000
+    x, targets = logits_of(g, T, V, dtype)
+    x[1] += 1000
+    x[2] -= 1000
+    a, h = torch.randn(T, generator=g, device=DEV), torch.randn(T, generator=g, device=DEV) * 0.1
+    _, lse, H, _, _ = rlq.token_logprobs_top(x, targets)
+    for shift in (0.5, 3.0, 200.0):
+        d = rlq.token_logprobs_backward(x, targets, lse + shift, H, dlp=a, dentropy=h)
+        want, tol = gradient(x, targets, lse + shift, H, a, h, 1.0)
+        assert bool(((d.to(D) - want).abs() <= tol).all())
+
+
 def test_gradient_against_differences():
     """A loss of both outputs, differentiated numerically in 64 bits."""
     g = gen(50)
@@ -429,7 +500,10 @@ def test_temperatures(temperature):
     check_forward(x, targets, 7, temperature, got)
     a, h = torch.randn(20, generator=g, device=DEV), torch.randn(20, generator=g, device=DEV)
     d = rlq.token_logprobs_backward(x, targets, got[1], got[2], dlp=a, dentropy=h, temperature=temperature)
-    want, tol = gradient(x, targets, got[1], got[2], a, h, temperature)
+    # (far from 0 the rows' own sums count, not the lse's rounding of them)
+    far = (got[1].abs() > 256)[:, None]
+    given, own = gradient(x, targets, got[1], got[2], a, h, temperature), gradient_of_rows(x, targets, got[2], a, h, temperature)
+    want, tol = (torch.where(far, o, e) for o, e in zip(own, given))
     assert bool(((d.to(D) - want).abs() <= tol).all())
 
 
