@@ -594,58 +594,59 @@ __device__ __forceinline__ float2 row_sums(const T *x, int V, int off, float c)
     return make_float2(m, log2f(s));
 }
 
-// A CTA takes BWD_ROUNDS x BWD_BATCH units a thread of one row.  In units of log 2, log2 p =
-// x c - L with c = log2(e) / temperature, L = lse log2(e), each a sum of two floats: one would
-// put an error of 2^-24 |x c| into the exponent, some 10^-6 of a likely token's probability, and
-// powers of two where a mask of -10^9 leaves a row nothing else.  There the lse itself has lost the
-// sum's logarithm: of a row with such an lse the first CTA forms the sum again, and takes all of the
-// row, since in place the others would overwrite what it reads.
-// (Five CTAs an SM: without that bound the far rows' part costs the bf16 kernel 10 registers and
-// 4096 x 128256 4%.)
+// A row and what its gradient takes.
 template <typename T>
-__global__ void __launch_bounds__(THREADS, 5) k_token_grad(const TokenGradArgs p, int parts)
-{
-    pdl_begin();
+struct GradRow {
     using E = Elem<T>;
-    constexpr int N = E::N;
-    const int64_t row = blockIdx.x / parts;
-    const int partno = (int)(blockIdx.x - row * parts), V = (int)p.V, t = threadIdx.x, threads = blockDim.x;
-    const T *x = reinterpret_cast<const T *>(p.logits) + row * p.ld;
-    T *dx = reinterpret_cast<T *>(p.dlogits) + row * p.ldd;
-    const int off = (int)((reinterpret_cast<uintptr_t>(x) & 15) / sizeof(T));
-    const int span = BWD_BATCH * BWD_ROUNDS * threads;
-    const int units = (off + V + N - 1) / N, u0 = partno * span, u1 = min(u0 + span, units);
-    const int whole0 = off ? 1 : 0, whole1 = (off + V) / N;
-    // the gradient's rows share the logits' 16-byte phase: whole units leave as one store
-    const bool vec = ((reinterpret_cast<uintptr_t>(dx) ^ reinterpret_cast<uintptr_t>(x)) & 15) == 0;
-    auto store = [&](int u, uint4 v) {
+    static constexpr int N = E::N;
+    const T *x;
+    T *dx;
+    int V, off, units, whole0, whole1;
+    bool vec, empty;
+    float lse, inv, a, b, at_target;
+    int ut, jt;
+
+    __device__ __forceinline__ GradRow(const TokenGradArgs &p, int64_t row)
+    {
+        V = (int)p.V;
+        x = reinterpret_cast<const T *>(p.logits) + row * p.ld;
+        dx = reinterpret_cast<T *>(p.dlogits) + row * p.ldd;
+        off = (int)((reinterpret_cast<uintptr_t>(x) & 15) / sizeof(T));
+        units = (off + V + N - 1) / N;
+        whole0 = off ? 1 : 0;
+        whole1 = (off + V) / N;
+        // the gradient's rows share the logits' 16-byte phase: whole units leave as one store
+        vec = ((reinterpret_cast<uintptr_t>(dx) ^ reinterpret_cast<uintptr_t>(x)) & 15) == 0;
+        const int64_t target = p.targets[row];
+        const float dlp = p.dlp ? p.dlp[row] : 0.0f, dH = p.dentropy ? p.dentropy[row] : 0.0f;
+        lse = p.lse[row];
+        empty = target < 0 || target >= V || (dlp == 0.0f && dH == 0.0f);
+        inv = 1.0f / p.temperature;
+        // (a row that met a NaN has lse NaN, which the maximum below would drop)
+        a = lse != lse ? lse : -(dlp + (dH == 0.0f ? 0.0f : dH * p.entropy[row])) * inv;
+        b = -dH * LN2 * inv;
+        at_target = dlp * inv;
+        const int te = (int)target + off;
+        ut = te / N;
+        jt = te - ut * N;
+    }
+    __device__ __forceinline__ void store(int u, uint4 v) const
+    {
         if (vec && u >= whole0 && u < whole1)
             __stcs(reinterpret_cast<uint4 *>(dx + ((int64_t)u * N - off)), v);
         else
             store_cut(dx, u * N - off, V, v);
-    };
-    const int64_t target = p.targets[row];
-    const float dlp = p.dlp ? p.dlp[row] : 0.0f, dH = p.dentropy ? p.dentropy[row] : 0.0f, lse = p.lse[row];
-    if (target < 0 || target >= V || (dlp == 0.0f && dH == 0.0f)) {  // an empty row
-        for (int u = u0 + t; u < u1; u += threads)
-            store(u, make_uint4(0, 0, 0, 0));
-        return;
     }
-    const double L = (double)lse * 1.4426950408889634074;
-    const float inv = 1.0f / p.temperature;
-    // (a row that met a NaN has lse NaN, which the maximum below would drop)
-    const float a = lse != lse ? lse : -(dlp + (dH == 0.0f ? 0.0f : dH * p.entropy[row])) * inv;
-    const float b = -dH * LN2 * inv, at_target = dlp * inv;
-    const float2 a2 = make_float2(a, a), b2 = make_float2(b, b), c2 = make_float2(p.c_hi, p.c_hi),
-                 cl2 = make_float2(p.c_lo, p.c_lo);
-    const int te = (int)target + off, ut = te / N, jt = te - ut * N;
-    // unit w's gradient, from logits less `ref` with log2 of their sum L_hi + L_lo
-    auto unit = [&](int w, const uint4 &v, auto minus_ref, float L_hi, float L_lo) {
-        const float2 nL2 = make_float2(-L_hi, -L_hi), nLl2 = make_float2(-L_lo, -L_lo);
+    // Unit w's gradient, from logits less ref(...) with log2 of their sum L_hi + L_lo.
+    template <typename F>
+    __device__ __forceinline__ void unit(const TokenGradArgs &p, int w, const uint4 &v, float L_hi, float L_lo, F less_ref) const
+    {
+        const float2 a2 = make_float2(a, a), b2 = make_float2(b, b), c2 = make_float2(p.c_hi, p.c_hi),
+                     cl2 = make_float2(p.c_lo, p.c_lo), nL2 = make_float2(-L_hi, -L_hi), nLl2 = make_float2(-L_lo, -L_lo);
         float2 f[N / 2];
 #pragma unroll
         for (int j = 0; j < N / 2; ++j) {
-            const float2 e = minus_ref(E::get2(v, j));
+            const float2 e = less_ref(E::get2(v, j));
             float2 z = __fadd2_rn(__ffma2_rn(e, c2, nL2), __ffma2_rn(e, cl2, nLl2));
             // (logits of -inf: 2^LOWEST is 0)
             z = make_float2(fmaxf(z.x, LOWEST), fmaxf(z.y, LOWEST));
@@ -662,31 +663,68 @@ __global__ void __launch_bounds__(THREADS, 5) k_token_grad(const TokenGradArgs p
                 }
         }
         store(w, E::pack(f));
-    };
+    }
+};
+
+// A row whose lse is FAR from 0 or infinite, by one CTA.  (A call, and five CTAs an SM, so that it costs
+// the others nothing: 4096 x 128256 bf16 284 us, 292 without the bound; 2048 x 1000 5.3, 5.5 as a
+// part of the kernel.)
+template <typename T>
+__device__ __noinline__ void far_row(const TokenGradArgs &p, int64_t row)
+{
+    const GradRow<T> g(p, row);
+    const int t = threadIdx.x, threads = blockDim.x;
+    const double L = (double)g.lse * 1.4426950408889634074;
     float L_hi = (float)L, L_lo = (float)(L - L_hi);
-    if (fabsf(lse) > FAR) {
-        if (partno > 0)
-            return;
-        const float2 own = row_sums(x, V, off, p.c_hi);
-        const float own_lse = fmaf(own.x, inv, LN2 * own.y);
-        // (an lse that is not these logits' stays what it is; without logits above -inf all is 0)
-        const bool same = own_lse == lse || fabsf(own_lse - lse) <= fabsf(lse) * 0x1p-22f;
-        const bool none = own.x == -INFINITY && lse == -INFINITY;
-        const float ref = same && !none ? own.x : 0.0f;
-        if (same) {
-            L_hi = own.y;
-            L_lo = 0.0f;
-        }
-        const Part<T> all = {x, V, off, 0, units, whole0, whole1};
+    const float2 own = row_sums(g.x, g.V, g.off, p.c_hi);
+    const float own_lse = fmaf(own.x, g.inv, LN2 * own.y);
+    // (an lse that is not these logits' stays what it is; without logits above -inf all is 0)
+    const bool same = own_lse == g.lse || fabsf(own_lse - g.lse) <= fabsf(g.lse) * 0x1p-22f;
+    const bool none = own.x == -INFINITY && g.lse == -INFINITY;
+    const float nref = same && !none ? -own.x : 0.0f;
+    if (same) {
+        L_hi = own.y;
+        L_lo = 0.0f;
+    }
+    const Part<T> all = {g.x, g.V, g.off, 0, g.units, g.whole0, g.whole1};
 #pragma unroll 1
-        for (int w = t; w < units; w += threads) {
-            if (none)
-                store(w, make_uint4(0, 0, 0, 0));
-            else
-                unit(w, all.load(w), [&](float2 e) { return __fadd2_rn(e, make_float2(-ref, -ref)); }, L_hi, L_lo);
-        }
+    for (int w = t; w < g.units; w += threads) {
+        if (none)
+            g.store(w, make_uint4(0, 0, 0, 0));
+        else
+            g.unit(p, w, all.load(w), L_hi, L_lo, [&](float2 e) { return __fadd2_rn(e, make_float2(nref, nref)); });
+    }
+}
+
+// A CTA takes BWD_ROUNDS x BWD_BATCH units a thread of one row.  In units of log 2, log2 p =
+// x c - L with c = log2(e) / temperature, L = lse log2(e), each a sum of two floats: one would
+// put an error of 2^-24 |x c| into the exponent, some 10^-6 of a likely token's probability, and
+// powers of two where a mask of -10^9 leaves a row nothing else.  There the lse itself has lost the
+// sum's logarithm: of a row with such an lse the first CTA forms the sum again, and takes all of the
+// row, since in place the others would overwrite what it reads.
+template <typename T>
+__global__ void __launch_bounds__(THREADS, 5) k_token_grad(const __grid_constant__ TokenGradArgs p, int parts)
+{
+    pdl_begin();
+    using E = Elem<T>;
+    constexpr int N = E::N;
+    const int64_t row = blockIdx.x / parts;
+    const int partno = (int)(blockIdx.x - row * parts), t = threadIdx.x, threads = blockDim.x;
+    const GradRow<T> g(p, row);
+    const int span = BWD_BATCH * BWD_ROUNDS * threads;
+    const int u0 = partno * span, u1 = min(u0 + span, g.units);
+    if (g.empty) {
+        for (int u = u0 + t; u < u1; u += threads)
+            g.store(u, make_uint4(0, 0, 0, 0));
         return;
     }
+    if (fabsf(g.lse) > FAR) {
+        if (partno == 0)
+            far_row<T>(p, row);
+        return;
+    }
+    const double L = (double)g.lse * 1.4426950408889634074;
+    const float L_hi = (float)L, L_lo = (float)(L - L_hi);
 #pragma unroll 1
     for (int r = 0; r < BWD_ROUNDS; ++r) {
         const int u = u0 + t + r * BWD_BATCH * threads;
@@ -695,14 +733,14 @@ __global__ void __launch_bounds__(THREADS, 5) k_token_grad(const TokenGradArgs p
         for (int i = 0; i < BWD_BATCH; ++i) {
             const int w = u + i * threads;
             if (w < u1)
-                v[i] = w >= whole0 && w < whole1 ? ld_row(x + ((int64_t)w * N - off)) : load_cut(x, w * N - off, V);
+                v[i] = w >= g.whole0 && w < g.whole1 ? ld_row(g.x + ((int64_t)w * N - g.off)) : load_cut(g.x, w * N - g.off, g.V);
         }
 #pragma unroll
         for (int i = 0; i < BWD_BATCH; ++i) {
             const int w = u + i * threads;
             if (w >= u1)
                 break;
-            unit(w, v[i], [](float2 e) { return e; }, L_hi, L_lo);
+            g.unit(p, w, v[i], L_hi, L_lo, [](float2 e) { return e; });
         }
     }
 }
