@@ -16,7 +16,7 @@
 // Bound by memory (2 bytes a value read once, 17/32 written per direction) where there is enough
 // of it: rows of 8192 x 14336 in 48.4 us (0.91 of HBM), both ways 14336 x 4096 in 30.3 (0.87;
 // the phases of a tile), read back 25.7 (0.86).  Small ones are bound by launch and load latency
-// (333 x 18944: 4.6 us, 1 x 4096: 2.0).
+// (333 x 18944: 4.5 us, 1 x 4096: 1.5).
 #include <cuda_runtime.h>
 
 #include "rlq_elem.cuh"
@@ -25,8 +25,9 @@
 namespace rlq {
 namespace {
 
-constexpr int THREADS = 256, WARPS = THREADS / 32;
-constexpr int BOTH_CTAS_SM = 5;
+// Rows' kernels, 1001 x 18944, written and read back: 17.8 us; 18.3 in CTAs of 256, 22.1 of 64.
+constexpr int THREADS = 128, WARPS = THREADS / 32;
+constexpr int BOTH_THREADS = 256, BOTH_CTAS_SM = 5;
 
 // 16-byte global -> shared copy; src_bytes = 0 writes zeros.
 __device__ __forceinline__ void cp_async16_zfill(void *dst, const void *src, uint32_t src_bytes)
@@ -306,7 +307,7 @@ __device__ __forceinline__ void both_tile(const BothArgs &p, uint32_t *tile, uin
     }
 }
 
-__global__ void __launch_bounds__(THREADS, BOTH_CTAS_SM) k_mx_both(const BothArgs p)
+__global__ void __launch_bounds__(BOTH_THREADS, BOTH_CTAS_SM) k_mx_both(const BothArgs p)
 {
     pdl_begin();
     __shared__ __align__(16) uint32_t tile[128 * 68 + 3 * 8];
@@ -393,7 +394,7 @@ cudaError_t launch_quant_mxfp4(const uint16_t *x, int64_t M, int64_t K, int64_t 
 {
     if (qT) {
         const BothArgs p = {x, M, K, ldx, q, ldq, s, qT, ldqT, sT, (int)((K + 127) / 128), (int)((M + 127) / 128)};
-        return launch_pdl(k_mx_both, dim3((unsigned)((int64_t)p.ctiles * p.rtiles)), dim3(THREADS), 0, st, p);
+        return launch_pdl(k_mx_both, dim3((unsigned)((int64_t)p.ctiles * p.rtiles)), dim3(BOTH_THREADS), 0, st, p);
     }
     // Four column tiles a warp where they make a full wave of warps, else two (8192 x 14336: 48.2
     // and 51.6 us; 333 x 18944: 6.1 and 4.6).
