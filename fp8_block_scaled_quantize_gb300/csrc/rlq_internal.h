@@ -139,6 +139,7 @@ struct TokenStatsArgs {
     float *lp, *lse, *entropy;  // [rows]
     int64_t *top_ids;           // [rows][top]
     float *top_lp;              // [rows][top]
+    float inv_hi, inv_lo;       // set by the launch: 1 / temperature as a sum of two floats
 };
 constexpr int MAX_TOKEN_TOP = 64;
 cudaError_t launch_token_stats(const TokenStatsArgs &p, cudaStream_t st);
@@ -152,7 +153,8 @@ struct TokenGradArgs {
     const float *lse, *entropy, *dlp, *dentropy;  // [rows]; dlp or (entropy and) dentropy may be NULL
     void *dlogits;
     int64_t ldd;
-    float c_hi, c_lo;  // set by the launch: log2(e) / temperature as a sum of two floats
+    float c_hi, c_lo;      // set by the launch: log2(e) / temperature as a sum of two floats
+    float inv_hi, inv_lo;  // and 1 / temperature
 };
 cudaError_t launch_token_grad(const TokenGradArgs &p, cudaStream_t st);
 

@@ -69,6 +69,16 @@ __device__ __forceinline__ Sums join(Sums v, float c)
     return {m, s, w};
 }
 
+// m / temperature + ls, rounded once but for ls's last place: the reciprocal is the sum of two floats
+// (rounded to one, it takes up to 2^-24 of m / temperature more, and every probability that the
+// gradient forms of the lse with it: 1.4e-5 next to 256).
+__device__ __forceinline__ float lse_of(float m, float ls, float inv_hi, float inv_lo)
+{
+    const float z = m * inv_hi;
+    // (where that overflows, the low part's product would be an infinity of its own sign)
+    return fabsf(z) < INFINITY ? fmaf(m, inv_hi, fmaf(m, inv_lo, ls)) : z + ls;
+}
+
 // Unsigned integers in the order of the floats, and back (what lies below -inf is -inf).
 __device__ __forceinline__ uint32_t key_of(float x)
 {
@@ -377,7 +387,7 @@ __global__ void __launch_bounds__(THREADS, CTAS_SM) k_token_stats(const TokenSta
     float xt = 0.0f;
     if (t == 0)
         xt = E::load(x + target);
-    const float c = 1.4426950408889634f / p.temperature, inv_t = 1.0f / p.temperature;
+    const float c = 1.4426950408889634f / p.temperature, inv_t = p.inv_hi;
     const float2 c2 = make_float2(c, c);
     float m = -INFINITY;
     float others = -INFINITY;  // (kTop) the largest logit outside the batch of the thread's maximum
@@ -432,7 +442,7 @@ __global__ void __launch_bounds__(THREADS, CTAS_SM) k_token_stats(const TokenSta
         const bool none = o.s == 0.0f;  // every logit is -inf
         // (NaN targets make their sum NaN; +inf - +inf too)
         p.lp[row] = none ? -INFINITY : (xt - o.m) * inv_t - ls;
-        p.lse[row] = none ? -INFINITY : fmaf(o.m, inv_t, ls);
+        p.lse[row] = none ? -INFINITY : lse_of(o.m, ls, p.inv_hi, p.inv_lo);
         p.entropy[row] = none ? 0.0f : LN2 * (l2 - o.w / o.s);
         if (kTop) {
             row_m = o.m;
@@ -621,7 +631,7 @@ struct GradRow {
         const float dlp = p.dlp ? p.dlp[row] : 0.0f, dH = p.dentropy ? p.dentropy[row] : 0.0f;
         lse = p.lse[row];
         empty = target < 0 || target >= V || (dlp == 0.0f && dH == 0.0f);
-        inv = 1.0f / p.temperature;
+        inv = p.inv_hi;
         // (a row that met a NaN has lse NaN, which the maximum below would drop)
         a = lse != lse ? lse : -(dlp + (dH == 0.0f ? 0.0f : dH * p.entropy[row])) * inv;
         b = -dH * LN2 * inv;
@@ -677,7 +687,7 @@ __device__ __noinline__ void far_row(const TokenGradArgs &p, int64_t row)
     const double L = (double)g.lse * 1.4426950408889634074;
     float L_hi = (float)L, L_lo = (float)(L - L_hi);
     const float2 own = row_sums(g.x, g.V, g.off, p.c_hi);
-    const float own_lse = fmaf(own.x, g.inv, LN2 * own.y);
+    const float own_lse = lse_of(own.x, LN2 * own.y, p.inv_hi, p.inv_lo);
     // (an lse that is not these logits' stays what it is; without logits above -inf all is 0)
     const bool same = own_lse == g.lse || fabsf(own_lse - g.lse) <= fabsf(g.lse) * 0x1p-22f;
     const bool none = own.x == -INFINITY && g.lse == -INFINITY;
@@ -757,8 +767,17 @@ cudaError_t launch_grad(const TokenGradArgs &p, cudaStream_t st)
 
 }  // namespace
 
-cudaError_t launch_token_stats(const TokenStatsArgs &p, cudaStream_t st)
+// 1 / temperature as the sum of two floats.
+static void reciprocal(float temperature, float *hi, float *lo)
 {
+    *hi = 1.0f / temperature;
+    *lo = (float)(1.0 / (double)temperature - (double)*hi);
+}
+
+cudaError_t launch_token_stats(const TokenStatsArgs &args, cudaStream_t st)
+{
+    TokenStatsArgs p = args;
+    reciprocal(p.temperature, &p.inv_hi, &p.inv_lo);
     if (p.dtype == RLQ_DTYPE_F32)
         return p.top ? launch_stats<uint32_t, true>(p, st) : launch_stats<uint32_t, false>(p, st);
     return p.top ? launch_stats<uint16_t, true>(p, st) : launch_stats<uint16_t, false>(p, st);
@@ -770,6 +789,7 @@ cudaError_t launch_token_grad(const TokenGradArgs &args, cudaStream_t st)
     const double c = 1.4426950408889634074 / (double)p.temperature;
     p.c_hi = (float)c;
     p.c_lo = (float)(c - (double)p.c_hi);
+    reciprocal(p.temperature, &p.inv_hi, &p.inv_lo);
     return p.dtype == RLQ_DTYPE_F32 ? launch_grad<uint32_t>(p, st) : launch_grad<uint16_t>(p, st);
 }
 
