@@ -789,8 +789,9 @@ Plan make_plan(int64_t M, int64_t N, int64_t K, bool f32, int sms, bool pairs, b
     const double direct = f32 ? 4.5e6 : 2.9e6;  // bytes a microsecond of outputs stored by the lanes
     Plan best = {};
     double least = 1e300;
-    // (a pair's ring is too short for few tokens: 1, 38912 x 1600: 9.4 alone, 14.1)
-    for (int tile = 256; pairs && M > 128 && tile >= 128; tile -= 64) {
+    // (a pair's ring is too short for few tokens: 1, 38912 x 1600: 9.4 alone, 14.1; without a device there
+    // are no SMs, and the launch says so)
+    for (int tile = 256; pairs && sms > 1 && M > 128 && tile >= 128; tile -= 64) {
         const int64_t rows = staged ? M : N, cols = staged ? N : M;
         const int64_t units = ((rows + 255) / 256) * ((cols + tile - 1) / tile), slots = sms / 2;
         const double cost = 4.4 + longer((double)((units + slots - 1) / slots),
