@@ -1013,6 +1013,17 @@ rlq_status rlq_diag_arm_gemm_stall(void)
     return RLQ_OK;
 }
 
+rlq_status rlq_diag_gemm_mxfp4_cut(int64_t M, int64_t N, int64_t K, rlq_dtype dtype, int aligned, int32_t *cut)
+{
+    RLQ_REQUIRE(M > 0 && N > 0 && K > 0, RLQ_ERR_INVALID_ARG, "a size is not positive (M=%lld, N=%lld, K=%lld)",
+                (long long)M, (long long)N, (long long)K);
+    RLQ_REQUIRE(M < MAX_DIM && N < MAX_DIM && K < MAX_DIM, RLQ_ERR_UNSUPPORTED, "dimension beyond 2^31");
+    RLQ_REQUIRE(dtype == RLQ_DTYPE_BF16 || dtype == RLQ_DTYPE_F32, RLQ_ERR_INVALID_ARG, "unknown dtype %d", (int)dtype);
+    RLQ_REQUIRE(cut, RLQ_ERR_INVALID_ARG, "cut is NULL");
+    gemm_mxfp4_cut(M, N, K, dtype == RLQ_DTYPE_F32, aligned != 0, cut);
+    return RLQ_OK;
+}
+
 const char *rlq_status_string(rlq_status status)
 {
     switch (status) {

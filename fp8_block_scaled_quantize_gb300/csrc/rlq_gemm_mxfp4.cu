@@ -830,17 +830,55 @@ Plan make_plan(int64_t M, int64_t N, int64_t K, bool f32, int sms, bool pairs, b
     return best;
 }
 
+// The plan's tiles: (A tile, B tile) units for `slots` pairs, single CTAs or (two to an SM) twice as many.
+struct Cut {
+    Plan plan;
+    bool staged;             // A is X, and y is stored by TMA; else A is W
+    int64_t a_rows, b_rows;
+    int tile_b;              // rows of a B tile
+    int64_t a_tiles, b_tiles;
+    int slots;
+};
+
+Cut make_cut(int64_t M, int64_t N, int64_t K, bool f32, bool pairs, bool aligned)
+{
+    const int sms = device_sms();
+    Cut c;
+    c.plan = make_plan(M, N, K, f32, sms, pairs, aligned);
+    c.staged = c.plan.pair && aligned;
+    c.a_rows = c.staged ? M : N;
+    c.b_rows = c.staged ? N : M;
+    c.tile_b = c.b_rows < c.plan.tile_b ? (int)c.b_rows : c.plan.tile_b;
+    const int tile_a = c.plan.pair ? 2 * BM : BM;
+    c.a_tiles = (c.a_rows + tile_a - 1) / tile_a;
+    c.b_tiles = (c.b_rows + c.tile_b - 1) / c.tile_b;
+    c.slots = c.plan.pair ? sms / 2 : c.plan.two ? 2 * sms : sms;
+    return c;
+}
+
 }  // namespace
+
+void gemm_mxfp4_cut(int64_t M, int64_t N, int64_t K, bool f32, bool aligned, int32_t *cut)
+{
+    const Cut c = make_cut(M, N, K, f32, true, aligned);
+    const int64_t units = c.a_tiles * c.b_tiles;
+    cut[0] = c.plan.pair;
+    cut[1] = c.staged;
+    cut[2] = c.tile_b;
+    cut[3] = c.plan.splits;
+    cut[4] = c.plan.two;
+    cut[5] = c.plan.splits > 1 ? 1 : (int32_t)((units + c.slots - 1) / c.slots);
+}
 
 rlq_status launch_gemm_mxfp4(const uint8_t *xq, int64_t ldxq, const uint8_t *xs, const uint8_t *wq, int64_t ldwq,
                              const uint8_t *ws, void *y, bool f32, int64_t ldy, int64_t M, int64_t N, int64_t K,
                              cudaStream_t st)
 {
-    const int sms = device_sms();
     Params p = {};
     p.y = y;
     p.ldy = ldy;
     if (K == 0) {
+        const int sms = device_sms();
         p.a_rows = (int)N;
         p.b_rows = (int)M;
         const int64_t blocks = (M * N + THREADS - 1) / THREADS;
@@ -854,9 +892,10 @@ rlq_status launch_gemm_mxfp4(const uint8_t *xq, int64_t ldxq, const uint8_t *xs,
     p.timeout_ns = wait_limit_ns();
     p.withhold = take_stall();
     const bool aligned = ((uintptr_t)y & 15) == 0 && ldy * (f32 ? 4 : 2) % 16 == 0;
-    const Plan plan = make_plan(M, N, K, f32, sms, !p.withhold, aligned);
+    const Cut cut = make_cut(M, N, K, f32, !p.withhold, aligned);
+    const Plan &plan = cut.plan;
     const bool pair = plan.pair;
-    p.staged = pair && aligned;
+    p.staged = cut.staged;
     p.ragged = N * (f32 ? 4 : 2) % 16 != 0;
     struct Operand {
         const uint8_t *q;
@@ -866,14 +905,13 @@ rlq_status launch_gemm_mxfp4(const uint8_t *xq, int64_t ldxq, const uint8_t *xs,
     };
     const Operand x = {xq, ldxq, xs, M}, w = {wq, ldwq, ws, N};
     const Operand &A = p.staged ? x : w, &B = p.staged ? w : x;
-    p.a_rows = (int)A.rows;
-    p.b_rows = (int)B.rows;
-    p.tile_b = B.rows < plan.tile_b ? (int)B.rows : plan.tile_b;
-    p.b_tiles = (int)((B.rows + p.tile_b - 1) / p.tile_b);
-    const int64_t a_tiles = (A.rows + (pair ? 2 * BM : BM) - 1) / (pair ? 2 * BM : BM);
-    if (a_tiles * p.b_tiles >= (int64_t)1 << 30)
+    p.a_rows = (int)cut.a_rows;
+    p.b_rows = (int)cut.b_rows;
+    p.tile_b = cut.tile_b;
+    p.b_tiles = (int)cut.b_tiles;
+    if (cut.a_tiles * cut.b_tiles >= (int64_t)1 << 30)
         return fail(RLQ_ERR_UNSUPPORTED, "output of %lld x %lld has too many tiles", (long long)M, (long long)N);
-    p.units = (int)a_tiles * p.b_tiles;
+    p.units = (int)(cut.a_tiles * cut.b_tiles);
     p.splits = plan.splits;
     p.kps = (p.kstages + p.splits - 1) / p.splits;
 
@@ -897,7 +935,6 @@ rlq_status launch_gemm_mxfp4(const uint8_t *xq, int64_t ldxq, const uint8_t *xs,
     p.overlap = n16 > 224;
     const int room = (two ? 232448 / 2 - 1024 : 232448) - 1024 - BARS_BYTES - (pair ? STAGING_BYTES : 0);
     p.stages = room / p.stage_bytes < MAX_STAGES ? room / p.stage_bytes : MAX_STAGES;
-    const int slots = pair ? sms / 2 : two ? 2 * sms : sms;
     p.splits_inv = (uint32_t)((65536 + p.splits - 1) / p.splits);
     CUtensorMap maps[5] = {};
     rlq_status r = encode(&maps[0], A.q, false, (K + 1) / 2, A.rows, A.ld, BM);
@@ -911,7 +948,7 @@ rlq_status launch_gemm_mxfp4(const uint8_t *xq, int64_t ldxq, const uint8_t *xs,
         r = encode_out(&maps[4], y, f32, M, N, ldy);
     if (r != RLQ_OK)
         return r;
-    const int work = p.units < slots ? p.units : slots;
+    const int work = p.units < cut.slots ? p.units : cut.slots;
     if (pair)
         return f32 ? launch<true, true>(maps, p, 2 * work, 2, st) : launch<true, false>(maps, p, 2 * work, 2, st);
     const int grid = p.splits > 1 ? p.splits * p.units : work;

@@ -242,6 +242,8 @@ cudaError_t launch_dequant_mxfp4(const uint8_t *q, int64_t ldq, const uint8_t *s
 rlq_status launch_gemm_mxfp4(const uint8_t *xq, int64_t ldxq, const uint8_t *xs, const uint8_t *wq, int64_t ldwq,
                              const uint8_t *ws, void *y, bool f32, int64_t ldy, int64_t M, int64_t N, int64_t K,
                              cudaStream_t st);
+// How the current device cuts that product (rlq_diag_gemm_mxfp4_cut).
+void gemm_mxfp4_cut(int64_t M, int64_t N, int64_t K, bool f32, bool aligned, int32_t *cut);
 // Its translation unit's error word, read and cleared (0: none).
 cudaError_t take_mxfp4_error_word(cudaStream_t st, unsigned long long *word);
 

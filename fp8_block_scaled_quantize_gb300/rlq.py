@@ -68,6 +68,7 @@ _SIGS = {
     "rlq_check": [_P],
     "rlq_diag_bounded_wait": [_I, _P],
     "rlq_diag_arm_gemm_stall": [],
+    "rlq_diag_gemm_mxfp4_cut": [_I, _I, _I, ctypes.c_int, ctypes.c_int, _P],
 }
 
 STATUS = {0: "RLQ_OK", 1: "RLQ_ERR_INVALID_ARG", 2: "RLQ_ERR_UNSUPPORTED", 3: "RLQ_ERR_MISALIGNED",
@@ -315,6 +316,14 @@ def rlq_diag_bounded_wait(timeout_us, stream):
 
 def rlq_diag_arm_gemm_stall():
     return _call("rlq_diag_arm_gemm_stall")
+
+
+def rlq_diag_gemm_mxfp4_cut(M, N, K, dtype, aligned) -> tuple:
+    """(pairs, staged outputs, rows of a tile, CTAs that share a contraction, two CTAs to an SM, tiles
+    of the busiest CTA or pair)."""
+    out = (ctypes.c_int32 * 6)()
+    _call("rlq_diag_gemm_mxfp4_cut", M, N, K, dtype, int(aligned), out)
+    return tuple(out)
 
 
 def rlq_status_string(status: int) -> str:

@@ -799,6 +799,21 @@ rlq_status rlq_diag_bounded_wait(int64_t timeout_us, rlq_stream_t stream);
  */
 rlq_status rlq_diag_arm_gemm_stall(void);
 
+/*
+ * Diagnostic: how rlq_gemm_mxfp4 cuts a product of these sizes on the current device, so that
+ * a test can tell which of the kernel's paths its shapes take.  `aligned`: y and its pitch are on
+ * 16-byte boundaries.  cut (host memory, 6 entries, output):
+ *   [0] 1: CTA pairs, 0: single CTAs
+ *   [1] 1: outputs staged in shared memory and stored by TMA, 0: by the lanes
+ *   [2] rows of a tile: with [1] of W, else tokens (pairs: by 256 of the other operand; single
+ *       CTAs: by 128 rows of W)
+ *   [3] CTAs that share a tile's contraction, 1 .. 8
+ *   [4] 1: two CTAs to an SM
+ *   [5] tiles that the busiest CTA or pair works on
+ * M, N, K >= 1.  Host-only.
+ */
+rlq_status rlq_diag_gemm_mxfp4_cut(int64_t M, int64_t N, int64_t K, rlq_dtype dtype, int aligned, int32_t *cut);
+
 /* Static description of a status code. */
 const char *rlq_status_string(rlq_status status);
 
