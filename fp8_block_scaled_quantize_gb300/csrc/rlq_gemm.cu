@@ -1108,6 +1108,15 @@ uint64_t wait_limit_ns()
     return ns;
 }
 
+bool pair_mode_enabled()
+{
+    static const bool on = [] {
+        const char *e = std::getenv("RLQ_GEMM_PAIR");
+        return !(e && e[0] == '0');
+    }();
+    return on;
+}
+
 rlq_status encode_tile_map(CUtensorMap_st *map, const void *base, bool bf16, int64_t rows, int64_t cols, int64_t ld)
 {
     auto enc = get_encode_fn();
@@ -1209,16 +1218,6 @@ int plan_splits(int64_t R, int64_t C, int64_t L, int sms, int64_t ws_cap)
         }
     }
     return best;
-}
-
-// Pairs of CTAs (cta_group::2 MMAs) unless RLQ_GEMM_PAIR=0 is set in the environment.
-bool pair_mode_enabled()
-{
-    static const bool on = [] {
-        const char *e = std::getenv("RLQ_GEMM_PAIR");
-        return !(e && e[0] == '0');
-    }();
-    return on;
 }
 
 template <int kMode, bool kBMN, bool kPair>

@@ -860,7 +860,7 @@ Cut make_cut(int64_t M, int64_t N, int64_t K, bool f32, bool pairs, bool aligned
 
 void gemm_mxfp4_cut(int64_t M, int64_t N, int64_t K, bool f32, bool aligned, int32_t *cut)
 {
-    const Cut c = make_cut(M, N, K, f32, true, aligned);
+    const Cut c = make_cut(M, N, K, f32, pair_mode_enabled(), aligned);
     const int64_t units = c.a_tiles * c.b_tiles;
     cut[0] = c.plan.pair;
     cut[1] = c.staged;
@@ -892,7 +892,7 @@ rlq_status launch_gemm_mxfp4(const uint8_t *xq, int64_t ldxq, const uint8_t *xs,
     p.timeout_ns = wait_limit_ns();
     p.withhold = take_stall();
     const bool aligned = ((uintptr_t)y & 15) == 0 && ldy * (f32 ? 4 : 2) % 16 == 0;
-    const Cut cut = make_cut(M, N, K, f32, !p.withhold, aligned);
+    const Cut cut = make_cut(M, N, K, f32, pair_mode_enabled() && !p.withhold, aligned);
     const Plan &plan = cut.plan;
     const bool pair = plan.pair;
     p.staged = cut.staged;

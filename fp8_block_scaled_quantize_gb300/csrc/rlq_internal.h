@@ -161,6 +161,8 @@ cudaError_t launch_token_grad(const TokenGradArgs &p, cudaStream_t st);
 // ---- device-side waits and tensor maps (rlq_gemm.cu) ----
 // Limit of a device-side wait (RLQ_WAIT_TIMEOUT_MS, default one second).
 uint64_t wait_limit_ns();
+// Pairs of CTAs (cta_group::2 MMAs) unless RLQ_GEMM_PAIR=0 is set in the environment.
+bool pair_mode_enabled();
 // Tensor map of a bf16 or 8-bit matrix [rows][cols], pitch ld elements, for loads of
 // 128 x 128 boxes, unswizzled; what lies outside the matrix arrives as zeros.
 rlq_status encode_tile_map(struct CUtensorMap_st *map, const void *base, bool bf16, int64_t rows, int64_t cols,

@@ -1,5 +1,9 @@
 """GPU tests of the MXFP4 product on CTA pairs, every width of tile with either way out, and of which
 cuts the product's shapes take on the device that the tests run on."""
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -77,3 +81,30 @@ def gen(seed):
     g = torch.Generator(device=DEV)
     g.manual_seed(seed)
     return g
+
+
+_MODE_SCRIPT = """
+import sys, torch
+sys.path[:0] = [sys.argv[1], sys.argv[1] + "/tests"]
+import mx_ref as R
+from fp8_block_scaled_quantize_gb300 import rlq
+g = torch.Generator(device="cuda")
+g.manual_seed(5)
+for M, N, K in ((258, 9792, 1081), (7405, 259, 1625), (2100, 1024, 1056)):
+    xq, xs, x = R.operand(g, M, K, -1, 1)
+    wq, ws, w = R.operand(g, N, K, -1, 1)
+    y = rlq.gemm_mxfp4(xq, xs, wq, ws, out_dtype=torch.float32)
+    rlq.check()
+    assert torch.equal(y.double(), x @ w.t())
+    print(rlq.rlq_diag_gemm_mxfp4_cut(M, N, K, rlq.DTYPE_F32, N % 4 == 0)[0])
+"""
+
+
+@pytest.mark.parametrize("mode,pairs", [("0", {"0"}), ("1", {"1"})])
+def test_no_pairs_where_the_environment_says_so(mode, pairs):
+    """RLQ_GEMM_PAIR=0 (no CTA pairs) holds for this product as for the others, and the sums are the same."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", _MODE_SCRIPT, root], env=dict(os.environ, RLQ_GEMM_PAIR=mode), capture_output=True,
+                       text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
+    assert set(r.stdout.split()) == pairs
