@@ -319,24 +319,23 @@ __global__ void __launch_bounds__(THREADS)
             }
         }
         if (one) {
-            if constexpr (kPair) {
-                if (!ok) {
-                    // the copies complete on the even CTA's barriers: give them time to land
+            // behind the MMA warp's last commit a normal run has consumed every copy; a
+            // CTA that gave up waits (bounded) for those still in flight
+            volatile uint32_t never = 0;
+            mbar_wait(teardown, 0, &never, p.timeout_ns, SITE_TEARDOWN);
+            if (!ok || *abort_flag || p.withhold) {
+                int first = it > p.stages ? it - p.stages : 0;
+                if (p.withhold && first == 0)
+                    first = 1;
+                // (pairs: both CTAs' copies complete on the even CTA's barriers, and neither CTA leaves
+                // before the other)
+                for (int j = first; (!kPair || rank == 0) && j < it; ++j)
+                    mbar_wait(full(j % p.stages), (uint32_t)(j / p.stages) & 1u, &never, 20000000ull, SITE_DRAIN);
+                if (kPair) {
+                    // a stage that only one of the two asked for never completes: time to land
                     const uint64_t t0 = global_timer_ns();
                     while (global_timer_ns() - t0 < 200000ull)
                         __nanosleep(1000);
-                }
-            } else {
-                // behind the MMA warp's last commit a normal run has consumed every copy; a
-                // CTA that gave up waits (bounded) for those still in flight
-                volatile uint32_t never = 0;
-                mbar_wait(teardown, 0, &never, p.timeout_ns, SITE_TEARDOWN);
-                if (!ok || *abort_flag || p.withhold) {
-                    int first = it > p.stages ? it - p.stages : 0;
-                    if (p.withhold && first == 0)
-                        first = 1;
-                    for (int j = first; j < it; ++j)
-                        mbar_wait(full(j % p.stages), (uint32_t)(j / p.stages) & 1u, &never, 20000000ull, SITE_DRAIN);
                 }
             }
         }
@@ -892,7 +891,7 @@ rlq_status launch_gemm_mxfp4(const uint8_t *xq, int64_t ldxq, const uint8_t *xs,
     p.timeout_ns = wait_limit_ns();
     p.withhold = take_stall();
     const bool aligned = ((uintptr_t)y & 15) == 0 && ldy * (f32 ? 4 : 2) % 16 == 0;
-    const Cut cut = make_cut(M, N, K, f32, pair_mode_enabled() && !p.withhold, aligned);
+    const Cut cut = make_cut(M, N, K, f32, pair_mode_enabled(), aligned);
     const Plan &plan = cut.plan;
     const bool pair = plan.pair;
     p.staged = cut.staged;

@@ -788,7 +788,8 @@ rlq_status rlq_diag_bounded_wait(int64_t timeout_us, rlq_stream_t stream);
  * FProp / DGrad / WGrad entry points, rlq_gemm_gated_fprop of more than 8 tokens,
  * rlq_gemm_mxfp4) or
  * in the next rlq_gated_backward, whichever is first.  A GEMM's launch runs on
- * single CTAs, and the TMA producer of every CTA withholds the loads of its first pipeline
+ * single CTAs (rlq_gemm_mxfp4's as it is cut, on pairs too), and the TMA producer of every CTA
+ * withholds the loads of its first pipeline
  * stage, so nothing ever arrives on that stage's barrier: the MMA warp's
  * bounded wait runs out (RLQ_WAIT_TIMEOUT_MS, 1 s by default), it records a
  * timeout and raises the CTA's abort flag, and the CTA drains its copies in

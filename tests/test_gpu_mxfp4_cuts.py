@@ -108,3 +108,26 @@ def test_no_pairs_where_the_environment_says_so(mode, pairs):
                        text=True, timeout=300)
     assert r.returncode == 0, r.stderr[-2000:]
     assert set(r.stdout.split()) == pairs
+
+
+@pytest.mark.parametrize("M,N,K,dtype", [(2100, 1024, 1056, "f32"), (2100, 5120, 512, "bf16"), (7405, 259, 1625, "f32"),
+                                         (258, 9792, 1081, "bf16"), (1000, 3000, 64, "bf16"), (132, 20533, 1482, "f32")])
+def test_a_pairs_bounded_wait_runs_out_and_the_next_call_is_right(M, N, K, dtype):
+    """The diagnostic withholds both CTAs' first loads: one tile a pair and several, either way out, a
+    ring that fills up and one that does not.  Every wait ends, the copies in flight are waited for,
+    the error is reported once, and the next call is right."""
+    g = gen(31)
+    t = DTYPES[dtype][0]
+    assert cut(M, N, K, dtype)[0] == 1
+    xq, xs, x = R.operand(g, M, K, -1, 1)
+    wq, ws, w = R.operand(g, N, K, -1, 1)
+    want = (x @ w.t()).float().to(t)
+    rlq.rlq_diag_arm_gemm_stall()
+    rlq.gemm_mxfp4(xq, xs, wq, ws, out_dtype=t)
+    with pytest.raises(rlq.RlqError) as e:
+        rlq.check()
+    assert e.value.status == 5 and "MXFP4" in str(e.value)
+    rlq.check()
+    for _ in range(2):
+        assert torch.equal(rlq.gemm_mxfp4(xq, xs, wq, ws, out_dtype=t), want)
+        rlq.check()
