@@ -149,7 +149,7 @@ __device__ __forceinline__ void st_async4(uint32_t addr, uint32_t bar, const uin
 // The cluster's barrier without an order of memory (a release would wait for this thread's
 // part of a saturated memory system): what has to be seen behind it is either the
 // initialisation of barriers, which has a fence of its own, or comes with a barrier's count.
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_arrive_relaxed() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
 template <bool kF32>
@@ -271,7 +271,7 @@ __global__ void __launch_bounds__(THREADS)
     tc_fence_before();
     __syncthreads();
     if (group > 1)
-        cluster_arrive();  // this CTA's barriers are initialised
+        cluster_arrive_relaxed();  // this CTA's barriers are initialised
     if (kPair)
         cluster_wait();  // and the other's
     tc_fence_after();
@@ -426,7 +426,7 @@ __global__ void __launch_bounds__(THREADS)
             if (!kPair && p.splits > 1) {
                 // every CTA's stages are used up: their memory takes the parts
                 cluster_wait();
-                cluster_arrive();
+                cluster_arrive_relaxed();
                 cluster_wait();
                 met = true;
             }
@@ -532,7 +532,7 @@ __global__ void __launch_bounds__(THREADS)
         // One unit a cluster.  The warps that have met the others' barrier add the parts.
         if (!met) {
             cluster_wait();
-            cluster_arrive();
+            cluster_arrive_relaxed();
             cluster_wait();
         }
         if (warp >= EPI_WARP0) {
@@ -590,7 +590,7 @@ __global__ void __launch_bounds__(THREADS)
         }
     }
     if (group > 1) {  // no CTA leaves while another may still signal it
-        cluster_arrive();
+        cluster_arrive_relaxed();
         cluster_wait();
     }
     if (warp == 1) {
