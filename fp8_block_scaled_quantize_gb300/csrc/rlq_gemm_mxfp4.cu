@@ -26,12 +26,13 @@
 //     SMs, a cluster of up to 8 CTAs shares a tile's contraction; each CTA sends its part, 16 bytes
 //     at a time, to the CTA that adds those tokens, parts in rank order (read from the
 //     others' memory instead, 256 x 4096 x 4096 took 16.2 us for 11.8).
-// Bound by: few tokens, the weights' bytes (64 tokens, 128256 x 4096, fp32 out: 52 us, 0.89 of HBM; one
-// token, 14336 x 4096: 9.5 us, 0.49: start, first loads and end are half of it); many tokens,
+// Bound by: few tokens, the weights' bytes (64 tokens, 128256 x 4096, fp32 out: 52 us, 0.88 of HBM; one
+// token, 14336 x 4096: 9.5-10.0 us, 0.46-0.48: start, first loads and end are half of it); many tokens,
 // shared memory, which the copies fill with 35 KB a stage while the MMAs read both operands from
-// it (8192 x 14336 x 4096: 145 us, 6.6 PFLOP/s, 0.86 of four times the bf16 rate; without
+// it (8192 x 14336 x 4096: 145 us, 6.6 PFLOP/s, 0.88 of four times the bf16 rate; without
 // the copies 132, with a quarter of the MMAs 120); short contractions, the outputs.
-// Every wait is bounded as in the FP8 GEMM; what ran out is reported by rlq_check.
+// Every wait is bounded as in the FP8 GEMM; what ran out is reported by rlq_check, and a CTA that gave up
+// waits for its copies in flight before it leaves.  No pairs where RLQ_GEMM_PAIR=0.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>

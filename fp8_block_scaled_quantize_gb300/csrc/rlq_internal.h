@@ -17,8 +17,8 @@ namespace rlq {
 // the stream be scheduled as soon as every block of this grid has started.  The
 // next kernel's blocks can then be resident and waiting when this grid ends,
 // instead of being launched only afterwards.  No kernel reads or writes global memory
-// before the wait (the gated block's kernels send L2 prefetch hints for their weights), so
-// the ordering of the stream is unchanged.
+// before the wait (the gated block's kernels and the MXFP4 product send L2 prefetch hints for
+// their weights), so the ordering of the stream is unchanged.
 #ifdef __CUDACC__
 __device__ __forceinline__ void pdl_begin()
 {

@@ -14,8 +14,8 @@
 // columns of each at a time: their 16 scale bytes are one piece.
 //
 // Bound by memory (2 bytes a value read once, 17/32 written per direction) where there is enough
-// of it: rows of 8192 x 14336 in 48.4 us (0.91 of HBM), both ways 14336 x 4096 in 30.3 (0.87;
-// the phases of a tile), read back 25.7 (0.86).  Small ones are bound by launch and load latency
+// of it: rows of 8192 x 14336 in 48.4 us (0.90 of HBM), both ways 14336 x 4096 in 30.3 (0.87;
+// the phases of a tile), read back 25.7 (0.85).  Small ones are bound by launch and load latency
 // (333 x 18944: 4.5 us, 1 x 4096: 1.5).
 #include <cuda_runtime.h>
 

@@ -919,7 +919,8 @@ def token_logprobs_top(logits: torch.Tensor, targets: torch.Tensor, top: int = 0
     """Log probabilities of the int64 ``targets`` under bf16 or fp32 ``logits`` [rows, V]
     divided by ``temperature``, each row's log-sum-exp and entropy, and the ``top`` (at most
     64, or V) most likely tokens with their log probabilities, among equal logits the lowest
-    token first.
+    token first.  Masks should be -inf: where numbers such as -1e9 leave a row fewer tokens than
+    ``top``, it takes many times as long.
 
     Returns (lp [rows] f32, lse [rows] f32, entropy [rows] f32, ids [rows, top] int64,
     top_lp [rows, top] f32)."""
